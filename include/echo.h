@@ -427,6 +427,184 @@ typedef struct echo_mla_args {
 int echo_mla_workspace_bytes(int32_t B, int32_t n_q, int32_t k, size_t *bytes);
 int echo_sparse_mla_decode(const echo_mla_args *args, void *stream);
 
+/*
+ * Block rows (block-level / GQA variant): the layouts the block calls below read and
+ * write.  A row holds block_tokens tokens of one KV head, keys and values of head_dim
+ * each; block_tokens is a multiple of 16, head_dim is 64 or 128, and the row's length in
+ * 16-bit elements (echo_block_row_elems, at most 65536) is the echo_pool.row_elems of a
+ * pool of such rows.
+ *   ECHO_BLOCK_BF16  [2][block_tokens][head_dim] bf16: keys, then values
+ *   ECHO_BLOCK_FP4   sub-blocks of 16 tokens, 18 * head_dim bytes each:
+ *       key codes    [16 tokens][head_dim / 2]
+ *       value codes  [2][8][8 tokens][head_dim / 16]: half p holds tokens 8p..8p+7, part r
+ *                    dims r * head_dim / 8 and up
+ *       key scales   [16 tokens][head_dim / 16]
+ *       value scales [2][head_dim / 16][8 tokens]
+ *     A code is an e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit), two to a byte,
+ *     the lower dimension in the low nibble; a scale is an e4m3 number, one per token and
+ *     16 dimensions; an entry stands for code * scale, exactly representable in bf16.
+ *     Written as s = e4m3(max |x| / 6) (round to nearest even, at most 448) and the
+ *     nearest code to x / s (ties to the even code): 4.5 bits per entry.  Values above
+ *     2688 saturate, infinities and NaN are not kept, and a zero may carry either sign.
+ * With a table shared by the KV heads, block `id` of KV head h is row id * n_kv_heads + h.
+ */
+#define ECHO_BLOCK_BF16 0
+#define ECHO_BLOCK_FP4 1
+
+int echo_block_row_elems(int32_t format, int32_t block_tokens, int32_t head_dim, int32_t *row_elems);
+
+/*
+ * Block tables and slot maps from request lengths: request b goes from old_len[b] to
+ * new_len[b] tokens (either way), its blocks come from and return to a stack of free block
+ * ids.  With nb(n) = ceil(n / block_tokens):
+ *   shrinking requests push table[b][nb(new) .. nb(old)) in (b, i) order onto the stack;
+ *   then growing requests pop, in (b, i) order, the entries table[b][nb(old) .. nb(new)).
+ *   A request whose growth no longer fits gets nothing, nor does any later one that needs
+ *   a block (ECHO_DEV_POOL_EXHAUSTED); what it had stays.
+ *   The new tokens of all requests, in (b, position) order, are listed in
+ *   slot_map[i] = table[b][p / block_tokens] * block_tokens + p % block_tokens and
+ *   positions[i] = p, request b's from cu_new[b] on; both are -1 for a request left
+ *   without its blocks and for the entries after the last token.
+ *   old_len, new_len [B] int32 device
+ *   table       [B][max_blocks] int32 device; entries past nb(new) are left as they were
+ *   free_blocks [n_blocks] int32 device: the stack's entries 0 .. *free_count
+ *   free_count, free_count_out [1] int32 device, different addresses: the stack's height
+ *               before and after (hand the second to the next call as its first)
+ *   slot_map, positions [max_new] int32 device (positions optional)
+ *   cu_new      [B + 1] int32 device, optional: exclusive sums of the new tokens, total last
+ *   len_out     [B] int32 device, optional, none of the inputs: the lengths in effect (a
+ *               request left without its blocks keeps old_len)
+ * A length outside [0, max_blocks * block_tokens] is clamped, more than max_new new tokens
+ * are left out of the lists, a stack height outside [0, n_blocks] is clamped and ids
+ * outside [0, n_blocks) are not handed out; each sets ECHO_DEV_BAD_INDEX.  All buffers but
+ * `table` and `free_blocks` are read-only or write-only, so a call repeated on the same
+ * inputs gives the same outputs.  Limits: B <= 16384, B * max_blocks * block_tokens and
+ * n_blocks * block_tokens below 2^31.  Launches 1 kernel.
+ */
+typedef struct echo_block_tables_args {
+    const int32_t *old_len;
+    const int32_t *new_len;
+    int32_t B, block_tokens;
+    int32_t *table;
+    int32_t *free_blocks;
+    int32_t max_blocks, n_blocks;
+    const int32_t *free_count;
+    int32_t *free_count_out;
+    int32_t *slot_map;
+    int32_t *positions;
+    int32_t *cu_new;
+    int32_t *len_out;
+    int32_t max_new;
+    int32_t *dev_status;
+} echo_block_tables_args;
+
+int echo_block_tables(const echo_block_tables_args *args, void *stream);
+
+/*
+ * Queries and keys of T new tokens, normalised per head, rotated, and the keys and values
+ * written to their cache rows, in one pass over the projections' output:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (per head; a NULL weight: y = x)
+ *   pairs (a, b) of y's first rope_dim entries become (a cos - b sin, b cos + a sin) with
+ *   the cosine and sine of the token's position; the other entries stay.
+ * All in fp32, rounded to bf16 once; the values v pass through unchanged.  ECHO_BLOCK_FP4
+ * rows then quantise the bf16 keys and values.
+ *   q  [T][n_heads][head_dim] bf16, k, v [T][n_kv_heads][head_dim] bf16: device, 16-byte
+ *      aligned, tokens q_stride / k_stride / v_stride elements apart (multiples of 8), e.g.
+ *      slices of one fused projection.  v is optional without a cache and v_out
+ *   q_weight, k_weight [head_dim] fp32 device, optional
+ *   cos_sin  [max_pos][rope_dim] fp32 device, 16-byte aligned: rope_dim / 2 cosines, then
+ *      the sines, of each position
+ *   interleaved  0: pairs are (i, i + rope_dim / 2); 1: (2i, 2i + 1)
+ *   positions  [T] int32 device; a negative one marks a padding token: it is left out
+ *      altogether; one >= max_pos is left out with ECHO_DEV_BAD_INDEX
+ *   q_out    [T][n_heads][head_dim] bf16 (may be q itself when q is contiguous)
+ *   k_out, v_out [T][n_kv_heads][head_dim] bf16, optional: the keys and values as a later
+ *      read of the cache gives them (ECHO_BLOCK_FP4: after quantisation)
+ *   slot_map [T] int32 device, optional (NULL: no cache write): token i goes to token
+ *      slot % block_tokens of block slot / block_tokens; negative: not written.  A row
+ *      outside [0, n_rows) sets ECHO_DEV_BAD_INDEX and is not written; two tokens of one
+ *      call with the same slot leave one of the two there
+ *   rows     [n_rows][R] cache rows, 16-byte aligned: device memory, or the pinned, mapped
+ *      host pool (written through)
+ * rope_dim is a multiple of 16 up to head_dim.  Launches 1 kernel.
+ */
+typedef struct echo_qk_norm_rope_args {
+    const uint16_t *q;
+    const uint16_t *k;
+    const uint16_t *v;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t T, n_heads, n_kv_heads, head_dim;
+    const float *q_weight;
+    const float *k_weight;
+    float eps;
+    int32_t interleaved;
+    const float *cos_sin;
+    int32_t max_pos, rope_dim;
+    const int32_t *positions;
+    uint16_t *q_out;
+    uint16_t *k_out;
+    uint16_t *v_out;
+    const int32_t *slot_map;
+    uint16_t *rows;
+    int32_t n_rows, format, block_tokens;
+    int32_t *dev_status;
+} echo_qk_norm_rope_args;
+
+int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
+
+/*
+ * Decode attention over block rows (grouped-query: n_heads / n_kv_heads query heads share
+ * a KV head).  Query j of request b stands at position len - 1 of a context of
+ * len = ctx_len[b] - (n_q - 1 - j) tokens and sees the tokens
+ *   p < len  and  (window == 0  or  p >= len - window  or  p < sinks)
+ * whose block is held: s_p = scale * q . k_p, out = sum_p softmax(s)_p v_p,
+ * lse = log sum_p exp(s_p); no token: out = 0, lse = -inf.
+ *   q       [B][n_q][n_heads][head_dim] bf16 device, 16-byte aligned
+ *   rows    [n_rows][R] cache rows of `format`, 16-byte aligned (a pool's gpu_kv, or any
+ *           array of rows)
+ *   table   int32 device.  sel == NULL: entry i covers tokens i * block_tokens and up,
+ *           [B][max_blocks] block ids shared by the KV heads when table_heads == 1,
+ *           [B][n_kv_heads][max_blocks] rows when table_heads == n_kv_heads (such as the
+ *           out_slot of a recall with the KV heads folded into the requests); only entries
+ *           that some query sees are read.  A negative entry is a block that is not held;
+ *           one outside the rows also sets ECHO_DEV_BAD_INDEX
+ *   sel     optional, laid out as table: entry i covers the tokens of block sel[..][i] (a
+ *           selection's block indices; negative: no entry).  Each entry counts, also when
+ *           a block is listed twice; the n_q queries share the list
+ *   ctx_len [B] int32 device; above max_blocks * block_tokens (sel == NULL) it is clamped
+ *           with ECHO_DEV_BAD_INDEX
+ *   out     [B][n_q][n_heads][head_dim] bf16 device; lse [B][n_q][n_heads] fp32 device,
+ *           optional
+ *   workspace  device, 256-byte aligned, echo_block_attention_workspace_bytes() bytes; one
+ *           workspace serves calls that run one after another
+ * Tokens no query of the request sees may hold any bytes.  Scores, the softmax and both
+ * sums are fp32; the softmax weights enter the value product in 16 bits (bf16 rows: bf16,
+ * ECHO_BLOCK_FP4: fp16).  ECHO_BLOCK_FP4 takes the queries to fp16 scaled by a power of two
+ * of their row: an entry below 2^-24 of its row's largest is rounded to that grid.
+ * 1 <= n_q <= 64, n_q * n_heads / n_kv_heads <= 1024.  Launches 1 kernel, or 2 when
+ * contexts are split over several CTAs (the second merges their partial results).
+ */
+typedef struct echo_block_attention_args {
+    const uint16_t *q;
+    const uint16_t *rows;
+    int32_t n_rows, format, block_tokens, head_dim;
+    const int32_t *table;
+    const int32_t *sel;
+    int32_t table_heads, max_blocks;
+    const int32_t *ctx_len;
+    int32_t B, n_q, n_heads, n_kv_heads;
+    int32_t sinks, window;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *dev_status;
+} echo_block_attention_args;
+
+int echo_block_attention_workspace_bytes(int32_t rows_per_kv_head, int32_t head_dim, size_t *bytes);
+int echo_block_attention(const echo_block_attention_args *args, void *stream);
+
 /* Stages of echo_decode_step, in order (timing events are recorded before each
    stage and after the last).  The EMA is computed by the recall's last kernel, so
    the ECHO_STAGE_EMA interval is empty; the constant is kept for the event layout. */
@@ -584,7 +762,8 @@ const char *echo_last_error_string(void);
 /* Library version, (major << 16) | minor (1.1: echo_stage's direct-to-slot fields;
    1.2: echo_prefill_indexer_score, echo_ema_update_strided, n_q up to 65536 in
    top-k and recall; 1.3: echo_sparse_mla_decode; 1.4: echo_pool.row_elems,
-   echo_stage.flags; 1.5: echo_pool_validate, echo_pool_validate_host). */
+   echo_stage.flags; 1.5: echo_pool_validate, echo_pool_validate_host; 1.6: block rows,
+   echo_block_tables, echo_qk_norm_rope, echo_block_attention). */
 int32_t echo_version(void);
 
 /* Storage law of the metadata arrays of one pool (section 5.1): 4*n_h + 13*n_g. */

@@ -28,11 +28,13 @@ VAL_FIELDS = ("slot_state", "slot_map", "row_map", "counter", "reserve", "free",
 INF = 0x7FFFFFFF
 H_INDEX, D_INDEX, KV_ELEMS, KV_BYTES = 64, 128, 576, 1152
 STAGE_APPEND, STAGE_INDEXER, STAGE_TOPK, STAGE_RECALL, STAGE_EMA, NUM_STAGES = range(6)
+BLOCK_BF16, BLOCK_FP4 = 0, 1
 STAT_FIELDS = ("steps", "selected", "unique_rows", "hits", "misses", "recalled", "unrecalled",
                "evicted", "staged", "staged_used", "appended")
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 
 class EchoError(RuntimeError):
@@ -83,6 +85,29 @@ class c_step_args(ctypes.Structure):
                 ("stage_events", ctypes.POINTER(_P))]
 
 
+class c_block_tables_args(ctypes.Structure):
+    _fields_ = [("old_len", _P), ("new_len", _P), ("B", _I32), ("block_tokens", _I32), ("table", _P),
+                ("free_blocks", _P), ("max_blocks", _I32), ("n_blocks", _I32), ("free_count", _P),
+                ("free_count_out", _P), ("slot_map", _P), ("positions", _P), ("cu_new", _P), ("len_out", _P),
+                ("max_new", _I32), ("dev_status", _P)]
+
+
+class c_qk_norm_rope_args(ctypes.Structure):
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("q_stride", _I64), ("k_stride", _I64), ("v_stride", _I64),
+                ("T", _I32), ("n_heads", _I32), ("n_kv_heads", _I32), ("head_dim", _I32), ("q_weight", _P),
+                ("k_weight", _P), ("eps", ctypes.c_float), ("interleaved", _I32), ("cos_sin", _P), ("max_pos", _I32),
+                ("rope_dim", _I32), ("positions", _P), ("q_out", _P), ("k_out", _P), ("v_out", _P), ("slot_map", _P),
+                ("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32), ("dev_status", _P)]
+
+
+class c_block_attention_args(ctypes.Structure):
+    _fields_ = [("q", _P), ("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32),
+                ("head_dim", _I32), ("table", _P), ("sel", _P), ("table_heads", _I32), ("max_blocks", _I32),
+                ("ctx_len", _P), ("B", _I32), ("n_q", _I32), ("n_heads", _I32), ("n_kv_heads", _I32),
+                ("sinks", _I32), ("window", _I32), ("scale", ctypes.c_float), ("out", _P), ("lse", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("dev_status", _P)]
+
+
 _lib = None
 
 
@@ -116,6 +141,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "echo_prefill_indexer_score": ([ctypes.POINTER(c_prefill_args), _P], S),
         "echo_mla_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)], S),
         "echo_sparse_mla_decode": ([ctypes.POINTER(c_mla_args), _P], S),
+        "echo_block_row_elems": ([_I32, _I32, _I32, ctypes.POINTER(_I32)], S),
+        "echo_block_tables": ([ctypes.POINTER(c_block_tables_args), _P], S),
+        "echo_qk_norm_rope": ([ctypes.POINTER(c_qk_norm_rope_args), _P], S),
+        "echo_block_attention_workspace_bytes": ([_I32, _I32, ctypes.POINTER(ctypes.c_size_t)], S),
+        "echo_block_attention": ([ctypes.POINTER(c_block_attention_args), _P], S),
         "echo_decode_step": ([ctypes.POINTER(c_step_args), _P], S),
         "echo_decode_step_host": ([ctypes.POINTER(c_step_args), _P, _P, _P, _I32], S),
         "echo_step_graph_create": ([ctypes.POINTER(c_step_args), ctypes.POINTER(_P)], S),
@@ -415,6 +445,182 @@ def echo_ema_update_strided(s_hat, kth, kth_stride: int, alpha: float = 0.5, str
     _check(load_library().echo_ema_update_strided(_dev(s_hat, "s_hat"), _dev(kth, "kth"), int(s_hat.numel()),
                                                   int(kth_stride), float(alpha), _stream(stream)),
            "echo_ema_update_strided")
+
+
+# ---------------------------------------------------------------------------
+# block rows (block-level / GQA): tables, norm + rotation into the cache, attention
+# ---------------------------------------------------------------------------
+
+def block_row_elems(fmt: int, block_tokens: int, head_dim: int) -> int:
+    """16-bit elements of one block row (BLOCK_BF16 or BLOCK_FP4): the row length of a
+    Pool whose rows the block calls read."""
+    n = _I32()
+    _check(load_library().echo_block_row_elems(fmt, block_tokens, head_dim, ctypes.byref(n)), "echo_block_row_elems")
+    return n.value
+
+
+def rope_table(max_pos: int, rope_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """cos_sin [max_pos][rope_dim] fp32 of echo_qk_norm_rope: rope_dim / 2 cosines, then the
+    sines, of position * base^(-2i / rope_dim), angles in 64 bits."""
+    inv = float(base) ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64) / rope_dim)
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], 1).float().to(device)
+
+
+def _typed(t, name: str, dtypes, shape=None, contiguous: bool = True):
+    """The pointer of an optional CUDA tensor on the current device, its type and shape
+    checked (None in `shape`: any size)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise EchoError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise EchoError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype not in dtypes:
+        raise EchoError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise EchoError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise EchoError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_BF16 = (torch.bfloat16, torch.int16)
+_INT = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+def make_block_tables_args(old_len, new_len, block_tokens: int, table, free_blocks, free_count, free_count_out,
+                           slot_map, positions=None, cu_new=None, len_out=None,
+                           dev_status=None) -> c_block_tables_args:
+    """Arguments of echo_block_tables (see include/echo.h): built once, used step after step;
+    keeps its tensors alive.  All int32: old_len, new_len, len_out [B], table
+    [B][max_blocks], free_blocks [n_blocks], free_count, free_count_out [1], slot_map,
+    positions [max_new], cu_new [B + 1]."""
+    B = int(old_len.shape[0])
+    a = c_block_tables_args()
+    a.old_len, a.new_len = _typed(old_len, "old_len", _INT, (B,)), _typed(new_len, "new_len", _INT, (B,))
+    a.B, a.block_tokens = B, int(block_tokens)
+    a.table = _typed(table, "table", _INT, (B, None))
+    a.free_blocks = _typed(free_blocks, "free_blocks", _INT, (None,))
+    a.max_blocks, a.n_blocks = int(table.shape[1]), int(free_blocks.shape[0])
+    a.free_count = _typed(free_count, "free_count", _INT, (1,))
+    a.free_count_out = _typed(free_count_out, "free_count_out", _INT, (1,))
+    a.slot_map, a.max_new = _typed(slot_map, "slot_map", _INT, (None,)), int(slot_map.shape[0])
+    a.positions = _typed(positions, "positions", _INT, (a.max_new,))
+    a.cu_new = _typed(cu_new, "cu_new", _INT, (B + 1,))
+    a.len_out = _typed(len_out, "len_out", _INT, (B,))
+    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a._keep = (old_len, new_len, table, free_blocks, free_count, free_count_out, slot_map, positions, cu_new,
+               len_out, dev_status)
+    return a
+
+
+def echo_block_tables(args: c_block_tables_args, stream=None):
+    """Block tables, slot map and positions of a step from request lengths."""
+    _check((_lib or load_library()).echo_block_tables(ctypes.byref(args), _stream(stream)), "echo_block_tables")
+
+
+def _heads(t, name: str, T: int, H, D: int):
+    """A [T][H][D] bf16 view whose heads are contiguous: its pointer and token stride."""
+    if t is None:
+        return None, 0
+    p = _typed(t, name, _BF16, (T, H, D), contiguous=False)
+    if T and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+        raise EchoError(f"{name} must have contiguous heads (strides (any, {D}, 1), got {t.stride()})")
+    return p, (t.stride(0) if T > 1 else t.shape[1] * D)
+
+
+def make_qk_norm_rope_args(q, k, v, positions, cos_sin, q_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                           interleaved: bool = False, slot_map=None, rows=None, fmt: int = BLOCK_BF16,
+                           block_tokens: int = 16, k_out=None, v_out=None,
+                           dev_status=None) -> c_qk_norm_rope_args:
+    """Arguments of echo_qk_norm_rope (see include/echo.h).  q [T][n_heads][D], k, v
+    [T][n_kv_heads][D] bf16 (views of a fused projection: heads contiguous, any token
+    stride); positions, slot_map [T] int32; cos_sin [max_pos][rope_dim] fp32; weights [D]
+    fp32; rows [n_rows][R] 16-bit, device or pinned host; outputs contiguous."""
+    T, H, D = (int(n) for n in q.shape)
+    Hk = int(k.shape[1])
+    a = c_qk_norm_rope_args()
+    (a.q, a.q_stride), (a.k, a.k_stride) = _heads(q, "q", T, H, D), _heads(k, "k", T, Hk, D)
+    a.v, a.v_stride = _heads(v, "v", T, Hk, D)
+    a.T, a.n_heads, a.n_kv_heads, a.head_dim = T, H, Hk, D
+    a.q_weight, a.k_weight = _typed(q_weight, "q_weight", _F32, (D,)), _typed(k_weight, "k_weight", _F32, (D,))
+    a.eps, a.interleaved = float(eps), int(bool(interleaved))
+    a.cos_sin = _typed(cos_sin, "cos_sin", _F32, (None, None))
+    a.max_pos, a.rope_dim = int(cos_sin.shape[0]), int(cos_sin.shape[1])
+    a.positions = _typed(positions, "positions", _INT, (T,))
+    a.q_out = _typed(q_out, "q_out", _BF16, (T, H, D))
+    a.k_out, a.v_out = _typed(k_out, "k_out", _BF16, (T, Hk, D)), _typed(v_out, "v_out", _BF16, (T, Hk, D))
+    a.format, a.block_tokens = int(fmt), int(block_tokens)
+    if slot_map is not None:
+        if rows is None or rows.dim() != 2 or rows.element_size() != 2 or not rows.is_contiguous():
+            raise EchoError("a slot_map needs contiguous 16-bit rows [n_rows][R]")
+        R = block_row_elems(a.format, a.block_tokens, D)
+        if int(rows.shape[1]) != R:
+            raise EchoError(f"rows have {rows.shape[1]} elements, blocks of {block_tokens} tokens need {R}")
+        if not rows.is_cuda and not rows.is_pinned():
+            raise EchoError("rows must be a CUDA tensor or pinned host memory")
+        a.slot_map = _typed(slot_map, "slot_map", _INT, (T,))
+        a.rows, a.n_rows = _typed(rows, "rows", (rows.dtype,)) if rows.is_cuda else rows.data_ptr(), int(rows.shape[0])
+    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a._keep = (q, k, v, positions, cos_sin, q_out, q_weight, k_weight, slot_map, rows, k_out, v_out, dev_status)
+    return a
+
+
+def echo_qk_norm_rope(args: c_qk_norm_rope_args, stream=None):
+    """Per-head norm and rotation of q and k, k and v written to their cache rows."""
+    _check((_lib or load_library()).echo_qk_norm_rope(ctypes.byref(args), _stream(stream)), "echo_qk_norm_rope")
+
+
+class BlockAttentionWorkspace:
+    """Scratch of echo_block_attention for n_q * n_heads / n_kv_heads query rows per KV head
+    (any batch size and context length).  Serves calls that run one after another: two
+    streams, or two graphs that may be replayed at once, need one each."""
+
+    def __init__(self, rows_per_kv_head: int, head_dim: int, device="cuda"):
+        n = ctypes.c_size_t()
+        _check(load_library().echo_block_attention_workspace_bytes(rows_per_kv_head, head_dim, ctypes.byref(n)),
+               "echo_block_attention_workspace_bytes")
+        self.buf = torch.empty(n.value + 256, dtype=torch.uint8, device=device)
+        self.base = (self.buf.data_ptr() + 255) & ~255
+        self.bytes = n.value
+
+
+def make_block_attention_args(q, rows, table, ctx_len, n_kv_heads: int, scale: float, out, lse,
+                              ws: BlockAttentionWorkspace, fmt: int = BLOCK_BF16, block_tokens: int = 64, sel=None,
+                              sinks: int = 0, window: int = 0, dev_status=None) -> c_block_attention_args:
+    """Arguments of echo_block_attention (see include/echo.h).  q, out [B][n_q][n_heads][D]
+    bf16; rows [n_rows][R] 16-bit; table (and sel) int32 [B][max_blocks] of block ids shared
+    by the KV heads, or [B][n_kv_heads][max_blocks] of rows; ctx_len [B] int32; lse
+    [B][n_q][n_heads] fp32 or None."""
+    B, n_q, H, D = (int(n) for n in q.shape)
+    if rows.dim() != 2 or rows.element_size() != 2:
+        raise EchoError("rows must be 16-bit [n_rows][R]")
+    R = block_row_elems(fmt, block_tokens, D)
+    if int(rows.shape[1]) != R:
+        raise EchoError(f"rows have {rows.shape[1]} elements, blocks of {block_tokens} tokens need {R}")
+    shape = (B, None) if table.dim() == 2 else (B, int(n_kv_heads), None)
+    a = c_block_attention_args()
+    a.q, a.rows = _typed(q, "q", _BF16, (B, n_q, H, D)), _typed(rows, "rows", (rows.dtype,))
+    a.n_rows, a.format, a.block_tokens, a.head_dim = int(rows.shape[0]), int(fmt), int(block_tokens), D
+    a.table = _typed(table, "table", _INT, shape)
+    a.sel = _typed(sel, "sel", _INT, tuple(table.shape))
+    a.table_heads, a.max_blocks = 1 if table.dim() == 2 else int(n_kv_heads), int(table.shape[-1])
+    a.ctx_len = _typed(ctx_len, "ctx_len", _INT, (B,))
+    a.B, a.n_q, a.n_heads, a.n_kv_heads = B, n_q, H, int(n_kv_heads)
+    a.sinks, a.window, a.scale = int(sinks), int(window), float(scale)
+    a.out = _typed(out, "out", _BF16, (B, n_q, H, D))
+    a.lse = _typed(lse, "lse", _F32, (B, n_q, H))
+    a.workspace, a.workspace_bytes = ws.base, ws.bytes
+    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a._keep = (q, rows, table, ctx_len, out, lse, ws, sel, dev_status)
+    return a
+
+
+def echo_block_attention(args: c_block_attention_args, stream=None):
+    """Decode attention over block rows."""
+    _check((_lib or load_library()).echo_block_attention(ctypes.byref(args), _stream(stream)), "echo_block_attention")
 
 
 class StepBuffers:

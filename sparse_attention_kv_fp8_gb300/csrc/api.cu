@@ -8,6 +8,7 @@
 #include <mutex>
 #include <new>
 
+#include "block_rows.cuh"
 #include "cache_common.cuh"
 
 namespace echo_host {
@@ -56,6 +57,10 @@ int launch_ema(float *s_hat, const float *kth, int n, int stride, float alpha, c
 int launch_prefill_indexer(const echo_prefill_args *a, cudaStream_t stream);
 size_t mla_workspace_bytes(int32_t B, int32_t n_q, int32_t k);
 int launch_sparse_mla(const echo_mla_args *a, cudaStream_t stream);
+int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream);
+int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream);
+size_t block_attention_workspace_bytes(int32_t rows, int32_t head_dim);
+int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stream);
 int noalloc_workspace(int32_t n_g, int32_t rows, cudaStream_t stream, echo_workspace *out);
 int launch_validate(const echo_pool *p, const echo_stage *stage, int32_t *report, int32_t *status, cudaStream_t s);
 int validate_host(const echo_pool *p, const int32_t *reserve, int32_t reserve_len, int32_t *report);
@@ -163,7 +168,7 @@ int echo_selftest_wait_timeout(int32_t which, int32_t *dev_status, void *stream)
   return launch_wait_probe(which, dev_status, static_cast<cudaStream_t>(stream));
 }
 
-int32_t echo_version(void) { return (1 << 16) | 5; }
+int32_t echo_version(void) { return (1 << 16) | 6; }
 
 int64_t echo_metadata_bytes(int64_t n_h, int64_t n_g) {
   return static_cast<int64_t>(sizeof(int32_t)) * n_h +
@@ -379,6 +384,104 @@ int echo_sparse_mla_decode(const echo_mla_args *a, void *stream) {
   REQUIRE(a->workspace_bytes >= mla_workspace_bytes(a->B, a->n_q, a->k), "workspace smaller than "
           "echo_mla_workspace_bytes()");
   return launch_sparse_mla(a, static_cast<cudaStream_t>(stream));
+}
+
+// a block-row layout the block calls serve
+static int check_block_rows(int32_t format, int32_t block_tokens, int32_t head_dim) {
+  REQUIRE(format == ECHO_BLOCK_BF16 || format == ECHO_BLOCK_FP4, "unknown block format %d", format);
+  REQUIRE(head_dim == 64 || head_dim == 128, "head_dim must be 64 or 128 (got %d)", head_dim);
+  REQUIRE(block_tokens > 0 && block_tokens % echo::kSubTokens == 0, "block_tokens must be a positive multiple of %d (got %d)",
+          echo::kSubTokens, block_tokens);
+  REQUIRE(echo::block_row_elems(format, block_tokens, head_dim) <= 65536, "rows of %d tokens of %d dims are longer than 65536 elements",
+          block_tokens, head_dim);
+  return ECHO_OK;
+}
+
+int echo_block_row_elems(int32_t format, int32_t block_tokens, int32_t head_dim, int32_t *row_elems) {
+  g_err[0] = 0;
+  REQUIRE(row_elems, "row_elems is NULL");
+  TRY(check_block_rows(format, block_tokens, head_dim));
+  *row_elems = static_cast<int32_t>(echo::block_row_elems(format, block_tokens, head_dim));
+  return ECHO_OK;
+}
+
+int echo_block_tables(const echo_block_tables_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->B >= 0 && a->B <= 16384, "B must be in [0, 16384] (got %d)", a->B);
+  REQUIRE(a->block_tokens >= 1 && a->max_blocks >= 1 && a->n_blocks >= 1, "block sizes must be positive");
+  REQUIRE(a->max_new >= 0 && a->max_new <= (1 << 30), "max_new must be in [0, 2^30] (got %d)", a->max_new);
+  REQUIRE(static_cast<long long>(a->max_blocks) * a->block_tokens <= ((1ll << 31) - 1) / (a->B > 0 ? a->B : 1),
+          "B * max_blocks * block_tokens must be below 2^31");
+  REQUIRE(static_cast<long long>(a->n_blocks) * a->block_tokens <= (1ll << 31) - 1, "n_blocks * block_tokens must be below 2^31");
+  REQUIRE(a->free_count && a->free_count_out && a->free_blocks, "block tables pointer is NULL");
+  REQUIRE(a->B == 0 || (a->old_len && a->new_len && a->table), "block tables pointer is NULL");
+  REQUIRE(a->max_new == 0 || a->slot_map, "slot_map is NULL");
+  REQUIRE(a->free_count != a->free_count_out, "free_count and free_count_out must be different addresses");
+  REQUIRE(!a->len_out || (a->len_out != a->old_len && a->len_out != a->new_len), "len_out must not be one of the inputs");
+  return launch_block_tables(a, static_cast<cudaStream_t>(stream));
+}
+
+int echo_qk_norm_rope(const echo_qk_norm_rope_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->T >= 0 && a->n_heads >= 1 && a->n_kv_heads >= 1, "bad sizes (T %d, n_heads %d, n_kv_heads %d)", a->T,
+          a->n_heads, a->n_kv_heads);
+  REQUIRE(a->n_heads <= 65536 && a->n_kv_heads <= 65536, "too many heads");
+  REQUIRE(a->head_dim == 64 || a->head_dim == 128, "head_dim must be 64 or 128 (got %d)", a->head_dim);
+  REQUIRE(a->rope_dim >= 16 && a->rope_dim % 16 == 0 && a->rope_dim <= a->head_dim,
+          "rope_dim must be a multiple of 16 in [16, head_dim] (got %d)", a->rope_dim);
+  REQUIRE(a->max_pos >= 1, "max_pos must be >= 1");
+  REQUIRE(std::isfinite(a->eps) && a->eps >= 0.f, "eps must be finite and >= 0");
+  REQUIRE(a->interleaved == 0 || a->interleaved == 1, "interleaved must be 0 or 1");
+  TRY(check_block_rows(a->format, a->slot_map ? a->block_tokens : echo::kSubTokens, a->head_dim));
+  REQUIRE(static_cast<long long>(a->T) * (a->n_heads + 2ll * a->n_kv_heads) * a->head_dim <= (1ll << 38), "call too large");
+  if (a->T == 0) return ECHO_OK;
+  REQUIRE(a->q && a->k && a->cos_sin && a->positions && a->q_out, "norm + rope pointer is NULL");
+  REQUIRE(aligned(a->q, 16) && aligned(a->k, 16) && aligned(a->v, 16) && aligned(a->q_out, 16) && aligned(a->k_out, 16) &&
+              aligned(a->v_out, 16) && aligned(a->cos_sin, 16) && aligned(a->q_weight, 16) && aligned(a->k_weight, 16),
+          "q, k, v, the weights, cos_sin and the outputs must be 16-byte aligned");
+  REQUIRE(a->q_stride % 8 == 0 && a->k_stride % 8 == 0 && (!a->v || a->v_stride % 8 == 0), "token strides must be multiples of 8");
+  REQUIRE(a->v || (!a->slot_map && !a->v_out), "v is NULL, but a cache or v_out takes it");
+  if (a->slot_map) {
+    REQUIRE(a->rows && a->n_rows >= 1, "slot_map given without rows");
+    REQUIRE(aligned(a->rows, 16), "rows must be 16-byte aligned");
+    TRY(check_device_accessible(a->rows, "rows"));
+  }
+  return launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int echo_block_attention_workspace_bytes(int32_t rows_per_kv_head, int32_t head_dim, size_t *bytes) {
+  g_err[0] = 0;
+  REQUIRE(bytes, "bytes is NULL");
+  REQUIRE(rows_per_kv_head >= 1 && rows_per_kv_head <= 1024, "rows_per_kv_head must be in [1, 1024] (got %d)", rows_per_kv_head);
+  REQUIRE(head_dim == 64 || head_dim == 128, "head_dim must be 64 or 128 (got %d)", head_dim);
+  *bytes = block_attention_workspace_bytes(rows_per_kv_head, head_dim);
+  return ECHO_OK;
+}
+
+int echo_block_attention(const echo_block_attention_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->B >= 0 && a->n_q >= 1 && a->n_q <= 64, "bad sizes (B %d, n_q %d)", a->B, a->n_q);
+  REQUIRE(a->n_kv_heads >= 1 && a->n_heads >= 1 && a->n_heads % a->n_kv_heads == 0,
+          "n_heads must be a multiple of n_kv_heads (got %d, %d)", a->n_heads, a->n_kv_heads);
+  REQUIRE(static_cast<long long>(a->n_q) * (a->n_heads / a->n_kv_heads) <= 1024, "n_q * n_heads / n_kv_heads must be at most 1024");
+  TRY(check_block_rows(a->format, a->block_tokens, a->head_dim));
+  REQUIRE(a->table_heads == 1 || a->table_heads == a->n_kv_heads, "table_heads must be 1 or n_kv_heads (got %d)", a->table_heads);
+  REQUIRE(a->max_blocks >= 1 && static_cast<long long>(a->max_blocks) * a->block_tokens <= (1ll << 31) - 1024,
+          "max_blocks * block_tokens must be positive and below 2^31 - 1024");
+  REQUIRE(a->sinks >= 0 && a->window >= 0 && a->sinks <= (1 << 30) && a->window <= (1 << 30), "sinks and window must be in [0, 2^30]");
+  REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
+  REQUIRE(std::isfinite(a->scale), "scale must be finite");
+  REQUIRE(static_cast<long long>(a->B) * a->n_q * a->n_heads <= (1ll << 31) - 1, "B * n_q * n_heads too large");
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->q && a->rows && a->table && a->ctx_len && a->out && a->workspace, "block attention pointer is NULL");
+  REQUIRE(aligned(a->q, 16) && aligned(a->rows, 16) && aligned(a->out, 16), "q, rows and out must be 16-byte aligned");
+  REQUIRE(aligned(a->workspace, 256), "workspace must be 256-byte aligned");
+  REQUIRE(a->workspace_bytes >= block_attention_workspace_bytes(a->n_q * (a->n_heads / a->n_kv_heads), a->head_dim),
+          "workspace smaller than echo_block_attention_workspace_bytes()");
+  return launch_block_attention(a, static_cast<cudaStream_t>(stream));
 }
 
 int echo_prefill_indexer_score(const echo_prefill_args *a, void *stream) {

@@ -1,0 +1,215 @@
+// block_tables.cu -- block tables and slot maps of a serving step, from request lengths.
+//
+// Request b goes from old_len[b] to new_len[b] tokens.  With nb(n) = ceil(n / bs):
+//   f_b = max(0, nb(old) - nb(new)) blocks return to the free stack,
+//   a_b = max(0, nb(new) - nb(old)) blocks are taken from it,
+//   n_b = max(0, new - old) tokens are listed with their slots.
+// Everything follows from the exclusive sums F, A, N of the three: freed block i of b is
+// entry count + F_b + i of the stack, grown block i of b is entry top - 1 - (A_b + i) with
+// top = count + sum f, and token i of the list belongs to the b with N_b <= i < N_{b+1}.
+//
+// One launch: every CTA forms the three sums itself (B <= 16384 lengths, read from L2; the
+// sums stay in shared memory) and then takes its share of the blocks and of the list, so
+// no CTA waits for another.  A stack entry at or above `count` is read where it comes from
+// (the shrinking request's table), never from the stack the same launch is writing.
+// Bound by latency for a decode step and by the list's stores for prefill chunks.
+#include "echo_common.cuh"
+
+namespace echo {
+
+constexpr int kTabThreads = 512;
+constexpr int kTabPer = 4;  // list entries of a thread (one 16-byte store each)
+
+struct TablesParams {
+  const int32_t *old_len, *new_len;
+  int32_t B, bs;
+  int32_t *table;
+  int32_t *free_blocks;
+  int32_t max_blocks, n_blocks;
+  const int32_t *free_count;
+  int32_t *free_count_out;
+  int32_t *slot_map, *positions, *cu_new, *len_out;
+  int32_t max_new;
+  int32_t *status;
+};
+
+// the largest i in [0, n) with cu[i] <= x (cu ascending, cu[0] <= x): the owner of entry x
+// of a list whose exclusive sums are cu
+__device__ __forceinline__ int owner_of(const int32_t *cu, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesParams P) {
+  extern __shared__ int32_t tab_smem[];
+  int32_t *cuN = tab_smem, *cuA = cuN + P.B + 1, *cuF = cuA + P.B + 1;
+  __shared__ int32_t warp_sum[3][kTabThreads / 32];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int cap = P.max_blocks * P.bs;
+  const int count0 = *P.free_count;
+  const int count = min(max(count0, 0), P.n_blocks);
+  int bad = count != count0;
+
+  // ===== exclusive sums over the requests: a run of consecutive requests per thread =====
+  const int per = (P.B + kTabThreads - 1) / kTabThreads;
+  const int b0 = min(t * per, P.B), b1 = min(b0 + per, P.B);
+  int32_t n = 0, a = 0, f = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int o0 = P.old_len[b], w0 = P.new_len[b];
+    const int o = min(max(o0, 0), cap), w = min(max(w0, 0), cap);
+    bad |= (o != o0) | (w != w0);
+    const int no = (o + P.bs - 1) / P.bs, nw = (w + P.bs - 1) / P.bs;
+    cuN[b] = n, cuA[b] = a, cuF[b] = f;  // sums within the thread's run for now
+    n += max(w - o, 0), a += max(nw - no, 0), f += max(no - nw, 0);
+  }
+  int32_t sn = n, sa = a, sf = f;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int xn = __shfl_up_sync(~0u, sn, d), xa = __shfl_up_sync(~0u, sa, d), xf = __shfl_up_sync(~0u, sf, d);
+    if (lane >= d) sn += xn, sa += xa, sf += xf;
+  }
+  if (lane == 31) warp_sum[0][warp] = sn, warp_sum[1][warp] = sa, warp_sum[2][warp] = sf;
+  __syncthreads();
+  int32_t en = sn - n, ea = sa - a, ef = sf - f, tn = 0, ta = 0, tf = 0;
+#pragma unroll
+  for (int w = 0; w < kTabThreads / 32; ++w) {
+    const int xn = warp_sum[0][w], xa = warp_sum[1][w], xf = warp_sum[2][w];
+    if (w < warp) en += xn, ea += xa, ef += xf;
+    tn += xn, ta += xa, tf += xf;
+  }
+  for (int b = b0; b < b1; ++b) cuN[b] += en, cuA[b] += ea, cuF[b] += ef;
+  if (t == 0) cuN[P.B] = tn, cuA[P.B] = ta, cuF[P.B] = tf;
+  __syncthreads();
+  const int top = min(count + tf, P.n_blocks);
+  bad |= count + tf > P.n_blocks;
+  // growth is granted in request order while it fits: b gets its blocks iff A_{b+1} <= top
+  const bool exhausted = ta > top;
+
+  // entry s of the stack after the pushes
+  auto stack_at = [&](int s) -> int32_t {
+    if (s < count) return P.free_blocks[s];
+    const int j = s - count, b = owner_of(cuF, P.B, j);
+    const int w = min(max(P.new_len[b], 0), cap);
+    return P.table[static_cast<size_t>(b) * P.max_blocks + (w + P.bs - 1) / P.bs + (j - cuF[b])];
+  };
+  auto grown = [&](int j) -> int32_t {  // the j-th block handed out
+    const int32_t id = stack_at(top - 1 - j);
+    return static_cast<uint32_t>(id) < static_cast<uint32_t>(P.n_blocks) ? id : -1;
+  };
+
+  const int gthreads = gridDim.x * kTabThreads, gt = blockIdx.x * kTabThreads + t;
+  // ===== the list of new tokens: four entries per thread =====
+  const int listed = min(tn, P.max_new);
+  const bool wide = ((reinterpret_cast<uintptr_t>(P.slot_map) | reinterpret_cast<uintptr_t>(P.positions)) & 15) == 0;
+  bad |= tn > P.max_new;
+  for (int i0 = gt * kTabPer; i0 < P.max_new; i0 += gthreads * kTabPer) {
+    int32_t slot[kTabPer], pos[kTabPer];
+    int b = -1, nend = 0, o = 0, nbo = 0, blk = -1, id = -1;
+    bool have = false;
+#pragma unroll
+    for (int u = 0; u < kTabPer; ++u) {
+      const int i = i0 + u;
+      slot[u] = pos[u] = -1;
+      if (i >= listed) continue;
+      if (b < 0 || i >= nend) {
+        b = b < 0 ? owner_of(cuN, P.B, i) : b + 1;
+        while (cuN[b + 1] <= i) ++b;
+        nend = cuN[b + 1];
+        o = min(max(P.old_len[b], 0), cap);
+        nbo = (o + P.bs - 1) / P.bs;
+        blk = -1;
+        have = cuA[b + 1] == cuA[b] || cuA[b + 1] <= top;
+      }
+      if (!have) continue;
+      const int p = o + (i - cuN[b]), k = p / P.bs;
+      if (k != blk) {
+        blk = k;
+        id = k < nbo ? P.table[static_cast<size_t>(b) * P.max_blocks + k] : grown(cuA[b] + k - nbo);
+        if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(P.n_blocks)) id = -1, bad = 1;
+      }
+      if (id >= 0) slot[u] = id * P.bs + (p - k * P.bs), pos[u] = p;
+    }
+    if (wide && i0 + kTabPer <= P.max_new) {
+      *reinterpret_cast<int4 *>(P.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (P.positions) *reinterpret_cast<int4 *>(P.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kTabPer; ++u)
+        if (i0 + u < P.max_new) {
+          P.slot_map[i0 + u] = slot[u];
+          if (P.positions) P.positions[i0 + u] = pos[u];
+        }
+    }
+  }
+  // ===== the blocks that moved =====
+  for (int j = gt; j < ta; j += gthreads) {
+    const int b = owner_of(cuA, P.B, j);
+    if (cuA[b + 1] > top) break;  // this request and every later one with a need get nothing
+    const int o = min(max(P.old_len[b], 0), cap);
+    const int32_t id = grown(j);
+    bad |= id < 0;
+    P.table[static_cast<size_t>(b) * P.max_blocks + (o + P.bs - 1) / P.bs + (j - cuA[b])] = id;
+  }
+  for (int j = gt; j < tf; j += gthreads) {
+    const int32_t id = stack_at(count + j);
+    bad |= static_cast<uint32_t>(id) >= static_cast<uint32_t>(P.n_blocks);
+    if (count + j < P.n_blocks) P.free_blocks[count + j] = id;
+  }
+  // ===== per-request outputs =====
+  for (int b = gt; b <= P.B; b += gthreads) {
+    if (P.cu_new) P.cu_new[b] = cuN[b];
+    if (P.len_out && b < P.B) {
+      const bool have = cuA[b + 1] == cuA[b] || cuA[b + 1] <= top;
+      P.len_out[b] = min(max(have ? P.new_len[b] : P.old_len[b], 0), cap);
+    }
+  }
+  if (blockIdx.x == 0 && t == 0) {
+    int taken = ta;
+    if (exhausted) taken = cuA[owner_of(cuA, P.B + 1, top)];  // the largest sum that fits
+    *P.free_count_out = top - taken;
+    if (exhausted) set_status(P.status, ECHO_DEV_POOL_EXHAUSTED);
+  }
+  if (bad) set_status(P.status, ECHO_DEV_BAD_INDEX);
+}
+
+}  // namespace echo
+
+namespace echo_host {
+
+int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream) {
+  echo::TablesParams P{};
+  P.old_len = a->old_len;
+  P.new_len = a->new_len;
+  P.B = a->B;
+  P.bs = a->block_tokens;
+  P.table = a->table;
+  P.free_blocks = a->free_blocks;
+  P.max_blocks = a->max_blocks;
+  P.n_blocks = a->n_blocks;
+  P.free_count = a->free_count;
+  P.free_count_out = a->free_count_out;
+  P.slot_map = a->slot_map;
+  P.positions = a->positions;
+  P.cu_new = a->cu_new;
+  P.len_out = a->len_out;
+  P.max_new = a->max_new;
+  P.status = a->dev_status;
+  const size_t smem = 3 * (static_cast<size_t>(a->B) + 1) * sizeof(int32_t);
+  static std::atomic<bool> attr[kMaxDevices];
+  if (int rr = smem_limit_once(attr, echo::block_tables_kernel, 3 * (16384 + 1) * sizeof(int32_t),
+                               "block tables smem attribute"))
+    return rr;
+  const int per_cta = echo::kTabThreads * echo::kTabPer;
+  const int want = a->max_new / per_cta + (a->max_new % per_cta != 0);
+  const int grid = want < 1 ? 1 : want > 304 ? 304 : want;
+  echo::block_tables_kernel<<<grid, echo::kTabThreads, smem, stream>>>(P);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block tables launch");
+}
+
+}  // namespace echo_host
