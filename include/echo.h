@@ -578,8 +578,8 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  *   workspace  device, 256-byte aligned, echo_block_attention_workspace_bytes() bytes; one
  *           workspace serves calls that run one after another
  * Tokens no query of the request sees may hold any bytes.  Scores, the softmax and both
- * sums are fp32; the softmax weights enter the value product in 16 bits (bf16 rows: bf16,
- * ECHO_BLOCK_FP4: fp16).  ECHO_BLOCK_FP4 takes the queries to fp16 scaled by a power of two
+ * sums are fp32; the softmax weights enter the value product as two bf16 terms (bf16 rows)
+ * or in fp16 (ECHO_BLOCK_FP4).  ECHO_BLOCK_FP4 takes the queries to fp16 scaled by a power of two
  * of their row: an entry below 2^-24 of its row's largest is rounded to that grid.
  * 1 <= n_q <= 64, n_q * n_heads / n_kv_heads <= 1024.  Launches 1 kernel, or 2 when
  * contexts are split over several CTAs (the second merges their partial results).

@@ -16,7 +16,9 @@
 //   A warp is a worker of its own: it takes every kWarps-th chunk (16 or 32 tokens) of the
 //     CTA's range, keeps its own m, l and O, and fills its own ring of shared-memory stages
 //     with cp.async, ahead of the chunk it computes and across the borders of requests; no
-//     barrier runs inside the stream.  The warps of a CTA merge at the end of each (b, h).
+//     barrier runs inside the stream.  Where its next 32 sub-blocks lie is looked up by its
+//     32 lanes at once (table, selection, window, request borders) into a small list.  The
+//     warps of a CTA merge at the end of each (b, h).
 //   Lazy maximum: m moves only when some score exceeds it by 2^8, so the rescaling of O (and
 //     the shuffles that find a column's maximum) run a few times per stream instead of once
 //     per chunk; the result is the same softmax, its terms scaled by at most 2^8.
@@ -29,6 +31,8 @@
 //     inside a (b, h) leaves a partial result; a second kernel merges those in order (no
 //     atomics: results do not depend on timing).  When the contexts are short or the
 //     (b, h) pairs fill the GPU, a CTA takes a whole (b, h) and the second kernel is left out.
+#include <cmath>
+
 #include "block_rows.cuh"
 
 namespace echo {
@@ -39,6 +43,7 @@ constexpr float kBaLazy = 8.f;    // log2 of how far a score may exceed the runn
 // 2^-24) begin 2^-21 below the running maximum instead of 2^-14
 constexpr float kBaLift = 7.f;
 constexpr int kBaNowhere = 0x7fffff00;  // position of a sub-block that is not there
+constexpr int kBaList = 64;        // entries of a warp's list of sub-blocks (two batches of 32)
 constexpr int kBaMaxRows = 32;    // query rows of one CTA's (b, h) (4 columns of 8)
 
 struct BlockAttnParams {
@@ -50,7 +55,8 @@ struct BlockAttnParams {
   const int32_t *ctx_len;
   int32_t B, n_q, n_heads, n_kv, group, mgroups;  // group: query heads per KV head
   int32_t sinks, window;
-  float scale_log2;
+  float scale_log2;                  // |scale| log2 e
+  uint32_t q_sign;                   // 0x80008000 for a negative scale
   uint16_t *out;
   float *lse;
   int32_t whole;                     // one CTA per (b, h, row group), nothing split
@@ -108,15 +114,17 @@ struct BaCfg {
   static constexpr int kThreads = WARPS * 32;
   static constexpr int kSteps = D / 16;                      // k-steps of S^T, dim tiles of O^T
   static constexpr int kRows = 8 * NT;
-  static constexpr int kMergeRow = D + 4;                    // floats; + 4: no bank conflicts
-  // shared memory: stages | merge buffers | q fragments | per-row values | scan
+  static constexpr int kMergeRow = D / 2 + 4;                // floats; + 4: no bank conflicts
+  // shared memory: stages | merge buffers | lists | q fragments | per-row values
   static constexpr int kOffMerge = WARPS * STAGES * kStageBytes;
-  static constexpr int kOffQ = kOffMerge + WARPS * 8 * kMergeRow * 4;
+  static constexpr int kOffList = kOffMerge + WARPS * 8 * kMergeRow * 4;
+  static constexpr int kOffQ = kOffList + WARPS * kBaList * 16;
   static constexpr int kOffMl = kOffQ + kSteps * NT * 32 * 8;
   static constexpr int kOffQs = kOffMl + WARPS * kRows * 8;
-  static constexpr int kOffMeta = kOffQs + kRows * 4;
-  static constexpr int kOffScan = kOffMeta + WARPS * STAGES * kSubs * 4;
-  static constexpr int kSmem = kOffScan + 64 * 8 + 64;
+  static constexpr int kOffFin = kOffQs + kRows * 4;
+  static_assert(kOffFin % 8 == 0 && kOffList % 16 == 0 && kOffMerge % 16 == 0, "alignment");
+  static constexpr int kSmem = kOffFin + kRows * 8;
+  static constexpr int kQRows = (kRows + WARPS - 1) / WARPS;  // query rows a warp lays out
 };
 
 __device__ __forceinline__ void ba_cp16(uint32_t dst, const void *src, bool on) {
@@ -174,11 +182,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// A place on the line of chunks: chunk g of the call is chunk g - start of the row group hm
-// (KV head * row groups + row group) of request b.
+// A place on the line of chunks, counted from the CTA's first chunk: the chunks start .. end
+// belong to row group hm (KV head * row groups + row group) of request b.
 struct LinePos {
   int b, hm;
-  int64_t start, end;  // the line's range of this (b, hm)
+  int start, end;
   ReqView v;
 };
 
@@ -187,17 +195,16 @@ __device__ __forceinline__ int chunks_of(const ReqView &v) {
   return (v.nsub + kSubs - 1) / kSubs;
 }
 
-// moves forward to the (b, hm) that holds chunk g (g < the line's length)
+// moves forward to the (b, hm) that holds chunk g (a chunk of the line)
 template <int kSubs>
-__device__ __forceinline__ void seek(const BlockAttnParams &P, LinePos &L, int64_t g) {
+__device__ __forceinline__ void seek(const BlockAttnParams &P, LinePos &L, int g) {
   while (g >= L.end) {
     const int heads = P.n_kv * P.mgroups;
     const int n = chunks_of<kSubs>(L.v);
     if (n > 0 && L.hm + 1 < heads) {
-      const int64_t step = (g - L.end) / n;  // whole heads of this request to pass over
-      const int by = static_cast<int>(min(static_cast<int64_t>(heads - 1 - L.hm), step + 1));
+      const int by = min(heads - 1 - L.hm, (g - L.end) / n + 1);  // row groups to pass over
       L.hm += by;
-      L.start = L.end + static_cast<int64_t>(by - 1) * n;
+      L.start = L.end + (by - 1) * n;
     } else {
       ++L.b;
       L.hm = 0;
@@ -206,6 +213,44 @@ __device__ __forceinline__ void seek(const BlockAttnParams &P, LinePos &L, int64
     }
     L.end = L.start + chunks_of<kSubs>(L.v);
   }
+}
+
+// One sub-block of a warp's list: where it lies, its first token's position, which of its
+// tokens some query sees (bits 0-15), and whether some query does not see all of them (edge).
+struct __align__(16) SubEntry {
+  const uint8_t *src;
+  int pos;
+  uint32_t flags;
+};
+constexpr uint32_t kBaEdge = 1u << 31;
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; }
+
+template <int FMT, int D>
+__device__ __forceinline__ SubEntry sub_entry(const BlockAttnParams &P, const LinePos &L, int s) {
+  SubEntry x{reinterpret_cast<const uint8_t *>(P.rows), kBaNowhere, kBaEdge};
+  if (s >= L.v.nsub) return x;
+  if (s >= L.v.n_first) s += L.v.skip;
+  const int h = L.hm / P.mgroups, e = s / P.bsub, in = s - e * P.bsub;
+  const int64_t at = (static_cast<int64_t>(L.b) * P.table_heads + (P.table_heads > 1 ? h : 0)) * P.max_blocks + e;
+  const int32_t id = __ldg(P.table + at);
+  const int32_t lb = P.sel ? __ldg(P.sel + at) : e;
+  // (a selected block past the 31-bit positions cannot be below any length)
+  if (id < 0 || lb < 0 || static_cast<int64_t>(lb) * P.bsub + in >= kBaNowhere / kSubTokens) return x;
+  const int64_t row = P.table_heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
+  if (row >= P.n_rows) {
+    set_status(P.status, ECHO_DEV_BAD_INDEX);
+    return x;
+  }
+  const int pos = (lb * P.bsub + in) * kSubTokens, last = pos + kSubTokens - 1;
+  x.src += row * P.row_bytes + static_cast<int64_t>(in) * (FMT == ECHO_BLOCK_FP4 ? Fp4Sub<D>::kBytes : kSubTokens * D * 2);
+  x.pos = pos;
+  // seen by some query: p < len and (p >= wlo or p < sinks)
+  const uint32_t seen = low_bits(L.v.len - pos) & ((0xffffu & ~low_bits(L.v.wlo - pos)) | low_bits(P.sinks - pos));
+  const int len_first = L.v.len - (P.n_q - 1), w_last = P.window ? L.v.len - P.window : 0;
+  const bool all = last < len_first && (pos >= w_last || last < P.sinks);
+  x.flags = seen | (all ? 0u : kBaEdge);
+  return x;
 }
 
 template <int FMT, int D, int NT, int WARPS, int STAGES>
@@ -221,204 +266,196 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
   uint2 *qfrag = reinterpret_cast<uint2 *>(ba_smem + C::kOffQ);
   float2 *ml = reinterpret_cast<float2 *>(ba_smem + C::kOffMl);       // [WARPS][kRows]
   float *qscale = reinterpret_cast<float *>(ba_smem + C::kOffQs);     // [kRows]
-  int32_t *meta = reinterpret_cast<int32_t *>(ba_smem + C::kOffMeta) + warp * STAGES * C::kSubs;
-  int64_t *scan = reinterpret_cast<int64_t *>(ba_smem + C::kOffScan);
+  SubEntry *list = reinterpret_cast<SubEntry *>(ba_smem + C::kOffList) + warp * kBaList;
+  float2 *fin = reinterpret_cast<float2 *>(ba_smem + C::kOffFin);     // [kRows]
   const int heads = P.n_kv * P.mgroups;
+  pdl_launch_dependents();  // (the merge waits for this grid's end all the same)
 
-  // ===== this CTA's range of the line =====
+  // ===== this CTA's range of the line: chunks 0 .. n_chunks from its first =====
   LinePos cur;
-  int64_t g0, g1;
+  int n_chunks;
   if (P.whole) {
     cur.b = blockIdx.x / heads;
     cur.hm = blockIdx.x - cur.b * heads;
-    cur.v = req_view(P, __ldg(P.ctx_len + cur.b));
+    const int ctx = __ldg(P.ctx_len + cur.b);
+    cur.v = req_view(P, ctx);
     cur.start = 0;
-    cur.end = chunks_of<C::kSubs>(cur.v);
-    g0 = 0;
-    g1 = cur.end;
-    if (threadIdx.x == 0 && cur.hm == 0) check_context(P, __ldg(P.ctx_len + cur.b));
+    n_chunks = cur.end = chunks_of<C::kSubs>(cur.v);
+    if (threadIdx.x == 0 && cur.hm == 0) check_context(P, ctx);
   } else {
-    // lengths of all requests' parts of the line: a run of requests per thread, summed
-    const int per_t = (P.B + C::kThreads - 1) / C::kThreads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per_t, P.B), b1 = min(b0 + per_t, P.B);
+    // lengths of all requests' parts of the line, by every warp for itself (no barrier): a
+    // run of requests per lane, summed
+    const int per_l = (P.B + 31) / 32;
+    const int b0 = min(lane * per_l, P.B), b1 = min(b0 + per_l, P.B);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
       const int ctx = __ldg(P.ctx_len + b);
       mine += chunks_of<C::kSubs>(req_view(P, ctx));
-      if (blockIdx.x == 0) check_context(P, ctx);
+      if (blockIdx.x == 0 && warp == 0) check_context(P, ctx);
     }
     mine *= heads;
-    int64_t s = mine;
+    int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t x = __shfl_up_sync(~0u, s, d);
-      if (lane >= d) s += x;
+      const int64_t x = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += x;
     }
-    if (lane == 31) scan[warp] = s;
-    __syncthreads();
-    int64_t before = s - mine, total = 0;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
-    }
-    __syncthreads();
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t total = __shfl_sync(~0u, upto, 31);
+    int64_t per = total < (1ll << 31) ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x
+                                      : (total + gridDim.x - 1) / gridDim.x;
     per = per < WARPS ? WARPS : per;
-    g0 = per * blockIdx.x;
-    g1 = min(total, g0 + per);
+    // requests with nothing to see are not on the line: their outputs are written here
+    for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
+      if (req_view(P, __ldg(P.ctx_len + b)).nsub > 0) continue;
+      const int64_t o0 = static_cast<int64_t>(b) * P.n_q * P.n_heads;
+      for (int i = threadIdx.x; i < P.n_q * P.n_heads * (D / 8); i += C::kThreads)
+        reinterpret_cast<uint4 *>(P.out + o0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (P.lse)
+        for (int i = threadIdx.x; i < P.n_q * P.n_heads; i += C::kThreads) P.lse[o0 + i] = -INFINITY;
+    }
+    const int64_t g0 = per * blockIdx.x;
     if (g0 >= total) {
       if (threadIdx.x == 0) P.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }
-    if (g0 >= before && g0 < before + mine) {  // one thread's run holds g0
-      int b = b0;
-      int64_t at = before;
-      for (;; ++b) {
-        const int64_t n = static_cast<int64_t>(chunks_of<C::kSubs>(req_view(P, __ldg(P.ctx_len + b)))) * heads;
-        if (g0 < at + n) break;
-        at += n;
+    n_chunks = static_cast<int>(min(total - g0, per));
+    int own_b = 0, own_hm = 0, own_start = 0;
+    const bool own = g0 >= upto - mine && g0 < upto;  // one lane's run holds g0
+    if (own) {
+      int64_t at = upto - mine;
+      int n;
+      for (own_b = b0;; ++own_b) {
+        n = chunks_of<C::kSubs>(req_view(P, __ldg(P.ctx_len + own_b)));
+        if (g0 < at + static_cast<int64_t>(n) * heads) break;
+        at += static_cast<int64_t>(n) * heads;
       }
-      scan[32] = b;
-      scan[33] = at;
+      own_hm = static_cast<int>((g0 - at) / n);
+      own_start = static_cast<int>(at + static_cast<int64_t>(own_hm) * n - g0);
     }
-    __syncthreads();
-    cur.b = static_cast<int>(scan[32]);
-    cur.hm = 0;
-    cur.start = scan[33];
+    const int src = __ffs(__ballot_sync(~0u, own)) - 1;
+    cur.b = __shfl_sync(~0u, own_b, src);
+    cur.hm = __shfl_sync(~0u, own_hm, src);
+    cur.start = __shfl_sync(~0u, own_start, src);
     cur.v = req_view(P, __ldg(P.ctx_len + cur.b));
     cur.end = cur.start + chunks_of<C::kSubs>(cur.v);
-    seek<C::kSubs>(P, cur, g0);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == C::kThreads - 1) {
       // where the range's last (b, hm) goes on, and whether it began here
       LinePos e = cur;
-      seek<C::kSubs>(P, e, g1 - 1);
+      seek<C::kSubs>(P, e, n_chunks - 1);
       int pieces = 0;
-      if (e.end > g1 && e.start >= g0) pieces = 1 + static_cast<int>((e.end - g1 + per - 1) / per);
+      if (e.end > n_chunks && e.start >= 0) pieces = 1 + static_cast<int>((e.end - n_chunks + per - 1) / per);
       P.tail[blockIdx.x] = make_int4(e.b, e.hm, pieces, 0);
     }
   }
 
-  // ===== the loader: rows of the chunk after next are looked up one chunk ahead =====
-  LinePos ld = cur;
-  int64_t ld_g = g0 + warp;
-  int32_t ld_row[C::kSubs], ld_pos[C::kSubs];
-  int ld_in[C::kSubs];  // sub-block inside its row
-  auto lookup = [&]() {
-    if (ld_g >= g1) return;
-    seek<C::kSubs>(P, ld, ld_g);
-    const int h = ld.hm / P.mgroups;
-    const int64_t tb = (static_cast<int64_t>(ld.b) * P.table_heads + (P.table_heads > 1 ? h : 0)) * P.max_blocks;
-    const int first = static_cast<int>(ld_g - ld.start) * C::kSubs;
-#pragma unroll
-    for (int u = 0; u < C::kSubs; ++u) {
-      int s = first + u;
-      ld_row[u] = -1;
-      ld_pos[u] = kBaNowhere;  // no token of a missing sub-block is below any length
-      ld_in[u] = 0;
-      if (s >= ld.v.nsub) continue;
-      if (s >= ld.v.n_first) s += ld.v.skip;
-      const int e = s / P.bsub, in = s - e * P.bsub;
-      const int32_t id = __ldg(P.table + tb + e);
-      const int32_t lb = P.sel ? __ldg(P.sel + tb + e) : e;
-      const int64_t row = P.table_heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
-      // (a selected block past the 31-bit positions cannot be below any length)
-      if (id < 0 || lb < 0 || static_cast<int64_t>(lb) * P.bsub + in >= kBaNowhere / kSubTokens) continue;
-      if (row >= P.n_rows) {
-        set_status(P.status, ECHO_DEV_BAD_INDEX);
-        continue;
-      }
-      ld_row[u] = static_cast<int32_t>(row);
-      ld_pos[u] = (lb * P.bsub + in) * kSubTokens;
-      ld_in[u] = in;
-    }
+  // ===== the queries of a (b, hm), a row per warp: loaded early, laid out as B fragments later
+  uint2 qrow[C::kQRows];
+  const bool q_lane = lane < D / 4;  // lane (s, c) = (k-step, column pair) of the fragments
+  auto row_index = [&](const LinePos &L, int rr) -> int64_t {  // (b, query token, head) of a row
+    const int h = L.hm / P.mgroups, rq = (L.hm - h * P.mgroups) * kBaMaxRows + rr, j = rq / P.group;
+    return rq < P.n_q * P.group ? (static_cast<int64_t>(L.b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group : -1;
   };
-  auto issue = [&](int st) {
-    if (ld_g < g1) {
-      uint32_t dst = smem_u32(stage_base + st * C::kStageBytes);
+  auto load_q = [&](const LinePos &L) {
 #pragma unroll
-      for (int u = 0; u < C::kSubs; ++u, dst += C::kSubBytes) {
-        if (lane == 0) meta[st * C::kSubs + u] = ld_pos[u];
-        const bool held = ld_row[u] >= 0;
-        const uint8_t *row = reinterpret_cast<const uint8_t *>(P.rows) + (held ? ld_row[u] : 0) * P.row_bytes;
-        if constexpr (C::kFp4) {
-          const uint8_t *src = row + static_cast<int64_t>(ld_in[u]) * C::kSubBytes;
-          constexpr int kPieces = C::kSubBytes / 16;
-#pragma unroll
-          for (int i = 0; i < (kPieces + 31) / 32; ++i) {
-            const int x = i * 32 + lane;
-            if ((i + 1) * 32 <= kPieces || x < kPieces) ba_cp16(dst + x * 16, src + x * 16, held);
-          }
-        } else {
-          // rows of 2 D bytes, 16-byte pieces XORed with the token so that ldmatrix reads
-          // 8 tokens from 8 different bank groups
-          const uint8_t *src = row + static_cast<int64_t>(ld_in[u]) * (kSubTokens * D * 2);
-          const int64_t vofs = static_cast<int64_t>(P.bsub) * kSubTokens * D * 2;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const int x = i * 32 + lane, tk = x / (D / 8), pc = x % (D / 8);
-            const int p = ld_pos[u] + tk;
-            // a token no query sees is read as zeros: its bytes may be anything
-            const bool on = held && p < ld.v.len && (p >= ld.v.wlo || p < P.sinks);
-            const uint32_t o = tk * (2 * D) + ((pc ^ (tk & 7)) << 4);
-            ba_cp16(dst + o, src + x * 16, on);
-            ba_cp16(dst + kSubTokens * D * 2 + o, src + vofs + x * 16, on);
-          }
-        }
+    for (int i = 0; i < C::kQRows; ++i) {
+      const int rr = warp + i * WARPS;
+      qrow[i] = make_uint2(0u, 0u);
+      const int64_t at = rr < C::kRows ? row_index(L, rr) : -1;
+      if (at < 0 || !q_lane) continue;
+      const uint16_t *src = P.q + at * D;
+      if constexpr (F16) {
+        qrow[i] = *reinterpret_cast<const uint2 *>(src + (D / 4) * c4 + 8 * (r8 >> 1) + 4 * (r8 & 1));
+      } else {
+        qrow[i].x = *reinterpret_cast<const uint32_t *>(src + 16 * r8 + 2 * c4);
+        qrow[i].y = *reinterpret_cast<const uint32_t *>(src + 16 * r8 + 2 * c4 + 8);
       }
     }
-    ba_commit();
-    ld_g += WARPS;
-    lookup();
   };
-  lookup();
+  auto store_q = [&]() {
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(s);
-
-  int st = 0;
-  int64_t g = g0 + warp;
-  for (;;) {  // the (b, hm) of this range, one after another
-    const int64_t pend = min(cur.end, g1);
-    const int h = cur.hm / P.mgroups, mg = cur.hm - h * P.mgroups;
-    const int row0 = mg * kBaMaxRows, rows = min(P.n_q * P.group - row0, C::kRows);
-    // ----- the queries of this (b, hm) as B fragments -----
-    if constexpr (F16) {
-      // a warp per row: the power of two that brings its largest entry to [1, 2)
-      for (int rr = warp; rr < C::kRows; rr += WARPS) {
-        float m = 0.f;
-        if (rr < rows) {
-          const int rq = row0 + rr, j = rq / P.group;
-          const uint16_t *src = P.q + ((static_cast<int64_t>(cur.b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group) * D;
-          for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(__uint_as_float(static_cast<uint32_t>(src[d]) << 16)));
-        }
+    for (int i = 0; i < C::kQRows; ++i) {
+      const int rr = warp + i * WARPS;
+      if (rr >= C::kRows) break;
+      uint2 f = qrow[i];
+      if constexpr (F16) {
+        // scaled by the power of two that brings the row's largest entry to [1, 2)
+        const float x0 = __uint_as_float(f.x << 16), x1 = __uint_as_float(f.x & 0xffff0000u);
+        const float x2 = __uint_as_float(f.y << 16), x3 = __uint_as_float(f.y & 0xffff0000u);
+        float m = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
         int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
         e = max(min(e, 126), -126);  // (zero rows, subnormal and infinite maxima)
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        f = make_uint2(pack2<true>(x0 * inv, x1 * inv), pack2<true>(x2 * inv, x3 * inv));
         if (lane == 0) qscale[rr] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
       }
-      __syncthreads();
+      f.x ^= P.q_sign, f.y ^= P.q_sign;
+      if (q_lane) qfrag[(r8 * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + c4] = f;
     }
-    for (int i = threadIdx.x; i < C::kSteps * NT * 32; i += C::kThreads) {
-      const int ln = i & 31, nt = (i >> 5) % NT, s = (i >> 5) / NT;
-      const int rr = nt * 8 + (ln >> 2), c = ln & 3;
-      uint2 f = make_uint2(0u, 0u);
-      if (rr < rows) {
-        const int rq = row0 + rr, j = rq / P.group;
-        const uint16_t *src = P.q + ((static_cast<int64_t>(cur.b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group) * D;
-        if constexpr (F16) {
-          const int d = (D / 4) * c + 8 * (s >> 1) + 4 * (s & 1);
-          const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
-          const float inv = __uint_as_float((254u << 23) - __float_as_uint(qscale[rr]));  // exact 1 / 2^e
-          f.x = pack2<true>(__uint_as_float(w.x << 16) * inv, __uint_as_float(w.x & 0xffff0000u) * inv);
-          f.y = pack2<true>(__uint_as_float(w.y << 16) * inv, __uint_as_float(w.y & 0xffff0000u) * inv);
+  };
+  load_q(cur);
+
+  // ===== the loader =====
+  // Entry i of the warp's list is sub-block i % kSubs of its chunk i / kSubs (chunk warp +
+  // WARPS * (i / kSubs) of the range).  Entries are made 32 at a time; the loader is at
+  // most (STAGES - 1) * kSubs < 32 entries ahead of the reader.
+  static_assert((STAGES - 1) * C::kSubs <= kBaList - 32 && 32 % C::kSubs == 0, "list length");
+  LinePos mine = cur;     // of the entry this lane makes
+  int made = 0, at = 0;   // entries made, entries loaded
+  auto issue = [&](int st) {
+    if (at == made) {     // (warp-uniform)
+      const int i = made + lane, g = warp + WARPS * (i / C::kSubs);
+      SubEntry x{reinterpret_cast<const uint8_t *>(P.rows), kBaNowhere, kBaEdge};
+      if (g < n_chunks) {
+        seek<C::kSubs>(P, mine, g);
+        x = sub_entry<FMT, D>(P, mine, (g - mine.start) * C::kSubs + i % C::kSubs);
+      }
+      list[i % kBaList] = x;
+      made += 32;
+      __syncwarp();
+    }
+    if (warp + WARPS * (at / C::kSubs) < n_chunks) {
+      uint32_t dst = smem_u32(stage_base + st * C::kStageBytes) + lane * 16;
+#pragma unroll
+      for (int u = 0; u < C::kSubs; ++u, dst += C::kSubBytes) {
+        const SubEntry x = list[(at + u) % kBaList];
+        const uint8_t *src = x.src + lane * 16;
+        if constexpr (C::kFp4) {
+          constexpr int kPieces = C::kSubBytes / 16;
+          const bool on = (x.flags & 0xffffu) != 0;
+#pragma unroll
+          for (int i = 0; i < (kPieces + 31) / 32; ++i)
+            if ((i + 1) * 32 <= kPieces || lane < kPieces - i * 32) ba_cp16(dst + i * 512, src + i * 512, on);
         } else {
-          f.x = *reinterpret_cast<const uint32_t *>(src + 16 * s + 2 * c);
-          f.y = *reinterpret_cast<const uint32_t *>(src + 16 * s + 2 * c + 8);
+          // rows of 2 D bytes, 16-byte pieces XORed with the token so that ldmatrix reads
+          // 8 tokens from 8 different bank groups; a token no query sees is read as zeros
+          // (its bytes may be anything)
+          const int64_t vofs = static_cast<int64_t>(P.bsub) * kSubTokens * D * 2;
+          constexpr int kPer = 256 / D;  // tokens of 32 pieces
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int tk = i * kPer + lane / (D / 8), pc = lane % (D / 8);
+            const uint32_t o = tk * (2 * D) + ((pc ^ (tk & 7)) << 4) - lane * 16;
+            const bool on = (x.flags >> tk) & 1;
+            ba_cp16(dst + o, src + i * 512, on);
+            ba_cp16(dst + kSubTokens * D * 2 + o, src + vofs + i * 512, on);
+          }
         }
       }
-      qfrag[i] = f;
     }
-    __syncthreads();
+    at += C::kSubs;
+    ba_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(s);
+  store_q();
+  __syncthreads();
+
+  int st = 0, g = warp, rd = 0;  // stage, chunk and list entry to compute
+  for (;;) {  // the (b, hm) of this range, one after another
+    const int pend = min(cur.end, n_chunks);
+    const int row0 = (cur.hm % P.mgroups) * kBaMaxRows;
     uint2 qreg[NT == 1 ? C::kSteps : 1];
     if constexpr (NT == 1) {
 #pragma unroll
@@ -434,7 +471,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
         cscale[nt][e] = P.scale_log2 * (F16 ? qscale[rr] : 1.f);
         clen[nt][e] = cur.v.len - (P.n_q - 1 - min((row0 + rr) / P.group, P.n_q - 1));
       }
-    const int len_first = cur.v.len - (P.n_q - 1), w_last = P.window ? cur.v.len - P.window : 0;
 
     float m[NT][2], l[NT][2], o[C::kSteps][NT][4];
 #pragma unroll
@@ -454,13 +490,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       issue(st == 0 ? STAGES - 1 : st - 1);
       const uint8_t *sp = stage_base + st * C::kStageBytes;
       int pos[C::kSubs];
-      bool edge = false;
+      uint32_t flags[C::kSubs], edge = 0;
 #pragma unroll
       for (int u = 0; u < C::kSubs; ++u) {
-        pos[u] = meta[st * C::kSubs + u];
-        const int last = pos[u] + kSubTokens - 1;
-        edge |= !(last < len_first && (pos[u] >= w_last || last < P.sinks));
+        const int2 x = *reinterpret_cast<const int2 *>(&list[(rd + u) % kBaList].pos);
+        pos[u] = x.x;
+        flags[u] = static_cast<uint32_t>(x.y);
+        edge |= flags[u] & kBaEdge;
       }
+      rd += C::kSubs;
 
       float s[C::kSubs][NT][4];
 #pragma unroll
@@ -523,30 +561,35 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       }
 
       // ----- softmax -----
-      bool grow = false;
+      if (edge) {
 #pragma unroll
-      for (int u = 0; u < C::kSubs; ++u)
+        for (int u = 0; u < C::kSubs; ++u)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = s[u][nt][e] * cscale[nt][e & 1];
-            if (edge) {
+            for (int e = 0; e < 4; ++e) {
               const int p = pos[u] + r8 + (e >> 1) * 8, n = clen[nt][e & 1];
               const bool see = p < n && (P.window == 0 || p >= n - P.window || p < P.sinks);
-              x = see ? x : -INFINITY;
+              s[u][nt][e] = see ? s[u][nt][e] : -INFINITY;
             }
-            s[u][nt][e] = x;
-            grow |= x > m[nt][e & 1] + kBaLazy;
-          }
+      }
+      bool grow = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nt][e] = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < C::kSubs; ++u) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[u][nt][e], s[u][nt][e + 2]));
+          grow |= fmaf(top[nt][e], cscale[nt][e], -m[nt][e]) > kBaLazy;
+        }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = m[nt][e];
-#pragma unroll
-            for (int u = 0; u < C::kSubs; ++u) x = fmaxf(x, fmaxf(s[u][nt][e], s[u][nt][e + 2]));
+            float x = fmaxf(m[nt][e], top[nt][e] * cscale[nt][e]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
             const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
@@ -556,18 +599,29 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
             for (int j = 0; j < C::kSteps; ++j) o[j][nt][e] *= f, o[j][nt][e + 2] *= f;
           }
       }
-      uint32_t pb[C::kSubs][NT][2];
+      // bf16 weights go in as two terms (a bf16 and the bf16 of what it leaves out): the cache's
+      // own type then costs no precision, and the tensor cores have the time
+      uint32_t pb[C::kSubs][NT][2], pr[C::kSubs][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kLift, m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kLift;
 #pragma unroll
         for (int u = 0; u < C::kSubs; ++u) {
-          const float p0 = ex2(s[u][nt][0] - m0), p1 = ex2(s[u][nt][1] - m1);
-          const float p2 = ex2(s[u][nt][2] - m0), p3 = ex2(s[u][nt][3] - m1);
+          float p0 = ex2(fmaf(s[u][nt][0], cscale[nt][0], -m0)), p1 = ex2(fmaf(s[u][nt][1], cscale[nt][1], -m1));
+          float p2 = ex2(fmaf(s[u][nt][2], cscale[nt][0], -m0)), p3 = ex2(fmaf(s[u][nt][3], cscale[nt][1], -m1));
+          if (edge) {  // (a zero scale leaves nothing of a masked score's infinity)
+            p0 = s[u][nt][0] == -INFINITY ? 0.f : p0, p1 = s[u][nt][1] == -INFINITY ? 0.f : p1;
+            p2 = s[u][nt][2] == -INFINITY ? 0.f : p2, p3 = s[u][nt][3] == -INFINITY ? 0.f : p3;
+          }
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
-          pb[u][nt][0] = movm_t(pack2<F16>(p0, p1));
-          pb[u][nt][1] = movm_t(pack2<F16>(p2, p3));
+          const uint32_t a = pack2<F16>(p0, p1), b = pack2<F16>(p2, p3);
+          pb[u][nt][0] = movm_t(a);
+          pb[u][nt][1] = movm_t(b);
+          if constexpr (!F16) {
+            pr[u][nt][0] = movm_t(pack2<F16>(p0 - __uint_as_float(a << 16), p1 - __uint_as_float(a & 0xffff0000u)));
+            pr[u][nt][1] = movm_t(pack2<F16>(p2 - __uint_as_float(b << 16), p3 - __uint_as_float(b & 0xffff0000u)));
+          }
         }
       }
 
@@ -591,26 +645,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
             const int grp = D == 128 ? r8 : r8 >> 1;
             sc[p] = e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(vp + Fp4Sub<D>::kValueScales + p * (D / 2) + grp * 8 + 2 * c4));
             if (edge) {  // a token no query sees: its scale may be NaN
-              const int t0 = pos[u] + 8 * p + 2 * c4;
-              const bool on0 = t0 < cur.v.len && (t0 >= cur.v.wlo || t0 < P.sinks);
-              const bool on1 = t0 + 1 < cur.v.len && (t0 + 1 >= cur.v.wlo || t0 + 1 < P.sinks);
-              sc[p] &= (on0 ? 0xffffu : 0u) | (on1 ? 0xffff0000u : 0u);
+              const uint32_t on = flags[u] >> (8 * p + 2 * c4);
+              sc[p] &= (on & 1 ? 0xffffu : 0u) | (on & 2 ? 0xffff0000u : 0u);
             }
           }
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
+            // nibbles of tokens t, t + 1 side by side, even dims in one word, odd in another:
+            // each byte then converts to the (t, t + 1) pair of one dim
             uint32_t f[2][2][4];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) e2m1x8_to_half2(w[p][t][i], f[p][t]);
+            for (int p = 0; p < 2; ++p) {
+              constexpr uint32_t kLow = 0x0f0f0f0fu;
+              const uint32_t t0 = w[p][0][i], t1 = w[p][1][i];
+              e2m1x8_to_half2((t0 & kLow) | ((t1 << 4) & ~kLow), f[p][0]);
+              e2m1x8_to_half2(((t0 >> 4) & kLow) | (t1 & ~kLow), f[p][1]);
+            }
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              // dims (2j, 2j + 1) of tokens t, t + 1 -> (t, t + 1) of each dim
-              const uint32_t a[4] = {hmul2(__byte_perm(f[0][0][b], f[0][1][b], 0x5410), sc[0]),
-                                     hmul2(__byte_perm(f[0][0][b], f[0][1][b], 0x7632), sc[0]),
-                                     hmul2(__byte_perm(f[1][0][b], f[1][1][b], 0x5410), sc[1]),
-                                     hmul2(__byte_perm(f[1][0][b], f[1][1][b], 0x7632), sc[1])};
+              const uint32_t a[4] = {hmul2(f[0][0][b], sc[0]), hmul2(f[0][1][b], sc[0]), hmul2(f[1][0][b], sc[1]),
+                                     hmul2(f[1][1][b], sc[1])};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[4 * i + b][nt], a, pb[u][nt][0], pb[u][nt][1]);
             }
@@ -623,7 +677,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
             uint32_t a[4];
             ldsm4_t(a, va + (((2 * j + ((lane >> 3) & 1)) ^ (tk & 7)) << 4));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[j][nt], a, pb[u][nt][0], pb[u][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<false>(o[j][nt], a, pb[u][nt][0], pb[u][nt][1]);
+              mma16816<false>(o[j][nt], a, pr[u][nt][0], pr[u][nt][1]);
+            }
           }
         }
       }
@@ -631,6 +688,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
     }
 
     // ----- merge the warps; the result, or this piece's part of it -----
+    const bool more = pend < n_chunks;
+    LinePos nxt = cur;
+    if (more) {  // the next queries are on their way while the warps merge
+      seek<C::kSubs>(P, nxt, pend);
+      load_q(nxt);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -640,130 +703,150 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
         if (r8 == 0) ml[warp * C::kRows + nt * 8 + 2 * c4 + e] = make_float2(m[nt][e], l[nt][e]);
       }
     __syncthreads();
-    const bool split = !P.whole && (cur.start < g0 || cur.end > g1);
-    const int slot = 2 * blockIdx.x + (cur.start < g0 ? 0 : 1);
+    if (more) store_q();
+    if (warp == WARPS - 1 && lane < C::kRows) {  // maximum and sum of a row
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * C::kRows + lane].x);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float2 v = ml[w * C::kRows + lane];
+        sum += v.x == -INFINITY ? 0.f : v.y * ex2(v.x - top);
+      }
+      fin[lane] = make_float2(top, sum);
+    }
+    const bool split = !P.whole && (cur.start < 0 || cur.end > n_chunks);
+    const int slot = 2 * blockIdx.x + (cur.start < 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * C::kRows + nt * 8 + 2 * c4 + e].x);
-        const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
-        float *dst = merge + (warp * 8 + 2 * c4 + e) * C::kMergeRow;
-#pragma unroll
-        for (int j = 0; j < C::kSteps; ++j) {
-          // 4-bit rows: dim r8 * D/8 + 2j + i is kept at (2j + i) * 8 + r8, bf16 rows: dim
-          // 16j + 8i + r8 at its own place (the same expression)
-          dst[16 * j + r8] = o[j][nt][e] * f;
-          dst[16 * j + 8 + r8] = o[j][nt][e + 2] * f;
-        }
+        f[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 8 * D / 2; i += C::kThreads) {
-        const int rr = i / (D / 2), d = 2 * (i % (D / 2)), row = nt * 8 + rr;
-        int a0 = d, a1 = d + 1;
-        if constexpr (C::kFp4) {
-          a0 = (d % (D / 8)) * 8 + d / (D / 8);
-          a1 = a0 + 8;
-        }
-        float top = -INFINITY, sum = 0.f, x0 = 0.f, x1 = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * C::kRows + row].x);
+      for (int hf = 0; hf < 2; ++hf) {  // half of the dims at a time
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-          const float2 v = ml[w * C::kRows + row];
-          sum += v.x == -INFINITY ? 0.f : v.y * ex2(v.x - top);
-          x0 += merge[(w * 8 + rr) * C::kMergeRow + a0];
-          x1 += merge[(w * 8 + rr) * C::kMergeRow + a1];
+        for (int e = 0; e < 2; ++e) {
+          float *dst = merge + (warp * 8 + 2 * c4 + e) * C::kMergeRow + 2 * r8;
+#pragma unroll
+          for (int j = 0; j < C::kSteps / 2; ++j) {
+            const float *x = o[hf * (C::kSteps / 2) + j][nt];
+            *reinterpret_cast<float2 *>(dst + 16 * j) = make_float2(x[e] * f[e], x[e + 2] * f[e]);
+          }
         }
-        if (split) {
-          *reinterpret_cast<float2 *>(P.part_o + (static_cast<int64_t>(slot) * C::kRows + row) * D + d) = make_float2(x0, x1);
-          if (d == 0) reinterpret_cast<float2 *>(P.part_ml)[slot * C::kRows + row] = make_float2(top, sum);
-        } else if (row < rows) {
-          const int rq = row0 + row, j = rq / P.group;
-          const int64_t oh = (static_cast<int64_t>(cur.b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
-          const float inv = sum > 0.f ? 1.f / sum : sum;  // (a NaN sum stays one)
-          *reinterpret_cast<uint32_t *>(P.out + oh * D + d) = pack2<false>(x0 * inv, x1 * inv);
-          if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum, kLift);
+        __syncthreads();
+        // a thread adds four neighbouring values of a row: tile j of this half, fragment rows
+        // r and r + 1, both halves of the tile
+        for (int i = threadIdx.x; i < 8 * D / 8; i += C::kThreads) {
+          const int rr = i / (D / 8), k = i % (D / 8), j = hf * (C::kSteps / 2) + k / 4, r = 2 * (k % 4), row = nt * 8 + rr;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) {
+            const float4 y = *reinterpret_cast<const float4 *>(merge + (w * 8 + rr) * C::kMergeRow + 4 * k);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+          // x.x, x.y: fragment row r (tile rows r, r + 8); x.z, x.w: row r + 1
+          int d0, d1;
+          float2 a, b;
+          if constexpr (C::kFp4) {  // tile rows (r, r + 8) are dims r * D/8 + 2 j + (0, 1)
+            d0 = r * (D / 8) + 2 * j, d1 = d0 + D / 8;
+            a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
+          } else {                  // dims 16 j + r and 16 j + 8 + r
+            d0 = 16 * j + r, d1 = d0 + 8;
+            a = make_float2(x.x, x.z), b = make_float2(x.y, x.w);
+          }
+          const float2 v = fin[row];
+          if (split) {
+            float *part = P.part_o + (static_cast<int64_t>(slot) * C::kRows + row) * D;
+            *reinterpret_cast<float2 *>(part + d0) = a;
+            *reinterpret_cast<float2 *>(part + d1) = b;
+            if (k == 0 && hf == 0) reinterpret_cast<float2 *>(P.part_ml)[slot * C::kRows + row] = v;
+          } else {
+            const int64_t oh = row_index(cur, row);
+            if (oh >= 0) {
+              const float inv = v.y > 0.f ? 1.f / v.y : v.y;  // (a NaN sum stays one)
+              *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
+              *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
+              if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y, kLift);
+            }
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
-    if (pend >= g1) break;
-    seek<C::kSubs>(P, cur, pend);
+    if (!more) break;
+    cur = nxt;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Merge of the pieces of each (b, hm) that was cut: block (i, y) takes the one that begins
-// in CTA i's range and goes on past it, rows y of it.  The pieces' weights 2^(m_s - max m)
-// are formed once per row; D / 2 threads of each row then add the pieces in order.
-constexpr int kBaCombThreads = 128;
+// Merge of the pieces of each (b, hm) that was cut: block (i, y) takes row y of the one that
+// begins in CTA i's range and goes on past it.  D / 4 threads add a piece's row at a time
+// (kBaCombThreads / (D / 4) pieces side by side, their first loads issued before it is known
+// how many there are: one round trip to L2 in the usual case), then the groups in order.
+constexpr int kBaCombThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kBaCombThreads) block_attn_combine_kernel(const BlockAttnParams P, int rows_pad,
                                                                                  float lift) {
-  constexpr int kSlots = 2 * kBaMaxGrid;
-  __shared__ float wgt[kSlots];
-  __shared__ float red[2][kBaCombThreads / 32];
-  const int cta = blockIdx.x, row = blockIdx.y, t = threadIdx.x;
+  constexpr int kLanes = D / 4, kGroups = kBaCombThreads / kLanes;
+  __shared__ float2 sml[kGroups];
+  __shared__ __align__(16) float so[kGroups][D];
+  const int cta = blockIdx.x, row = blockIdx.y, grp = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
   pdl_wait();
-  // requests with nothing to see are not on the line (without a split, their own CTA, whose
-  // stream is empty, writes the same)
-  const int heads = P.n_kv * P.mgroups;
-  for (int64_t i = cta; i < static_cast<int64_t>(P.B) * heads; i += gridDim.x) {
-    const int b = static_cast<int>(i / heads);
-    if (req_view(P, __ldg(P.ctx_len + b)).nsub > 0) continue;
-    const int hm = static_cast<int>(i - static_cast<int64_t>(b) * heads), h = hm / P.mgroups;
-    const int rq = (hm - h * P.mgroups) * kBaMaxRows + row;
-    if (rq >= P.n_q * P.group) continue;
-    const int j = rq / P.group;
-    const int64_t oh = (static_cast<int64_t>(b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
-    for (int d = t; d < D; d += kBaCombThreads) P.out[oh * D + d] = 0;
-    if (t == 0 && P.lse) P.lse[oh] = -INFINITY;
-  }
+  // piece 0 is CTA i's second slot, piece s > 0 the first slot of CTA i + s
+  auto slot_row = [&](int s) {
+    return static_cast<int64_t>(s == 0 ? 2 * cta + 1 : 2 * min(cta + s, kBaMaxGrid - 1)) * rows_pad + row;
+  };
   const int4 tail = P.tail[cta];
+  float2 v = reinterpret_cast<const float2 *>(P.part_ml)[slot_row(grp)];
+  float4 x = *reinterpret_cast<const float4 *>(P.part_o + slot_row(grp) * D + d);
   const int pieces = tail.z;
   if (pieces == 0) return;
   const int h = tail.y / P.mgroups;
   const int rq = (tail.y - h * P.mgroups) * kBaMaxRows + row;
   if (rq >= P.n_q * P.group) return;
-  // piece 0 is CTA i's second slot, piece s > 0 the first slot of CTA i + s
-  auto slot_of = [&](int s) { return s == 0 ? 2 * cta + 1 : 2 * (cta + s); };
-  float top = -INFINITY;
-  for (int s = t; s < pieces; s += kBaCombThreads) top = fmaxf(top, P.part_ml[2 * (static_cast<int64_t>(slot_of(s)) * rows_pad + row)]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if ((t & 31) == 0) red[0][t >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kBaCombThreads / 32; ++w) top = fmaxf(top, red[0][w]);
-  float sum = 0.f;
-  for (int s = t; s < pieces; s += kBaCombThreads) {
-    const float2 v = *reinterpret_cast<const float2 *>(P.part_ml + 2 * (static_cast<int64_t>(slot_of(s)) * rows_pad + row));
-    const float w = v.x == -INFINITY ? 0.f : ex2(v.x - top);
-    wgt[s] = w;
-    sum = fmaf(w, v.y, sum);
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = grp; s < pieces;) {
+    const float top = fmaxf(m, v.x);
+    const float fa = m == -INFINITY ? 0.f : ex2(m - top), fb = v.x == -INFINITY ? 0.f : ex2(v.x - top);
+    m = top;
+    l = l * fa + v.y * fb;
+    acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
+    acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
+    s += kGroups;
+    if (s < pieces) {
+      v = reinterpret_cast<const float2 *>(P.part_ml)[slot_row(s)];
+      x = *reinterpret_cast<const float4 *>(P.part_o + slot_row(s) * D + d);
+    }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  if ((t & 31) == 0) red[1][t >> 5] = sum;
+  if (d == 0) sml[grp] = make_float2(m, l);
+  *reinterpret_cast<float4 *>(&so[grp][d]) = acc;
   __syncthreads();
-  sum = 0.f;
+  if (grp != 0) return;
+  float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kBaCombThreads / 32; ++w) sum += red[1][w];
+  for (int k = 0; k < kGroups; ++k) top = fmaxf(top, sml[k].x);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const float2 w = sml[k];
+    const float f = w.x == -INFINITY ? 0.f : ex2(w.x - top);
+    const float4 a = *reinterpret_cast<const float4 *>(&so[k][d]);
+    sum += w.y * f;
+    y.x += a.x * f, y.y += a.y * f, y.z += a.z * f, y.w += a.w * f;
+  }
   const int j = rq / P.group;
   const int64_t oh = (static_cast<int64_t>(tail.x) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
   const float inv = sum > 0.f ? 1.f / sum : sum;
-  for (int d = t; d < D; d += kBaCombThreads) {
-    float x = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < pieces; ++s) x = fmaf(wgt[s], P.part_o[(static_cast<int64_t>(slot_of(s)) * rows_pad + row) * D + d], x);
-    const __nv_bfloat16 y = __float2bfloat16_rn(x * inv);
-    P.out[oh * D + d] = *reinterpret_cast<const uint16_t *>(&y);
-  }
-  if (t == 0 && P.lse) P.lse[oh] = ba_lse(top, sum, lift);
+  *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
+      make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
+  if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum, lift);
 }
 
 }  // namespace echo
@@ -815,7 +898,8 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   const int rows = P.n_q * P.group;
   P.mgroups = (rows + echo::kBaMaxRows - 1) / echo::kBaMaxRows;
   P.sinks = a->sinks, P.window = a->window;
-  P.scale_log2 = a->scale * 1.4426950408889634f;
+  P.scale_log2 = std::fabs(a->scale) * 1.4426950408889634f;
+  P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
   P.out = a->out, P.lse = a->lse;
   P.status = a->dev_status;
   const int pad = ba_row_pad(rows < echo::kBaMaxRows ? rows : echo::kBaMaxRows);
@@ -829,15 +913,19 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   // tokens a context can show at most
   int64_t most = static_cast<int64_t>(P.max_blocks) * a->block_tokens;
   if (!P.sel && P.window && most > P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31) most = P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31;
-  P.whole = most <= 256;
+  // Whole (b, h) per CTA, or the line cut into equal pieces?  Whole costs the waves' longest
+  // context; cutting costs an equal share plus the second kernel and the piece borders.
+  const int64_t waves = (pairs + sms - 1) / sms, extra = a->format == ECHO_BLOCK_FP4 ? 1024 : 512;
+  P.whole = waves * most <= pairs * most / sms + extra;
   int grid = P.whole ? static_cast<int>(pairs) : sms;
   if (grid > echo::kBaMaxGrid && !P.whole) grid = echo::kBaMaxGrid;
-#define BA_GO(FMT, D, W, S, S4)                              \
-  (pad == 8    ? launch_ba<FMT, D, 1, W, S>(P, grid, stream) \
-   : pad == 16 ? launch_ba<FMT, D, 2, W, S>(P, grid, stream) \
-               : launch_ba<FMT, D, 4, W, S4>(P, grid, stream))
-  if (a->format == ECHO_BLOCK_FP4) return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 8, 4, 4) : BA_GO(ECHO_BLOCK_FP4, 64, 8, 4, 4);
-  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 6, 4, 3) : BA_GO(ECHO_BLOCK_BF16, 64, 6, 4, 3);
+#define BA_GO(FMT, D, W1, S1, W2, S2, W4, S4)                  \
+  (pad == 8    ? launch_ba<FMT, D, 1, W1, S1>(P, grid, stream) \
+   : pad == 16 ? launch_ba<FMT, D, 2, W2, S2>(P, grid, stream) \
+               : launch_ba<FMT, D, 4, W4, S4>(P, grid, stream))
+  if (a->format == ECHO_BLOCK_FP4)
+    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 12, 3, 8, 4, 8, 4) : BA_GO(ECHO_BLOCK_FP4, 64, 12, 3, 8, 4, 8, 4);
+  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 6, 4, 6, 4) : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 6, 4, 6, 4);
 #undef BA_GO
 }
 

@@ -5,10 +5,11 @@
 //
 // A head is read by head_dim / 8 lanes, one 16-byte load each, and never leaves registers
 // until its results are stored: the mean is a shuffle sum over those lanes, the partner of
-// a half-split pair sits in the lane rope_dim / 16 away (a shuffle), of an interleaved pair
-// in the same lane; a 4-bit scale covers 16 dimensions, so two neighbouring lanes.  A lane
-// group takes kHeads heads of one token: their loads are issued together (bytes in flight)
-// and the token's cosines and sines are read once for them.  Bound by HBM.
+// a half-split pair sits in the lane rope_dim / 16 away (a shuffle of the bf16 pairs as
+// loaded), of an interleaved pair in the same lane; a 4-bit scale covers 16 dimensions, so
+// two neighbouring lanes.  A warp takes kHeads heads of one kind (q, k or v) of its tokens:
+// their loads are issued together (bytes in flight), and cosines, sines and weights are read
+// and multiplied once for them.  Bound by HBM.
 #include "block_rows.cuh"
 
 namespace echo {
@@ -30,8 +31,7 @@ struct RopeParams {
   uint16_t *rows;
   int32_t n_rows, format, bs;
   int64_t row_elems;
-  int32_t heads;      // q + k + v heads that have work
-  int32_t chunks;     // lane groups per token
+  int32_t q_chunks, k_chunks, chunks;  // warps per token group: of q, of k (and of v), in all
   int32_t *status;
 };
 
@@ -90,120 +90,142 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t scale) {
   return pack_bf16x8(x);
 }
 
-template <int D, int kHeads>
+// Kinds of heads, in the order of a token's chunks; a warp works on one kind.
+enum RopeKind { kRopeQ, kRopeK, kRopeV };
+
+template <int D, int kHeads, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams P) {
-  constexpr int kLanes = D / 8;  // lanes of a head
-  const int64_t group = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) / kLanes;
-  const int l = threadIdx.x % kLanes, d0 = 8 * l;
-  // groups of one warp may belong to different tokens: shuffles run over the whole warp,
-  // so no lane leaves early
-  const int64_t tok = group / P.chunks;
-  const int chunk = static_cast<int>(group - tok * P.chunks);
+  constexpr int kLanes = D / 8;          // lanes of a head
+  constexpr int kTokens = 32 / kLanes;   // tokens of a warp
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
+  const int64_t tb = wid / P.chunks;
+  int chunk = static_cast<int>(wid - tb * P.chunks);
+  const int lane = threadIdx.x & 31, l = lane % kLanes, d0 = 8 * l;
+  const int64_t tok = tb * kTokens + lane / kLanes;
+  if (tb * kTokens >= P.T) return;       // (the whole warp)
   const int64_t t = min(tok, static_cast<int64_t>(P.T) - 1);
   const int pos = __ldg(P.positions + t);
   const bool in = tok < P.T && pos >= 0 && pos < P.max_pos;
   if (tok < P.T && pos >= P.max_pos && l == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
-  const int slot = P.slot_map ? __ldg(P.slot_map + t) : -1;
-  const int nk = P.n_heads + P.n_kv_heads;
 
+  const int kind = chunk < P.q_chunks ? kRopeQ : chunk < P.q_chunks + P.k_chunks ? kRopeK : kRopeV;
+  const int h0 = (kind == kRopeQ ? chunk : (chunk - P.q_chunks) % P.k_chunks) * kHeads;
+  const int heads = kind == kRopeQ ? P.n_heads : P.n_kv_heads;
+  const uint16_t *src = (kind == kRopeQ   ? P.q + t * P.q_stride
+                         : kind == kRopeK ? P.k + t * P.k_stride
+                                          : P.v + t * P.v_stride) + static_cast<int64_t>(h0) * D + d0;
   uint4 raw[kHeads];
 #pragma unroll
   for (int u = 0; u < kHeads; ++u) {
-    const int h = chunk * kHeads + u;
     raw[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && h < P.heads) {
-      const uint16_t *src = h < P.n_heads ? P.q + t * P.q_stride + static_cast<int64_t>(h) * D
-                            : h < nk      ? P.k + t * P.k_stride + static_cast<int64_t>(h - P.n_heads) * D
-                                          : P.v + t * P.v_stride + static_cast<int64_t>(h - nk) * D;
-      raw[u] = *reinterpret_cast<const uint4 *>(src + d0);
-    }
+    if (in && h0 + u < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + u * D);
   }
-  // the rotation as y' = y * c + partner * s, with the sign of the sine folded in
+
+  // y = r * (x * c + partner * s): the cosine times the own weight, the signed sine times
+  // the partner's
   const int half = P.rope_dim >> 1;
-  const bool rot = d0 < P.rope_dim;
-  const bool low = d0 < half;
-  float c[8], s[8];
+  const bool rot = d0 < P.rope_dim, low = d0 < half;
+  const float *wt = kind == kRopeQ ? P.q_weight : P.k_weight;
+  const int pd = kInter || !rot ? d0 : low ? d0 + half : d0 - half;   // the partners' dims
+  float2 c[4], s[4];
+  if (kind != kRopeV) {
+    float cw[8], sw[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-  if (in && rot && chunk * kHeads < nk) {
-    const float *row = P.cos_sin + static_cast<int64_t>(pos) * P.rope_dim;
-    if (P.interleaved) {
-      const float4 cc = *reinterpret_cast<const float4 *>(row + d0 / 2);
-      const float4 ss = *reinterpret_cast<const float4 *>(row + half + d0 / 2);
-      const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+    for (int i = 0; i < 8; ++i) cw[i] = 1.f, sw[i] = 0.f;
+    if (in && rot) {
+      const float *row = P.cos_sin + static_cast<int64_t>(pos) * P.rope_dim;
+      if constexpr (kInter) {
+        const float4 cc = *reinterpret_cast<const float4 *>(row + d0 / 2);
+        const float4 ss = *reinterpret_cast<const float4 *>(row + half + d0 / 2);
+        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[2 * i] = c[2 * i + 1] = cv[i], s[2 * i] = -sv[i], s[2 * i + 1] = sv[i];
-    } else {
-      const float *cr = row + (low ? d0 : d0 - half);
+        for (int i = 0; i < 4; ++i) cw[2 * i] = cw[2 * i + 1] = cv[i], sw[2 * i] = -sv[i], sw[2 * i + 1] = sv[i];
+      } else {
+        const float *cr = row + (low ? d0 : d0 - half);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 cc = reinterpret_cast<const float4 *>(cr)[i];
+          const float4 ss = reinterpret_cast<const float4 *>(cr + half)[i];
+          cw[4 * i] = cc.x, cw[4 * i + 1] = cc.y, cw[4 * i + 2] = cc.z, cw[4 * i + 3] = cc.w;
+          sw[4 * i] = ss.x, sw[4 * i + 1] = ss.y, sw[4 * i + 2] = ss.z, sw[4 * i + 3] = ss.w;
+        }
+        if (low) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sw[i] = -sw[i];
+        }
+      }
+    }
+    if (wt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 cc = reinterpret_cast<const float4 *>(cr)[i];
-        const float4 ss = reinterpret_cast<const float4 *>(cr + half)[i];
-        c[4 * i] = cc.x, c[4 * i + 1] = cc.y, c[4 * i + 2] = cc.z, c[4 * i + 3] = cc.w;
-        s[4 * i] = ss.x, s[4 * i + 1] = ss.y, s[4 * i + 2] = ss.z, s[4 * i + 3] = ss.w;
-      }
-      if (low) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = -s[i];
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(wt + d0) + i);
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(wt + pd) + i);
+        cw[4 * i] *= a.x, cw[4 * i + 1] *= a.y, cw[4 * i + 2] *= a.z, cw[4 * i + 3] *= a.w;
+        if constexpr (kInter) sw[4 * i] *= b.y, sw[4 * i + 1] *= b.x, sw[4 * i + 2] *= b.w, sw[4 * i + 3] *= b.z;
+        else sw[4 * i] *= b.x, sw[4 * i + 1] *= b.y, sw[4 * i + 2] *= b.z, sw[4 * i + 3] *= b.w;
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = make_float2(cw[2 * i], cw[2 * i + 1]), s[i] = make_float2(sw[2 * i], sw[2 * i + 1]);
   }
   // the lane that holds the other half of this lane's pairs (half-split)
-  const int partner = (threadIdx.x & 31 & ~(kLanes - 1)) + (rot ? (low ? l + half / 8 : l - half / 8) : l);
+  const int partner = (lane & ~(kLanes - 1)) + pd / 8;
+  const int slot = P.slot_map && kind != kRopeQ ? __ldg(P.slot_map + t) : -1;
   const int64_t blk = slot >= 0 ? slot / P.bs : 0;
   const int off = slot >= 0 ? slot - static_cast<int>(blk) * P.bs : 0;
 
 #pragma unroll
   for (int u = 0; u < kHeads; ++u) {
-    const int h = chunk * kHeads + u;
-    const bool is_q = h < P.n_heads, is_v = h >= nk;
-    float x[8];
-    unpack_bf16x8(raw[u], x);
-    const float *wt = is_q ? P.q_weight : P.k_weight;
-    float ss = 0.f;
+    if (h0 + u >= heads) break;          // (warp-uniform)
+    uint4 o = raw[u];                    // a value head passes through
+    if (kind != kRopeV) {
+      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      uint32_t pw[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int i = 0; i < 4; ++i) {
+        pw[i] = kInter ? __byte_perm(w[i], 0, 0x1032) : __shfl_sync(~0u, w[i], partner);
+        if (!rot) pw[i] = 0;             // (0 * inf would reach the entries that stay)
+      }
+      float2 x[4], r2 = make_float2(1.f, 1.f);
 #pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
-    if (!is_v && wt) {
-      const float r = 1.f / sqrtf(ss * (1.f / D) + P.eps);
-      const float4 w0 = __ldg(reinterpret_cast<const float4 *>(wt + d0)), w1 = __ldg(reinterpret_cast<const float4 *>(wt + d0) + 1);
-      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      if (wt) {
+        float2 q2 = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+        for (int i = 1; i < 4; ++i) q2 = __ffma2_rn(x[i], x[i], q2);
+        float ss = q2.x + q2.y;
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
+        r2.x = r2.y = rsqrtf(fmaf(ss, 1.f / D, P.eps));
+      }
+      uint32_t ow[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = make_float2(__uint_as_float(pw[i] << 16), __uint_as_float(pw[i] & 0xffff0000u));
+        const float2 y = __fmul2_rn(__ffma2_rn(p, s[i], __fmul2_rn(x[i], c[i])), r2);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+        ow[i] = *reinterpret_cast<const uint32_t *>(&b);
+      }
+      o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
     }
-    float y[8];
-    if (P.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(~0u, x[i], partner);
-    }
-    uint4 o = raw[u];  // a value head passes through
-    if (!is_v) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], s[i], x[i] * c[i]);
-      o = pack_bf16x8(x);
-    }
-    const bool live = in && h < P.heads;
-    if (is_q) {
-      if (live) *reinterpret_cast<uint4 *>(P.q_out + (t * P.n_heads + h) * D + d0) = o;
+    if (kind == kRopeQ) {
+      if (in) *reinterpret_cast<uint4 *>(P.q_out + (t * P.n_heads + h0 + u) * D + d0) = o;
+      continue;
     }
     uint32_t codes = 0, scale = 0;
-    if (P.format == ECHO_BLOCK_FP4) {  // (every lane: the scale is a shuffle)
+    if (P.format == ECHO_BLOCK_FP4) {    // (every lane: the scale is a shuffle)
+      float x[8];
       unpack_bf16x8(o, x);
       codes = quantise8(x, scale);
     }
-    if (is_q || !live) continue;
-    const int hk = is_v ? h - nk : h - P.n_heads;
-    uint16_t *out = is_v ? P.v_out : P.k_out;
+    if (!in) continue;
+    uint16_t *out = kind == kRopeV ? P.v_out : P.k_out;
     if (out) {
-      *reinterpret_cast<uint4 *>(out + (t * P.n_kv_heads + hk) * D + d0) =
+      *reinterpret_cast<uint4 *>(out + (t * P.n_kv_heads + h0 + u) * D + d0) =
           P.format == ECHO_BLOCK_FP4 ? dequantise8(codes, scale) : o;
     }
-    if (slot < 0 || !P.rows) continue;
-    const int64_t row = blk * P.n_kv_heads + hk;
+    if (slot < 0) continue;
+    const int64_t row = blk * P.n_kv_heads + h0 + u;
     if (row >= P.n_rows) {
       if (l == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
       continue;
@@ -213,17 +235,17 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
       using Sub = Fp4Sub<D>;
       uint8_t *sub = reinterpret_cast<uint8_t *>(base) + off / kSubTokens * Sub::kBytes;
       const int tk = off % kSubTokens;
-      if (!is_v) {
+      if (kind == kRopeK) {
         *reinterpret_cast<uint32_t *>(sub + tk * (D / 2) + l * 4) = codes;
         if (!(l & 1)) sub[Sub::kKeyScales + tk * (D / 16) + l / 2] = static_cast<uint8_t>(scale);
       } else {
-        constexpr int kPart = D / 8;  // dims of a part: 16 (two lanes) or 8 (one lane)
+        constexpr int kPart = D / 8;     // dims of a part: 16 (two lanes) or 8 (one lane)
         *reinterpret_cast<uint32_t *>(sub + Sub::kValues + (tk / 8) * (4 * D) + ((d0 / kPart) * 8 + tk % 8) * (D / 16) +
                                       (d0 % kPart) / 2) = codes;
         if (!(l & 1)) sub[Sub::kValueScales + (tk / 8) * (D / 2) + (l / 2) * 8 + tk % 8] = static_cast<uint8_t>(scale);
       }
     } else {
-      *reinterpret_cast<uint4 *>(base + (is_v ? static_cast<int64_t>(P.bs) * D : 0) + static_cast<int64_t>(off) * D + d0) = o;
+      *reinterpret_cast<uint4 *>(base + (kind == kRopeV ? static_cast<int64_t>(P.bs) * D : 0) + static_cast<int64_t>(off) * D + d0) = o;
     }
   }
 }
@@ -232,13 +254,22 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
 
 namespace echo_host {
 
-template <int D, int kHeads>
-static cudaError_t launch_rope(echo::RopeParams P, cudaStream_t stream) {
-  P.chunks = (P.heads + kHeads - 1) / kHeads;
-  const int64_t threads = static_cast<int64_t>(P.T) * P.chunks * (D / 8);
-  const int64_t grid = (threads + echo::kRopeThreads - 1) / echo::kRopeThreads;
-  echo::qk_norm_rope_kernel<D, kHeads><<<static_cast<unsigned>(grid), echo::kRopeThreads, 0, stream>>>(P);
+template <int D, int kHeads, bool kInter>
+static cudaError_t launch_rope(echo::RopeParams P, bool values, cudaStream_t stream) {
+  P.q_chunks = (P.n_heads + kHeads - 1) / kHeads;
+  P.k_chunks = (P.n_kv_heads + kHeads - 1) / kHeads;
+  P.chunks = P.q_chunks + (values ? 2 : 1) * P.k_chunks;
+  constexpr int kTokens = 256 / D;
+  const int64_t warps = (static_cast<int64_t>(P.T) + kTokens - 1) / kTokens * P.chunks;
+  const int64_t grid = (warps * 32 + echo::kRopeThreads - 1) / echo::kRopeThreads;
+  echo::qk_norm_rope_kernel<D, kHeads, kInter><<<static_cast<unsigned>(grid), echo::kRopeThreads, 0, stream>>>(P);
   return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, bool many, cudaStream_t stream) {
+  if (many) return P.interleaved ? launch_rope<D, 8, true>(P, values, stream) : launch_rope<D, 8, false>(P, values, stream);
+  return P.interleaved ? launch_rope<D, 1, true>(P, values, stream) : launch_rope<D, 1, false>(P, values, stream);
 }
 
 int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream) {
@@ -256,11 +287,9 @@ int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream) {
   P.row_elems = echo::block_row_elems(a->format, a->block_tokens, a->head_dim);
   P.status = a->dev_status;
   // value heads have work only when something takes them
-  P.heads = a->n_heads + a->n_kv_heads + (a->v && (a->slot_map || a->v_out) ? a->n_kv_heads : 0);
-  const bool many = static_cast<int64_t>(a->T) * P.heads >= 16384;
-  cudaError_t e;
-  if (a->head_dim == 128) e = many ? launch_rope<128, 4>(P, stream) : launch_rope<128, 1>(P, stream);
-  else e = many ? launch_rope<64, 4>(P, stream) : launch_rope<64, 1>(P, stream);
+  const bool values = a->v && (a->slot_map || a->v_out);
+  const bool many = static_cast<int64_t>(a->T) * (a->n_heads + 2 * a->n_kv_heads) >= 16384;
+  const cudaError_t e = a->head_dim == 128 ? launch_rope_dim<128>(P, values, many, stream) : launch_rope_dim<64>(P, values, many, stream);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "qk norm + rope launch");
 }
 
