@@ -924,7 +924,7 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
    : pad == 16 ? launch_ba<FMT, D, 2, W2, S2>(P, grid, stream) \
                : launch_ba<FMT, D, 4, W4, S4>(P, grid, stream))
   if (a->format == ECHO_BLOCK_FP4)
-    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 12, 3, 8, 4, 8, 4) : BA_GO(ECHO_BLOCK_FP4, 64, 12, 3, 8, 4, 8, 4);
+    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 12, 3, 8, 4) : BA_GO(ECHO_BLOCK_FP4, 64, 12, 3, 8, 4, 8, 4);
   return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 6, 4, 6, 4) : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 6, 4, 6, 4);
 #undef BA_GO
 }

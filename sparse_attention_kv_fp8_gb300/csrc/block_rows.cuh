@@ -60,9 +60,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
   return h;
 }
 
-__device__ __forceinline__ uint32_t e4m3_from_float(float x) {
+__device__ __forceinline__ uint32_t e4m3_from_half(__half x) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  const uint32_t two = __half_as_ushort(x);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(two));
   return r & 0xffu;
 }
 

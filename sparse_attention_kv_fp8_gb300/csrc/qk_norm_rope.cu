@@ -3,18 +3,15 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * weight;  (a, b) -> (a cos - b sin, b cos + a sin)
 //
-// A head is read by head_dim / 8 lanes, one 16-byte load each, and never leaves registers
-// until its results are stored: the mean is a shuffle sum over those lanes, the partner of
-// a half-split pair sits in the lane rope_dim / 16 away (a shuffle of the bf16 pairs as
-// loaded), of an interleaved pair in the same lane; a 4-bit scale covers 16 dimensions, so
-// two neighbouring lanes.  A warp takes kHeads heads of one kind (q, k or v) of its tokens:
-// their loads are issued together (bytes in flight), and cosines, sines and weights are read
-// and multiplied once for them.  Bound by HBM.
+// A head is held by head_dim / 8 lanes, 16 bytes each, and never leaves registers until its
+// results are stored; the mean is a shuffle sum over those lanes.  A warp takes `span` heads
+// of one kind (q, k or v) of its tokens, kBatch at a time with the next batch's loads in
+// flight; cosines, sines and weights are read and multiplied once for them.  Bound by HBM.
 #include "block_rows.cuh"
 
 namespace echo {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 struct RopeParams {
   const uint16_t *q, *k, *v;
@@ -31,6 +28,7 @@ struct RopeParams {
   uint16_t *rows;
   int32_t n_rows, format, bs;
   int64_t row_elems;
+  int32_t span, kv_span;               // heads of a warp: q, and k or v
   int32_t q_chunks, k_chunks, chunks;  // warps per token group: of q, of k (and of v), in all
   int32_t *status;
 };
@@ -54,24 +52,28 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One lane's 8 entries as 4-bit codes: the scale of the 16 dimensions it shares with its
-// neighbour (lane ^ 1), s = e4m3(amax / 6) by IEEE division, and the nearest codes to x / s.
-// x has 8 significant bits and s at most 4, so x / s is a rounding border of the code grid
-// exactly or at least 2^-8 away from it: rounding x * (1 / s) to fp16 (11 bits) gives the
-// border back in the first case and stays off it in the second, and the hardware's
-// round-half-to-even then decides as the definition does.
+// One lane's 8 entries as 4-bit codes, with the scale of the 16 dimensions it shares with its
+// neighbour (lane ^ 1): s = e4m3(amax / 6) and the nearest codes to x / s, ties to even.
+// No exact division is needed.  x has 8 significant bits and s at most 4, so x / s lies on a
+// border between codes (3 bits) exactly or at least 2^-8 away from it; amax / 6 and the
+// borders between scales (5 bits) likewise.  A product with the reciprocal, off by 2^-22,
+// rounded to fp16 (11 bits), is the border itself in the first case and stays on its side in
+// the second, and the hardware's round-half-to-even then decides as the definition does.
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t &scale) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
   amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-  scale = e4m3_from_float(__fdiv_rn(amax, 6.f));
+  scale = e4m3_from_half(__float2half_rn(amax * (1.f / 6.f)));
   const uint32_t sh = e4m3x2_to_half2(scale);
   const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffff)));
-  const float r = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+  const float r = s > 0.f ? __fdividef(1.f, s) : 0.f;
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __half2float(__float2half_rn(fminf(fmaxf(x[i] * r, -8.f), 8.f)));
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(__floats2half2_rn(x[2 * i] * r, x[2 * i + 1] * r));
+    y[2 * i] = f.x, y[2 * i + 1] = f.y;
+  }
   return e2m1x8_from_float(y);
 }
 
@@ -93,14 +95,244 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t scale) {
 // Kinds of heads, in the order of a token's chunks; a warp works on one kind.
 enum RopeKind { kRopeQ, kRopeK, kRopeV };
 
-template <int D, int kHeads, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams P) {
+__device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t float2_to_bf16x2(float2 x) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+// the factor 1 / sqrt(mean x^2 + eps) of a head, from each lane's part of the sum
+template <int D>
+__device__ __forceinline__ float norm_factor(float ss, float eps) {
+#pragma unroll
+  for (int d = D / 16; d > 0; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
+  return rsqrtf(fmaf(ss, 1.f / D, eps));
+}
+
+// Where the keys and values of one token go.
+struct RopeDst {
+  const RopeParams &P;
+  int64_t t, blk;
+  int off;
+  bool in;
+  // the row of KV head h, null when it is not written
+  __device__ __forceinline__ uint16_t *row(int h, bool report) const {
+    if (blk < 0) return nullptr;
+    const int64_t r = blk * P.n_kv_heads + h;
+    if (r >= P.n_rows) {
+      if (report) set_status(P.status, ECHO_DEV_BAD_INDEX);
+      return nullptr;
+    }
+    return P.rows + r * P.row_elems;
+  }
+};
+
+// Rotated heads that stay bf16 (queries, and keys of bf16 rows).  A lane holds both ends of
+// its pairs: two units of four dims, half a rotation apart (half-split), or side by side
+// (interleaved, and the dims past the rotation), so nothing but the norm's sum crosses lanes.
+template <int D, int kBatch, bool kInter>
+__device__ __forceinline__ void rope_pairs(const RopeParams &P, const RopeDst &W, const uint16_t *src, const float *wt,
+                                           int pos, bool is_q, int h0, int h1, int l) {
+  const int half = P.rope_dim >> 1, rl = P.rope_dim >> 3;  // lanes that rotate
+  const bool rot = l < rl;
+  const int ua = kInter ? 8 * l : rot ? 4 * l : P.rope_dim + 8 * (l - rl), ub = kInter || !rot ? ua + 4 : ua + half;
+  uint2 ra[kBatch], rb[kBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      ra[u] = rb[u] = make_uint2(0u, 0u);
+      if (h + u < h1) {  // (whatever the position: the loads need not wait for it)
+        ra[u] = *reinterpret_cast<const uint2 *>(src + static_cast<int64_t>(h + u) * D + ua);
+        rb[u] = *reinterpret_cast<const uint2 *>(src + static_cast<int64_t>(h + u) * D + ub);
+      }
+    }
+  };
+  load(h0);
+  // u' = r (a ca - b sb),  v' = r (b cb + a sa): cosine or sine times the operand's weight
+  // (half-split: unit a against unit b; interleaved: within each unit, see below)
+  float ca[4], cb[4], sa[4], sb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ca[i] = cb[i] = 1.f, sa[i] = sb[i] = 0.f;
+  if (W.in && rot) {
+    const float *row = P.cos_sin + static_cast<int64_t>(pos) * P.rope_dim + 4 * l;
+    const float4 c = *reinterpret_cast<const float4 *>(row), s = *reinterpret_cast<const float4 *>(row + half);
+    if constexpr (kInter) {  // pairs 4l .. 4l + 3: two in unit a, two in unit b
+      ca[0] = ca[1] = c.x, ca[2] = ca[3] = c.y, cb[0] = cb[1] = c.z, cb[2] = cb[3] = c.w;
+      sa[0] = sa[1] = s.x, sa[2] = sa[3] = s.y, sb[0] = sb[1] = s.z, sb[2] = sb[3] = s.w;
+    } else {
+      ca[0] = cb[0] = c.x, ca[1] = cb[1] = c.y, ca[2] = cb[2] = c.z, ca[3] = cb[3] = c.w;
+      sa[0] = sb[0] = s.x, sa[1] = sb[1] = s.y, sa[2] = sb[2] = s.z, sa[3] = sb[3] = s.w;
+    }
+  }
+  if (wt) {
+    const float4 wa = __ldg(reinterpret_cast<const float4 *>(wt + ua)), wb = __ldg(reinterpret_cast<const float4 *>(wt + ub));
+    const float a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ca[i] *= a[i], cb[i] *= b[i], sa[i] *= a[i], sb[i] *= b[i];
+  }
+  for (int h = h0; h < h1; h += kBatch) {
+    uint2 oa[kBatch], ob[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float2 a0 = bf16x2_to_float2(ra[u].x), a1 = bf16x2_to_float2(ra[u].y);
+      const float2 b0 = bf16x2_to_float2(rb[u].x), b1 = bf16x2_to_float2(rb[u].y);
+      float2 r = make_float2(1.f, 1.f);
+      if (wt) {
+        const float2 q = __ffma2_rn(a0, a0, __ffma2_rn(a1, a1, __ffma2_rn(b0, b0, __fmul2_rn(b1, b1))));
+        r.x = r.y = norm_factor<D>(q.x + q.y, P.eps);
+      }
+      float2 u0, u1, v0, v1;
+      if constexpr (kInter) {
+        // the pair (x, y) of a unit: (x c - y s, y c + x s), weights folded into each operand
+        u0 = make_float2(fmaf(-a0.y, sa[1], a0.x * ca[0]), fmaf(a0.x, sa[0], a0.y * ca[1]));
+        u1 = make_float2(fmaf(-a1.y, sa[3], a1.x * ca[2]), fmaf(a1.x, sa[2], a1.y * ca[3]));
+        v0 = make_float2(fmaf(-b0.y, sb[1], b0.x * cb[0]), fmaf(b0.x, sb[0], b0.y * cb[1]));
+        v1 = make_float2(fmaf(-b1.y, sb[3], b1.x * cb[2]), fmaf(b1.x, sb[2], b1.y * cb[3]));
+      } else if (rot) {
+        const float2 nb0 = make_float2(-sb[0], -sb[1]), nb1 = make_float2(-sb[2], -sb[3]);
+        u0 = __ffma2_rn(b0, nb0, __fmul2_rn(a0, make_float2(ca[0], ca[1])));
+        u1 = __ffma2_rn(b1, nb1, __fmul2_rn(a1, make_float2(ca[2], ca[3])));
+        v0 = __ffma2_rn(a0, make_float2(sa[0], sa[1]), __fmul2_rn(b0, make_float2(cb[0], cb[1])));
+        v1 = __ffma2_rn(a1, make_float2(sa[2], sa[3]), __fmul2_rn(b1, make_float2(cb[2], cb[3])));
+      } else {               // (0 * inf would reach the entries that stay)
+        u0 = __fmul2_rn(a0, make_float2(ca[0], ca[1])), u1 = __fmul2_rn(a1, make_float2(ca[2], ca[3]));
+        v0 = __fmul2_rn(b0, make_float2(cb[0], cb[1])), v1 = __fmul2_rn(b1, make_float2(cb[2], cb[3]));
+      }
+      if constexpr (kInter) {
+        if (!rot) {
+          u0 = make_float2(a0.x * ca[0], a0.y * ca[1]), u1 = make_float2(a1.x * ca[2], a1.y * ca[3]);
+          v0 = make_float2(b0.x * cb[0], b0.y * cb[1]), v1 = make_float2(b1.x * cb[2], b1.y * cb[3]);
+        }
+      }
+      oa[u] = make_uint2(float2_to_bf16x2(__fmul2_rn(u0, r)), float2_to_bf16x2(__fmul2_rn(u1, r)));
+      ob[u] = make_uint2(float2_to_bf16x2(__fmul2_rn(v0, r)), float2_to_bf16x2(__fmul2_rn(v1, r)));
+    }
+    if (h + kBatch < h1) load(h + kBatch);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (!W.in || h + u >= h1) continue;
+      auto store = [&](uint16_t *dst) {
+        __stcs(reinterpret_cast<uint2 *>(dst + ua), oa[u]);
+        __stcs(reinterpret_cast<uint2 *>(dst + ub), ob[u]);
+      };
+      if (is_q) {
+        store(P.q_out + (W.t * P.n_heads + h + u) * D);
+      } else {
+        if (P.k_out) store(P.k_out + (W.t * P.n_kv_heads + h + u) * D);
+        if (uint16_t *row = W.row(h + u, l == 0)) store(row + static_cast<int64_t>(W.off) * D);
+      }
+    }
+  }
+}
+
+// Values, and keys of 4-bit rows: a lane holds 8 neighbouring dims, as the rows do; the
+// partners of half-split pairs come from another lane.
+template <int D, int kBatch, bool kInter>
+__device__ __forceinline__ void rope_rows(const RopeParams &P, const RopeDst &W, const uint16_t *src, const float *wt,
+                                          int pos, bool is_v, int h0, int h1, int l, int lane) {
+  constexpr int kLanes = D / 8;
+  const int half = P.rope_dim >> 1, d0 = 8 * l;
+  const bool rot = d0 < P.rope_dim, low = d0 < half, fp4 = P.format == ECHO_BLOCK_FP4;
+  const int pd = kInter || !rot ? d0 : low ? d0 + half : d0 - half;   // the partners' dims
+  const int partner = (lane & ~(kLanes - 1)) + pd / 8;
+  uint4 raw[kBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (h + u < h1) raw[u] = *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(h + u) * D + d0);
+    }
+  };
+  load(h0);
+  // y = r (x c + partner s): the cosine times the own weight, the signed sine times the partner's
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  if (!is_v) {
+    if (W.in && rot) {
+      const float *row = P.cos_sin + static_cast<int64_t>(pos) * P.rope_dim;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = kInter ? (d0 + i) / 2 : (low ? d0 : d0 - half) + i;
+        const bool neg = kInter ? i % 2 == 0 : low;
+        c[i] = __ldg(row + k);
+        s[i] = neg ? -__ldg(row + half + k) : __ldg(row + half + k);
+      }
+    }
+    if (wt) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] *= __ldg(wt + d0 + i), s[i] *= __ldg(wt + pd + (kInter ? i ^ 1 : i));
+    }
+  }
+  for (int h = h0; h < h1; h += kBatch) {
+    uint4 cur[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) cur[u] = raw[u];
+    if (h + kBatch < h1) load(h + kBatch);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      uint4 o = cur[u];
+      if (!is_v) {
+        uint32_t w[4] = {cur[u].x, cur[u].y, cur[u].z, cur[u].w};
+        float2 x[4], q = make_float2(0.f, 0.f), r = make_float2(1.f, 1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = bf16x2_to_float2(w[i]);
+          q = __ffma2_rn(x[i], x[i], q);
+        }
+        if (wt) r.x = r.y = norm_factor<D>(q.x + q.y, P.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pw = kInter ? __byte_perm(w[i], 0, 0x1032) : __shfl_sync(~0u, w[i], partner);
+          if (!rot) pw = 0;
+          const float2 y = __ffma2_rn(bf16x2_to_float2(pw), make_float2(s[2 * i], s[2 * i + 1]),
+                                      __fmul2_rn(x[i], make_float2(c[2 * i], c[2 * i + 1])));
+          w[i] = float2_to_bf16x2(__fmul2_rn(y, r));
+        }
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      uint32_t codes = 0, scale = 0;
+      if (fp4) {             // (every lane: the scale is a shuffle)
+        float x[8];
+        unpack_bf16x8(o, x);
+        codes = quantise8(x, scale);
+      }
+      if (!W.in || h + u >= h1) continue;
+      uint16_t *out = is_v ? P.v_out : P.k_out;
+      if (out) {
+        *reinterpret_cast<uint4 *>(out + (W.t * P.n_kv_heads + h + u) * D + d0) = fp4 ? dequantise8(codes, scale) : o;
+      }
+      uint16_t *row = W.row(h + u, l == 0);
+      if (!row) continue;
+      if (fp4) {
+        using Sub = Fp4Sub<D>;
+        uint8_t *sub = reinterpret_cast<uint8_t *>(row) + W.off / kSubTokens * Sub::kBytes;
+        const int tk = W.off % kSubTokens;
+        if (!is_v) {
+          *reinterpret_cast<uint32_t *>(sub + tk * (D / 2) + l * 4) = codes;
+          if (!(l & 1)) sub[Sub::kKeyScales + tk * (D / 16) + l / 2] = static_cast<uint8_t>(scale);
+        } else {
+          constexpr int kPart = D / 8;     // dims of a part: 16 (two lanes) or 8 (one lane)
+          *reinterpret_cast<uint32_t *>(sub + Sub::kValues + (tk / 8) * (4 * D) + ((d0 / kPart) * 8 + tk % 8) * (D / 16) +
+                                        (d0 % kPart) / 2) = codes;
+          if (!(l & 1)) sub[Sub::kValueScales + (tk / 8) * (D / 2) + (l / 2) * 8 + tk % 8] = static_cast<uint8_t>(scale);
+        }
+      } else {
+        *reinterpret_cast<uint4 *>(row + (is_v ? static_cast<int64_t>(P.bs) * D : 0) + static_cast<int64_t>(W.off) * D + d0) = o;
+      }
+    }
+  }
+}
+
+template <int D, int kBatch, bool kInter>
+__global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const RopeParams P) {
   constexpr int kLanes = D / 8;          // lanes of a head
   constexpr int kTokens = 32 / kLanes;   // tokens of a warp
   const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
   const int64_t tb = wid / P.chunks;
-  int chunk = static_cast<int>(wid - tb * P.chunks);
-  const int lane = threadIdx.x & 31, l = lane % kLanes, d0 = 8 * l;
+  const int chunk = static_cast<int>(wid - tb * P.chunks);
+  const int lane = threadIdx.x & 31, l = lane % kLanes;
   const int64_t tok = tb * kTokens + lane / kLanes;
   if (tb * kTokens >= P.T) return;       // (the whole warp)
   const int64_t t = min(tok, static_cast<int64_t>(P.T) - 1);
@@ -109,167 +341,41 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
   if (tok < P.T && pos >= P.max_pos && l == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
 
   const int kind = chunk < P.q_chunks ? kRopeQ : chunk < P.q_chunks + P.k_chunks ? kRopeK : kRopeV;
-  const int h0 = (kind == kRopeQ ? chunk : (chunk - P.q_chunks) % P.k_chunks) * kHeads;
-  const int heads = kind == kRopeQ ? P.n_heads : P.n_kv_heads;
-  const uint16_t *src = (kind == kRopeQ   ? P.q + t * P.q_stride
-                         : kind == kRopeK ? P.k + t * P.k_stride
-                                          : P.v + t * P.v_stride) + static_cast<int64_t>(h0) * D + d0;
-  uint4 raw[kHeads];
-#pragma unroll
-  for (int u = 0; u < kHeads; ++u) {
-    raw[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && h0 + u < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + u * D);
-  }
-
-  // y = r * (x * c + partner * s): the cosine times the own weight, the signed sine times
-  // the partner's
-  const int half = P.rope_dim >> 1;
-  const bool rot = d0 < P.rope_dim, low = d0 < half;
-  const float *wt = kind == kRopeQ ? P.q_weight : P.k_weight;
-  const int pd = kInter || !rot ? d0 : low ? d0 + half : d0 - half;   // the partners' dims
-  float2 c[4], s[4];
-  if (kind != kRopeV) {
-    float cw[8], sw[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cw[i] = 1.f, sw[i] = 0.f;
-    if (in && rot) {
-      const float *row = P.cos_sin + static_cast<int64_t>(pos) * P.rope_dim;
-      if constexpr (kInter) {
-        const float4 cc = *reinterpret_cast<const float4 *>(row + d0 / 2);
-        const float4 ss = *reinterpret_cast<const float4 *>(row + half + d0 / 2);
-        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cw[2 * i] = cw[2 * i + 1] = cv[i], sw[2 * i] = -sv[i], sw[2 * i + 1] = sv[i];
-      } else {
-        const float *cr = row + (low ? d0 : d0 - half);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 cc = reinterpret_cast<const float4 *>(cr)[i];
-          const float4 ss = reinterpret_cast<const float4 *>(cr + half)[i];
-          cw[4 * i] = cc.x, cw[4 * i + 1] = cc.y, cw[4 * i + 2] = cc.z, cw[4 * i + 3] = cc.w;
-          sw[4 * i] = ss.x, sw[4 * i + 1] = ss.y, sw[4 * i + 2] = ss.z, sw[4 * i + 3] = ss.w;
-        }
-        if (low) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sw[i] = -sw[i];
-        }
-      }
-    }
-    if (wt) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(wt + d0) + i);
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(wt + pd) + i);
-        cw[4 * i] *= a.x, cw[4 * i + 1] *= a.y, cw[4 * i + 2] *= a.z, cw[4 * i + 3] *= a.w;
-        if constexpr (kInter) sw[4 * i] *= b.y, sw[4 * i + 1] *= b.x, sw[4 * i + 2] *= b.w, sw[4 * i + 3] *= b.z;
-        else sw[4 * i] *= b.x, sw[4 * i + 1] *= b.y, sw[4 * i + 2] *= b.z, sw[4 * i + 3] *= b.w;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = make_float2(cw[2 * i], cw[2 * i + 1]), s[i] = make_float2(sw[2 * i], sw[2 * i + 1]);
-  }
-  // the lane that holds the other half of this lane's pairs (half-split)
-  const int partner = (lane & ~(kLanes - 1)) + pd / 8;
+  const int h0 = kind == kRopeQ ? chunk * P.span : (chunk - P.q_chunks) % P.k_chunks * P.kv_span;
+  const int h1 = kind == kRopeQ ? min(h0 + P.span, P.n_heads) : min(h0 + P.kv_span, P.n_kv_heads);
   const int slot = P.slot_map && kind != kRopeQ ? __ldg(P.slot_map + t) : -1;
-  const int64_t blk = slot >= 0 ? slot / P.bs : 0;
-  const int off = slot >= 0 ? slot - static_cast<int>(blk) * P.bs : 0;
-
-#pragma unroll
-  for (int u = 0; u < kHeads; ++u) {
-    if (h0 + u >= heads) break;          // (warp-uniform)
-    uint4 o = raw[u];                    // a value head passes through
-    if (kind != kRopeV) {
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-      uint32_t pw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pw[i] = kInter ? __byte_perm(w[i], 0, 0x1032) : __shfl_sync(~0u, w[i], partner);
-        if (!rot) pw[i] = 0;             // (0 * inf would reach the entries that stay)
-      }
-      float2 x[4], r2 = make_float2(1.f, 1.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-      if (wt) {
-        float2 q2 = __fmul2_rn(x[0], x[0]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) q2 = __ffma2_rn(x[i], x[i], q2);
-        float ss = q2.x + q2.y;
-#pragma unroll
-        for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
-        r2.x = r2.y = rsqrtf(fmaf(ss, 1.f / D, P.eps));
-      }
-      uint32_t ow[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = make_float2(__uint_as_float(pw[i] << 16), __uint_as_float(pw[i] & 0xffff0000u));
-        const float2 y = __fmul2_rn(__ffma2_rn(p, s[i], __fmul2_rn(x[i], c[i])), r2);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
-        ow[i] = *reinterpret_cast<const uint32_t *>(&b);
-      }
-      o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-    }
-    if (kind == kRopeQ) {
-      if (in) *reinterpret_cast<uint4 *>(P.q_out + (t * P.n_heads + h0 + u) * D + d0) = o;
-      continue;
-    }
-    uint32_t codes = 0, scale = 0;
-    if (P.format == ECHO_BLOCK_FP4) {    // (every lane: the scale is a shuffle)
-      float x[8];
-      unpack_bf16x8(o, x);
-      codes = quantise8(x, scale);
-    }
-    if (!in) continue;
-    uint16_t *out = kind == kRopeV ? P.v_out : P.k_out;
-    if (out) {
-      *reinterpret_cast<uint4 *>(out + (t * P.n_kv_heads + h0 + u) * D + d0) =
-          P.format == ECHO_BLOCK_FP4 ? dequantise8(codes, scale) : o;
-    }
-    if (slot < 0) continue;
-    const int64_t row = blk * P.n_kv_heads + h0 + u;
-    if (row >= P.n_rows) {
-      if (l == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
-      continue;
-    }
-    uint16_t *base = P.rows + row * P.row_elems;
-    if (P.format == ECHO_BLOCK_FP4) {
-      using Sub = Fp4Sub<D>;
-      uint8_t *sub = reinterpret_cast<uint8_t *>(base) + off / kSubTokens * Sub::kBytes;
-      const int tk = off % kSubTokens;
-      if (kind == kRopeK) {
-        *reinterpret_cast<uint32_t *>(sub + tk * (D / 2) + l * 4) = codes;
-        if (!(l & 1)) sub[Sub::kKeyScales + tk * (D / 16) + l / 2] = static_cast<uint8_t>(scale);
-      } else {
-        constexpr int kPart = D / 8;     // dims of a part: 16 (two lanes) or 8 (one lane)
-        *reinterpret_cast<uint32_t *>(sub + Sub::kValues + (tk / 8) * (4 * D) + ((d0 / kPart) * 8 + tk % 8) * (D / 16) +
-                                      (d0 % kPart) / 2) = codes;
-        if (!(l & 1)) sub[Sub::kValueScales + (tk / 8) * (D / 2) + (l / 2) * 8 + tk % 8] = static_cast<uint8_t>(scale);
-      }
-    } else {
-      *reinterpret_cast<uint4 *>(base + (kind == kRopeV ? static_cast<int64_t>(P.bs) * D : 0) + static_cast<int64_t>(off) * D + d0) = o;
-    }
-  }
+  const int blk = slot >= 0 ? slot / P.bs : -1;
+  const RopeDst W{P, t, blk, slot - blk * P.bs, in};
+  if (kind == kRopeQ || (kind == kRopeK && P.format == ECHO_BLOCK_BF16))
+    rope_pairs<D, kBatch, kInter>(P, W, kind == kRopeQ ? P.q + t * P.q_stride : P.k + t * P.k_stride,
+                                  kind == kRopeQ ? P.q_weight : P.k_weight, pos, kind == kRopeQ, h0, h1, l);
+  else
+    rope_rows<D, kBatch, kInter>(P, W, kind == kRopeK ? P.k + t * P.k_stride : P.v + t * P.v_stride, P.k_weight, pos,
+                                 kind == kRopeV, h0, h1, l, lane);
 }
 
 }  // namespace echo
 
 namespace echo_host {
 
-template <int D, int kHeads, bool kInter>
-static cudaError_t launch_rope(echo::RopeParams P, bool values, cudaStream_t stream) {
-  P.q_chunks = (P.n_heads + kHeads - 1) / kHeads;
-  P.k_chunks = (P.n_kv_heads + kHeads - 1) / kHeads;
+template <int D, int kBatch, bool kInter>
+static cudaError_t launch_rope(echo::RopeParams P, bool values, int span, int kv_span, cudaStream_t stream) {
+  P.span = span;
+  P.kv_span = kv_span;
+  P.q_chunks = (P.n_heads + span - 1) / span;
+  P.k_chunks = (P.n_kv_heads + kv_span - 1) / kv_span;
   P.chunks = P.q_chunks + (values ? 2 : 1) * P.k_chunks;
   constexpr int kTokens = 256 / D;
   const int64_t warps = (static_cast<int64_t>(P.T) + kTokens - 1) / kTokens * P.chunks;
   const int64_t grid = (warps * 32 + echo::kRopeThreads - 1) / echo::kRopeThreads;
-  echo::qk_norm_rope_kernel<D, kHeads, kInter><<<static_cast<unsigned>(grid), echo::kRopeThreads, 0, stream>>>(P);
+  echo::qk_norm_rope_kernel<D, kBatch, kInter><<<static_cast<unsigned>(grid), echo::kRopeThreads, 0, stream>>>(P);
   return cudaGetLastError();
 }
 
 template <int D>
 static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, bool many, cudaStream_t stream) {
-  if (many) return P.interleaved ? launch_rope<D, 8, true>(P, values, stream) : launch_rope<D, 8, false>(P, values, stream);
-  return P.interleaved ? launch_rope<D, 1, true>(P, values, stream) : launch_rope<D, 1, false>(P, values, stream);
+  if (many) return P.interleaved ? launch_rope<D, 4, true>(P, values, 16, 8, stream) : launch_rope<D, 4, false>(P, values, 16, 8, stream);
+  return P.interleaved ? launch_rope<D, 1, true>(P, values, 1, 1, stream) : launch_rope<D, 1, false>(P, values, 1, 1, stream);
 }
 
 int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream) {
