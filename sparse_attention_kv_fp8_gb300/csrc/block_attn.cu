@@ -30,10 +30,13 @@
 //     the lengths on the device (a ragged batch costs no idle SMs).  A piece that ends
 //     inside a (b, h) leaves a partial result; a second kernel merges those in order (no
 //     atomics: results do not depend on timing).  When the contexts are short or the
-//     (b, h) pairs fill the GPU, a CTA takes a whole (b, h) and the second kernel is left out.
+//     (b, h) pairs fill the GPU, a CTA, or a cluster of up to 8 that merges over distributed
+//     shared memory, takes a whole (b, h) and the second kernel is left out.
+#include <algorithm>
 #include <cmath>
 
 #include "block_rows.cuh"
+#include "cluster_select.cuh"
 
 namespace echo {
 
@@ -43,6 +46,7 @@ constexpr float kBaLazy = 8.f;    // log2 of how far a score may exceed the runn
 // 2^-24) begin 2^-21 below the running maximum instead of 2^-14
 constexpr float kBaLift = 7.f;
 constexpr int kBaNowhere = 0x7fffff00;  // position of a sub-block that is not there
+constexpr int kBaMaxCluster = 8;  // CTAs of a (b, h) that merge over distributed shared memory
 constexpr int kBaList = 64;        // entries of a warp's list of sub-blocks (two batches of 32)
 constexpr int kBaMaxRows = 32;    // query rows of one CTA's (b, h) (4 columns of 8)
 
@@ -59,7 +63,7 @@ struct BlockAttnParams {
   uint32_t q_sign;                   // 0x80008000 for a negative scale
   uint16_t *out;
   float *lse;
-  int32_t whole;                     // one CTA per (b, h, row group), nothing split
+  int32_t cluster;                   // CTAs of a (b, h, row group), a cluster; 0: the line is cut
   float *part_o;                     // [2 * grid][rows][D]
   float *part_ml;                    // [2 * grid][rows][2]
   int4 *tail;                        // [grid]: (b, h * mgroups + mg, pieces, 0)
@@ -170,6 +174,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// a shared-memory address of this CTA, in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
 // log of a row's sum of weights 2^(x - top + lift)
 __device__ __forceinline__ float ba_lse(float top, float sum, float lift) {
   return top == -INFINITY ? -INFINITY : (top - lift + log2f(sum)) * 0.693147180559945309f;
@@ -274,14 +284,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
   // ===== this CTA's range of the line: chunks 0 .. n_chunks from its first =====
   LinePos cur;
   int n_chunks;
-  if (P.whole) {
-    cur.b = blockIdx.x / heads;
-    cur.hm = blockIdx.x - cur.b * heads;
+  if (P.cluster) {
+    const int pair = blockIdx.x / P.cluster, rank = blockIdx.x - pair * P.cluster;
+    cur.b = pair / heads;
+    cur.hm = pair - cur.b * heads;
     const int ctx = __ldg(P.ctx_len + cur.b);
     cur.v = req_view(P, ctx);
-    cur.start = 0;
-    n_chunks = cur.end = chunks_of<C::kSubs>(cur.v);
-    if (threadIdx.x == 0 && cur.hm == 0) check_context(P, ctx);
+    const int n = chunks_of<C::kSubs>(cur.v);
+    const int first = static_cast<int>(static_cast<int64_t>(n) * rank / P.cluster);
+    cur.start = -first;
+    cur.end = n - first;
+    n_chunks = static_cast<int>(static_cast<int64_t>(n) * (rank + 1) / P.cluster) - first;
+    if (threadIdx.x == 0 && rank == 0 && cur.hm == 0) check_context(P, ctx);
   } else {
     // lengths of all requests' parts of the line, by every warp for itself (no barrier): a
     // run of requests per lane, summed
@@ -502,51 +516,60 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
 
       float s[C::kSubs][NT][4];
 #pragma unroll
-      for (int u = 0; u < C::kSubs; ++u) {
+      for (int u = 0; u < C::kSubs; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
-        const uint8_t *kp = sp + u * C::kSubBytes;
-        if constexpr (C::kFp4) {
-          constexpr int kWords = D / 32;  // 32-bit words of codes a lane reads per token
-          uint32_t wa[kWords], wb[kWords], sa, sb;
+      if constexpr (C::kFp4) {
+        constexpr int kWords = D / 32;  // 32-bit words of codes a lane reads per token
+        uint32_t wa[C::kSubs][kWords], wb[C::kSubs][kWords], ha[C::kSubs], hb[C::kSubs];  // tokens r8, r8 + 8
+#pragma unroll
+        for (int u = 0; u < C::kSubs; ++u) {
+          const uint8_t *kp = sp + u * C::kSubBytes;
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4 *>(kp + lane * 16);
             const uint4 y = *reinterpret_cast<const uint4 *>(kp + 8 * (D / 2) + lane * 16);
-            wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
-            wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
-            sa = *reinterpret_cast<const uint16_t *>(kp + Fp4Sub<D>::kKeyScales + lane * 2);
-            sb = *reinterpret_cast<const uint16_t *>(kp + Fp4Sub<D>::kKeyScales + 8 * (D / 16) + lane * 2);
+            wa[u][0] = x.x, wa[u][1] = x.y, wa[u][2] = x.z, wa[u][3] = x.w;
+            wb[u][0] = y.x, wb[u][1] = y.y, wb[u][2] = y.z, wb[u][3] = y.w;
+            ha[u] = e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(kp + Fp4Sub<D>::kKeyScales + lane * 2));
+            hb[u] = e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(kp + Fp4Sub<D>::kKeyScales + 8 * (D / 16) + lane * 2));
           } else {
             const uint2 x = *reinterpret_cast<const uint2 *>(kp + lane * 8);
             const uint2 y = *reinterpret_cast<const uint2 *>(kp + 8 * (D / 2) + lane * 8);
-            wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
-            sa = kp[Fp4Sub<D>::kKeyScales + lane];
-            sb = kp[Fp4Sub<D>::kKeyScales + 8 * (D / 16) + lane];
+            wa[u][0] = x.x, wa[u][1] = x.y, wb[u][0] = y.x, wb[u][1] = y.y;
+            ha[u] = e4m3x2_to_half2(kp[Fp4Sub<D>::kKeyScales + lane]);
+            hb[u] = e4m3x2_to_half2(kp[Fp4Sub<D>::kKeyScales + 8 * (D / 16) + lane]);
           }
-          const uint32_t ha = e4m3x2_to_half2(sa), hb = e4m3x2_to_half2(sb);
+        }
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) {
+        for (int i = 0; i < kWords; ++i) {
+          uint2 q[2][NT];  // (read once for the chunk's sub-blocks)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) q[t][nt] = NT == 1 ? qreg[NT == 1 ? 2 * i + t : 0] : qfrag[((2 * i + t) * NT + nt) * 32 + lane];
+#pragma unroll
+          for (int u = 0; u < C::kSubs; ++u) {
             const bool hi = D == 128 && i >= kWords / 2;
-            const uint32_t sca = __byte_perm(ha, 0, hi ? 0x3232 : 0x1010), scb = __byte_perm(hb, 0, hi ? 0x3232 : 0x1010);
+            const uint32_t sa = __byte_perm(ha[u], 0, hi ? 0x3232 : 0x1010), sb = __byte_perm(hb[u], 0, hi ? 0x3232 : 0x1010);
             uint32_t fa[4], fb[4];
-            e2m1x8_to_half2(wa[i], fa);
-            e2m1x8_to_half2(wb[i], fb);
+            e2m1x8_to_half2(wa[u][i], fa);
+            e2m1x8_to_half2(wb[u][i], fb);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              const uint32_t a[4] = {hmul2(fa[2 * t], sca), hmul2(fb[2 * t], scb), hmul2(fa[2 * t + 1], sca),
-                                     hmul2(fb[2 * t + 1], scb)};
+              const uint32_t a[4] = {hmul2(fa[2 * t], sa), hmul2(fb[2 * t], sb), hmul2(fa[2 * t + 1], sa),
+                                     hmul2(fb[2 * t + 1], sb)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 q = NT == 1 ? qreg[NT == 1 ? 2 * i + t : 0] : qfrag[((2 * i + t) * NT + nt) * 32 + lane];
-                mma16816<true>(s[u][nt], a, q.x, q.y);
-              }
+              for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[u][nt], a, q[t][nt].x, q[t][nt].y);
             }
           }
-        } else {
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < C::kSubs; ++u) {
           const int tk = (lane & 7) + (lane & 8);
-          const uint32_t ka = smem_u32(kp) + tk * (2 * D);
+          const uint32_t ka = smem_u32(sp + u * C::kSubBytes) + tk * (2 * D);
 #pragma unroll
           for (int i = 0; i < C::kSteps; ++i) {
             uint32_t a[4];
@@ -715,7 +738,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       }
       fin[lane] = make_float2(top, sum);
     }
-    const bool split = !P.whole && (cur.start < 0 || cur.end > n_chunks);
+    const bool split = !P.cluster && (cur.start < 0 || cur.end > n_chunks);
+    float *shared_o = reinterpret_cast<float *>(ba_smem);  // [kRows][D], where the stages were
     const int slot = 2 * blockIdx.x + (cur.start < 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -760,7 +784,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
             a = make_float2(x.x, x.z), b = make_float2(x.y, x.w);
           }
           const float2 v = fin[row];
-          if (split) {
+          if (P.cluster > 1) {
+            *reinterpret_cast<float2 *>(shared_o + row * D + d0) = a;
+            *reinterpret_cast<float2 *>(shared_o + row * D + d1) = b;
+          } else if (split) {
             float *part = P.part_o + (static_cast<int64_t>(slot) * C::kRows + row) * D;
             *reinterpret_cast<float2 *>(part + d0) = a;
             *reinterpret_cast<float2 *>(part + d1) = b;
@@ -782,6 +809,50 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
     cur = nxt;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  // ----- a cluster: each CTA joins every CS-th row over all CTAs' shared memory, in rank order
+  if (P.cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
+    const int rank = blockIdx.x % P.cluster;
+    for (int i = threadIdx.x;; i += C::kThreads) {
+      const int row = rank + P.cluster * (i / (D / 4)), d = 4 * (i % (D / 4));
+      if (row >= C::kRows) break;
+      const int64_t oh = row_index(cur, row);
+      if (oh < 0) continue;
+      const uint32_t fin_at = smem_u32(fin + row), o_at = smem_u32(ba_smem) + (row * D + d) * 4;
+      float2 v[kBaMaxCluster];
+      float4 x[kBaMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kBaMaxCluster; ++r) {
+        v[r] = make_float2(-INFINITY, 0.f);
+        x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < P.cluster) {
+          const uint32_t fa = peer_smem(fin_at, r), oa = peer_smem(o_at, r);
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[r].x), "=f"(v[r].y) : "r"(fa) : "memory");
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[r].x), "=f"(x[r].y), "=f"(x[r].z), "=f"(x[r].w)
+                       : "r"(oa)
+                       : "memory");
+        }
+      }
+      float top = -INFINITY, sum = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < kBaMaxCluster; ++r) top = fmaxf(top, v[r].x);
+#pragma unroll
+      for (int r = 0; r < kBaMaxCluster; ++r) {
+        const float f = v[r].x == -INFINITY ? 0.f : ex2(v[r].x - top);
+        sum += v[r].y * f;
+        y.x += x[r].x * f, y.y += x[r].y * f, y.z += x[r].z * f, y.w += x[r].w * f;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : sum;
+      *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
+          make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
+      if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum, kLift);
+    }
+    cluster_arrive();  // (no CTA's shared memory goes while another reads it)
+    cluster_wait();
+  }
 }
 
 // Merge of the pieces of each (b, hm) that was cut: block (i, y) takes row y of the one that
@@ -861,24 +932,45 @@ size_t block_attention_workspace_bytes(int32_t rows, int32_t head_dim) {
 }
 
 template <int FMT, int D, int NT, int WARPS, int STAGES>
-static int launch_ba(const echo::BlockAttnParams &P, int grid, cudaStream_t stream) {
+static int launch_ba(echo::BlockAttnParams P, int64_t pairs, int64_t most, int sms, cudaStream_t stream) {
   using C = echo::BaCfg<FMT, D, NT, WARPS, STAGES>;
   static_assert(C::kSmem <= 232448, "block attention: shared memory of one CTA");
   auto kernel = echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES>;
   static std::atomic<bool> attr[kMaxDevices];
   if (int rr = smem_limit_once(attr, kernel, C::kSmem, "block attention smem attribute")) return rr;
-  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(P);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
-  if (P.whole) return ECHO_OK;
+  // A cluster per (b, h), or the line of all chunks cut into equal pieces?  The cluster grows
+  // while it fits the GPU and every warp still gets a chunk.  Clusters cost the waves' longest
+  // context; cutting costs an equal share plus the second kernel and the piece borders: about
+  // the time of 1024 bf16 or 1536 4-bit tokens (measured for 8 to 256 pairs of 512 to 8192
+  // tokens: at 64 pairs of 1024, 9 against 14 us in bf16; at 8 pairs of 8192, 43 against 14
+  // before clusters).
+  int cs = 1;
+  while (cs < echo::kBaMaxCluster && pairs * cs * 2 <= sms * 7 / 8 && most > static_cast<int64_t>(cs) * WARPS * C::kTokens) cs *= 2;
+  const int64_t waves = (pairs * cs + sms - 1) / sms, extra = C::kFp4 ? 1536 : 1024;
+  const bool whole = waves * most / cs <= pairs * most / sms + extra;
+  P.cluster = whole ? cs : 0;
+  const unsigned grid = whole ? static_cast<unsigned>(pairs * cs) : static_cast<unsigned>(std::min(sms, echo::kBaMaxGrid));
   cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  if (whole && cs > 1) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cs;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+  if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
+  if (whole) return ECHO_OK;
   cfg.gridDim = dim3(grid, C::kRows);
   cfg.blockDim = dim3(echo::kBaCombThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cfg.dynamicSmemBytes = 0;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows), C::kFp4 ? echo::kBaLift : 0.f);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block attention merge launch");
@@ -913,19 +1005,13 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   // tokens a context can show at most
   int64_t most = static_cast<int64_t>(P.max_blocks) * a->block_tokens;
   if (!P.sel && P.window && most > P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31) most = P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31;
-  // Whole (b, h) per CTA, or the line cut into equal pieces?  Whole costs the waves' longest
-  // context; cutting costs an equal share plus the second kernel and the piece borders.
-  const int64_t waves = (pairs + sms - 1) / sms, extra = a->format == ECHO_BLOCK_FP4 ? 1024 : 512;
-  P.whole = waves * most <= pairs * most / sms + extra;
-  int grid = P.whole ? static_cast<int>(pairs) : sms;
-  if (grid > echo::kBaMaxGrid && !P.whole) grid = echo::kBaMaxGrid;
 #define BA_GO(FMT, D, W1, S1, W2, S2, W4, S4)                  \
-  (pad == 8    ? launch_ba<FMT, D, 1, W1, S1>(P, grid, stream) \
-   : pad == 16 ? launch_ba<FMT, D, 2, W2, S2>(P, grid, stream) \
-               : launch_ba<FMT, D, 4, W4, S4>(P, grid, stream))
+  (pad == 8    ? launch_ba<FMT, D, 1, W1, S1>(P, pairs, most, sms, stream) \
+   : pad == 16 ? launch_ba<FMT, D, 2, W2, S2>(P, pairs, most, sms, stream) \
+               : launch_ba<FMT, D, 4, W4, S4>(P, pairs, most, sms, stream))
   if (a->format == ECHO_BLOCK_FP4)
     return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 12, 3, 8, 4) : BA_GO(ECHO_BLOCK_FP4, 64, 12, 3, 8, 4, 8, 4);
-  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 6, 4, 6, 4) : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 6, 4, 6, 4);
+  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 7, 3, 7, 3) : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 6, 4, 6, 4);
 #undef BA_GO
 }
 

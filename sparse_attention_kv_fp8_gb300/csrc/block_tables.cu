@@ -17,8 +17,8 @@
 
 namespace echo {
 
-constexpr int kTabThreads = 512;
-constexpr int kTabPer = 4;  // list entries of a thread (one 16-byte store each)
+constexpr int kTabThreads = 256;
+constexpr int kTabPer = 4;  // list entries of a thread at a time
 
 struct TablesParams {
   const int32_t *old_len, *new_len;
@@ -103,51 +103,44 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
   };
 
   const int gthreads = gridDim.x * kTabThreads, gt = blockIdx.x * kTabThreads + t;
-  // ===== the list of new tokens: four entries per thread =====
+  const int rt = gthreads - 1 - gt;  // the blocks go to the other end's threads: both at once
+  // ===== the list of new tokens: kTabPer entries per thread at a time, their owners found
+  // first, then their blocks' ids read together =====
   const int listed = min(tn, P.max_new);
-  const bool wide = ((reinterpret_cast<uintptr_t>(P.slot_map) | reinterpret_cast<uintptr_t>(P.positions)) & 15) == 0;
   bad |= tn > P.max_new;
-  for (int i0 = gt * kTabPer; i0 < P.max_new; i0 += gthreads * kTabPer) {
-    int32_t slot[kTabPer], pos[kTabPer];
-    int b = -1, nend = 0, o = 0, nbo = 0, blk = -1, id = -1;
-    bool have = false;
+  for (int base = gt; base < P.max_new; base += gthreads * kTabPer) {
+    int p[kTabPer], k[kTabPer], id[kTabPer];
+    const int32_t *from[kTabPer];
 #pragma unroll
     for (int u = 0; u < kTabPer; ++u) {
-      const int i = i0 + u;
-      slot[u] = pos[u] = -1;
+      const int i = base + u * gthreads;
+      from[u] = nullptr;
+      p[u] = k[u] = id[u] = -1;
       if (i >= listed) continue;
-      if (b < 0 || i >= nend) {
-        b = b < 0 ? owner_of(cuN, P.B, i) : b + 1;
-        while (cuN[b + 1] <= i) ++b;
-        nend = cuN[b + 1];
-        o = min(max(P.old_len[b], 0), cap);
-        nbo = (o + P.bs - 1) / P.bs;
-        blk = -1;
-        have = cuA[b + 1] == cuA[b] || cuA[b + 1] <= top;
-      }
-      if (!have) continue;
-      const int p = o + (i - cuN[b]), k = p / P.bs;
-      if (k != blk) {
-        blk = k;
-        id = k < nbo ? P.table[static_cast<size_t>(b) * P.max_blocks + k] : grown(cuA[b] + k - nbo);
-        if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(P.n_blocks)) id = -1, bad = 1;
-      }
-      if (id >= 0) slot[u] = id * P.bs + (p - k * P.bs), pos[u] = p;
+      const int b = owner_of(cuN, P.B, i);
+      if (cuA[b + 1] != cuA[b] && cuA[b + 1] > top) continue;  // left without its blocks
+      const int o = min(max(P.old_len[b], 0), cap), nbo = (o + P.bs - 1) / P.bs;
+      p[u] = o + (i - cuN[b]);
+      k[u] = p[u] / P.bs;
+      const int s = top - 1 - (cuA[b] + k[u] - nbo);
+      if (k[u] < nbo) from[u] = P.table + static_cast<size_t>(b) * P.max_blocks + k[u];
+      else if (s < count) from[u] = P.free_blocks + s;
+      else id[u] = stack_at(s);
     }
-    if (wide && i0 + kTabPer <= P.max_new) {
-      *reinterpret_cast<int4 *>(P.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      if (P.positions) *reinterpret_cast<int4 *>(P.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
 #pragma unroll
-      for (int u = 0; u < kTabPer; ++u)
-        if (i0 + u < P.max_new) {
-          P.slot_map[i0 + u] = slot[u];
-          if (P.positions) P.positions[i0 + u] = pos[u];
-        }
+    for (int u = 0; u < kTabPer; ++u)
+      if (from[u]) id[u] = *from[u];
+#pragma unroll
+    for (int u = 0; u < kTabPer; ++u) {
+      const int i = base + u * gthreads;
+      if (i >= P.max_new) continue;
+      if (p[u] >= 0 && static_cast<uint32_t>(id[u]) >= static_cast<uint32_t>(P.n_blocks)) p[u] = -1, bad = 1;
+      P.slot_map[i] = p[u] >= 0 ? id[u] * P.bs + (p[u] - k[u] * P.bs) : -1;
+      if (P.positions) P.positions[i] = p[u];
     }
   }
   // ===== the blocks that moved =====
-  for (int j = gt; j < ta; j += gthreads) {
+  for (int j = rt; j < ta; j += gthreads) {
     const int b = owner_of(cuA, P.B, j);
     if (cuA[b + 1] > top) break;  // this request and every later one with a need get nothing
     const int o = min(max(P.old_len[b], 0), cap);
@@ -155,13 +148,13 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
     bad |= id < 0;
     P.table[static_cast<size_t>(b) * P.max_blocks + (o + P.bs - 1) / P.bs + (j - cuA[b])] = id;
   }
-  for (int j = gt; j < tf; j += gthreads) {
+  for (int j = rt; j < tf; j += gthreads) {
     const int32_t id = stack_at(count + j);
     bad |= static_cast<uint32_t>(id) >= static_cast<uint32_t>(P.n_blocks);
     if (count + j < P.n_blocks) P.free_blocks[count + j] = id;
   }
   // ===== per-request outputs =====
-  for (int b = gt; b <= P.B; b += gthreads) {
+  for (int b = rt; b <= P.B; b += gthreads) {
     if (P.cu_new) P.cu_new[b] = cuN[b];
     if (P.len_out && b < P.B) {
       const bool have = cuA[b + 1] == cuA[b] || cuA[b + 1] <= top;
@@ -204,9 +197,9 @@ int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream) {
   if (int rr = smem_limit_once(attr, echo::block_tables_kernel, 3 * (16384 + 1) * sizeof(int32_t),
                                "block tables smem attribute"))
     return rr;
-  const int per_cta = echo::kTabThreads * echo::kTabPer;
-  const int want = a->max_new / per_cta + (a->max_new % per_cta != 0);
-  const int grid = want < 1 ? 1 : want > 304 ? 304 : want;
+  // an entry per thread while that fits the GPU (four CTAs per SM), then more entries each
+  const int want = a->max_new / echo::kTabThreads + (a->max_new % echo::kTabThreads != 0);
+  const int grid = want < 1 ? 1 : want > 608 ? 608 : want;
   echo::block_tables_kernel<<<grid, echo::kTabThreads, smem, stream>>>(P);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block tables launch");

@@ -136,13 +136,18 @@ class Attn:
 
 
 FORMATS = [(BF16, 128), (FP4, 128), (BF16, 64), (FP4, 64)]
+# Blocks of the table beyond the contexts: tables that may hold long contexts take the path
+# that cuts all contexts into equal pieces and merges them in a second kernel, others a CTA
+# or a cluster per (request, KV head).
+WIDE = 60000
 
 
 @pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens", [[0], [1], [0, 1, 2], [15, 16, 17, 31, 32, 33], [63, 64, 65, 0, 127, 128, 129, 200],
                                   [700, 3, 0, 1025, 64, 0]])
-def test_lengths(fmt, D, lens):
-    a = Attn(fmt, D, 64, 8, 2, 1, lens, seed=len(lens))
+def test_lengths(fmt, D, lens, wide):
+    a = Attn(fmt, D, 64, 8, 2, 1, lens, seed=len(lens), cap=WIDE // 64 if wide else None)
     echo.echo_block_attention(a.args())
     a.check()
 
@@ -150,8 +155,9 @@ def test_lengths(fmt, D, lens):
 @pytest.mark.parametrize("fmt,D", FORMATS)
 @pytest.mark.parametrize("Hq,Hkv,n_q", [(1, 1, 1), (3, 1, 1), (7, 1, 2), (16, 1, 1), (12, 4, 3), (20, 2, 3), (33, 1, 1),
                                         (8, 8, 4), (64, 8, 5), (48, 1, 2)])
-def test_groups_and_query_tokens(fmt, D, Hq, Hkv, n_q):
-    a = Attn(fmt, D, 32, Hq, Hkv, n_q, [330, 5, 1, 77], seed=Hq)
+@pytest.mark.parametrize("wide", [False, True])
+def test_groups_and_query_tokens(fmt, D, Hq, Hkv, n_q, wide):
+    a = Attn(fmt, D, 32, Hq, Hkv, n_q, [330, 5, 1, 77], seed=Hq, cap=WIDE // 32 if wide else None)
     echo.echo_block_attention(a.args())
     a.check()
 
@@ -173,8 +179,17 @@ def test_window_and_sinks(fmt, D, sinks, window):
     a.check()
 
 
+@pytest.mark.parametrize("fmt,D", FORMATS)
+def test_a_long_window_over_cut_contexts(fmt, D):
+    a = Attn(fmt, D, 64, 4, 1, 2, [2600, 0, 700, 1], sinks=70, window=1800, seed=5)
+    b = Attn(fmt, D, 64, 4, 1, 2, [2600, 0, 700, 1], sinks=70, window=50000, seed=6, cap=WIDE // 64)
+    for x in (a, b):
+        echo.echo_block_attention(x.args())
+        x.check()
+
+
 @pytest.mark.parametrize("fmt", [BF16, FP4])
-@pytest.mark.parametrize("k,bs,window", [(1, 64, 0), (5, 64, 0), (16, 16, 0), (9, 32, 40)])
+@pytest.mark.parametrize("k,bs,window", [(1, 64, 0), (5, 64, 0), (16, 16, 0), (9, 32, 40), (600, 64, 0)])
 def test_recalled_selections(fmt, k, bs, window):
     a = Attn(fmt, 128, bs, 8, 2, 2, [500, 1, 0, 130], sel=k, window=window, sinks=4 if window else 0, seed=k)
     echo.echo_block_attention(a.args())
@@ -234,6 +249,15 @@ def test_query_magnitudes(fmt, qscale):
 
 
 @pytest.mark.parametrize("fmt", [BF16, FP4])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
+def test_scales(fmt, scale):
+    a = Attn(fmt, 128, 64, 8, 2, 2, [400, 65, 0], seed=11, sinks=2, window=90)
+    a.scale = scale
+    echo.echo_block_attention(a.args())
+    a.check()
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP4])
 def test_a_growing_maximum_rescales_what_came_before(fmt):
     """Scores that climb by 300 over the context (and one late peak) move the running
     maximum many times; early tokens end up far below."""
@@ -252,10 +276,11 @@ def test_a_growing_maximum_rescales_what_came_before(fmt):
     a.check()
 
 
+@pytest.mark.parametrize("cap", [None, WIDE // 64])
 @pytest.mark.parametrize("fmt", [BF16, FP4])
-def test_a_long_ragged_batch(fmt):
+def test_a_long_ragged_batch(fmt, cap):
     """Contexts split over many CTAs beside short and empty ones."""
-    a = Attn(fmt, 128, 64, 8, 1, 1, [9000, 0, 17, 3000, 1, 64], seed=13)
+    a = Attn(fmt, 128, 64, 8, 1, 1, [9000, 0, 17, 3000, 1, 64], seed=13, cap=cap)
     echo.echo_block_attention(a.args())
     a.check()
     first = a.out.clone(), a.lse.clone()
@@ -289,8 +314,8 @@ def test_rows_past_4_gib():
 def test_captured_graphs_share_a_workspace_in_turn():
     """Two captured calls of different shapes with one workspace, replayed one after another
     on a side stream, with the lengths changed between replays."""
-    x = Attn(BF16, 128, 64, 8, 1, 1, [3000, 40], seed=16)
-    y = Attn(FP4, 128, 64, 8, 1, 1, [2500, 0, 900], seed=17)
+    x = Attn(BF16, 128, 64, 8, 1, 1, [3000, 40], seed=16, cap=WIDE // 64)
+    y = Attn(FP4, 128, 64, 8, 1, 1, [2500, 0, 900], seed=17, cap=WIDE // 64)
     y.ws = x.ws
     st = torch.cuda.Stream()
     graphs = []
