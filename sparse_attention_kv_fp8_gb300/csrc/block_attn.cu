@@ -205,7 +205,8 @@ __device__ __forceinline__ int chunks_of(const ReqView &v) {
   return (v.nsub + kSubs - 1) / kSubs;
 }
 
-// moves forward to the (b, hm) that holds chunk g (a chunk of the line)
+// moves forward to the (b, hm) that holds chunk g (a chunk of the line; past the last request
+// there is nothing, and the walk ends)
 template <int kSubs>
 __device__ __forceinline__ void seek(const BlockAttnParams &P, LinePos &L, int g) {
   while (g >= L.end) {
@@ -215,11 +216,16 @@ __device__ __forceinline__ void seek(const BlockAttnParams &P, LinePos &L, int g
       const int by = min(heads - 1 - L.hm, (g - L.end) / n + 1);  // row groups to pass over
       L.hm += by;
       L.start = L.end + (by - 1) * n;
-    } else {
+    } else if (L.b + 1 < P.B) {
       ++L.b;
       L.hm = 0;
       L.start = L.end;
       L.v = req_view(P, __ldg(P.ctx_len + L.b));
+    } else {
+      L.start = L.end;
+      L.end = 0x7fffffff;
+      L.v.nsub = 0;
+      return;
     }
     L.end = L.start + chunks_of<kSubs>(L.v);
   }
@@ -337,8 +343,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
     const bool own = g0 >= upto - mine && g0 < upto;  // one lane's run holds g0
     if (own) {
       int64_t at = upto - mine;
-      int n;
-      for (own_b = b0;; ++own_b) {
+      int n = 1;
+      for (own_b = b0; own_b < b1; ++own_b) {
         n = chunks_of<C::kSubs>(req_view(P, __ldg(P.ctx_len + own_b)));
         if (g0 < at + static_cast<int64_t>(n) * heads) break;
         at += static_cast<int64_t>(n) * heads;
@@ -939,15 +945,18 @@ static int launch_ba(echo::BlockAttnParams P, int64_t pairs, int64_t most, int s
   static std::atomic<bool> attr[kMaxDevices];
   if (int rr = smem_limit_once(attr, kernel, C::kSmem, "block attention smem attribute")) return rr;
   // A cluster per (b, h), or the line of all chunks cut into equal pieces?  The cluster grows
-  // while it fits the GPU and every warp still gets a chunk.  Clusters cost the waves' longest
-  // context; cutting costs an equal share plus the second kernel and the piece borders: about
-  // the time of 1024 bf16 or 1536 4-bit tokens (measured for 8 to 256 pairs of 512 to 8192
-  // tokens: at 64 pairs of 1024, 9 against 14 us in bf16; at 8 pairs of 8192, 43 against 14
-  // before clusters).
+  // while it fits the GPU and every warp still gets a chunk.  Clusters cost the longest
+  // context of their waves; cutting costs an equal share plus the second kernel and the piece
+  // borders, about the time of `extra` tokens.  Measured with equal contexts, bf16 / 4-bit: 64
+  // pairs of 1024 tokens 12 / 10 us a CTA each against 14 / 16 cut, 128 pairs of 4096 37 / 23
+  // against 43 / 27, 8 pairs of 8192 43 / 36 against 14 / 12.  The host does not know the
+  // contexts, only how long they may be: past 4 `extra` tokens a CTA, what an uneven batch
+  // would cost is more than clusters save (152 pairs of 16384 to 32768 tokens in 4 bits: 125
+  // us whole, 107 cut).
   int cs = 1;
   while (cs < echo::kBaMaxCluster && pairs * cs * 2 <= sms * 7 / 8 && most > static_cast<int64_t>(cs) * WARPS * C::kTokens) cs *= 2;
-  const int64_t waves = (pairs * cs + sms - 1) / sms, extra = C::kFp4 ? 1536 : 1024;
-  const bool whole = waves * most / cs <= pairs * most / sms + extra;
+  const int64_t waves = (pairs * cs + sms - 1) / sms, extra = C::kFp4 ? 1536 : 1024, share = waves * most / cs;
+  const bool whole = share <= pairs * most / sms + extra && share <= 4 * extra;
   P.cluster = whole ? cs : 0;
   const unsigned grid = whole ? static_cast<unsigned>(pairs * cs) : static_cast<unsigned>(std::min(sms, echo::kBaMaxGrid));
   cudaLaunchConfig_t cfg{};

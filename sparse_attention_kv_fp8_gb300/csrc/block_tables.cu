@@ -18,7 +18,6 @@
 namespace echo {
 
 constexpr int kTabThreads = 256;
-constexpr int kTabPer = 4;  // list entries of a thread at a time
 
 struct TablesParams {
   const int32_t *old_len, *new_len;
@@ -104,39 +103,57 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
 
   const int gthreads = gridDim.x * kTabThreads, gt = blockIdx.x * kTabThreads + t;
   const int rt = gthreads - 1 - gt;  // the blocks go to the other end's threads: both at once
-  // ===== the list of new tokens: kTabPer entries per thread at a time, their owners found
-  // first, then their blocks' ids read together =====
+  // ===== the list of new tokens =====
   const int listed = min(tn, P.max_new);
   bad |= tn > P.max_new;
-  for (int base = gt; base < P.max_new; base += gthreads * kTabPer) {
-    int p[kTabPer], k[kTabPer], id[kTabPer];
-    const int32_t *from[kTabPer];
-#pragma unroll
-    for (int u = 0; u < kTabPer; ++u) {
-      const int i = base + u * gthreads;
-      from[u] = nullptr;
-      p[u] = k[u] = id[u] = -1;
-      if (i >= listed) continue;
-      const int b = owner_of(cuN, P.B, i);
-      if (cuA[b + 1] != cuA[b] && cuA[b + 1] > top) continue;  // left without its blocks
-      const int o = min(max(P.old_len[b], 0), cap), nbo = (o + P.bs - 1) / P.bs;
-      p[u] = o + (i - cuN[b]);
-      k[u] = p[u] / P.bs;
-      const int s = top - 1 - (cuA[b] + k[u] - nbo);
-      if (k[u] < nbo) from[u] = P.table + static_cast<size_t>(b) * P.max_blocks + k[u];
-      else if (s < count) from[u] = P.free_blocks + s;
-      else id[u] = stack_at(s);
+  // the slot and position of the token at entry i < listed of the list, request b its owner
+  auto entry = [&](int i, int b, int32_t &slot, int32_t &pos) {
+    slot = pos = -1;
+    if (cuA[b + 1] != cuA[b] && cuA[b + 1] > top) return;  // left without its blocks
+    const int o = min(max(P.old_len[b], 0), cap), nbo = (o + P.bs - 1) / P.bs;
+    const int p = o + (i - cuN[b]), k = p / P.bs;
+    const int32_t id = k < nbo ? P.table[static_cast<size_t>(b) * P.max_blocks + k] : stack_at(top - 1 - (cuA[b] + k - nbo));
+    if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(P.n_blocks)) bad = 1;
+    else slot = id * P.bs + (p - k * P.bs), pos = p;
+  };
+  const bool wide = ((reinterpret_cast<uintptr_t>(P.slot_map) | reinterpret_cast<uintptr_t>(P.positions)) & 15) == 0;
+  if (P.max_new <= gthreads || !wide) {  // an entry per thread: the shortest chain of loads
+    for (int i = gt; i < P.max_new; i += gthreads) {
+      int32_t slot = -1, pos = -1;
+      if (i < listed) entry(i, owner_of(cuN, P.B, i), slot, pos);
+      P.slot_map[i] = slot;
+      if (P.positions) P.positions[i] = pos;
     }
+  } else {                               // four neighbours: one search and mostly one id
+    for (int i = 4 * gt; i < P.max_new; i += 4 * gthreads) {
+      int32_t slot[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
+      if (i < listed) {
+        int b = owner_of(cuN, P.B, i);
+        entry(i, b, slot[0], pos[0]);
+        // entries that follow it in its block
+        const int same = slot[0] >= 0 ? min(P.bs - 1 - pos[0] % P.bs, cuN[b + 1] - 1 - i) : 0;
 #pragma unroll
-    for (int u = 0; u < kTabPer; ++u)
-      if (from[u]) id[u] = *from[u];
+        for (int u = 1; u < 4; ++u) {
+          if (i + u >= listed) continue;
+          if (u <= same) {
+            slot[u] = slot[0] + u, pos[u] = pos[0] + u;
+          } else {
+            while (cuN[b + 1] <= i + u) ++b;
+            entry(i + u, b, slot[u], pos[u]);
+          }
+        }
+      }
+      if (i + 4 <= P.max_new) {
+        *reinterpret_cast<int4 *>(P.slot_map + i) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        if (P.positions) *reinterpret_cast<int4 *>(P.positions + i) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      } else {
 #pragma unroll
-    for (int u = 0; u < kTabPer; ++u) {
-      const int i = base + u * gthreads;
-      if (i >= P.max_new) continue;
-      if (p[u] >= 0 && static_cast<uint32_t>(id[u]) >= static_cast<uint32_t>(P.n_blocks)) p[u] = -1, bad = 1;
-      P.slot_map[i] = p[u] >= 0 ? id[u] * P.bs + (p[u] - k[u] * P.bs) : -1;
-      if (P.positions) P.positions[i] = p[u];
+        for (int u = 0; u < 4; ++u)
+          if (i + u < P.max_new) {
+            P.slot_map[i + u] = slot[u];
+            if (P.positions) P.positions[i + u] = pos[u];
+          }
+      }
     }
   }
   // ===== the blocks that moved =====
@@ -197,7 +214,7 @@ int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream) {
   if (int rr = smem_limit_once(attr, echo::block_tables_kernel, 3 * (16384 + 1) * sizeof(int32_t),
                                "block tables smem attribute"))
     return rr;
-  // an entry per thread while that fits the GPU (four CTAs per SM), then more entries each
+  // an entry per thread while that fits the GPU (four CTAs per SM), then four and more each
   const int want = a->max_new / echo::kTabThreads + (a->max_new % echo::kTabThreads != 0);
   const int grid = want < 1 ? 1 : want > 608 ? 608 : want;
   echo::block_tables_kernel<<<grid, echo::kTabThreads, smem, stream>>>(P);

@@ -250,19 +250,29 @@ __device__ __forceinline__ void rope_rows(const RopeParams &P, const RopeDst &W,
 #pragma unroll
   for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
   if (!is_v) {
+    auto four = [](const float *p, float *to) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+      to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+    };
     if (W.in && rot) {
       const float *row = P.cos_sin + static_cast<int64_t>(pos) * P.rope_dim;
+      float cv[8], sv[8];
+      if constexpr (kInter) {
+        four(row + d0 / 2, cv), four(row + half + d0 / 2, sv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = kInter ? (d0 + i) / 2 : (low ? d0 : d0 - half) + i;
-        const bool neg = kInter ? i % 2 == 0 : low;
-        c[i] = __ldg(row + k);
-        s[i] = neg ? -__ldg(row + half + k) : __ldg(row + half + k);
+        for (int i = 0; i < 8; ++i) c[i] = cv[i / 2], s[i] = i % 2 == 0 ? -sv[i / 2] : sv[i / 2];
+      } else {
+        const float *at = row + (low ? d0 : d0 - half);
+        four(at, cv), four(at + 4, cv + 4), four(at + half, sv), four(at + half + 4, sv + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = cv[i], s[i] = low ? -sv[i] : sv[i];
       }
     }
     if (wt) {
+      float wo[8], wp[8];
+      four(wt + d0, wo), four(wt + d0 + 4, wo + 4), four(wt + pd, wp), four(wt + pd + 4, wp + 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] *= __ldg(wt + d0 + i), s[i] *= __ldg(wt + pd + (kInter ? i ^ 1 : i));
+      for (int i = 0; i < 8; ++i) c[i] *= wo[i], s[i] *= wp[kInter ? i ^ 1 : i];
     }
   }
   for (int h = h0; h < h1; h += kBatch) {

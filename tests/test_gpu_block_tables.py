@@ -66,7 +66,8 @@ def test_small_steps(old, new, bs):
 
 
 @pytest.mark.parametrize("B,L,new,bs", [(1, 40000, 20000, 64), (37, 900, 1, 64), (64, 32768, 2, 64), (511, 50, 60, 16),
-                                        (513, 300, 300, 7), (2000, 100, 5, 16), (16384, 30, 9, 16)])
+                                        (513, 300, 300, 7), (2000, 100, 5, 16), (16384, 30, 9, 16),
+                                        (100, 10000, 9000, 64), (90, 9000, 9000, 3), (16000, 80, 60, 2)])
 @pytest.mark.parametrize("seed", [1, 2])
 def test_random_steps(B, L, new, bs, seed):
     s = Step(*lengths(B, L, new, seed), bs, seed)
@@ -106,6 +107,12 @@ def test_unaligned_lists_and_too_few_entries(shift):
     echo.echo_block_tables(s.args)
     s.check(echo.DEV_BAD_INDEX)
     s = Step([3], [3], 16, 4, max_new=0)
+    echo.echo_block_tables(s.args)
+    s.check()
+    s = Step(*lengths(70, 9000, 9000, 3), 16, 3, shift=shift)
+    echo.echo_block_tables(s.args)
+    s.check()
+    s = Step([], [], 16, 3, n_free=2, n_blocks=2)
     echo.echo_block_tables(s.args)
     s.check()
 
