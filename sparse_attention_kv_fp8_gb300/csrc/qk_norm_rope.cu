@@ -382,10 +382,17 @@ static cudaError_t launch_rope(echo::RopeParams P, bool values, int span, int kv
   return cudaGetLastError();
 }
 
-template <int D>
-static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, bool many, cudaStream_t stream) {
-  if (many) return P.interleaved ? launch_rope<D, 4, true>(P, values, 16, 8, stream) : launch_rope<D, 4, false>(P, values, 16, 8, stream);
-  return P.interleaved ? launch_rope<D, 1, true>(P, values, 1, 1, stream) : launch_rope<D, 1, false>(P, values, 1, 1, stream);
+// How many heads a warp takes (q, then k or v), and how many of them at a time.  Few heads in
+// all: one each, the shortest chain; many: long runs, cosines and weights read once for them.
+// In warps at one head each (T / (256 / D) times the heads), us for 1, 2 of 8 and 4, 4 of 16
+// and 8 heads: 2560 warps 4.2 / 6.2 / 8.3, 10240 8.2 / 6.2 / 9.0, 81920 42.6 / 22.6 / 24.8
+// (heads of 64), 163840 67.7 / 36.8 / 36.2, 655360 256 / 127 / 119 (heads of 128).
+template <int D, bool kInter>
+static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, cudaStream_t stream) {
+  const int64_t warps = (static_cast<int64_t>(P.T) + 256 / D - 1) / (256 / D) * (P.n_heads + (values ? 2 : 1) * static_cast<int64_t>(P.n_kv_heads));
+  if (warps <= 4096) return launch_rope<D, 1, kInter>(P, values, 1, 1, stream);
+  if (warps <= 163840) return launch_rope<D, 2, kInter>(P, values, 8, 4, stream);
+  return launch_rope<D, 4, kInter>(P, values, 16, 8, stream);
 }
 
 int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream) {
@@ -404,8 +411,9 @@ int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream) {
   P.status = a->dev_status;
   // value heads have work only when something takes them
   const bool values = a->v && (a->slot_map || a->v_out);
-  const bool many = static_cast<int64_t>(a->T) * (a->n_heads + 2 * a->n_kv_heads) >= 16384;
-  const cudaError_t e = a->head_dim == 128 ? launch_rope_dim<128>(P, values, many, stream) : launch_rope_dim<64>(P, values, many, stream);
+  const cudaError_t e = a->head_dim == 128
+                            ? (a->interleaved ? launch_rope_dim<128, true>(P, values, stream) : launch_rope_dim<128, false>(P, values, stream))
+                            : (a->interleaved ? launch_rope_dim<64, true>(P, values, stream) : launch_rope_dim<64, false>(P, values, stream));
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "qk norm + rope launch");
 }
 

@@ -100,7 +100,7 @@ class Rope:
 CASES = [
     (1, 64, 8, 128, 128, False), (1, 1, 1, 64, 64, True), (2, 6, 2, 64, 32, False), (3, 5, 5, 128, 16, True),
     (7, 8, 1, 128, 64, False), (33, 7, 3, 64, 16, False), (130, 32, 8, 128, 128, True), (300, 64, 8, 128, 96, False),
-    (500, 40, 8, 64, 48, True),
+    (500, 40, 8, 64, 48, True), (2001, 18, 3, 128, 128, False), (700, 5, 4, 64, 32, True),
 ]
 
 
@@ -108,6 +108,14 @@ CASES = [
 @pytest.mark.parametrize("T,Hq,Hk,D,rd,inter", CASES)
 def test_norm_rope_and_cache(T, Hq, Hk, D, rd, inter, fmt):
     r = Rope(T, Hq, Hk, D, rd, inter, fmt, bs=[16, 64, 48][T % 3], seed=T, norm=T % 2 == 1, fused=T != 7)
+    echo.echo_qk_norm_rope(r.args())
+    r.check()
+
+
+@pytest.mark.parametrize("fmt,D,inter", [(BF16, 128, False), (FP4, 128, True), (FP4, 64, False), (BF16, 64, True)])
+def test_a_long_chunk(fmt, D, inter):
+    """Enough heads for the longest runs per warp (16 and 8, cut short by the head counts)."""
+    r = Rope(9001, 35 if D == 128 else 70, 2 if D == 128 else 5, D, D, inter, fmt, 64, seed=2)
     echo.echo_qk_norm_rope(r.args())
     r.check()
 
