@@ -45,6 +45,7 @@ constexpr float kBaLazy = 8.f;    // log2 of how far a score may exceed the runn
 // fp16 softmax weights are kept 2^7 up: at most 2^(7 + 8), and the subnormals (a grid of
 // 2^-24) begin 2^-21 below the running maximum instead of 2^-14
 constexpr float kBaLift = 7.f;
+constexpr float kBaNone = -3.4028234664e38f;  // (no score seen: finite, so that differences with it are too)
 constexpr int kBaNowhere = 0x7fffff00;  // position of a sub-block that is not there
 constexpr int kBaMaxCluster = 8;  // CTAs of a (b, h) that merge over distributed shared memory
 constexpr int kBaList = 64;        // entries of a warp's list of sub-blocks (two batches of 32)
@@ -131,7 +132,10 @@ struct BaCfg {
   static constexpr int kQRows = (kRows + WARPS - 1) / WARPS;  // query rows a warp lays out
 };
 
-__device__ __forceinline__ void ba_cp16(uint32_t dst, const void *src, bool on) {
+__device__ __forceinline__ void ba_cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ba_cp16_or_zeros(uint32_t dst, const void *src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16u : 0u) : "memory");
 }
 __device__ __forceinline__ void ba_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -180,9 +184,9 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// log of a row's sum of weights 2^(x - top + lift)
-__device__ __forceinline__ float ba_lse(float top, float sum, float lift) {
-  return top == -INFINITY ? -INFINITY : (top - lift + log2f(sum)) * 0.693147180559945309f;
+// log of a row's sum of weights 2^(x - top)
+__device__ __forceinline__ float ba_lse(float top, float sum) {
+  return top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -278,6 +282,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r8 = lane >> 2, c4 = lane & 3;  // fragment row and column pair
   uint8_t *stage_base = ba_smem + warp * STAGES * C::kStageBytes;
+  const uint32_t stage_u32 = smem_u32(stage_base) + lane * 16;
   float *merge = reinterpret_cast<float *>(ba_smem + C::kOffMerge);
   uint2 *qfrag = reinterpret_cast<uint2 *>(ba_smem + C::kOffQ);
   float2 *ml = reinterpret_cast<float2 *>(ba_smem + C::kOffMl);       // [WARPS][kRows]
@@ -422,31 +427,35 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
   // most (STAGES - 1) * kSubs < 32 entries ahead of the reader.
   static_assert((STAGES - 1) * C::kSubs <= kBaList - 32 && 32 % C::kSubs == 0, "list length");
   LinePos mine = cur;     // of the entry this lane makes
-  int made = 0, at = 0;   // entries made, entries loaded
+  int at = 0;             // entries loaded
+  int to_load = (n_chunks - warp + WARPS - 1) / WARPS;  // chunks of this warp still to load
   auto issue = [&](int st) {
-    if (at == made) {     // (warp-uniform)
-      const int i = made + lane, g = warp + WARPS * (i / C::kSubs);
-      SubEntry x{reinterpret_cast<const uint8_t *>(P.rows), kBaNowhere, kBaEdge};
-      if (g < n_chunks) {
-        seek<C::kSubs>(P, mine, g);
-        x = sub_entry<FMT, D>(P, mine, (g - mine.start) * C::kSubs + i % C::kSubs);
+    if (to_load > 0) {    // (warp-uniform)
+      --to_load;
+      if ((at & 31) == 0) {
+        const int i = at + lane, g = warp + WARPS * (i / C::kSubs);
+        SubEntry x{reinterpret_cast<const uint8_t *>(P.rows), kBaNowhere, kBaEdge};
+        if (g < n_chunks) {
+          seek<C::kSubs>(P, mine, g);
+          x = sub_entry<FMT, D>(P, mine, (g - mine.start) * C::kSubs + i % C::kSubs);
+        }
+        list[i % kBaList] = x;
+        __syncwarp();
       }
-      list[i % kBaList] = x;
-      made += 32;
-      __syncwarp();
-    }
-    if (warp + WARPS * (at / C::kSubs) < n_chunks) {
-      uint32_t dst = smem_u32(stage_base + st * C::kStageBytes) + lane * 16;
+      uint32_t dst = stage_u32 + st * C::kStageBytes;
 #pragma unroll
       for (int u = 0; u < C::kSubs; ++u, dst += C::kSubBytes) {
-        const SubEntry x = list[(at + u) % kBaList];
+        const SubEntry x = list[at % kBaList + u];  // (kSubs divides kBaList)
         const uint8_t *src = x.src + lane * 16;
         if constexpr (C::kFp4) {
+          // (what a sub-block that no query sees leaves here is never used: its scores are
+          // masked and its value scales replaced by zeros)
           constexpr int kPieces = C::kSubBytes / 16;
-          const bool on = (x.flags & 0xffffu) != 0;
+          if (x.flags & 0xffffu) {
 #pragma unroll
-          for (int i = 0; i < (kPieces + 31) / 32; ++i)
-            if ((i + 1) * 32 <= kPieces || lane < kPieces - i * 32) ba_cp16(dst + i * 512, src + i * 512, on);
+            for (int i = 0; i < (kPieces + 31) / 32; ++i)
+              if ((i + 1) * 32 <= kPieces || lane < kPieces - i * 32) ba_cp16(dst + i * 512, src + i * 512);
+          }
         } else {
           // rows of 2 D bytes, 16-byte pieces XORed with the token so that ldmatrix reads
           // 8 tokens from 8 different bank groups; a token no query sees is read as zeros
@@ -458,13 +467,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
             const int tk = i * kPer + lane / (D / 8), pc = lane % (D / 8);
             const uint32_t o = tk * (2 * D) + ((pc ^ (tk & 7)) << 4) - lane * 16;
             const bool on = (x.flags >> tk) & 1;
-            ba_cp16(dst + o, src + i * 512, on);
-            ba_cp16(dst + kSubTokens * D * 2 + o, src + vofs + i * 512, on);
+            ba_cp16_or_zeros(dst + o, src + i * 512, on);
+            ba_cp16_or_zeros(dst + kSubTokens * D * 2 + o, src + vofs + i * 512, on);
           }
         }
       }
+      at += C::kSubs;
     }
-    at += C::kSubs;
     ba_commit();
   };
 #pragma unroll
@@ -492,10 +501,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
         clen[nt][e] = cur.v.len - (P.n_q - 1 - min((row0 + rr) / P.group, P.n_q - 1));
       }
 
+    // what is taken off a column's scores (its running maximum less the lift), sum, output
     float m[NT][2], l[NT][2], o[C::kSteps][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kBaNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < C::kSteps; ++j)
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       uint32_t flags[C::kSubs], edge = 0;
 #pragma unroll
       for (int u = 0; u < C::kSubs; ++u) {
-        const int2 x = *reinterpret_cast<const int2 *>(&list[(rd + u) % kBaList].pos);
+        const int2 x = *reinterpret_cast<const int2 *>(&list[rd % kBaList + u].pos);
         pos[u] = x.x;
         flags[u] = static_cast<uint32_t>(x.y);
         edge |= flags[u] & kBaEdge;
@@ -611,17 +621,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
           top[nt][e] = -INFINITY;
 #pragma unroll
           for (int u = 0; u < C::kSubs; ++u) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[u][nt][e], s[u][nt][e + 2]));
-          grow |= fmaf(top[nt][e], cscale[nt][e], -m[nt][e]) > kBaLazy;
+          grow |= fmaf(top[nt][e], cscale[nt][e], -m[nt][e]) > kBaLazy + kLift;
         }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(m[nt][e], top[nt][e] * cscale[nt][e]);
+            float x = fmaxf(m[nt][e], fmaf(top[nt][e], cscale[nt][e], -kLift));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-            const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
+            const float f = ex2(m[nt][e] - x);
             m[nt][e] = x;
             l[nt][e] *= f;
 #pragma unroll
@@ -633,11 +643,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       uint32_t pb[C::kSubs][NT][2], pr[C::kSubs][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kLift, m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kLift;
 #pragma unroll
         for (int u = 0; u < C::kSubs; ++u) {
-          float p0 = ex2(fmaf(s[u][nt][0], cscale[nt][0], -m0)), p1 = ex2(fmaf(s[u][nt][1], cscale[nt][1], -m1));
-          float p2 = ex2(fmaf(s[u][nt][2], cscale[nt][0], -m0)), p3 = ex2(fmaf(s[u][nt][3], cscale[nt][1], -m1));
+          float p0 = ex2(fmaf(s[u][nt][0], cscale[nt][0], -m[nt][0])), p1 = ex2(fmaf(s[u][nt][1], cscale[nt][1], -m[nt][1]));
+          float p2 = ex2(fmaf(s[u][nt][2], cscale[nt][0], -m[nt][0])), p3 = ex2(fmaf(s[u][nt][3], cscale[nt][1], -m[nt][1]));
           if (edge) {  // (a zero scale leaves nothing of a masked score's infinity)
             p0 = s[u][nt][0] == -INFINITY ? 0.f : p0, p1 = s[u][nt][1] == -INFINITY ? 0.f : p1;
             p2 = s[u][nt][2] == -INFINITY ? 0.f : p2, p3 = s[u][nt][3] == -INFINITY ? 0.f : p3;
@@ -729,6 +738,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+        if (m[nt][e] == kBaNone) m[nt][e] = -INFINITY;
         if (r8 == 0) ml[warp * C::kRows + nt * 8 + 2 * c4 + e] = make_float2(m[nt][e], l[nt][e]);
       }
     __syncthreads();
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
               const float inv = v.y > 0.f ? 1.f / v.y : v.y;  // (a NaN sum stays one)
               *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
               *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
-              if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y, kLift);
+              if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y);
             }
           }
         }
@@ -854,7 +864,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       const float inv = sum > 0.f ? 1.f / sum : sum;
       *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
           make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
-      if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum, kLift);
+      if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum);
     }
     cluster_arrive();  // (no CTA's shared memory goes while another reads it)
     cluster_wait();
@@ -868,8 +878,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
 constexpr int kBaCombThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kBaCombThreads) block_attn_combine_kernel(const BlockAttnParams P, int rows_pad,
-                                                                                 float lift) {
+__global__ void __launch_bounds__(kBaCombThreads) block_attn_combine_kernel(const BlockAttnParams P, int rows_pad) {
   constexpr int kLanes = D / 4, kGroups = kBaCombThreads / kLanes;
   __shared__ float2 sml[kGroups];
   __shared__ __align__(16) float so[kGroups][D];
@@ -923,7 +932,7 @@ __global__ void __launch_bounds__(kBaCombThreads) block_attn_combine_kernel(cons
   const float inv = sum > 0.f ? 1.f / sum : sum;
   *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
       make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
-  if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum, lift);
+  if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum);
 }
 
 }  // namespace echo
@@ -981,7 +990,7 @@ static int launch_ba(echo::BlockAttnParams P, int64_t pairs, int64_t most, int s
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows), C::kFp4 ? echo::kBaLift : 0.f);
+  e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows));
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block attention merge launch");
 }
 
