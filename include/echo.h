@@ -573,8 +573,8 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  *           a block is listed twice; the n_q queries share the list
  *   ctx_len [B] int32 device; above max_blocks * block_tokens (sel == NULL) it is clamped
  *           with ECHO_DEV_BAD_INDEX
- *   out     [B][n_q][n_heads][head_dim] bf16 device; lse [B][n_q][n_heads] fp32 device,
- *           optional
+ *   out     [B][n_q][n_heads][head_dim] bf16 device, 16-byte aligned, apart from q; lse
+ *           [B][n_q][n_heads] fp32 device, optional
  *   workspace  device, 256-byte aligned, echo_block_attention_workspace_bytes() bytes; one
  *           workspace serves calls that run one after another
  * Tokens no query of the request sees may hold any bytes.  Scores, the softmax and both
@@ -582,7 +582,10 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  * or in fp16 (ECHO_BLOCK_FP4).  ECHO_BLOCK_FP4 takes the queries to fp16 scaled by a power of two
  * of their row: an entry below 2^-24 of its row's largest is rounded to that grid.
  * 1 <= n_q <= 64, n_q * n_heads / n_kv_heads <= 1024.  Launches 1 kernel, or 2 when
- * contexts are split over several CTAs (the second merges their partial results).
+ * contexts are cut into pieces (the second merges their partial results): the choice goes by
+ * B, the heads and how long a context may be (max_blocks, window), not by the contexts, so a
+ * captured call serves any contexts.  The kernel depends on format, head_dim and
+ * n_q * n_heads / n_kv_heads: make one call of a kind outside capture first.
  */
 typedef struct echo_block_attention_args {
     const uint16_t *q;

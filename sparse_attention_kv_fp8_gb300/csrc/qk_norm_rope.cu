@@ -6,7 +6,11 @@
 // A head is held by head_dim / 8 lanes, 16 bytes each, and never leaves registers until its
 // results are stored; the mean is a shuffle sum over those lanes.  A warp takes `span` heads
 // of one kind (q, k or v) of its tokens, kBatch at a time with the next batch's loads in
-// flight; cosines, sines and weights are read and multiplied once for them.  Bound by HBM.
+// flight; cosines, sines and weights are read and multiplied once for them.  Bound by HBM:
+// 16384 tokens x (64 + 8 + 8) heads of 128 in 119 us, 5.7 TB/s of the 6.67 TB/s that a copy
+// reaches here (0.86; 8-byte accesses and 32 warps an SM: with one 16-byte load per lane, the
+// partners shuffled between lanes and 16 warps it was 180 us); 8191 tokens x 40 heads of 64
+// into a 4-bit cache 22.6 us (0.60; launch and tail), a decode step's tokens 4 us (latency).
 #include "block_rows.cuh"
 
 namespace echo {

@@ -47,19 +47,17 @@ class Attn:
                 self.table = np.where(held[:, None], ids, -1).astype(np.int32)
                 n_rows = B * Hkv * nblk + spare
             else:
-                ids = g.permutation(B * nblk + spare)[:B * nblk].reshape(B, nblk).astype(np.int32)
-                self.table = np.where(held, ids, -1).astype(np.int32)
-                n_rows = (B * nblk + spare) * Hkv
+                self.table = np.full((B, nblk), -1, np.int32)
+                self.table[held] = g.permutation(int(held.sum()) + spare)[:int(held.sum())]
+                n_rows = (int(held.sum()) + spare) * Hkv
             self.logical = np.broadcast_to(np.arange(nblk), (B, Hkv, nblk))
         R = echo.block_row_elems(fmt, bs, D)
         self.rows_np = np.full((n_rows, 2 * R), 0xFF, np.uint8)      # NaN in bf16, NaN scales in 4 bits
         self.kv = {}
         for b in range(B):
             for h in range(Hkv):
-                for i in range(self.table.shape[-1]):
+                for i in np.nonzero((self.table[b, h] if self.table.ndim == 3 else self.table[b]) >= 0)[0]:
                     row, lb = self.row(b, h, i), int(self.logical[b, h, i])
-                    if row < 0 or lb < 0:
-                        continue
                     for off in range(bs):
                         p = lb * bs + off
                         if self.seen_by_some(b, p) and (row, off) not in self.kv:
@@ -106,7 +104,7 @@ class Attn:
         for b in range(self.B):
             for h in range(self.Hkv):
                 tok = []                                    # (position, k, v), entry after entry
-                for i in range(self.table.shape[-1]):
+                for i in np.nonzero((self.table[b, h] if self.table.ndim == 3 else self.table[b]) >= 0)[0]:
                     row, lb = self.row(b, h, i), int(self.logical[b, h, i])
                     if 0 <= row < self.rows_np.shape[0] and lb >= 0:
                         tok += [(lb * self.bs + o, *self.kv[row, o]) for o in range(self.bs) if (row, o) in self.kv]
@@ -311,11 +309,12 @@ def test_rows_past_4_gib():
     a.check()
 
 
-def test_captured_graphs_share_a_workspace_in_turn():
+@pytest.mark.parametrize("cap", [None, WIDE // 64])
+def test_captured_graphs_share_a_workspace_in_turn(cap):
     """Two captured calls of different shapes with one workspace, replayed one after another
     on a side stream, with the lengths changed between replays."""
-    x = Attn(BF16, 128, 64, 8, 1, 1, [3000, 40], seed=16, cap=WIDE // 64)
-    y = Attn(FP4, 128, 64, 8, 1, 1, [2500, 0, 900], seed=17, cap=WIDE // 64)
+    x = Attn(BF16, 128, 64, 8, 1, 1, [3000, 40], seed=16, cap=cap)
+    y = Attn(FP4, 128, 64, 8, 1, 1, [2500, 0, 900], seed=17, cap=cap)
     y.ws = x.ws
     st = torch.cuda.Stream()
     graphs = []
@@ -335,3 +334,26 @@ def test_captured_graphs_share_a_workspace_in_turn():
             for g in graphs:
                 g.replay()
         x.check(), y.check()
+
+
+def test_two_streams_with_a_workspace_each():
+    """Calls in flight at once on two streams, each with its own workspace."""
+    a = [Attn(f, 128, 64, 8, 1, 1, [2000, 30, 700], seed=18 + i, cap=c)
+         for i, (f, c) in enumerate(((BF16, WIDE // 64), (FP4, WIDE // 64), (BF16, None), (FP4, None)))]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, x in enumerate(a):
+            with torch.cuda.stream(streams[i % 2]):
+                echo.echo_block_attention(x.args())
+    for x in a:
+        x.check()
+
+
+@pytest.mark.parametrize("cap", [None, WIDE // 16])
+def test_thousands_of_requests(cap):
+    lens = np.zeros(5000, int)
+    lens[[0, 17, 18, 2500, 4998, 4999]] = [5, 100, 33, 64, 1, 40]
+    a = Attn(FP4, 64, 16, 2, 1, 1, [int(x) for x in lens], seed=22, cap=cap)
+    echo.echo_block_attention(a.args())
+    a.check()
