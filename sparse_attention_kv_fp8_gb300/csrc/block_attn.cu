@@ -502,16 +502,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       for (int s = 0; s < C::kSteps; ++s) qreg[s] = qfrag[s * 32 + lane];
     }
     float cscale[NT][2];
-    int clen[NT][2];  // tokens below which a column's query sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = nt * 8 + 2 * c4 + e;
-        cscale[nt][e] = P.scale_log2 * (F16 ? qscale[rr] : 1.f);
-        clen[nt][e] = cur.v.len - (P.n_q - 1 - min((row0 + rr) / P.group, P.n_q - 1));
-      }
-
+      for (int e = 0; e < 2; ++e) cscale[nt][e] = P.scale_log2 * (F16 ? qscale[nt * 8 + 2 * c4 + e] : 1.f);
     // what is taken off a column's scores (its running maximum less the lift), sum, output
     float m[NT][2], l[NT][2], o[C::kSteps][NT][4];
 #pragma unroll
@@ -613,15 +607,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAt
       // ----- softmax -----
       if (edge) {
 #pragma unroll
-        for (int u = 0; u < C::kSubs; ++u)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int e = 0; e < 2; ++e) {
+            // tokens below which this column's query sees
+            const int j = min((row0 + nt * 8 + 2 * c4 + e) / P.group, P.n_q - 1), n = cur.v.len - (P.n_q - 1 - j);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int p = pos[u] + r8 + (e >> 1) * 8, n = clen[nt][e & 1];
-              const bool see = p < n && (P.window == 0 || p >= n - P.window || p < P.sinks);
-              s[u][nt][e] = see ? s[u][nt][e] : -INFINITY;
-            }
+            for (int u = 0; u < C::kSubs; ++u)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int p = pos[u] + r8 + 8 * k;
+                const bool see = p < n && (P.window == 0 || p >= n - P.window || p < P.sinks);
+                s[u][nt][e + 2 * k] = see ? s[u][nt][e + 2 * k] : -INFINITY;
+              }
+          }
       }
       bool grow = false;
       float top[NT][2];
