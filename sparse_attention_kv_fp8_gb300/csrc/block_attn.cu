@@ -956,6 +956,29 @@ size_t block_attention_workspace_bytes(int32_t rows, int32_t head_dim) {
   return echo::kBaMaxGrid * sizeof(int4) + 2 * echo::kBaMaxGrid * pad * (2 + static_cast<size_t>(head_dim)) * sizeof(float);
 }
 
+// How many clusters of 2, 4 or 8 CTAs of a kernel the device holds at once (an SM holds one CTA,
+// and a cluster sits in one group of SMs: 76, 36 and 15 here, not 152 SMs' worth: 16 clusters
+// of 8 take 14.4 us where 15 take 8.4).  Asked once per kernel and device.
+template <typename K>
+static int clusters_at_once(K kernel, cudaLaunchConfig_t cfg, int cs, int dev, std::atomic<int> (&known)[kMaxDevices][4]) {
+  const int k = cs == 2 ? 1 : cs == 4 ? 2 : 3;
+  int n = known[dev][k].load(std::memory_order_relaxed);
+  if (n) return n - 1;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(cs);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][k].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <int FMT, int D, int NT, int WARPS, int STAGES>
 static int launch_ba(echo::BlockAttnParams P, int64_t pairs, int64_t most, int sms, cudaStream_t stream) {
   using C = echo::BaCfg<FMT, D, NT, WARPS, STAGES>;
@@ -972,18 +995,22 @@ static int launch_ba(echo::BlockAttnParams P, int64_t pairs, int64_t most, int s
   // contexts, only how long they may be: past 4 `extra` tokens a CTA, what an uneven batch
   // would cost is more than clusters save (152 pairs of 16384 to 32768 tokens in 4 bits: 125
   // us whole, 107 cut).
-  int cs = 1;
-  while (cs < echo::kBaMaxCluster && pairs * cs * 2 <= sms * 7 / 8 && most > static_cast<int64_t>(cs) * WARPS * C::kTokens) cs *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  static std::atomic<int> known[kMaxDevices][4];
+  int dev = 0, cs = 1;
+  cudaGetDevice(&dev);  // (below kMaxDevices: checked with the attribute above)
+  while (cs < echo::kBaMaxCluster && most > static_cast<int64_t>(cs) * WARPS * C::kTokens &&
+         pairs <= clusters_at_once(kernel, cfg, 2 * cs, dev, known))
+    cs *= 2;
   const int64_t waves = (pairs * cs + sms - 1) / sms, extra = C::kFp4 ? 1536 : 1024, share = waves * most / cs;
   const bool whole = share <= pairs * most / sms + extra && share <= 4 * extra;
   P.cluster = whole ? cs : 0;
   const unsigned grid = whole ? static_cast<unsigned>(pairs * cs) : static_cast<unsigned>(std::min(sms, echo::kBaMaxGrid));
-  cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
   cfg.attrs = at;
   if (whole && cs > 1) {
     at[0].id = cudaLaunchAttributeClusterDimension;
