@@ -45,6 +45,7 @@
 // 0.8 us to merge the warps, 1.3 us a cluster, 4 us a second kernel).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "block_rows.cuh"
 #include "cluster_select.cuh"
@@ -284,8 +285,8 @@ __device__ __forceinline__ SubEntry sub_entry(const BlockAttnParams &P, const Li
   return x;
 }
 
-template <int FMT, int D, int NT, int WARPS, int STAGES>
-__global__ void __launch_bounds__(WARPS * 32, 1) block_attn_kernel(const BlockAttnParams P) {
+template <int FMT, int D, int NT, int WARPS, int STAGES, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const BlockAttnParams P) {
   using C = BaCfg<FMT, D, NT, WARPS, STAGES>;
   constexpr bool F16 = C::kFp4;
   constexpr float kLift = F16 ? kBaLift : 0.f;
@@ -956,79 +957,109 @@ size_t block_attention_workspace_bytes(int32_t rows, int32_t head_dim) {
   return echo::kBaMaxGrid * sizeof(int4) + 2 * echo::kBaMaxGrid * pad * (2 + static_cast<size_t>(head_dim)) * sizeof(float);
 }
 
-// How many clusters of 2, 4 or 8 CTAs of a kernel the device holds at once (an SM holds one CTA,
-// and a cluster sits in one group of SMs: 76, 36 and 15 here, not 152 SMs' worth: 16 clusters
-// of 8 take 14.4 us where 15 take 8.4).  Asked once per kernel and device.
-template <typename K>
-static int clusters_at_once(K kernel, cudaLaunchConfig_t cfg, int cs, int dev, std::atomic<int> (&known)[kMaxDevices][4]) {
-  const int k = cs == 2 ? 1 : cs == 4 ? 2 : 3;
-  int n = known[dev][k].load(std::memory_order_relaxed);
-  if (n) return n - 1;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(cs);
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  known[dev][k].store(n + 1, std::memory_order_relaxed);
-  return n;
-}
-
-template <int FMT, int D, int NT, int WARPS, int STAGES>
-static int launch_ba(echo::BlockAttnParams P, int64_t pairs, int64_t most, int sms, cudaStream_t stream) {
+// One shape of the kernel: WARPS warps with STAGES stages each, CTAS CTAs to an SM.
+template <int FMT, int D, int NT, int WARPS, int STAGES, int CTAS>
+struct BaShape {
   using C = echo::BaCfg<FMT, D, NT, WARPS, STAGES>;
-  static_assert(C::kSmem <= 232448, "block attention: shared memory of one CTA");
-  auto kernel = echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES>;
-  static std::atomic<bool> attr[kMaxDevices];
-  if (int rr = smem_limit_once(attr, kernel, C::kSmem, "block attention smem attribute")) return rr;
-  // A cluster per (b, h), or the line of all chunks cut into equal pieces?  The cluster grows
-  // while it fits the GPU and every warp still gets a chunk.  Clusters cost the longest
-  // context of their waves; cutting costs an equal share plus the second kernel and the piece
-  // borders, about the time of `extra` tokens.  Measured with equal contexts, bf16 / 4-bit: 64
-  // pairs of 1024 tokens 12 / 10 us a CTA each against 14 / 16 cut, 128 pairs of 4096 37 / 23
-  // against 43 / 27, 8 pairs of 8192 43 / 36 against 14 / 12.  The host does not know the
-  // contexts, only how long they may be: past 4 `extra` tokens a CTA, what an uneven batch
-  // would cost is more than clusters save (152 pairs of 16384 to 32768 tokens in 4 bits: 125
-  // us whole, 107 cut).
-  cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
-  static std::atomic<int> known[kMaxDevices][4];
-  int dev = 0, cs = 1;
-  cudaGetDevice(&dev);  // (below kMaxDevices: checked with the attribute above)
-  while (cs < echo::kBaMaxCluster && most > static_cast<int64_t>(cs) * WARPS * C::kTokens &&
-         pairs <= clusters_at_once(kernel, cfg, 2 * cs, dev, known))
-    cs *= 2;
-  const int64_t waves = (pairs * cs + sms - 1) / sms, extra = C::kFp4 ? 1536 : 1024, share = waves * most / cs;
-  const bool whole = share <= pairs * most / sms + extra && share <= 4 * extra;
-  P.cluster = whole ? cs : 0;
-  const unsigned grid = whole ? static_cast<unsigned>(pairs * cs) : static_cast<unsigned>(std::min(sms, echo::kBaMaxGrid));
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3(grid);
-  cfg.attrs = at;
-  if (whole && cs > 1) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cs;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
+  static_assert(C::kSmem <= (CTAS == 1 ? 232448 : 115712), "block attention: shared memory of one CTA");
+
+  static int prepare(int *dev) {
+    static std::atomic<bool> attr[kMaxDevices];
+    cudaGetDevice(dev);
+    return smem_limit_once(attr, echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES, CTAS>, C::kSmem, "block attention smem attribute");
   }
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
-  if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
-  if (whole) return ECHO_OK;
-  cfg.gridDim = dim3(grid, C::kRows);
-  cfg.blockDim = dim3(echo::kBaCombThreads);
-  cfg.dynamicSmemBytes = 0;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows));
-  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block attention merge launch");
+
+  // How many clusters of 2, 4 or 8 CTAs the device holds at once (a cluster sits in one group
+  // of SMs: 76, 36 and 15 here, not 152 SMs' worth: 16 clusters of 8 take 14.4 us where 15
+  // take 8.4).  Asked once per shape and device.
+  static int clusters_at_once(int cs, int dev) {
+    static std::atomic<int> known[kMaxDevices][4];
+    const int k = cs == 2 ? 1 : cs == 4 ? 2 : 3;
+    int n = known[dev][k].load(std::memory_order_relaxed);
+    if (n) return n - 1;
+    cudaLaunchConfig_t cfg = config(cs, nullptr);
+    cudaLaunchAttribute at = cluster(cs);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES, CTAS>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[dev][k].store(n + 1, std::memory_order_relaxed);
+    return n;
+  }
+
+  // P.cluster CTAs per (b, h), or (0) the line cut into a piece per CTA
+  static int launch(echo::BlockAttnParams P, int cs, int64_t pairs, int sms, cudaStream_t stream) {
+    P.cluster = cs;
+    const int64_t grid = cs ? pairs * cs : std::min(sms * CTAS, echo::kBaMaxGrid);
+    cudaLaunchConfig_t cfg = config(grid, stream);
+    cudaLaunchAttribute at = cluster(cs);
+    cfg.attrs = &at;
+    cfg.numAttrs = cs > 1 ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES, CTAS>, P);
+    if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
+    if (cs) return ECHO_OK;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), C::kRows);
+    cfg.blockDim = dim3(echo::kBaCombThreads);
+    cfg.dynamicSmemBytes = 0;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows));
+    return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block attention merge launch");
+  }
+
+ private:
+  static cudaLaunchConfig_t config(int64_t grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    return cfg;
+  }
+  static cudaLaunchAttribute cluster(int cs) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    return at;
+  }
+};
+
+// How the work of a call is laid over the CTAs: a cluster of them per (b, h), one CTA per (b,
+// h) with two to an SM, or the line of all chunks cut into equal pieces.  Costs are counted
+// in the tokens an SM works through.  Whole (b, h) cost their waves times the longest context;
+// cutting costs an equal share, the second kernel (`extra`) and a piece border per (b, h)
+// (`border`: the warps of an SM end together; overlapped by the other SMs where HBM is the
+// bound).  Measured with equal contexts, bf16 / 4-bit, us: 64 pairs of 1024 tokens 12 / 10 a
+// CTA each against 14 / 16 cut; 8 pairs of 8192 43 / 36 a CTA each, 14 / 12 cut, 12 / 12 a
+// cluster of 8 each; 512 pairs of 512 20.7 / 18.6 with two CTAs an SM, 29 / 27 with one, 512
+// pairs of 2048 67 / 39 against 73 / 51 cut.  The host does not know the contexts, only how
+// long they may be: past 4 `extra` tokens a CTA, what an uneven batch would cost is more than
+// whole (b, h) save (152 pairs of 16384 to 32768 tokens in 4 bits: 125 us whole, 103 cut).
+template <class Wide, class Narrow>
+static int ba_go(const echo::BlockAttnParams &P, int64_t pairs, int64_t most, int sms, cudaStream_t stream) {
+  using C = typename Wide::C;
+  constexpr int64_t extra = C::kFp4 ? 1536 : 1024, border = C::kFp4 ? 1000 : 200;
+  const int64_t cut = pairs * most / sms + extra;
+  int dev = 0;
+  if constexpr (!std::is_void<Narrow>::value) {
+    const int64_t waves = (pairs + 2 * sms - 1) / (2 * sms);
+    if (pairs > sms && most <= 4 * extra && 2 * waves * most <= cut + pairs * border / sms) {
+      if (int rr = Narrow::prepare(&dev)) return rr;
+      return Narrow::launch(P, 1, pairs, sms, stream);
+    }
+  }
+  if (int rr = Wide::prepare(&dev)) return rr;
+  // the cluster grows while the device holds them all and every warp still gets a chunk
+  int cs = 1;
+  while (cs < echo::kBaMaxCluster && most > static_cast<int64_t>(cs) * C::kThreads / 32 * C::kTokens &&
+         pairs <= Wide::clusters_at_once(2 * cs, dev))
+    cs *= 2;
+  const int64_t share = (pairs * cs + sms - 1) / sms * most / cs;
+  return Wide::launch(P, share <= cut && share <= 4 * extra ? cs : 0, pairs, sms, stream);
 }
 
 int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stream) {
@@ -1060,17 +1091,21 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   // tokens a context can show at most
   int64_t most = static_cast<int64_t>(P.max_blocks) * a->block_tokens;
   if (!P.sel && P.window && most > P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31) most = P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31;
-  // Warps and stages of the one CTA an SM holds, for 8, 16 and 32 query rows: as many warps
-  // as registers and shared memory allow in multiples of the 4 schedulers (4-bit rows, bound
-  // by instructions: 12 warps of 3 stages 334 us, 16 of 2 318 us, 14 of 2 355 us for 16 x
+  // Warps and stages for 8, 16 and 32 query rows, of one CTA an SM and of one of two: as many
+  // warps as registers and shared memory allow in multiples of the 4 schedulers (4-bit rows,
+  // bound by instructions: 12 warps of 3 stages 334 us, 16 of 2 318 us, 14 of 2 355 us for 16 x
   // 131072 tokens x 8 KV heads), or enough bytes in flight (bf16 rows, bound by HBM).
-#define BA_GO(FMT, D, W1, S1, W2, S2, W4, S4)                                   \
-  (pad == 8    ? launch_ba<FMT, D, 1, W1, S1>(P, pairs, most, sms, stream)      \
-   : pad == 16 ? launch_ba<FMT, D, 2, W2, S2>(P, pairs, most, sms, stream)      \
-               : launch_ba<FMT, D, 4, W4, S4>(P, pairs, most, sms, stream))
+#define BA_SHAPE(FMT, D, NT, W, S, CTAS) BaShape<FMT, D, NT, W, S, CTAS>
+#define BA_GO(FMT, D, W1, S1, V1, T1, W2, S2, V2, T2, W4, S4)                                                                  \
+  (pad == 8    ? ba_go<BA_SHAPE(FMT, D, 1, W1, S1, 1), BA_SHAPE(FMT, D, 1, V1, T1, 2)>(P, pairs, most, sms, stream)            \
+   : pad == 16 ? ba_go<BA_SHAPE(FMT, D, 2, W2, S2, 1), BA_SHAPE(FMT, D, 2, V2, T2, 2)>(P, pairs, most, sms, stream)            \
+               : ba_go<BA_SHAPE(FMT, D, 4, W4, S4, 1), void>(P, pairs, most, sms, stream))
   if (a->format == ECHO_BLOCK_FP4)
-    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 12, 3, 8, 4) : BA_GO(ECHO_BLOCK_FP4, 64, 16, 2, 16, 4, 8, 4);
-  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 7, 3, 7, 3) : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 7, 3, 8, 3);
+    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 8, 2, 12, 3, 6, 3, 8, 4)
+                              : BA_GO(ECHO_BLOCK_FP4, 64, 16, 2, 8, 2, 16, 4, 8, 4, 8, 4);
+  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 4, 3, 7, 3, 4, 2, 7, 3)
+                            : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 4, 3, 7, 3, 4, 2, 8, 3);
+#undef BA_SHAPE
 #undef BA_GO
 }
 

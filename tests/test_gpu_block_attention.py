@@ -357,3 +357,13 @@ def test_thousands_of_requests(cap):
     a = Attn(FP4, 64, 16, 2, 1, 1, [int(x) for x in lens], seed=22, cap=cap)
     echo.echo_block_attention(a.args())
     a.check()
+
+
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("Hq,n_q,window", [(8, 1, 0), (8, 2, 0), (3, 5, 40), (8, 3, 0)])
+def test_many_short_requests(fmt, D, Hq, n_q, window):
+    """More (request, KV head) pairs than SMs: two CTAs to an SM where the rows allow it."""
+    lens = [int(x) for x in np.random.default_rng(Hq + n_q).integers(0, 130, 190)]
+    a = Attn(fmt, D, 16, Hq, 1, n_q, lens, sinks=3 if window else 0, window=window, seed=23)
+    echo.echo_block_attention(a.args())
+    a.check()
