@@ -31,7 +31,8 @@
 //     inside a (b, h) leaves a partial result; a second kernel merges those in order (no
 //     atomics: results do not depend on timing).  When the contexts are short or the
 //     (b, h) pairs fill the GPU, a CTA, or a cluster of up to 8 that merges over distributed
-//     shared memory, takes a whole (b, h) and the second kernel is left out.
+//     shared memory, takes a whole (b, h) and the second kernel is left out; with more pairs
+//     than SMs two smaller CTAs share an SM, one streaming while the other starts or merges.
 //
 // Measured on a GB300 (8 KV heads of 128, 8 query heads each; HBM's measured copy rate is
 // 6.67 TB/s): 16 requests of 16384 to 32768 tokens 236 us in bf16 (6.8 TB/s), 95 us in 4 bits
@@ -1047,9 +1048,12 @@ static int ba_go(const echo::BlockAttnParams &P, int64_t pairs, int64_t most, in
   int dev = 0;
   if constexpr (!std::is_void<Narrow>::value) {
     const int64_t waves = (pairs + 2 * sms - 1) / (2 * sms);
-    if (pairs > sms && most <= 4 * extra && 2 * waves * most <= cut + pairs * border / sms) {
+    const bool whole = most <= 4 * extra && 2 * waves * most <= cut + pairs * border / sms;
+    // (cutting with two CTAs an SM, one computes while the other merges: 512 pairs of 8192 tokens
+    // in 4 bits 109 -> 103 us, 256 of 16384 101 -> 100, but 128 of 131072 318 -> 331)
+    if (pairs > sms && (whole || (C::kFp4 && C::kRows == 8 && most <= 16384))) {
       if (int rr = Narrow::prepare(&dev)) return rr;
-      return Narrow::launch(P, 1, pairs, sms, stream);
+      return Narrow::launch(P, whole ? 1 : 0, pairs, sms, stream);
     }
   }
   if (int rr = Wide::prepare(&dev)) return rr;

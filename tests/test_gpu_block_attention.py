@@ -161,7 +161,7 @@ def test_groups_and_query_tokens(fmt, D, Hq, Hkv, n_q, wide):
 
 
 @pytest.mark.parametrize("fmt", [BF16, FP4])
-@pytest.mark.parametrize("bs", [16, 48, 128])
+@pytest.mark.parametrize("bs", [16, 48, 128, 256])
 @pytest.mark.parametrize("heads", [False, True])
 def test_block_sizes_and_tables_per_head(fmt, bs, heads):
     a = Attn(fmt, 128, bs, 8, 4, 1, [300, 1, 49, 128], heads=heads, seed=bs)
@@ -365,5 +365,16 @@ def test_many_short_requests(fmt, D, Hq, n_q, window):
     """More (request, KV head) pairs than SMs: two CTAs to an SM where the rows allow it."""
     lens = [int(x) for x in np.random.default_rng(Hq + n_q).integers(0, 130, 190)]
     a = Attn(fmt, D, 16, Hq, 1, n_q, lens, sinks=3 if window else 0, window=window, seed=23)
+    echo.echo_block_attention(a.args())
+    a.check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_contexts_cut_with_two_ctas_an_sm(D):
+    """More pairs than SMs whose tables may hold 16384 tokens each: 4-bit rows, cut into twice
+    as many pieces as SMs."""
+    lens = [int(x) for x in np.random.default_rng(31).integers(0, 200, 160)]
+    lens[7], lens[100] = 2100, 0
+    a = Attn(FP4, D, 16, 8, 1, 1, lens, seed=32, cap=16384 // 16)
     echo.echo_block_attention(a.args())
     a.check()
