@@ -14,7 +14,7 @@
 // (the shrinking request's table), never from the stack the same launch is writing.
 // Bound by latency: 64 decoding requests 4.1 us (one CTA: lengths, sums, search, id, store, an
 // entry per thread; four entries in a row per thread took 7.4 us), 256 requests in a mixed
-// step with a list of 2^20 entries 8.4 us (8 MB of stores would take 1.3 us; the search and
+// step with a list of 2^20 entries 8.2 us (8 MB of stores would take 1.3 us; the search and
 // the divisions of 608 CTAs are most of it).
 #include "echo_common.cuh"
 
@@ -24,7 +24,7 @@ constexpr int kTabThreads = 256;
 
 struct TablesParams {
   const int32_t *old_len, *new_len;
-  int32_t B, bs;
+  int32_t B, bs, shift;  // shift: log2 of bs, or -1
   int32_t *table;
   int32_t *free_blocks;
   int32_t max_blocks, n_blocks;
@@ -34,6 +34,15 @@ struct TablesParams {
   int32_t max_new;
   int32_t *status;
 };
+
+// block of position p, blocks of n tokens (a shift for a power of two: the divisions were a
+// quarter of the kernel's instructions)
+__device__ __forceinline__ int block_of(const TablesParams &P, uint32_t p) {
+  return static_cast<int>(P.shift >= 0 ? p >> P.shift : p / static_cast<uint32_t>(P.bs));
+}
+__device__ __forceinline__ int blocks_of(const TablesParams &P, int n) {
+  return block_of(P, static_cast<uint32_t>(n) + static_cast<uint32_t>(P.bs) - 1);
+}
 
 // the largest i in [0, n) with cu[i] <= x (cu ascending, cu[0] <= x): the owner of entry x
 // of a list whose exclusive sums are cu
@@ -65,7 +74,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
     const int o0 = P.old_len[b], w0 = P.new_len[b];
     const int o = min(max(o0, 0), cap), w = min(max(w0, 0), cap);
     bad |= (o != o0) | (w != w0);
-    const int no = (o + P.bs - 1) / P.bs, nw = (w + P.bs - 1) / P.bs;
+    const int no = blocks_of(P, o), nw = blocks_of(P, w);
     cuN[b] = n, cuA[b] = a, cuF[b] = f;  // sums within the thread's run for now
     n += max(w - o, 0), a += max(nw - no, 0), f += max(no - nw, 0);
   }
@@ -97,7 +106,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
     if (s < count) return P.free_blocks[s];
     const int j = s - count, b = owner_of(cuF, P.B, j);
     const int w = min(max(P.new_len[b], 0), cap);
-    return P.table[static_cast<size_t>(b) * P.max_blocks + (w + P.bs - 1) / P.bs + (j - cuF[b])];
+    return P.table[static_cast<size_t>(b) * P.max_blocks + blocks_of(P, w) + (j - cuF[b])];
   };
   auto grown = [&](int j) -> int32_t {  // the j-th block handed out
     const int32_t id = stack_at(top - 1 - j);
@@ -113,8 +122,8 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
   auto entry = [&](int i, int b, int32_t &slot, int32_t &pos) {
     slot = pos = -1;
     if (cuA[b + 1] != cuA[b] && cuA[b + 1] > top) return;  // left without its blocks
-    const int o = min(max(P.old_len[b], 0), cap), nbo = (o + P.bs - 1) / P.bs;
-    const int p = o + (i - cuN[b]), k = p / P.bs;
+    const int o = min(max(P.old_len[b], 0), cap), nbo = blocks_of(P, o);
+    const int p = o + (i - cuN[b]), k = block_of(P, p);
     const int32_t id = k < nbo ? P.table[static_cast<size_t>(b) * P.max_blocks + k] : stack_at(top - 1 - (cuA[b] + k - nbo));
     if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(P.n_blocks)) bad = 1;
     else slot = id * P.bs + (p - k * P.bs), pos = p;
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
         int b = owner_of(cuN, P.B, i);
         entry(i, b, slot[0], pos[0]);
         // entries that follow it in its block
-        const int same = slot[0] >= 0 ? min(P.bs - 1 - pos[0] % P.bs, cuN[b + 1] - 1 - i) : 0;
+        const int same = slot[0] >= 0 ? min(P.bs - 1 - (pos[0] - block_of(P, pos[0]) * P.bs), cuN[b + 1] - 1 - i) : 0;
 #pragma unroll
         for (int u = 1; u < 4; ++u) {
           if (i + u >= listed) continue;
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
     const int o = min(max(P.old_len[b], 0), cap);
     const int32_t id = grown(j);
     bad |= id < 0;
-    P.table[static_cast<size_t>(b) * P.max_blocks + (o + P.bs - 1) / P.bs + (j - cuA[b])] = id;
+    P.table[static_cast<size_t>(b) * P.max_blocks + blocks_of(P, o) + (j - cuA[b])] = id;
   }
   for (int j = rt; j < tf; j += gthreads) {
     const int32_t id = stack_at(count + j);
@@ -200,6 +209,9 @@ int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream) {
   P.new_len = a->new_len;
   P.B = a->B;
   P.bs = a->block_tokens;
+  P.shift = -1;
+  for (int k = 0; k < 31; ++k)
+    if (a->block_tokens == 1 << k) P.shift = k;
   P.table = a->table;
   P.free_blocks = a->free_blocks;
   P.max_blocks = a->max_blocks;
