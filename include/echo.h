@@ -447,6 +447,8 @@ int echo_sparse_mla_decode(const echo_mla_args *args, void *stream);
  *     nearest code to x / s (ties to the even code): 4.5 bits per entry.  Values above
  *     2688 saturate, infinities and NaN are not kept, and a zero may carry either sign.
  * With a table shared by the KV heads, block `id` of KV head h is row id * n_kv_heads + h.
+ * The kernels of the block calls are programmatic launches: they may be made ready while the
+ * kernel before them on the stream still runs, and touch no memory until it has completed.
  */
 #define ECHO_BLOCK_BF16 0
 #define ECHO_BLOCK_FP4 1

@@ -35,10 +35,10 @@
 //     than SMs two smaller CTAs share an SM, one streaming while the other starts or merges.
 //
 // Measured on a GB300 (8 KV heads of 128, 8 query heads each; HBM's measured copy rate is
-// 6.67 TB/s): 16 requests of 16384 to 32768 tokens 236 us in bf16 (6.8 TB/s), 95 us in 4 bits
-// (4.7 TB/s); of up to 131072 tokens 314 us in 4 bits (6.0 TB/s), 427 us with two query
-// tokens; a window of 4096 and 4 sinks of 64 requests 165 us in bf16 (6.5 TB/s); one request
-// of 1000 tokens 8 us.  bf16 is bound by HBM.  4-bit rows are bound by instructions, above
+// 6.67 TB/s): 16 requests of 16384 to 32768 tokens 236 us in bf16 (6.8 TB/s), 94 us in 4 bits
+// (4.8 TB/s); of up to 131072 tokens 314 us in 4 bits (6.0 TB/s), 423 us with two query
+// tokens; a window of 4096 and 4 sinks of 64 requests 164 us in bf16 (6.6 TB/s); one request
+// of 1000 tokens 6 us.  bf16 is bound by HBM.  4-bit rows are bound by instructions, above
 // all the conversions: some 600 per warp and 32 tokens, the integer pipe 64% and the issue
 // slots 66% busy (without the scales' multiplies 277 us instead of 318); with two query
 // tokens the registers leave 12 warps instead of 16 and the matrix pipe is 42% busy.  Short
@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   SubEntry *list = reinterpret_cast<SubEntry *>(ba_smem + C::kOffList) + warp * kBaList;
   float2 *fin = reinterpret_cast<float2 *>(ba_smem + C::kOffFin);     // [kRows]
   const int heads = P.n_kv * P.mgroups;
-  pdl_launch_dependents();  // (the merge waits for this grid's end all the same)
+  pdl_launch_dependents();  // (what follows waits for this grid's end all the same)
+  pdl_wait();
 
   // ===== this CTA's range of the line: chunks 0 .. n_chunks from its first =====
   LinePos cur;
@@ -895,6 +896,7 @@ __global__ void __launch_bounds__(kBaCombThreads) block_attn_combine_kernel(cons
   __shared__ float2 sml[kGroups];
   __shared__ __align__(16) float so[kGroups][D];
   const int cta = blockIdx.x, row = blockIdx.y, grp = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
+  pdl_launch_dependents();
   pdl_wait();
   // piece 0 is CTA i's second slot, piece s > 0 the first slot of CTA i + s
   auto slot_row = [&](int s) {
@@ -995,17 +997,15 @@ struct BaShape {
     P.cluster = cs;
     const int64_t grid = cs ? pairs * cs : std::min(sms * CTAS, echo::kBaMaxGrid);
     cudaLaunchConfig_t cfg = config(grid, stream);
-    cudaLaunchAttribute at = cluster(cs);
-    cfg.attrs = &at;
-    cfg.numAttrs = cs > 1 ? 1 : 0;
+    cudaLaunchAttribute at[2] = {pdl(), cluster(cs)};
+    cfg.attrs = at;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES, CTAS>, P);
     if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
     if (cs) return ECHO_OK;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), C::kRows);
     cfg.blockDim = dim3(echo::kBaCombThreads);
     cfg.dynamicSmemBytes = 0;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows));
     return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block attention merge launch");
@@ -1019,6 +1019,12 @@ struct BaShape {
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     return cfg;
+  }
+  static cudaLaunchAttribute pdl() {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return at;
   }
   static cudaLaunchAttribute cluster(int cs) {
     cudaLaunchAttribute at{};

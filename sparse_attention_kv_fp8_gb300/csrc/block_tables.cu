@@ -12,9 +12,9 @@
 // sums stay in shared memory) and then takes its share of the blocks and of the list, so
 // no CTA waits for another.  A stack entry at or above `count` is read where it comes from
 // (the shrinking request's table), never from the stack the same launch is writing.
-// Bound by latency: 64 decoding requests 4.1 us (one CTA: lengths, sums, search, id, store, an
-// entry per thread; four entries in a row per thread took 7.4 us), 256 requests in a mixed
-// step with a list of 2^20 entries 8.2 us (8 MB of stores would take 1.3 us; the search and
+// Bound by latency: 64 decoding requests 2.7 us (one CTA: lengths, sums, search, id, store, an
+// entry per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed
+// step with a list of 2^20 entries 8.3 us (8 MB of stores would take 1.3 us; the search and
 // the divisions of 608 CTAs are most of it).
 #include "echo_common.cuh"
 
@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
   int32_t *cuN = tab_smem, *cuA = cuN + P.B + 1, *cuF = cuA + P.B + 1;
   __shared__ int32_t warp_sum[3][kTabThreads / 32];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
   const int cap = P.max_blocks * P.bs;
   const int count0 = *P.free_count;
   const int count = min(max(count0, 0), P.n_blocks);
@@ -232,8 +234,7 @@ int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream) {
   // an entry per thread while that fits the GPU (four CTAs per SM), then four and more each
   const int want = a->max_new / echo::kTabThreads + (a->max_new % echo::kTabThreads != 0);
   const int grid = want < 1 ? 1 : want > 608 ? 608 : want;
-  echo::block_tables_kernel<<<grid, echo::kTabThreads, smem, stream>>>(P);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(echo::block_tables_kernel, dim3(grid), dim3(echo::kTabThreads), smem, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block tables launch");
 }
 

@@ -7,10 +7,10 @@
 // results are stored; the mean is a shuffle sum over those lanes.  A warp takes `span` heads
 // of one kind (q, k or v) of its tokens, kBatch at a time with the next batch's loads in
 // flight; cosines, sines and weights are read and multiplied once for them.  Bound by HBM:
-// 16384 tokens x (64 + 8 + 8) heads of 128 in 119 us, 5.7 TB/s of the 6.67 TB/s that a copy
-// reaches here (0.86; 8-byte accesses and 32 warps an SM: with one 16-byte load per lane, the
+// 16384 tokens x (64 + 8 + 8) heads of 128 in 117 us, 5.8 TB/s of the 6.67 TB/s that a copy
+// reaches here (0.87; 8-byte accesses and 32 warps an SM: with one 16-byte load per lane, the
 // partners shuffled between lanes and 16 warps it was 180 us); 8191 tokens x 40 heads of 64
-// into a 4-bit cache 22.6 us (0.60; launch and tail), a decode step's tokens 4 us (latency).
+// into a 4-bit cache 20.6 us (0.66; first loads and tail), a decode step's tokens 3 us (latency).
 #include "block_rows.cuh"
 
 namespace echo {
@@ -343,6 +343,8 @@ template <int D, int kBatch, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const RopeParams P) {
   constexpr int kLanes = D / 8;          // lanes of a head
   constexpr int kTokens = 32 / kLanes;   // tokens of a warp
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
   const int64_t tb = wid / P.chunks;
   const int chunk = static_cast<int>(wid - tb * P.chunks);
@@ -382,8 +384,8 @@ static cudaError_t launch_rope(echo::RopeParams P, bool values, int span, int kv
   constexpr int kTokens = 256 / D;
   const int64_t warps = (static_cast<int64_t>(P.T) + kTokens - 1) / kTokens * P.chunks;
   const int64_t grid = (warps * 32 + echo::kRopeThreads - 1) / echo::kRopeThreads;
-  echo::qk_norm_rope_kernel<D, kBatch, kInter><<<static_cast<unsigned>(grid), echo::kRopeThreads, 0, stream>>>(P);
-  return cudaGetLastError();
+  return launch_pdl(echo::qk_norm_rope_kernel<D, kBatch, kInter>, dim3(static_cast<unsigned>(grid)), dim3(echo::kRopeThreads),
+                    0, stream, P);
 }
 
 // How many heads a warp takes (q, then k or v), and how many of them at a time.  Few heads in

@@ -157,3 +157,77 @@ def test_attention_over_the_rows_a_block_recall_made_resident(fmt):
                 far, far_lse = ref.attention_bounds(fmt, D, np.full(G, len(tok)), *r)
                 assert (np.abs(got[b, 0, h * G:(h + 1) * G] - r[0]) <= far).all()
                 assert (np.abs(got_lse[b, 0, h * G:(h + 1) * G] - r[1]) <= far_lse).all()
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP4])
+def test_a_captured_decode_step(fmt):
+    """Tables, norm + rotation and attention of a decode step captured once into a graph and
+    replayed over static buffers: lengths, projections and the stack's height change between
+    replays, one request pauses, one ends and starts again."""
+    B, n_blocks, mb = 3, 24, 10
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    old, new, table, count, count_out, slot, pos = z(B), z(B), z(B, mb) - 1, z(1) + n_blocks, z(1), z(B), z(B)
+    free = torch.arange(n_blocks, dtype=torch.int32, device="cuda")
+    status, cs = z(1), echo.rope_table(512, RD)
+    x = torch.zeros(B, (Hq + 2 * Hk) * D, dtype=torch.bfloat16, device="cuda")
+    cut = lambda a, n: x[:, a * D:(a + n) * D].unflatten(1, (n, D))
+    e = lambda *n: torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    q, k, v, out, lse = e(B, Hq, D), e(B, Hk, D), e(B, Hk, D), e(B, 1, Hq, D), torch.zeros(B, 1, Hq, device="cuda")
+    rows = torch.full((n_blocks * Hk, echo.block_row_elems(fmt, BS, D)), -1, dtype=torch.int16, device="cuda")
+    # the list of new tokens is not the list of requests (a paused one has none): the graph
+    # attends with each request's newest query, gathered by cu_new
+    cu, qa = z(B + 1), e(B, 1, Hq, D)
+    tables = echo.make_block_tables_args(old, new, BS, table, free, count, count_out, slot, pos, cu, dev_status=status)
+    rope = echo.make_qk_norm_rope_args(cut(0, Hq), cut(Hq, Hk), cut(Hq + Hk, Hk), pos, cs, q, slot_map=slot, rows=rows,
+                                       fmt=fmt, block_tokens=BS, k_out=k, v_out=v, dev_status=status)
+    attn = echo.make_block_attention_args(qa, rows, table, new, Hk, D ** -0.5, out, lse,
+                                          echo.BlockAttentionWorkspace(Hq // Hk, D), fmt=fmt, block_tokens=BS,
+                                          dev_status=status)
+
+    def step():
+        echo.echo_block_tables(tables)
+        echo.echo_qk_norm_rope(rope)
+        qa.copy_(q.index_select(0, cu[:B].clamp(max=B - 1).long()).unsqueeze(1))
+        echo.echo_block_attention(attn)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    kv, lens = [[] for _ in range(B)], np.zeros(B, np.int32)
+    for t in range(40):
+        nxt = lens + 1
+        if t % 5 == 3:
+            nxt[1] = lens[1]                    # paused
+        if t == 20:
+            nxt[2] = 0                          # ended: its blocks return
+        old.copy_(dev(lens)), new.copy_(dev(nxt))
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        graph.replay()
+        count.copy_(count_out)
+        kc, vc, qn = (a.double().cpu().numpy() for a in (k, v, qa))
+        i = 0
+        for b in range(B):
+            if nxt[b] == 0:
+                kv[b] = []
+            elif nxt[b] > lens[b]:
+                kv[b].append((kc[i], vc[i]))
+                i += 1
+        lens = nxt
+        used = int((-(-lens // BS)).sum())
+        assert int(count) == n_blocks - used and int(status) == 0
+        got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for b in range(B):
+            for h in range(Hk):
+                hs = slice(h * (Hq // Hk), (h + 1) * (Hq // Hk))
+                kk = np.array([c[0][h] for c in kv[b]]).reshape(-1, D)
+                vv = np.array([c[1][h] for c in kv[b]]).reshape(-1, D)
+                r = ref.attention(qn[b, 0, hs], [(kk, vv)] * (Hq // Hk), D ** -0.5)
+                far, far_lse = ref.attention_bounds(fmt, D, np.full(Hq // Hk, len(kk)), *r)
+                assert (np.abs(got[b, 0, hs] - r[0]) <= far).all(), (t, b)
+                if len(kk):
+                    assert (np.abs(got_lse[b, 0, hs] - r[1]) <= far_lse).all()
+                else:
+                    assert (got_lse[b, 0, hs] == -np.inf).all()
