@@ -1,5 +1,5 @@
 // block_rows.cuh -- the block-row layouts of include/echo.h (one block of tokens of one
-// KV head per row) and the conversions of their 4-bit entries.
+// KV head per row), the conversions of their 4-bit entries, and the launch that the block calls share.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -74,3 +74,25 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 }  // namespace echo
+
+namespace echo_host {
+
+// Launch that may be made ready while the kernel before it on the stream still runs (programmatic
+// stream serialization): for kernels that call pdl_wait() before they touch any memory.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              Args &&...args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace echo_host

@@ -16,7 +16,7 @@
 // entry per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed
 // step with a list of 2^20 entries 8.3 us (8 MB of stores would take 1.3 us; the search and
 // the divisions of 608 CTAs are most of it).
-#include "echo_common.cuh"
+#include "block_rows.cuh"
 
 namespace echo {
 

@@ -389,24 +389,6 @@ namespace echo_host {
 void set_error(const char *fmt, ...);
 int cuda_fail(cudaError_t e, const char *what);
 
-// Launch that may be made ready while the kernel before it on the stream still runs (programmatic
-// stream serialization): for kernels that call pdl_wait() before they touch any memory.
-template <typename... Params, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                              Args &&...args) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-}
-
 // Devices a process may use with the library (per-device caches are this long).
 constexpr int kMaxDevices = 64;
 
