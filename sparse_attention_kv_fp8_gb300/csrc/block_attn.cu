@@ -237,7 +237,7 @@ __device__ __forceinline__ void seek(const BlockAttnParams &P, LinePos &L, int g
       ++L.b;
       L.hm = 0;
       L.start = L.end;
-      L.v = req_view(P, __ldg(P.ctx_len + L.b));
+      L.v = req_view(P, P.ctx_len[L.b]);
     } else {
       L.start = L.end;
       L.end = 0x7fffffff;
@@ -266,8 +266,8 @@ __device__ __forceinline__ SubEntry sub_entry(const BlockAttnParams &P, const Li
   if (s >= L.v.n_first) s += L.v.skip;
   const int h = L.hm / P.mgroups, e = s / P.bsub, in = s - e * P.bsub;
   const int64_t at = (static_cast<int64_t>(L.b) * P.table_heads + (P.table_heads > 1 ? h : 0)) * P.max_blocks + e;
-  const int32_t id = __ldg(P.table + at);
-  const int32_t lb = P.sel ? __ldg(P.sel + at) : e;
+  const int32_t id = P.table[at];
+  const int32_t lb = P.sel ? P.sel[at] : e;
   // (a selected block past the 31-bit positions cannot be below any length)
   if (id < 0 || lb < 0 || static_cast<int64_t>(lb) * P.bsub + in >= kBaNowhere / kSubTokens) return x;
   const int64_t row = P.table_heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     const int pair = blockIdx.x / P.cluster, rank = blockIdx.x - pair * P.cluster;
     cur.b = pair / heads;
     cur.hm = pair - cur.b * heads;
-    const int ctx = __ldg(P.ctx_len + cur.b);
+    const int ctx = P.ctx_len[cur.b];
     cur.v = req_view(P, ctx);
     const int n = chunks_of<C::kSubs>(cur.v);
     const int first = static_cast<int>(static_cast<int64_t>(n) * rank / P.cluster);
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     const int b0 = min(lane * per_l, P.B), b1 = min(b0 + per_l, P.B);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const int ctx = __ldg(P.ctx_len + b);
+      const int ctx = P.ctx_len[b];
       mine += chunks_of<C::kSubs>(req_view(P, ctx));
       if (blockIdx.x == 0 && warp == 0) check_context(P, ctx);
     }
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     per = per < WARPS ? WARPS : per;
     // requests with nothing to see are not on the line: their outputs are written here
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-      if (req_view(P, __ldg(P.ctx_len + b)).nsub > 0) continue;
+      if (req_view(P, P.ctx_len[b]).nsub > 0) continue;
       const int64_t o0 = static_cast<int64_t>(b) * P.n_q * P.n_heads;
       for (int i = threadIdx.x; i < P.n_q * P.n_heads * (D / 8); i += C::kThreads)
         reinterpret_cast<uint4 *>(P.out + o0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
       int64_t at = upto - mine;
       int n = 1;
       for (own_b = b0; own_b < b1; ++own_b) {
-        n = chunks_of<C::kSubs>(req_view(P, __ldg(P.ctx_len + own_b)));
+        n = chunks_of<C::kSubs>(req_view(P, P.ctx_len[own_b]));
         if (g0 < at + static_cast<int64_t>(n) * heads) break;
         at += static_cast<int64_t>(n) * heads;
       }
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     cur.b = __shfl_sync(~0u, own_b, src);
     cur.hm = __shfl_sync(~0u, own_hm, src);
     cur.start = __shfl_sync(~0u, own_start, src);
-    cur.v = req_view(P, __ldg(P.ctx_len + cur.b));
+    cur.v = req_view(P, P.ctx_len[cur.b]);
     cur.end = cur.start + chunks_of<C::kSubs>(cur.v);
     if (threadIdx.x == C::kThreads - 1) {
       // where the range's last (b, hm) goes on, and whether it began here

@@ -79,6 +79,8 @@ namespace echo_host {
 
 // Launch that may be made ready while the kernel before it on the stream still runs (programmatic
 // stream serialization): for kernels that call pdl_wait() before they touch any memory.
+// Their loads are plain ones: the non-coherent path (__ldg) is for data that nothing writes while
+// the kernel is there, and the kernel before it, still running then, may write any input.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                               Args &&...args) {

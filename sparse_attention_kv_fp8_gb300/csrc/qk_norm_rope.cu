@@ -170,7 +170,7 @@ __device__ __forceinline__ void rope_pairs(const RopeParams &P, const RopeDst &W
     }
   }
   if (wt) {
-    const float4 wa = __ldg(reinterpret_cast<const float4 *>(wt + ua)), wb = __ldg(reinterpret_cast<const float4 *>(wt + ub));
+    const float4 wa = *reinterpret_cast<const float4 *>(wt + ua), wb = *reinterpret_cast<const float4 *>(wt + ub);
     const float a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) ca[i] *= a[i], cb[i] *= b[i], sa[i] *= a[i], sb[i] *= b[i];
@@ -255,7 +255,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams &P, const RopeDst &W,
   for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
   if (!is_v) {
     auto four = [](const float *p, float *to) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+      const float4 v = *reinterpret_cast<const float4 *>(p);
       to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
     };
     if (W.in && rot) {
@@ -352,14 +352,14 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const Rop
   const int64_t tok = tb * kTokens + lane / kLanes;
   if (tb * kTokens >= P.T) return;       // (the whole warp)
   const int64_t t = min(tok, static_cast<int64_t>(P.T) - 1);
-  const int pos = __ldg(P.positions + t);
+  const int pos = P.positions[t];
   const bool in = tok < P.T && pos >= 0 && pos < P.max_pos;
   if (tok < P.T && pos >= P.max_pos && l == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
 
   const int kind = chunk < P.q_chunks ? kRopeQ : chunk < P.q_chunks + P.k_chunks ? kRopeK : kRopeV;
   const int h0 = kind == kRopeQ ? chunk * P.span : (chunk - P.q_chunks) % P.k_chunks * P.kv_span;
   const int h1 = kind == kRopeQ ? min(h0 + P.span, P.n_heads) : min(h0 + P.kv_span, P.n_kv_heads);
-  const int slot = P.slot_map && kind != kRopeQ ? __ldg(P.slot_map + t) : -1;
+  const int slot = P.slot_map && kind != kRopeQ ? P.slot_map[t] : -1;
   const int blk = slot >= 0 ? slot / P.bs : -1;
   const RopeDst W{P, t, blk, slot - blk * P.bs, in};
   if (kind == kRopeQ || (kind == kRopeK && P.format == ECHO_BLOCK_BF16))
