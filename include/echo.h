@@ -481,7 +481,8 @@ int echo_block_row_elems(int32_t format, int32_t block_tokens, int32_t head_dim,
  * outside [0, n_blocks) are not handed out; each sets ECHO_DEV_BAD_INDEX.  All buffers but
  * `table` and `free_blocks` are read-only or write-only, so a call repeated on the same
  * inputs gives the same outputs.  Limits: B <= 16384, B * max_blocks * block_tokens and
- * n_blocks * block_tokens below 2^31.  Launches 1 kernel.
+ * n_blocks * block_tokens below 2^31, B * max_blocks and n_blocks below 2^30.  Launches 1
+ * kernel.
  */
 typedef struct echo_block_tables_args {
     const int32_t *old_len;

@@ -414,6 +414,9 @@ int echo_block_tables(const echo_block_tables_args *a, void *stream) {
   REQUIRE(static_cast<long long>(a->max_blocks) * a->block_tokens <= ((1ll << 31) - 1) / (a->B > 0 ? a->B : 1),
           "B * max_blocks * block_tokens must be below 2^31");
   REQUIRE(static_cast<long long>(a->n_blocks) * a->block_tokens <= (1ll << 31) - 1, "n_blocks * block_tokens must be below 2^31");
+  // (counts of blocks, a stack's height plus what returns to it among them, stay within 31 bits)
+  REQUIRE(static_cast<long long>(a->B) * a->max_blocks < (1ll << 30) && a->n_blocks < (1 << 30),
+          "B * max_blocks and n_blocks must be below 2^30");
   REQUIRE(a->free_count && a->free_count_out && a->free_blocks, "block tables pointer is NULL");
   REQUIRE(a->B == 0 || (a->old_len && a->new_len && a->table), "block tables pointer is NULL");
   REQUIRE(a->max_new == 0 || a->slot_map, "slot_map is NULL");

@@ -63,7 +63,8 @@ def tables_args(**kw):
     (dict(n_blocks=1 << 26, block_tokens=64), b"below 2^31"), (dict(free_count=None), b"NULL"),
     (dict(free_blocks=None), b"NULL"), (dict(old_len=None), b"NULL"), (dict(table=None), b"NULL"),
     (dict(slot_map=None), b"slot_map"), (dict(free_count_out=80), b"different"), (dict(len_out=16), b"len_out"),
-    (dict(len_out=32), b"len_out"),
+    (dict(len_out=32), b"len_out"), (dict(B=1024, max_blocks=1 << 20, block_tokens=1), b"below 2^30"),
+    (dict(n_blocks=1 << 30, block_tokens=1), b"below 2^30"),
 ])
 def test_block_tables_refusals(lib, bad, why):
     assert lib.echo_block_tables(ctypes.byref(tables_args(**bad)), None) == echo.ECHO_EINVAL
