@@ -520,7 +520,8 @@ int echo_block_tables(const echo_block_tables_args *args, void *stream);
  *   interleaved  0: pairs are (i, i + rope_dim / 2); 1: (2i, 2i + 1)
  *   positions  [T] int32 device; a negative one marks a padding token: it is left out
  *      altogether; one >= max_pos is left out with ECHO_DEV_BAD_INDEX
- *   q_out    [T][n_heads][head_dim] bf16 (may be q itself when q is contiguous)
+ *   q_out    [T][n_heads][head_dim] bf16 (q_out, k_out and v_out may be q, k and v themselves
+ *      when those are contiguous)
  *   k_out, v_out [T][n_kv_heads][head_dim] bf16, optional: the keys and values as a later
  *      read of the cache gives them (ECHO_BLOCK_FP4: after quantisation)
  *   slot_map [T] int32 device, optional (NULL: no cache write): token i goes to token

@@ -612,6 +612,7 @@ def make_block_attention_args(q, rows, table, ctx_len, n_kv_heads: int, scale: f
     a.sinks, a.window, a.scale = int(sinks), int(window), float(scale)
     a.out = _typed(out, "out", _BF16, (B, n_q, H, D))
     a.lse = _typed(lse, "lse", _F32, (B, n_q, H))
+    _typed(ws.buf, "workspace", (torch.uint8,))
     a.workspace, a.workspace_bytes = ws.base, ws.bytes
     a.dev_status = _typed(dev_status, "dev_status", _INT)
     a._keep = (q, rows, table, ctx_len, out, lse, ws, sel, dev_status)

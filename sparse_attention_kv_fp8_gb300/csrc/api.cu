@@ -446,6 +446,10 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *a, void *stream) {
           "q, k, v, the weights, cos_sin and the outputs must be 16-byte aligned");
   REQUIRE(a->q_stride % 8 == 0 && a->k_stride % 8 == 0 && (!a->v || a->v_stride % 8 == 0), "token strides must be multiples of 8");
   REQUIRE(a->v || (!a->slot_map && !a->v_out), "v is NULL, but a cache or v_out takes it");
+  const int64_t q_row = static_cast<int64_t>(a->n_heads) * a->head_dim, k_row = static_cast<int64_t>(a->n_kv_heads) * a->head_dim;
+  REQUIRE(a->T == 1 || ((a->q_out != a->q || a->q_stride == q_row) && (a->k_out != a->k || a->k_stride == k_row) &&
+                        (!a->v || a->v_out != a->v || a->v_stride == k_row)),
+          "in place, the tokens of q, k and v must lie one after another");
   if (a->slot_map) {
     REQUIRE(a->rows && a->n_rows >= 1, "slot_map given without rows");
     REQUIRE(aligned(a->rows, 16), "rows must be 16-byte aligned");
@@ -481,6 +485,7 @@ int echo_block_attention(const echo_block_attention_args *a, void *stream) {
   if (a->B == 0) return ECHO_OK;
   REQUIRE(a->q && a->rows && a->table && a->ctx_len && a->out && a->workspace, "block attention pointer is NULL");
   REQUIRE(aligned(a->q, 16) && aligned(a->rows, 16) && aligned(a->out, 16), "q, rows and out must be 16-byte aligned");
+  REQUIRE(a->out != a->q, "out must not be q");
   REQUIRE(aligned(a->workspace, 256), "workspace must be 256-byte aligned");
   REQUIRE(a->workspace_bytes >= block_attention_workspace_bytes(a->n_q * (a->n_heads / a->n_kv_heads), a->head_dim),
           "workspace smaller than echo_block_attention_workspace_bytes()");

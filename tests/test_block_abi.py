@@ -90,6 +90,8 @@ def rope_args(**kw):
     (dict(block_tokens=20), b"block_tokens"), (dict(q=None), b"NULL"), (dict(positions=None), b"NULL"),
     (dict(cos_sin=None), b"NULL"), (dict(q_out=None), b"NULL"), (dict(q=18), b"16-byte"), (dict(cos_sin=68), b"16-byte"),
     (dict(k_out=8), b"16-byte"), (dict(q_stride=2052), b"multiples of 8"), (dict(v_stride=1), b"multiples of 8"),
+    (dict(q_out=16, q_stride=2056), b"one after another"), (dict(k_out=32, k_stride=2048), b"one after another"),
+    (dict(v_out=48, v_stride=2048), b"one after another"),
     (dict(v=None), b"v is NULL"), (dict(), b"without rows"), (dict(rows=8), b"16-byte"), (dict(rows=16, n_rows=0), b"without rows"),
 ])
 def test_qk_norm_rope_refusals(lib, bad, why):
@@ -115,7 +117,7 @@ def attn_args(**kw):
     (dict(window=-4), b"sinks"), (dict(n_rows=0), b"n_rows"), (dict(scale=float("inf")), b"finite"),
     (dict(q=None), b"NULL"), (dict(rows=None), b"NULL"), (dict(table=None), b"NULL"), (dict(out=None), b"NULL"),
     (dict(workspace=None), b"NULL"), (dict(q=24), b"16-byte"), (dict(rows=8), b"16-byte"), (dict(workspace=128), b"256-byte"),
-    (dict(workspace_bytes=100), b"smaller"), (dict(B=1 << 30), b"too large"),
+    (dict(workspace_bytes=100), b"smaller"), (dict(out=16), b"out must not"), (dict(B=1 << 30), b"too large"),
 ])
 def test_block_attention_refusals(lib, bad, why):
     assert lib.echo_block_attention(ctypes.byref(attn_args(**bad)), None) == echo.ECHO_EINVAL

@@ -378,3 +378,14 @@ def test_many_contexts_cut_with_two_ctas_an_sm(D):
     a = Attn(FP4, D, 16, 8, 1, 1, lens, seed=32, cap=16384 // 16)
     echo.echo_block_attention(a.args())
     a.check()
+
+
+def test_refused_workspaces_and_outputs():
+    a = Attn(BF16, 128, 64, 8, 2, 1, [3])
+    with pytest.raises(echo.EchoError, match="workspace"):
+        a.args(ws=echo.BlockAttentionWorkspace(4, 128, device="cpu"))
+    with pytest.raises(echo.EchoError, match="smaller"):
+        echo.echo_block_attention(echo.make_block_attention_args(
+            a.q.repeat(1, 4, 1, 1), a.rows, a.t, a.ctx, 2, 0.1, a.out.repeat(1, 4, 1, 1), None, a.ws))
+    with pytest.raises(echo.EchoError, match="out must not"):
+        echo.echo_block_attention(a.args(out=a.q))

@@ -173,6 +173,22 @@ def test_no_cache_no_values_and_in_place_queries():
 
 
 @pytest.mark.parametrize("fmt", [BF16, FP4])
+@pytest.mark.parametrize("T,inter", [(5, True), (301, False), (14000, False)])
+def test_queries_keys_and_values_in_place(T, inter, fmt):
+    r = Rope(T, 16, 4, 128, 64, inter, fmt, 32, fused=False)
+    echo.echo_qk_norm_rope(r.args())
+    rows = r.rows.clone()
+    r.rows.copy_(dev(r.rows_np.view(np.int16)))
+    a = echo.make_qk_norm_rope_args(r.q, r.k, r.v, r.pos, r.cs, r.q, r.wq, r.wk, 1e-5, inter, r.slot, r.rows, fmt, 32,
+                                    k_out=r.k, v_out=r.v, dev_status=r.status)
+    echo.echo_qk_norm_rope(a)
+    torch.cuda.synchronize()
+    for got, want in ((r.q, r.qo), (r.k, r.ko), (r.v, r.vo), (r.rows, rows)):
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert int(r.status) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP4])
 def test_rows_in_the_pinned_host_pool(fmt):
     r = Rope(60, 4, 2, 128, 128, False, fmt, 64, seed=6, host=True)
     echo.echo_qk_norm_rope(r.args())
