@@ -14,7 +14,7 @@
 // (the shrinking request's table), never from the stack the same launch is writing.
 // Bound by latency: 64 decoding requests 2.7 us (one CTA: lengths, sums, search, id, store, an
 // entry per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed
-// step with a list of 2^20 entries 8.3 us (8 MB of stores would take 1.3 us; the search and
+// step with a list of 2^20 entries 7.6 us (8 MB of stores would take 1.3 us; the search and
 // the divisions of 608 CTAs are most of it).
 #include "block_rows.cuh"
 
@@ -141,21 +141,17 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablesP
   } else {                               // four neighbours: one search and mostly one id
     for (int i = 4 * gt; i < P.max_new; i += 4 * gthreads) {
       int32_t slot[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
-      if (i < listed) {
-        int b = owner_of(cuN, P.B, i);
-        entry(i, b, slot[0], pos[0]);
-        // entries that follow it in its block
-        const int same = slot[0] >= 0 ? min(P.bs - 1 - (pos[0] - block_of(P, pos[0]) * P.bs), cuN[b + 1] - 1 - i) : 0;
+      // one look-up per block that they touch (mostly one, two where a block or a request ends)
+      int b = i < listed ? owner_of(cuN, P.B, i) : 0;
+      for (int u = 0; u < 4 && i + u < listed;) {
+        while (cuN[b + 1] <= i + u) ++b;
+        int32_t s0, p0;
+        entry(i + u, b, s0, p0);
+        const int run = s0 >= 0 ? min(P.bs - (p0 - block_of(P, p0) * P.bs), cuN[b + 1] - i - u) : 1;
 #pragma unroll
-        for (int u = 1; u < 4; ++u) {
-          if (i + u >= listed) continue;
-          if (u <= same) {
-            slot[u] = slot[0] + u, pos[u] = pos[0] + u;
-          } else {
-            while (cuN[b + 1] <= i + u) ++b;
-            entry(i + u, b, slot[u], pos[u]);
-          }
-        }
+        for (int v = 0; v < 4; ++v)
+          if (v >= u && v - u < run && s0 >= 0) slot[v] = s0 + (v - u), pos[v] = p0 + (v - u);
+        u += run;
       }
       if (i + 4 <= P.max_new) {
         *reinterpret_cast<int4 *>(P.slot_map + i) = make_int4(slot[0], slot[1], slot[2], slot[3]);
