@@ -12,10 +12,12 @@
 // sums stay in shared memory) and then takes its share of the blocks and of the list, so
 // no CTA waits for another.  A stack entry at or above `count` is read where it comes from
 // (the shrinking request's table), never from the stack the same launch is writing.
-// Bound by latency: 64 decoding requests 2.7 us (one CTA: lengths, sums, search, id, store, an
-// entry per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed
+// Bound by latency: 64 decoding requests 2.8 us (lengths, sums, search, id, store, an entry
+// per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed
 // step with a list of 2^20 entries 7.6 us (8 MB of stores would take 1.3 us; the search and
 // the divisions of 608 CTAs are most of it).
+#include <algorithm>
+
 #include "block_rows.cuh"
 
 namespace echo {
@@ -227,10 +229,16 @@ int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream) {
   if (int rr = smem_limit_once(attr, echo::block_tables_kernel, 3 * (16384 + 1) * sizeof(int32_t),
                                "block tables smem attribute"))
     return rr;
-  // an entry per thread while that fits the GPU (four CTAs per SM), then four and more each
-  const int want = a->max_new / echo::kTabThreads + (a->max_new % echo::kTabThreads != 0);
-  const int grid = want < 1 ? 1 : want > 608 ? 608 : want;
-  const cudaError_t e = launch_pdl(echo::block_tables_kernel, dim3(grid), dim3(echo::kTabThreads), smem, stream, P);
+  // an entry per thread while that fits the GPU (four CTAs per SM), then four and more each; and
+  // the tables' blocks, which may all be on their way back, four to a thread on up to 152 CTAs
+  // (finished requests on one CTA against 152: 125 requests of 26011 tokens in blocks of 32, 18
+  // of them finished, 20.3 / 3.9 us; 256 of 131072 in blocks of 16, 40 finished, 407 / 6.5; with
+  // nothing to return 64 requests take 2.8 / 2.9)
+  const auto ctas = [](int64_t n, int64_t each) { return (n + each - 1) / each; };
+  const int64_t by_list = ctas(a->max_new, echo::kTabThreads);
+  const int64_t by_blocks = std::min<int64_t>(152, ctas(static_cast<int64_t>(a->B) * a->max_blocks, 4 * echo::kTabThreads));
+  const int64_t grid = std::min<int64_t>(608, std::max<int64_t>({1, by_list, by_blocks}));
+  const cudaError_t e = launch_pdl(echo::block_tables_kernel, dim3(static_cast<unsigned>(grid)), dim3(echo::kTabThreads), smem, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block tables launch");
 }
 

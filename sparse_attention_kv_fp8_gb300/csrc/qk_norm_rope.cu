@@ -376,10 +376,15 @@ namespace echo_host {
 
 template <int D, int kBatch, bool kInter>
 static cudaError_t launch_rope(echo::RopeParams P, bool values, int span, int kv_span, cudaStream_t stream) {
-  P.span = span;
-  P.kv_span = kv_span;
-  P.q_chunks = (P.n_heads + span - 1) / span;
-  P.k_chunks = (P.n_kv_heads + kv_span - 1) / kv_span;
+  // equal runs of whole batches, none longer than the span (24 heads: 12 + 12, not 16 + 8)
+  const auto even = [](int heads, int most) {
+    const int runs = (heads + most - 1) / most, run = (heads + runs - 1) / runs;
+    return (run + kBatch - 1) / kBatch * kBatch;
+  };
+  P.span = even(P.n_heads, span);
+  P.kv_span = even(P.n_kv_heads, kv_span);
+  P.q_chunks = (P.n_heads + P.span - 1) / P.span;
+  P.k_chunks = (P.n_kv_heads + P.kv_span - 1) / P.kv_span;
   P.chunks = P.q_chunks + (values ? 2 : 1) * P.k_chunks;
   constexpr int kTokens = 256 / D;
   const int64_t warps = (static_cast<int64_t>(P.T) + kTokens - 1) / kTokens * P.chunks;

@@ -75,6 +75,16 @@ def test_random_steps(B, L, new, bs, seed):
     s.check()
 
 
+@pytest.mark.parametrize("B,L,bs", [(300, 3000, 4), (40, 30000, 16), (700, 900, 1)])
+def test_finished_requests_return_all_their_blocks(B, L, bs):
+    """Nine in ten end, the others go on by a token: far more blocks move than tokens come."""
+    old = np.random.default_rng(B).integers(0, L + 1, B)
+    s = Step(old, np.where(np.arange(B) % 10 == 3, old + 1, 0), bs, 4)
+    for _ in range(2):
+        echo.echo_block_tables(s.args)
+    s.check()
+
+
 @pytest.mark.parametrize("short", [1, 3, 1000])
 def test_growth_that_does_not_fit_is_left_out_in_order(short):
     old, new = lengths(200, 400, 200, 5)
