@@ -10,7 +10,7 @@
 // 16384 tokens x (64 + 8 + 8) heads of 128 in 117 us, 5.8 TB/s of the 6.67 TB/s that a copy
 // reaches here (0.87; 8-byte accesses and 32 warps an SM: with one 16-byte load per lane, the
 // partners shuffled between lanes and 16 warps it was 180 us); 8191 tokens x 40 heads of 64
-// into a 4-bit cache 20.6 us (0.66; first loads and tail), a decode step's tokens 3 us (latency).
+// into a 4-bit cache 19.8 us (0.69; first loads and tail), a decode step's tokens 3 us (latency).
 #include "block_rows.cuh"
 
 namespace echo {
@@ -402,6 +402,10 @@ template <int D, bool kInter>
 static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, cudaStream_t stream) {
   const int64_t warps = (static_cast<int64_t>(P.T) + 256 / D - 1) / (256 / D) * (P.n_heads + (values ? 2 : 1) * static_cast<int64_t>(P.n_kv_heads));
   if (warps <= 4096) return launch_rope<D, 1, kInter>(P, values, 1, 1, stream);
+  // (4-bit rows: batches of 4 spill where the quantisation stands, and long runs of batches of 2
+  // win sooner; 2 of 8 and 4, 2 of 16 and 8, 4 of 16 and 8: 34320 warps 10.7 / 15.6 / 16.9,
+  // 64000 18.9 / 18.6 / 18.0, 81920 20.7 / 19.8 / 23.2, 201340 50.5 / 47.4 / 53.4)
+  if (P.format == ECHO_BLOCK_FP4 && warps > 65536) return launch_rope<D, 2, kInter>(P, values, 16, 8, stream);
   if (warps <= 163840) return launch_rope<D, 2, kInter>(P, values, 8, 4, stream);
   return launch_rope<D, 4, kInter>(P, values, 16, 8, stream);
 }
