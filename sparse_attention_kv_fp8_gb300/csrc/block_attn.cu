@@ -126,7 +126,7 @@ template <int FMT, int D, int NT, int WARPS, int STAGES>
 struct BaCfg {
   static constexpr bool kFp4 = FMT == ECHO_BLOCK_FP4;
   static constexpr int kSubBytes = kFp4 ? 18 * D : 64 * D;  // K and V of 16 tokens
-  static constexpr int kSubs = kFp4 ? (D == 128 || NT == 2 ? 2 : 4) : (D == 128 ? 1 : 2);  // of a chunk
+  static constexpr int kSubs = kFp4 ? (D == 128 && NT == 4 ? 1 : D == 128 || NT >= 2 ? 2 : 4) : (D == 128 ? 1 : 2);  // of a chunk
   static constexpr int kTokens = kSubs * kSubTokens;
   static constexpr int kStageBytes = kSubs * kSubBytes;
   static constexpr int kThreads = WARPS * 32;
@@ -1101,20 +1101,24 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   // tokens a context can show at most
   int64_t most = static_cast<int64_t>(P.max_blocks) * a->block_tokens;
   if (!P.sel && P.window && most > P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31) most = P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31;
-  // Warps and stages for 8, 16 and 32 query rows, of one CTA an SM and of one of two: as many
-  // warps as registers and shared memory allow in multiples of the 4 schedulers (4-bit rows,
-  // bound by instructions: 12 warps of 3 stages 334 us, 16 of 2 318 us, 14 of 2 355 us for 16 x
-  // 131072 tokens x 8 KV heads), or enough bytes in flight (bf16 rows, bound by HBM).
+  // Warps and stages for 8, 16, 24 and 32 query rows, the first two of one CTA an SM and of one
+  // of two: as many warps as registers and shared memory allow in multiples of the 4 schedulers
+  // (4-bit rows, bound by instructions: 12 warps of 3 stages 334 us, 16 of 2 318 us, 14 of 2 355
+  // us for 16 x 131072 tokens x 8 KV heads), or enough bytes in flight (bf16 rows, bound by HBM).
+  // 20 rows as 24 instead of 32: 12 requests of up to 38624 tokens in 4 bits 179 -> 143 us (3
+  // stages; 4 take 148), 24 of 6479 in bf16 62 -> 52.5.  32 rows in chunks of 16 tokens: 183 ->
+  // 186 us, but nothing spills, and one request of 1000 tokens takes 10.2 us instead of 12.4.
 #define BA_SHAPE(FMT, D, NT, W, S, CTAS) BaShape<FMT, D, NT, W, S, CTAS>
-#define BA_GO(FMT, D, W1, S1, V1, T1, W2, S2, V2, T2, W4, S4)                                                                  \
+#define BA_GO(FMT, D, W1, S1, V1, T1, W2, S2, V2, T2, W3, S3, W4, S4)                                                          \
   (pad == 8    ? ba_go<BA_SHAPE(FMT, D, 1, W1, S1, 1), BA_SHAPE(FMT, D, 1, V1, T1, 2)>(P, pairs, most, sms, stream)            \
    : pad == 16 ? ba_go<BA_SHAPE(FMT, D, 2, W2, S2, 1), BA_SHAPE(FMT, D, 2, V2, T2, 2)>(P, pairs, most, sms, stream)            \
+   : rows <= 24 ? ba_go<BA_SHAPE(FMT, D, 3, W3, S3, 1), void>(P, pairs, most, sms, stream)                                      \
                : ba_go<BA_SHAPE(FMT, D, 4, W4, S4, 1), void>(P, pairs, most, sms, stream))
   if (a->format == ECHO_BLOCK_FP4)
-    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 8, 2, 12, 3, 6, 3, 8, 4)
-                              : BA_GO(ECHO_BLOCK_FP4, 64, 16, 2, 8, 2, 16, 4, 8, 4, 8, 4);
-  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 4, 3, 7, 3, 4, 2, 7, 3)
-                            : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 4, 3, 7, 3, 4, 2, 8, 3);
+    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 8, 2, 12, 3, 6, 3, 8, 3, 8, 3)
+                              : BA_GO(ECHO_BLOCK_FP4, 64, 16, 2, 8, 2, 16, 4, 8, 4, 12, 3, 8, 3);
+  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 4, 3, 7, 3, 4, 2, 7, 3, 7, 3)
+                            : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 4, 3, 7, 3, 4, 2, 8, 3, 8, 3);
 #undef BA_SHAPE
 #undef BA_GO
 }

@@ -160,6 +160,15 @@ def test_groups_and_query_tokens(fmt, D, Hq, Hkv, n_q, wide):
     a.check()
 
 
+@pytest.mark.parametrize("fmt,D", FORMATS)
+@pytest.mark.parametrize("Hq,Hkv,n_q", [(17, 1, 1), (10, 2, 4), (24, 2, 2), (25, 1, 1), (56, 1, 1), (3, 1, 19)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_that_fill_three_columns_and_one_more(fmt, D, Hq, Hkv, n_q, wide):
+    a = Attn(fmt, D, 32, Hq, Hkv, n_q, [1300, 17, 0, 33], sinks=3, window=400, seed=Hq, cap=WIDE // 32 if wide else None)
+    echo.echo_block_attention(a.args())
+    a.check()
+
+
 @pytest.mark.parametrize("fmt", [BF16, FP4])
 @pytest.mark.parametrize("bs", [16, 48, 128, 256])
 @pytest.mark.parametrize("heads", [False, True])
