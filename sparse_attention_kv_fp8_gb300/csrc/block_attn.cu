@@ -80,7 +80,8 @@ struct BlockAttnParams {
   int32_t cluster;                   // CTAs of a (b, h, row group), a cluster; 0: the line is cut
   float *part_o;                     // [2 * grid][rows][D]
   float *part_ml;                    // [2 * grid][rows][2]
-  int4 *tail;                        // [grid]: (b, h * mgroups + mg, pieces, 0)
+  int4 *tail;                        // (b, h * mgroups + mg, pieces, first CTA) of each
+  int32_t by_pair;                   // (b, h, row group), or of the last one of each CTA
   int32_t *status;
 };
 
@@ -346,6 +347,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     // requests with nothing to see are not on the line: their outputs are written here
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
       if (req_view(P, P.ctx_len[b]).nsub > 0) continue;
+      if (P.by_pair)
+        for (int i = threadIdx.x; i < heads; i += C::kThreads) P.tail[b * heads + i] = make_int4(0, 0, 0, 0);
       const int64_t o0 = static_cast<int64_t>(b) * P.n_q * P.n_heads;
       for (int i = threadIdx.x; i < P.n_q * P.n_heads * (D / 8); i += C::kThreads)
         reinterpret_cast<uint4 *>(P.out + o0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     }
     const int64_t g0 = per * blockIdx.x;
     if (g0 >= total) {
-      if (threadIdx.x == 0) P.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (threadIdx.x == 0 && !P.by_pair) P.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }
     n_chunks = static_cast<int>(min(total - g0, per));
@@ -377,14 +380,6 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     cur.start = __shfl_sync(~0u, own_start, src);
     cur.v = req_view(P, P.ctx_len[cur.b]);
     cur.end = cur.start + chunks_of<C::kSubs>(cur.v);
-    if (threadIdx.x == C::kThreads - 1) {
-      // where the range's last (b, hm) goes on, and whether it began here
-      LinePos e = cur;
-      seek<C::kSubs>(P, e, n_chunks - 1);
-      int pieces = 0;
-      if (e.end > n_chunks && e.start >= 0) pieces = 1 + static_cast<int>((e.end - n_chunks + per - 1) / per);
-      P.tail[blockIdx.x] = make_int4(e.b, e.hm, pieces, 0);
-    }
   }
 
   // ===== the queries of a (b, hm), a row per warp: loaded early, laid out as B fragments later
@@ -497,6 +492,12 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
 
   int st = 0, g = warp, rd = 0;  // stage, chunk and list entry to compute
   for (;;) {  // the (b, hm) of this range, one after another
+    if (threadIdx.x == 0 && !P.cluster && (P.by_pair ? cur.start >= 0 : cur.end >= n_chunks)) {
+      // how many pieces a (b, hm) that begins here has (its next CTAs' ranges are as long as this
+      // one's), or that it needs no merge here
+      const int pieces = cur.start >= 0 && cur.end > n_chunks ? 1 + (cur.end - 1) / n_chunks : 0;
+      P.tail[P.by_pair ? cur.b * (P.n_kv * P.mgroups) + cur.hm : blockIdx.x] = make_int4(cur.b, cur.hm, pieces, blockIdx.x);
+    }
     const int pend = min(cur.end, n_chunks);
     const int row0 = (cur.hm % P.mgroups) * kBaMaxRows;
     uint2 qreg[NT == 1 ? C::kSteps : 1];
@@ -884,28 +885,34 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   }
 }
 
-// Merge of the pieces of each (b, hm) that was cut: block (i, y) takes row y of the one that
-// begins in CTA i's range and goes on past it.  D / 4 threads add a piece's row at a time
-// (kBaCombThreads / (D / 4) pieces side by side, their first loads issued before it is known
-// how many there are: one round trip to L2 in the usual case), then the groups in order.
-constexpr int kBaCombThreads = 256;
+// Merge of the pieces of each (b, hm) that was cut: block (i, y) takes row y of the i-th one
+// (kPair), or of the one that begins in CTA i's range and goes on past it (its first loads then
+// go out before it is known how many pieces there are: one round trip to L2 in the usual
+// case).  D / 4 threads add a piece's row at a time, kGroups pieces side by side, then the
+// groups in order.  Few (b, hm) have many pieces each and leave most CTAs none to begin: with 32
+// rows 4864 blocks of 256 threads, nearly all without work, took 6.6 us.
+template <int D, bool kPair>
+struct BaComb {
+  static constexpr int kGroups = kPair ? 16 : 512 / D, kThreads = kGroups * (D / 4);
+};
 
-template <int D>
-__global__ void __launch_bounds__(kBaCombThreads) block_attn_combine_kernel(const BlockAttnParams P, int rows_pad) {
-  constexpr int kLanes = D / 4, kGroups = kBaCombThreads / kLanes;
+template <int D, bool kPair>
+__global__ void __launch_bounds__(BaComb<D, kPair>::kThreads) block_attn_combine_kernel(const BlockAttnParams P, int rows_pad) {
+  constexpr int kLanes = D / 4, kGroups = BaComb<D, kPair>::kGroups;
   __shared__ float2 sml[kGroups];
   __shared__ __align__(16) float so[kGroups][D];
-  const int cta = blockIdx.x, row = blockIdx.y, grp = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
+  const int row = blockIdx.y, grp = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
   pdl_launch_dependents();
   pdl_wait();
-  // piece 0 is CTA i's second slot, piece s > 0 the first slot of CTA i + s
+  const int4 tail = P.tail[blockIdx.x];
+  const int cta = kPair ? tail.w : blockIdx.x, pieces = tail.z;
+  if (kPair && pieces == 0) return;
+  // piece 0 is the first CTA's second slot, piece s > 0 the first slot of the s-th CTA from there
   auto slot_row = [&](int s) {
     return static_cast<int64_t>(s == 0 ? 2 * cta + 1 : 2 * min(cta + s, kBaMaxGrid - 1)) * rows_pad + row;
   };
-  const int4 tail = P.tail[cta];
   float2 v = reinterpret_cast<const float2 *>(P.part_ml)[slot_row(grp)];
   float4 x = *reinterpret_cast<const float4 *>(P.part_o + slot_row(grp) * D + d);
-  const int pieces = tail.z;
   if (pieces == 0) return;
   const int h = tail.y / P.mgroups;
   const int rq = (tail.y - h * P.mgroups) * kBaMaxRows + row;
@@ -996,6 +1003,7 @@ struct BaShape {
   static int launch(echo::BlockAttnParams P, int cs, int64_t pairs, int sms, cudaStream_t stream) {
     P.cluster = cs;
     const int64_t grid = cs ? pairs * cs : std::min(sms * CTAS, echo::kBaMaxGrid);
+    P.by_pair = !cs && 2 * pairs <= grid;
     cudaLaunchConfig_t cfg = config(grid, stream);
     cudaLaunchAttribute at[2] = {pdl(), cluster(cs)};
     cfg.attrs = at;
@@ -1003,15 +1011,19 @@ struct BaShape {
     cudaError_t e = cudaLaunchKernelEx(&cfg, echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES, CTAS>, P);
     if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
     if (cs) return ECHO_OK;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), C::kRows);
-    cfg.blockDim = dim3(echo::kBaCombThreads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D>, P, static_cast<int>(C::kRows));
+    e = P.by_pair ? combine<true>(cfg, pairs, P) : combine<false>(cfg, grid, P);
     return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block attention merge launch");
   }
 
  private:
+  template <bool kPair>
+  static cudaError_t combine(cudaLaunchConfig_t cfg, int64_t n, const echo::BlockAttnParams &P) {
+    cfg.gridDim = dim3(static_cast<unsigned>(n), C::kRows);
+    cfg.blockDim = dim3(echo::BaComb<D, kPair>::kThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, echo::block_attn_combine_kernel<D, kPair>, P, static_cast<int>(C::kRows));
+  }
   static cudaLaunchConfig_t config(int64_t grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
