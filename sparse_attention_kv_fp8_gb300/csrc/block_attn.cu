@@ -35,9 +35,9 @@
 //     than SMs two smaller CTAs share an SM, one streaming while the other starts or merges.
 //
 // Measured on a GB300 (8 KV heads of 128, 8 query heads each; HBM's measured copy rate is
-// 6.67 TB/s): 16 requests of 16384 to 32768 tokens 236 us in bf16 (6.8 TB/s), 94 us in 4 bits
-// (4.8 TB/s); of up to 131072 tokens 314 us in 4 bits (6.0 TB/s), 423 us with two query
-// tokens; a window of 4096 and 4 sinks of 64 requests 164 us in bf16 (6.6 TB/s); one request
+// 6.67 TB/s): 16 requests of 16384 to 32768 tokens 236 us in bf16 (6.8 TB/s), 93 us in 4 bits
+// (4.9 TB/s); of up to 131072 tokens 314 us in 4 bits (6.0 TB/s), 423 us with two query
+// tokens; a window of 4096 and 4 sinks of 64 requests 162 us in bf16 (6.6 TB/s); one request
 // of 1000 tokens 6 us.  bf16 is bound by HBM.  4-bit rows are bound by instructions, above
 // all the conversions: some 600 per warp and 32 tokens, the integer pipe 64% and the issue
 // slots 66% busy (without the scales' multiplies 277 us instead of 318); with two query
@@ -136,7 +136,11 @@ struct BaCfg {
   static constexpr int kMergeRow = D / 2 + 4;                // floats; + 4: no bank conflicts
   // shared memory: stages | merge buffers | lists | q fragments | per-row values
   static constexpr int kOffMerge = WARPS * STAGES * kStageBytes;
-  static constexpr int kOffList = kOffMerge + WARPS * 8 * kMergeRow * 4;
+  // parts of the output (8 rows, half of the dims) that the warps merge at a time: as many as
+  // shared memory has room for beside the stages
+  static constexpr int kParts = NT <= 2 ? 1 : kFp4 ? NT : 2;
+  static constexpr int kPart = WARPS * 8 * kMergeRow;        // floats
+  static constexpr int kOffList = kOffMerge + kParts * kPart * 4;
   static constexpr int kOffQ = kOffList + WARPS * kBaList * 16;
   static constexpr int kOffMl = kOffQ + kSteps * NT * 32 * 8;
   static constexpr int kOffQs = kOffMl + WARPS * kRows * 8;
@@ -771,69 +775,71 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     const bool split = !P.cluster && (cur.start < 0 || cur.end > n_chunks);
     float *shared_o = reinterpret_cast<float *>(ba_smem);  // [kRows][D], where the stages were
     const int slot = 2 * blockIdx.x + (cur.start < 0 ? 0 : 1);
+    float f[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * C::kRows + nt * 8 + 2 * c4 + e].x);
-        f[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
+        f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
       }
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {  // half of the dims at a time
+    for (int p0 = 0; p0 < 2 * NT; p0 += C::kParts) {  // parts p: rows 8 (p / 2) and up, half p % 2 of the dims
+#pragma unroll
+      for (int p = p0; p < p0 + C::kParts; ++p)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float *dst = merge + (warp * 8 + 2 * c4 + e) * C::kMergeRow + 2 * r8;
+          float *dst = merge + (p - p0) * C::kPart + (warp * 8 + 2 * c4 + e) * C::kMergeRow + 2 * r8;
 #pragma unroll
           for (int j = 0; j < C::kSteps / 2; ++j) {
-            const float *x = o[hf * (C::kSteps / 2) + j][nt];
-            *reinterpret_cast<float2 *>(dst + 16 * j) = make_float2(x[e] * f[e], x[e + 2] * f[e]);
+            const float *x = o[(p % 2) * (C::kSteps / 2) + j][p / 2];
+            *reinterpret_cast<float2 *>(dst + 16 * j) = make_float2(x[e] * f[p / 2][e], x[e + 2] * f[p / 2][e]);
           }
         }
-        __syncthreads();
-        // a thread adds four neighbouring values of a row: tile j of this half, fragment rows
-        // r and r + 1, both halves of the tile
-        for (int i = threadIdx.x; i < 8 * D / 8; i += C::kThreads) {
-          const int rr = i / (D / 8), k = i % (D / 8), j = hf * (C::kSteps / 2) + k / 4, r = 2 * (k % 4), row = nt * 8 + rr;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncthreads();
+      // a thread adds four neighbouring values of a row: tile j of this half, fragment rows
+      // r and r + 1, both halves of the tile
+      for (int i = threadIdx.x; i < C::kParts * D; i += C::kThreads) {
+        const int p = p0 + i / D, rr = i % D / (D / 8), k = i % (D / 8), hf = p % 2;
+        const int j = hf * (C::kSteps / 2) + k / 4, r = 2 * (k % 4), row = (p / 2) * 8 + rr;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < WARPS; ++w) {
-            const float4 y = *reinterpret_cast<const float4 *>(merge + (w * 8 + rr) * C::kMergeRow + 4 * k);
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-          }
-          // x.x, x.y: fragment row r (tile rows r, r + 8); x.z, x.w: row r + 1
-          int d0, d1;
-          float2 a, b;
-          if constexpr (C::kFp4) {  // tile rows (r, r + 8) are dims r * D/8 + 2 j + (0, 1)
-            d0 = r * (D / 8) + 2 * j, d1 = d0 + D / 8;
-            a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
-          } else {                  // dims 16 j + r and 16 j + 8 + r
-            d0 = 16 * j + r, d1 = d0 + 8;
-            a = make_float2(x.x, x.z), b = make_float2(x.y, x.w);
-          }
-          const float2 v = fin[row];
-          if (P.cluster > 1) {
-            *reinterpret_cast<float2 *>(shared_o + row * D + d0) = a;
-            *reinterpret_cast<float2 *>(shared_o + row * D + d1) = b;
-          } else if (split) {
-            float *part = P.part_o + (static_cast<int64_t>(slot) * C::kRows + row) * D;
-            *reinterpret_cast<float2 *>(part + d0) = a;
-            *reinterpret_cast<float2 *>(part + d1) = b;
-            if (k == 0 && hf == 0) reinterpret_cast<float2 *>(P.part_ml)[slot * C::kRows + row] = v;
-          } else {
-            const int64_t oh = row_index(cur, row);
-            if (oh >= 0) {
-              const float inv = v.y > 0.f ? 1.f / v.y : v.y;  // (a NaN sum stays one)
-              *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
-              *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
-              if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y);
-            }
+        for (int w = 0; w < WARPS; ++w) {
+          const float4 y = *reinterpret_cast<const float4 *>(merge + (p - p0) * C::kPart + (w * 8 + rr) * C::kMergeRow + 4 * k);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        // x.x, x.y: fragment row r (tile rows r, r + 8); x.z, x.w: row r + 1
+        int d0, d1;
+        float2 a, b;
+        if constexpr (C::kFp4) {  // tile rows (r, r + 8) are dims r * D/8 + 2 j + (0, 1)
+          d0 = r * (D / 8) + 2 * j, d1 = d0 + D / 8;
+          a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
+        } else {                  // dims 16 j + r and 16 j + 8 + r
+          d0 = 16 * j + r, d1 = d0 + 8;
+          a = make_float2(x.x, x.z), b = make_float2(x.y, x.w);
+        }
+        const float2 v = fin[row];
+        if (P.cluster > 1) {
+          *reinterpret_cast<float2 *>(shared_o + row * D + d0) = a;
+          *reinterpret_cast<float2 *>(shared_o + row * D + d1) = b;
+        } else if (split) {
+          float *part = P.part_o + (static_cast<int64_t>(slot) * C::kRows + row) * D;
+          *reinterpret_cast<float2 *>(part + d0) = a;
+          *reinterpret_cast<float2 *>(part + d1) = b;
+          if (k == 0 && hf == 0) reinterpret_cast<float2 *>(P.part_ml)[slot * C::kRows + row] = v;
+        } else {
+          const int64_t oh = row_index(cur, row);
+          if (oh >= 0) {
+            const float inv = v.y > 0.f ? 1.f / v.y : v.y;  // (a NaN sum stays one)
+            *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
+            *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
+            if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y);
           }
         }
-        __syncthreads();
       }
+      __syncthreads();
     }
     if (!more) break;
     cur = nxt;
@@ -979,13 +985,12 @@ struct BaShape {
     return smem_limit_once(attr, echo::block_attn_kernel<FMT, D, NT, WARPS, STAGES, CTAS>, C::kSmem, "block attention smem attribute");
   }
 
-  // How many clusters of 2, 4 or 8 CTAs the device holds at once (a cluster sits in one group
-  // of SMs: 76, 36 and 15 here, not 152 SMs' worth: 16 clusters of 8 take 14.4 us where 15
-  // take 8.4).  Asked once per shape and device.
+  // How many clusters of cs CTAs the device holds at once (a cluster sits in one group of SMs:
+  // 76 of 2, 36 of 4 and 15 of 8 here, not 152 SMs' worth: 16 clusters of 8 take 14.4 us where
+  // 15 take 8.4).  Asked once per shape and device.
   static int clusters_at_once(int cs, int dev) {
-    static std::atomic<int> known[kMaxDevices][4];
-    const int k = cs == 2 ? 1 : cs == 4 ? 2 : 3;
-    int n = known[dev][k].load(std::memory_order_relaxed);
+    static std::atomic<int> known[kMaxDevices][echo::kBaMaxCluster + 1];
+    int n = known[dev][cs].load(std::memory_order_relaxed);
     if (n) return n - 1;
     cudaLaunchConfig_t cfg = config(cs, nullptr);
     cudaLaunchAttribute at = cluster(cs);
@@ -995,7 +1000,7 @@ struct BaShape {
       cudaGetLastError();
       n = 0;
     }
-    known[dev][k].store(n + 1, std::memory_order_relaxed);
+    known[dev][cs].store(n + 1, std::memory_order_relaxed);
     return n;
   }
 
@@ -1052,16 +1057,19 @@ struct BaShape {
 // in the tokens an SM works through.  Whole (b, h) cost their waves times the longest context;
 // cutting costs an equal share, the second kernel (`extra`) and a piece border per (b, h)
 // (`border`: the warps of an SM end together; overlapped by the other SMs where HBM is the
-// bound).  Measured with equal contexts, bf16 / 4-bit, us: 64 pairs of 1024 tokens 12 / 10 a
-// CTA each against 14 / 16 cut; 8 pairs of 8192 43 / 36 a CTA each, 14 / 12 cut, 12 / 12 a
-// cluster of 8 each; 512 pairs of 512 20.7 / 18.6 with two CTAs an SM, 29 / 27 with one, 512
-// pairs of 2048 67 / 39 against 73 / 51 cut.  The host does not know the contexts, only how
-// long they may be: past 4 `extra` tokens a CTA, what an uneven batch would cost is more than
-// whole (b, h) save (152 pairs of 16384 to 32768 tokens in 4 bits: 125 us whole, 103 cut).
+// bound), all for heads of 128: of half as many dims twice the tokens take as long (144 pairs of
+// 8000 tokens of 64 dims 42.7 / 28.8 us cut, 38.2 / 23.4 a CTA each).  Measured, bf16 / 4-bit,
+// us: 64 pairs of up to 1000 tokens 8.8 / 8.8 in clusters of 2 against 13.1 / 14.6 cut; 8 pairs
+// of 8000 11.2 / 10.9 in clusters of 8, 12.4 / 13.5 cut, of 16000 16.9 / 14.5 and 19.9 / 15.2, with
+// 32 rows 34.4 / 26.9 and 28.8 / 23.5; 128 pairs of 4000 35 / 21 a CTA each, 39 / 26 cut; 512 pairs
+// of 512 20.7 / 18.6 with two CTAs an SM, 29 / 27 with one.  The host does not know the contexts,
+// only how long they may be: past 4 `extra` tokens a CTA, what an uneven batch would cost is
+// more than whole (b, h) save (152 pairs of 16384 to 32768 tokens in 4 bits: 125 us whole, 103 cut).
 template <class Wide, class Narrow>
 static int ba_go(const echo::BlockAttnParams &P, int64_t pairs, int64_t most, int sms, cudaStream_t stream) {
   using C = typename Wide::C;
-  constexpr int64_t extra = C::kFp4 ? 1536 : 1024, border = C::kFp4 ? 1000 : 200;
+  constexpr int64_t dims = 8 / C::kSteps, border = dims * (C::kFp4 ? 1000 : 200);
+  constexpr int64_t extra = dims * (C::kRows > 16 ? 1024 : C::kFp4 ? 1536 : 1280);
   const int64_t cut = pairs * most / sms + extra;
   int dev = 0;
   if constexpr (!std::is_void<Narrow>::value) {
@@ -1075,11 +1083,13 @@ static int ba_go(const echo::BlockAttnParams &P, int64_t pairs, int64_t most, in
     }
   }
   if (int rr = Wide::prepare(&dev)) return rr;
-  // the cluster grows while the device holds them all and every warp still gets a chunk
-  int cs = 1;
-  while (cs < echo::kBaMaxCluster && most > static_cast<int64_t>(cs) * C::kThreads / 32 * C::kTokens &&
-         pairs <= Wide::clusters_at_once(2 * cs, dev))
-    cs *= 2;
+  // the largest cluster that the device holds for every pair at once and whose warps all get a
+  // chunk (of any size: 16 pairs of 8000 tokens in 4 bits, 8 and 32 rows, 14.5 and 26.8 us in
+  // fours, 12.3 and 21.0 in sixes)
+  const int64_t fits = sms / pairs, useful = (most - 1) / (C::kThreads / 32 * C::kTokens) + 1;
+  int cs = static_cast<int>(std::min<int64_t>({echo::kBaMaxCluster, fits, useful}));
+  while (cs > 1 && pairs > Wide::clusters_at_once(cs, dev)) --cs;
+  cs = cs < 1 ? 1 : cs;
   const int64_t share = (pairs * cs + sms - 1) / sms * most / cs;
   return Wide::launch(P, share <= cut && share <= 4 * extra ? cs : 0, pairs, sms, stream);
 }
