@@ -71,7 +71,8 @@ struct BlockAttnParams {
   const int32_t *table, *sel;
   int32_t table_heads, max_blocks;
   const int32_t *ctx_len;
-  int32_t B, n_q, n_heads, n_kv, group, mgroups;  // group: query heads per KV head
+  int32_t B, n_q, n_heads, n_kv, group;  // group: query heads per KV head
+  int32_t mgroups, mrows;            // row groups of a KV head, and their rows
   int32_t sinks, window;
   float scale_log2;                  // |scale| log2 e
   uint32_t q_sign;                   // 0x80008000 for a negative scale
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   uint2 qrow[C::kQRows];
   const bool q_lane = lane < D / 4;  // lane (s, c) = (k-step, column pair) of the fragments
   auto row_index = [&](const LinePos &L, int rr) -> int64_t {  // (b, query token, head) of a row
-    const int h = L.hm / P.mgroups, rq = (L.hm - h * P.mgroups) * kBaMaxRows + rr, j = rq / P.group;
+    const int h = L.hm / P.mgroups, rq = (L.hm - h * P.mgroups) * P.mrows + rr, j = rq / P.group;
     return rq < P.n_q * P.group ? (static_cast<int64_t>(L.b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group : -1;
   };
   auto load_q = [&](const LinePos &L) {
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
       P.tail[P.by_pair ? cur.b * (P.n_kv * P.mgroups) + cur.hm : blockIdx.x] = make_int4(cur.b, cur.hm, pieces, blockIdx.x);
     }
     const int pend = min(cur.end, n_chunks);
-    const int row0 = (cur.hm % P.mgroups) * kBaMaxRows;
+    const int row0 = (cur.hm % P.mgroups) * P.mrows;
     uint2 qreg[NT == 1 ? C::kSteps : 1];
     if constexpr (NT == 1) {
 #pragma unroll
@@ -921,7 +922,7 @@ __global__ void __launch_bounds__(BaComb<D, kPair>::kThreads) block_attn_combine
   float4 x = *reinterpret_cast<const float4 *>(P.part_o + slot_row(grp) * D + d);
   if (pieces == 0) return;
   const int h = tail.y / P.mgroups;
-  const int rq = (tail.y - h * P.mgroups) * kBaMaxRows + row;
+  const int rq = (tail.y - h * P.mgroups) * P.mrows + row;
   if (rq >= P.n_q * P.group) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1107,6 +1108,8 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   P.group = a->n_heads / a->n_kv_heads;
   const int rows = P.n_q * P.group;
   P.mgroups = (rows + echo::kBaMaxRows - 1) / echo::kBaMaxRows;
+  // (48 rows as 24 + 24, not 32 + 16: 12 requests of up to 20000 tokens in 4 bits 200 -> 151 us)
+  P.mrows = ((rows + P.mgroups - 1) / P.mgroups + 7) / 8 * 8;
   P.sinks = a->sinks, P.window = a->window;
   P.scale_log2 = std::fabs(a->scale) * 1.4426950408889634f;
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
@@ -1123,24 +1126,28 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   // tokens a context can show at most
   int64_t most = static_cast<int64_t>(P.max_blocks) * a->block_tokens;
   if (!P.sel && P.window && most > P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31) most = P.sinks + static_cast<int64_t>(P.window) + P.n_q + 31;
-  // Warps and stages for 8, 16, 24 and 32 query rows, the first two of one CTA an SM and of one
-  // of two: as many warps as registers and shared memory allow in multiples of the 4 schedulers
+  // Warps and stages for 8, 16, 24 and 32 query rows, of a CTA with an SM to itself and of one of
+  // two: as many warps as registers and shared memory allow in multiples of the 4 schedulers
   // (4-bit rows, bound by instructions: 12 warps of 3 stages 334 us, 16 of 2 318 us, 14 of 2 355
   // us for 16 x 131072 tokens x 8 KV heads), or enough bytes in flight (bf16 rows, bound by HBM).
   // 20 rows as 24 instead of 32: 12 requests of up to 38624 tokens in 4 bits 179 -> 143 us (3
   // stages; 4 take 148), 24 of 6479 in bf16 62 -> 52.5.  32 rows in chunks of 16 tokens: 183 ->
   // 186 us, but nothing spills, and one request of 1000 tokens takes 10.2 us instead of 12.4.
+  // Two CTAs an SM for 512 pairs of up to 2000 tokens, 24 / 32 rows: 75 / 91 -> 61 / 77 us in 4
+  // bits, 89 / 118 -> 78 / 94 in bf16.
 #define BA_SHAPE(FMT, D, NT, W, S, CTAS) BaShape<FMT, D, NT, W, S, CTAS>
-#define BA_GO(FMT, D, W1, S1, V1, T1, W2, S2, V2, T2, W3, S3, W4, S4)                                                          \
-  (pad == 8    ? ba_go<BA_SHAPE(FMT, D, 1, W1, S1, 1), BA_SHAPE(FMT, D, 1, V1, T1, 2)>(P, pairs, most, sms, stream)            \
-   : pad == 16 ? ba_go<BA_SHAPE(FMT, D, 2, W2, S2, 1), BA_SHAPE(FMT, D, 2, V2, T2, 2)>(P, pairs, most, sms, stream)            \
-   : rows <= 24 ? ba_go<BA_SHAPE(FMT, D, 3, W3, S3, 1), void>(P, pairs, most, sms, stream)                                      \
-               : ba_go<BA_SHAPE(FMT, D, 4, W4, S4, 1), void>(P, pairs, most, sms, stream))
+#define BA_GO(FMT, D, NT, W, S, W2, S2) ba_go<BA_SHAPE(FMT, D, NT, W, S, 1), BA_SHAPE(FMT, D, NT, W2, S2, 2)>(P, pairs, most, sms, stream)
+#define BA_PICK(FMT, D, A1, A2, A3, A4) \
+  (P.mrows == 8 ? BA_GO(FMT, D, 1, A1) : P.mrows == 16 ? BA_GO(FMT, D, 2, A2) : P.mrows == 24 ? BA_GO(FMT, D, 3, A3) : BA_GO(FMT, D, 4, A4))
+  // (each: warps and stages of a CTA with an SM to itself, then of one of two)
+#define X(...) __VA_ARGS__
   if (a->format == ECHO_BLOCK_FP4)
-    return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_FP4, 128, 16, 2, 8, 2, 12, 3, 6, 3, 8, 3, 8, 3)
-                              : BA_GO(ECHO_BLOCK_FP4, 64, 16, 2, 8, 2, 16, 4, 8, 4, 12, 3, 8, 3);
-  return a->head_dim == 128 ? BA_GO(ECHO_BLOCK_BF16, 128, 8, 3, 4, 3, 7, 3, 4, 2, 7, 3, 7, 3)
-                            : BA_GO(ECHO_BLOCK_BF16, 64, 8, 3, 4, 3, 7, 3, 4, 2, 8, 3, 8, 3);
+    return a->head_dim == 128 ? BA_PICK(ECHO_BLOCK_FP4, 128, X(16, 2, 8, 2), X(12, 3, 6, 3), X(8, 3, 4, 3), X(8, 3, 4, 3))
+                              : BA_PICK(ECHO_BLOCK_FP4, 64, X(16, 2, 8, 2), X(16, 4, 8, 4), X(12, 3, 4, 3), X(8, 3, 4, 3));
+  return a->head_dim == 128 ? BA_PICK(ECHO_BLOCK_BF16, 128, X(8, 3, 4, 3), X(7, 3, 4, 2), X(7, 3, 4, 2), X(7, 3, 4, 2))
+                            : BA_PICK(ECHO_BLOCK_BF16, 64, X(8, 3, 4, 3), X(7, 3, 4, 2), X(8, 3, 4, 2), X(8, 3, 4, 2));
+#undef X
+#undef BA_PICK
 #undef BA_SHAPE
 #undef BA_GO
 }

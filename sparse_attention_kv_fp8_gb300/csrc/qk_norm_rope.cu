@@ -402,11 +402,14 @@ template <int D, bool kInter>
 static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, cudaStream_t stream) {
   const int64_t warps = (static_cast<int64_t>(P.T) + 256 / D - 1) / (256 / D) * (P.n_heads + (values ? 2 : 1) * static_cast<int64_t>(P.n_kv_heads));
   if (warps <= 4096) return launch_rope<D, 1, kInter>(P, values, 1, 1, stream);
-  // (4-bit rows: batches of 4 spill where the quantisation stands, and long runs of batches of 2
-  // win sooner; 2 of 8 and 4, 2 of 16 and 8, 4 of 16 and 8: 34320 warps 10.7 / 15.6 / 16.9,
-  // 64000 18.9 / 18.6 / 18.0, 81920 20.7 / 19.8 / 23.2, 201340 50.5 / 47.4 / 53.4)
-  if (P.format == ECHO_BLOCK_FP4 && warps > 65536) return launch_rope<D, 2, kInter>(P, values, 16, 8, stream);
-  if (warps <= 163840) return launch_rope<D, 2, kInter>(P, values, 8, 4, stream);
+  // Long runs want 8 and more KV heads: beside a warp's 16 query heads others would have 2 (16 + 4
+  // heads of 128, 8 and 4 against 16 and 8: 7311 tokens into 4-bit rows 24.2 / 31.0, 16000 into
+  // bf16 rows 42.3 / 44.5).  4-bit rows: batches of 4 spill where the quantisation stands, and
+  // long runs of batches of 2 win sooner (2 of 8 and 4, 2 of 16 and 8, 4 of 16 and 8: 64000 warps
+  // 18.9 / 18.6 / 18.0, 81920 20.7 / 19.8 / 23.2, 201340 50.5 / 47.4 / 53.4).
+  const bool fp4 = P.format == ECHO_BLOCK_FP4;
+  if (P.n_kv_heads < 8 || warps <= (fp4 ? 65536 : 163840)) return launch_rope<D, 2, kInter>(P, values, 8, 4, stream);
+  if (fp4) return launch_rope<D, 2, kInter>(P, values, 16, 8, stream);
   return launch_rope<D, 4, kInter>(P, values, 16, 8, stream);
 }
 
