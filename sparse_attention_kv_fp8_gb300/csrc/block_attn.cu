@@ -72,7 +72,7 @@ struct BlockAttnParams {
   int32_t table_heads, max_blocks;
   const int32_t *ctx_len;
   int32_t B, n_q, n_heads, n_kv, group;  // group: query heads per KV head
-  int32_t mgroups, mrows;            // row groups of a KV head, and their rows
+  int32_t mgroups;                   // row groups of a KV head (the kernel's kRows each)
   int32_t sinks, window;
   float scale_log2;                  // |scale| log2 e
   uint32_t q_sign;                   // 0x80008000 for a negative scale
@@ -315,6 +315,13 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   // ===== this CTA's range of the line: chunks 0 .. n_chunks from its first =====
   LinePos cur;
   int n_chunks;
+  // of a cut line: how many pieces a (b, hm) that begins here has (the next CTAs' ranges are as
+  // long as this one's), or that it needs no merge here
+  auto note_tail = [&](const LinePos &L) {
+    if (threadIdx.x != 0 || !(P.by_pair ? L.start >= 0 : L.end >= n_chunks)) return;
+    const int pieces = L.start >= 0 && L.end > n_chunks ? 1 + (L.end - 1) / n_chunks : 0;
+    P.tail[P.by_pair ? L.b * heads + L.hm : blockIdx.x] = make_int4(L.b, L.hm, pieces, blockIdx.x);
+  };
   if (P.cluster) {
     const int pair = blockIdx.x / P.cluster, rank = blockIdx.x - pair * P.cluster;
     cur.b = pair / heads;
@@ -385,13 +392,14 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     cur.start = __shfl_sync(~0u, own_start, src);
     cur.v = req_view(P, P.ctx_len[cur.b]);
     cur.end = cur.start + chunks_of<C::kSubs>(cur.v);
+    note_tail(cur);
   }
 
   // ===== the queries of a (b, hm), a row per warp: loaded early, laid out as B fragments later
   uint2 qrow[C::kQRows];
   const bool q_lane = lane < D / 4;  // lane (s, c) = (k-step, column pair) of the fragments
   auto row_index = [&](const LinePos &L, int rr) -> int64_t {  // (b, query token, head) of a row
-    const int h = L.hm / P.mgroups, rq = (L.hm - h * P.mgroups) * P.mrows + rr, j = rq / P.group;
+    const int h = L.hm / P.mgroups, rq = (L.hm - h * P.mgroups) * C::kRows + rr, j = rq / P.group;
     return rq < P.n_q * P.group ? (static_cast<int64_t>(L.b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group : -1;
   };
   auto load_q = [&](const LinePos &L) {
@@ -497,14 +505,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
 
   int st = 0, g = warp, rd = 0;  // stage, chunk and list entry to compute
   for (;;) {  // the (b, hm) of this range, one after another
-    if (threadIdx.x == 0 && !P.cluster && (P.by_pair ? cur.start >= 0 : cur.end >= n_chunks)) {
-      // how many pieces a (b, hm) that begins here has (its next CTAs' ranges are as long as this
-      // one's), or that it needs no merge here
-      const int pieces = cur.start >= 0 && cur.end > n_chunks ? 1 + (cur.end - 1) / n_chunks : 0;
-      P.tail[P.by_pair ? cur.b * (P.n_kv * P.mgroups) + cur.hm : blockIdx.x] = make_int4(cur.b, cur.hm, pieces, blockIdx.x);
-    }
     const int pend = min(cur.end, n_chunks);
-    const int row0 = (cur.hm % P.mgroups) * P.mrows;
+    const int row0 = (cur.hm % P.mgroups) * C::kRows;
     uint2 qreg[NT == 1 ? C::kSteps : 1];
     if constexpr (NT == 1) {
 #pragma unroll
@@ -844,6 +846,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     }
     if (!more) break;
     cur = nxt;
+    note_tail(cur);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   // ----- a cluster: each CTA joins every CS-th row over all CTAs' shared memory, in rank order
@@ -922,7 +925,7 @@ __global__ void __launch_bounds__(BaComb<D, kPair>::kThreads) block_attn_combine
   float4 x = *reinterpret_cast<const float4 *>(P.part_o + slot_row(grp) * D + d);
   if (pieces == 0) return;
   const int h = tail.y / P.mgroups;
-  const int rq = (tail.y - h * P.mgroups) * P.mrows + row;
+  const int rq = (tail.y - h * P.mgroups) * rows_pad + row;
   if (rq >= P.n_q * P.group) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1109,7 +1112,7 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   const int rows = P.n_q * P.group;
   P.mgroups = (rows + echo::kBaMaxRows - 1) / echo::kBaMaxRows;
   // (48 rows as 24 + 24, not 32 + 16: 12 requests of up to 20000 tokens in 4 bits 200 -> 151 us)
-  P.mrows = ((rows + P.mgroups - 1) / P.mgroups + 7) / 8 * 8;
+  const int mrows = ((rows + P.mgroups - 1) / P.mgroups + 7) / 8 * 8;
   P.sinks = a->sinks, P.window = a->window;
   P.scale_log2 = std::fabs(a->scale) * 1.4426950408889634f;
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
@@ -1138,7 +1141,7 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
 #define BA_SHAPE(FMT, D, NT, W, S, CTAS) BaShape<FMT, D, NT, W, S, CTAS>
 #define BA_GO(FMT, D, NT, W, S, W2, S2) ba_go<BA_SHAPE(FMT, D, NT, W, S, 1), BA_SHAPE(FMT, D, NT, W2, S2, 2)>(P, pairs, most, sms, stream)
 #define BA_PICK(FMT, D, A1, A2, A3, A4) \
-  (P.mrows == 8 ? BA_GO(FMT, D, 1, A1) : P.mrows == 16 ? BA_GO(FMT, D, 2, A2) : P.mrows == 24 ? BA_GO(FMT, D, 3, A3) : BA_GO(FMT, D, 4, A4))
+  (mrows == 8 ? BA_GO(FMT, D, 1, A1) : mrows == 16 ? BA_GO(FMT, D, 2, A2) : mrows == 24 ? BA_GO(FMT, D, 3, A3) : BA_GO(FMT, D, 4, A4))
   // (each: warps and stages of a CTA with an SM to itself, then of one of two)
 #define X(...) __VA_ARGS__
   if (a->format == ECHO_BLOCK_FP4)
