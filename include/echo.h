@@ -588,8 +588,8 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  * 1 <= n_q <= 64, n_q * n_heads / n_kv_heads <= 1024.  Launches 1 kernel, or 2 when
  * contexts are cut into pieces (the second merges their partial results): the choice goes by
  * B, the heads and how long a context may be (max_blocks, window), not by the contexts, so a
- * captured call serves any contexts.  The kernel depends on format, head_dim and
- * n_q * n_heads / n_kv_heads: make one call of a kind outside capture first.
+ * captured call serves any contexts.  The kernel depends on format, head_dim, n_q * n_heads /
+ * n_kv_heads, B and max_blocks: make one call of a kind outside capture first.
  */
 typedef struct echo_block_attention_args {
     const uint16_t *q;
