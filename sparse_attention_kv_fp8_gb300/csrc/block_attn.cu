@@ -759,7 +759,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
-        if (m[nt][e] == kBaNone) m[nt][e] = -INFINITY;
+        // no token seen (a sum that is NaN is a row's all the same: its maximum stays finite, so
+        // that no merge takes it for an empty part)
+        if (m[nt][e] == kBaNone && l[nt][e] == 0.f) m[nt][e] = -INFINITY;
         if (r8 == 0) ml[warp * C::kRows + nt * 8 + 2 * c4 + e] = make_float2(m[nt][e], l[nt][e]);
       }
     __syncthreads();
