@@ -581,7 +581,9 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  *           [B][n_q][n_heads] fp32 device, optional
  *   workspace  device, 256-byte aligned, echo_block_attention_workspace_bytes() bytes; one
  *           workspace serves calls that run one after another
- * Tokens no query of the request sees may hold any bytes.  Scores, the softmax and both
+ * Tokens no query of the request sees may hold any bytes.  A key that is not finite touches
+ * the queries that see its token and no other; so does a value, whose dimension of `out` is
+ * then not finite (infinite values may give NaN).  Scores, the softmax and both
  * sums are fp32; the softmax weights enter the value product as two bf16 terms (bf16 rows)
  * or in fp16 (ECHO_BLOCK_FP4).  ECHO_BLOCK_FP4 takes the queries to fp16 scaled by a power of two
  * of their row: an entry below 2^-24 of its row's largest is rounded to that grid.

@@ -503,6 +503,10 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   store_q();
   __syncthreads();
 
+  // the context of a row's query, and whether a query with context n sees position p
+  auto len_at = [&](int rq) { return cur.v.len - (P.n_q - 1 - min(rq / P.group, P.n_q - 1)); };
+  auto sees = [&](int n, int p) { return p < n && (P.window == 0 || p >= n - P.window || p < P.sinks); };
+
   int st = 0, g = warp, rd = 0;  // stage, chunk and list entry to compute
   for (;;) {  // the (b, hm) of this range, one after another
     const int pend = min(cur.end, n_chunks);
@@ -617,20 +621,62 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
 
       // ----- softmax -----
       if (edge) {
+        // Tokens that some of the request's queries see and others do not (n_q > 1): a value that is
+        // not finite would reach the others as 0 * infinity.  It becomes NaN here, in the rows that
+        // see the token, and the product below finds a zero in its place.
+        if (P.n_q > 1) {
+#pragma unroll
+          for (int u = 0; u < C::kSubs; ++u) {
+            const int first = cur.v.len - (P.n_q - 1) - pos[u], from = P.window ? cur.v.len - P.window - pos[u] : 0;
+            const uint32_t by_all = low_bits(first) & (~low_bits(from) | low_bits(P.sinks - pos[u]));
+            for (uint32_t some = flags[u] & 0xffffu & ~by_all; some; some &= some - 1) {  // (the same in all lanes)
+              const int t = __ffs(some) - 1;
+              uint8_t *vp = stage_base + st * C::kStageBytes + u * C::kSubBytes;
+              // what is not finite among the token's entries of this lane's output: bit 2 j + k of
+              // tile j's row r8 + 8 k (in 4 bits a NaN scale, of all of them at once)
+              uint32_t bad = 0;
+              uint8_t *sc = vp + Fp4Sub<D>::kValueScales + (t >> 3) * (D / 2) + (D == 128 ? r8 : r8 >> 1) * 8 + (t & 7);
+              auto entry = [&](int i) {  // row r8 + 8 (i % 2) of tile i / 2
+                return reinterpret_cast<uint16_t *>(vp + kSubTokens * D * 2 + t * (2 * D) + ((i ^ (t & 7)) << 4) + 2 * r8);
+              };
+              if constexpr (C::kFp4) {
+                bad = (*sc & 0x7f) == 0x7f ? ~0u : 0u;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2 * C::kSteps; ++i) bad |= (*entry(i) & 0x7f80) == 0x7f80 ? 1u << i : 0u;
+              }
+              if (!__any_sync(~0u, bad != 0)) continue;
+              __syncwarp();  // (read by every lane that shares it, then overwritten)
+              if constexpr (C::kFp4) {
+                if (bad) *sc = 0;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2 * C::kSteps; ++i)
+                  if (bad >> i & 1) *entry(i) = 0;
+              }
+              __syncwarp();
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (sees(len_at(row0 + nt * 8 + 2 * c4 + e), pos[u] + t))
+#pragma unroll
+                    for (int i = 0; i < 2 * C::kSteps; ++i)
+                      if (bad >> i & 1) o[i / 2][nt][e + 2 * (i % 2)] = NAN;
+            }
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             // tokens below which this column's query sees
-            const int j = min((row0 + nt * 8 + 2 * c4 + e) / P.group, P.n_q - 1), n = cur.v.len - (P.n_q - 1 - j);
+            const int n = len_at(row0 + nt * 8 + 2 * c4 + e);
 #pragma unroll
             for (int u = 0; u < C::kSubs; ++u)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int p = pos[u] + r8 + 8 * k;
-                const bool see = p < n && (P.window == 0 || p >= n - P.window || p < P.sinks);
-                s[u][nt][e + 2 * k] = see ? s[u][nt][e + 2 * k] : -INFINITY;
-              }
+              for (int k = 0; k < 2; ++k)
+                s[u][nt][e + 2 * k] = sees(n, pos[u] + r8 + 8 * k) ? s[u][nt][e + 2 * k] : -INFINITY;
           }
       }
       bool grow = false;
