@@ -587,7 +587,8 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  * sums are fp32; the softmax weights enter the value product as two bf16 terms (bf16 rows)
  * or in fp16 (ECHO_BLOCK_FP4).  ECHO_BLOCK_FP4 takes the queries to fp16 scaled by a power of two
  * of their row: an entry below 2^-24 of its row's largest is rounded to that grid.
- * 1 <= n_q <= 64, n_q * n_heads / n_kv_heads <= 1024.  Launches 1 kernel, or 2 when
+ * Limits: n_q in [1, 64], n_heads <= 65536, n_q * n_heads / n_kv_heads <= 1024, and B * n_kv_heads *
+ * ceil(n_q * n_heads / n_kv_heads / 32) * max_blocks * block_tokens / 16 below 2^37.  Launches 1 kernel, or 2 when
  * contexts are cut into pieces (the second merges their partial results): the choice goes by
  * B, the heads and how long a context may be (max_blocks, window), not by the contexts, so a
  * captured call serves any contexts.  The kernel depends on format, head_dim, n_q * n_heads /

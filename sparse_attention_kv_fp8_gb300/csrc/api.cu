@@ -481,7 +481,12 @@ int echo_block_attention(const echo_block_attention_args *a, void *stream) {
   REQUIRE(a->sinks >= 0 && a->window >= 0 && a->sinks <= (1 << 30) && a->window <= (1 << 30), "sinks and window must be in [0, 2^30]");
   REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
   REQUIRE(std::isfinite(a->scale), "scale must be finite");
+  REQUIRE(a->n_heads <= 65536, "too many heads");
   REQUIRE(static_cast<long long>(a->B) * a->n_q * a->n_heads <= (1ll << 31) - 1, "B * n_q * n_heads too large");
+  // (a CTA counts its share of all sub-blocks in 31 bits)
+  const long long groups = (static_cast<long long>(a->n_q) * (a->n_heads / a->n_kv_heads) + 31) / 32;
+  REQUIRE(a->B * groups * a->n_kv_heads * a->max_blocks * (a->block_tokens / echo::kSubTokens) < (1ll << 37),
+          "contexts too large: B * n_kv_heads * row groups * max_blocks * block_tokens / 16 must be below 2^37");
   if (a->B == 0) return ECHO_OK;
   REQUIRE(a->q && a->rows && a->table && a->ctx_len && a->out && a->workspace, "block attention pointer is NULL");
   REQUIRE(aligned(a->q, 16) && aligned(a->rows, 16) && aligned(a->out, 16), "q, rows and out must be 16-byte aligned");
