@@ -1171,8 +1171,9 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   P.part_ml = reinterpret_cast<float *>(P.tail + echo::kBaMaxGrid);
   P.part_o = P.part_ml + 2 * static_cast<size_t>(echo::kBaMaxGrid) * pad * 2;
   int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "block attention device");
   const int64_t pairs = static_cast<int64_t>(P.B) * P.n_kv * P.mgroups;
   // tokens a context can show at most
   int64_t most = static_cast<int64_t>(P.max_blocks) * a->block_tokens;
