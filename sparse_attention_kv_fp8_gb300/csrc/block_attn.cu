@@ -46,14 +46,13 @@
 // 0.8 us to merge the warps, 1.3 us a cluster, 4 us a second kernel).
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "block_rows.cuh"
 #include "cluster_select.cuh"
 
 namespace echo {
 
-constexpr int kBaMaxGrid = 456;   // CTAs of a split call (workspace pieces: two per CTA)
+constexpr int kBaMaxGrid = 304;   // CTAs of a cut call: two on each of 152 SMs (workspace pieces: two per CTA)
 constexpr float kBaLazy = 8.f;    // log2 of how far a score may exceed the running maximum
 // fp16 softmax weights are kept 2^7 up: at most 2^(7 + 8), and the subnormals (a grid of
 // 2^-24) begin 2^-21 below the running maximum instead of 2^-14
@@ -1124,15 +1123,13 @@ static int ba_go(const echo::BlockAttnParams &P, int64_t pairs, int64_t most, in
   constexpr int64_t extra = dims * (C::kRows > 16 ? 1024 : C::kFp4 ? 1536 : 1280);
   const int64_t cut = pairs * most / sms + extra;
   int dev = 0;
-  if constexpr (!std::is_void<Narrow>::value) {
-    const int64_t waves = (pairs + 2 * sms - 1) / (2 * sms);
-    const bool whole = most <= 4 * extra && 2 * waves * most <= cut + pairs * border / sms;
-    // (cutting with two CTAs an SM, one computes while the other merges: 512 pairs of 8192 tokens
-    // in 4 bits 109 -> 103 us, 256 of 16384 101 -> 100, but 128 of 131072 318 -> 331)
-    if (pairs > sms && (whole || (C::kFp4 && C::kRows == 8 && most <= 16384))) {
-      if (int rr = Narrow::prepare(&dev)) return rr;
-      return Narrow::launch(P, whole ? 1 : 0, pairs, sms, stream);
-    }
+  const int64_t waves = (pairs + 2 * sms - 1) / (2 * sms);
+  const bool whole = most <= 4 * extra && 2 * waves * most <= cut + pairs * border / sms;
+  // (cutting with two CTAs an SM, one computes while the other merges: 512 pairs of 8192 tokens
+  // in 4 bits 109 -> 103 us, 256 of 16384 101 -> 100, but 128 of 131072 318 -> 331)
+  if (pairs > sms && (whole || (C::kFp4 && C::kRows == 8 && most <= 16384))) {
+    if (int rr = Narrow::prepare(&dev)) return rr;
+    return Narrow::launch(P, whole ? 1 : 0, pairs, sms, stream);
   }
   if (int rr = Wide::prepare(&dev)) return rr;
   // the largest cluster that the device holds for every pair at once and whose warps all get a

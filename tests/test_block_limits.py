@@ -25,3 +25,11 @@ def test_attention_accepts_large_tables(lib):  # noqa: F811
     a = attn_args(B=1 << 13, n_heads=8, n_kv_heads=8, block_tokens=256, max_blocks=(1 << 16) - 1, workspace_bytes=1)
     assert lib.echo_block_attention(ctypes.byref(a), None) == echo.ECHO_EINVAL
     assert b"smaller" in lib.echo_last_error_string(), lib.echo_last_error_string()
+
+
+@pytest.mark.parametrize("rows,D,kept", [(8, 128, 8), (20, 64, 32), (1024, 128, 32)])
+def test_a_workspace_holds_what_the_largest_grid_writes(lib, rows, D, kept):  # noqa: F811
+    """Two CTAs on each of 152 SMs leave two partial results and a work item each, no more."""
+    n = ctypes.c_size_t()
+    assert lib.echo_block_attention_workspace_bytes(rows, D, ctypes.byref(n)) == echo.ECHO_OK
+    assert n.value == 304 * (16 + 2 * kept * (D + 2) * 4)
