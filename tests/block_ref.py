@@ -179,3 +179,21 @@ def block_tables(old, new, bs, table, free, count, max_new):
                 slot[i], pos[i] = table[b, p // bs] * bs + p % bs, p
         cu.append(cu[-1] + max(0, new[b] - old[b]))
     return table, free, len(stack), slot, pos, np.array(cu, np.int32), np.where(ok, new, old), not ok.all()
+
+
+def two_term_bounds(D, n, out, lse, av, mag, tiny, sv):
+    """attention_bounds of bf16 rows for softmax weights that enter the value product as two bf16
+    terms: what the first leaves out is at most 2^-8 of the weight, and the second is off by at
+    most 2^-8 of that, 2^-16 of the weight in all (a single term: 2^-8).  The product adds 2 n
+    terms, 16 at a time, each addition off by up to 2^-23 (the tensor cores cut off)."""
+    d = (D + 4) * 2.0 ** -24 * mag + 2.0 ** -22
+    rel = 2.0 ** -16 + 2.5 * d + (4 * n + 64) * 2.0 ** -24
+    return 2.0 ** -8 * np.abs(out) + rel[..., None] * av * (1 + 2.0 ** -7)
+
+
+def opposite_values(g, n, D):
+    """n tokens' values [n][D] (bf16), each odd token the negative of the one before it: with near
+    equal weights their sum is far below its terms."""
+    v = bf16_round(g.uniform(2, 4, (n, D)) * g.choice([-1.0, 1.0], (n, D)))
+    v[1::2] = -v[0:n - n % 2:2]
+    return v
