@@ -526,8 +526,9 @@ int echo_block_tables(const echo_block_tables_args *args, void *stream);
  *      read of the cache gives them (ECHO_BLOCK_FP4: after quantisation)
  *   slot_map [T] int32 device, optional (NULL: no cache write): token i goes to token
  *      slot % block_tokens of block slot / block_tokens; negative: not written.  A row
- *      outside [0, n_rows) sets ECHO_DEV_BAD_INDEX and is not written; two tokens of one
- *      call with the same slot leave one of the two there
+ *      outside [0, n_rows) sets ECHO_DEV_BAD_INDEX and is not written.  Two tokens of one
+ *      call must not have the same slot: it would hold some bytes of the one and some of the
+ *      other (no other slot is touched)
  *   rows     [n_rows][R] cache rows, 16-byte aligned: device memory, or the pinned, mapped
  *      host pool (written through)
  * rope_dim is a multiple of 16 up to head_dim.  Launches 1 kernel.
