@@ -446,6 +446,10 @@ int echo_sparse_mla_decode(const echo_mla_args *args, void *stream);
  *     Written as s = e4m3(max |x| / 6) (round to nearest even, at most 448) and the
  *     nearest code to x / s (ties to the even code): 4.5 bits per entry.  Values above
  *     2688 saturate, infinities and NaN are not kept, and a zero may carry either sign.
+ *     Groups whose largest entry is 6 * 2^-10 (0.00586) or less become zeros, and below
+ *     6 * 2^-6 (0.094) the scale has fewer than its 4 significant bits: for small keys or
+ *     values, such as those of layers without a norm, let the rows hold them times powers of
+ *     two, k_shift and v_shift in [-32, 32] of the calls that write and read them.
  * With a table shared by the KV heads, block `id` of KV head h is row id * n_kv_heads + h.
  * The kernels of the block calls are programmatic launches: they may be made ready while the
  * kernel before them on the stream still runs, and touch no memory until it has completed.
@@ -531,6 +535,8 @@ int echo_block_tables(const echo_block_tables_args *args, void *stream);
  *      other (no other slot is touched)
  *   rows     [n_rows][R] cache rows, 16-byte aligned: device memory, or the pinned, mapped
  *      host pool (written through)
+ *   k_shift, v_shift  ECHO_BLOCK_FP4: the rows take keys * 2^k_shift and values * 2^v_shift
+ *      (k_out and v_out are without them); 0 for ECHO_BLOCK_BF16
  * rope_dim is a multiple of 16 up to head_dim.  Launches 1 kernel.
  */
 typedef struct echo_qk_norm_rope_args {
@@ -553,6 +559,7 @@ typedef struct echo_qk_norm_rope_args {
     uint16_t *rows;
     int32_t n_rows, format, block_tokens;
     int32_t *dev_status;
+    int32_t k_shift, v_shift;
 } echo_qk_norm_rope_args;
 
 int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
@@ -582,6 +589,7 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  *           [B][n_q][n_heads] fp32 device, optional
  *   workspace  device, 256-byte aligned, echo_block_attention_workspace_bytes() bytes; one
  *           workspace serves calls that run one after another
+ *   k_shift, v_shift  as the rows were written: they hold keys * 2^k_shift, values * 2^v_shift
  * Tokens no query of the request sees may hold any bytes.  A key that is not finite touches
  * the queries that see its token and no other; so does a value, whose dimension of `out` is
  * then not finite (infinite values may give NaN).  Scores, the softmax and both
@@ -611,6 +619,7 @@ typedef struct echo_block_attention_args {
     void *workspace;
     size_t workspace_bytes;
     int32_t *dev_status;
+    int32_t k_shift, v_shift;
 } echo_block_attention_args;
 
 int echo_block_attention_workspace_bytes(int32_t rows_per_kv_head, int32_t head_dim, size_t *bytes);
@@ -774,7 +783,7 @@ const char *echo_last_error_string(void);
    1.2: echo_prefill_indexer_score, echo_ema_update_strided, n_q up to 65536 in
    top-k and recall; 1.3: echo_sparse_mla_decode; 1.4: echo_pool.row_elems,
    echo_stage.flags; 1.5: echo_pool_validate, echo_pool_validate_host; 1.6: block rows,
-   echo_block_tables, echo_qk_norm_rope, echo_block_attention). */
+   echo_block_tables, echo_qk_norm_rope, echo_block_attention; 1.7: k_shift, v_shift). */
 int32_t echo_version(void);
 
 /* Storage law of the metadata arrays of one pool (section 5.1): 4*n_h + 13*n_g. */

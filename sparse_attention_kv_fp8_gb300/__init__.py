@@ -97,7 +97,8 @@ class c_qk_norm_rope_args(ctypes.Structure):
                 ("T", _I32), ("n_heads", _I32), ("n_kv_heads", _I32), ("head_dim", _I32), ("q_weight", _P),
                 ("k_weight", _P), ("eps", ctypes.c_float), ("interleaved", _I32), ("cos_sin", _P), ("max_pos", _I32),
                 ("rope_dim", _I32), ("positions", _P), ("q_out", _P), ("k_out", _P), ("v_out", _P), ("slot_map", _P),
-                ("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32), ("dev_status", _P)]
+                ("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32), ("dev_status", _P),
+                ("k_shift", _I32), ("v_shift", _I32)]
 
 
 class c_block_attention_args(ctypes.Structure):
@@ -105,7 +106,8 @@ class c_block_attention_args(ctypes.Structure):
                 ("head_dim", _I32), ("table", _P), ("sel", _P), ("table_heads", _I32), ("max_blocks", _I32),
                 ("ctx_len", _P), ("B", _I32), ("n_q", _I32), ("n_heads", _I32), ("n_kv_heads", _I32),
                 ("sinks", _I32), ("window", _I32), ("scale", ctypes.c_float), ("out", _P), ("lse", _P),
-                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("dev_status", _P)]
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("dev_status", _P),
+                ("k_shift", _I32), ("v_shift", _I32)]
 
 
 _lib = None
@@ -533,12 +535,13 @@ def _heads(t, name: str, T: int, H, D: int):
 
 def make_qk_norm_rope_args(q, k, v, positions, cos_sin, q_out, q_weight=None, k_weight=None, eps: float = 1e-6,
                            interleaved: bool = False, slot_map=None, rows=None, fmt: int = BLOCK_BF16,
-                           block_tokens: int = 16, k_out=None, v_out=None,
-                           dev_status=None) -> c_qk_norm_rope_args:
+                           block_tokens: int = 16, k_out=None, v_out=None, dev_status=None, k_shift: int = 0,
+                           v_shift: int = 0) -> c_qk_norm_rope_args:
     """Arguments of echo_qk_norm_rope (see include/echo.h).  q [T][n_heads][D], k, v
     [T][n_kv_heads][D] bf16 (views of a fused projection: heads contiguous, any token
     stride); positions, slot_map [T] int32; cos_sin [max_pos][rope_dim] fp32; weights [D]
-    fp32; rows [n_rows][R] 16-bit, device or pinned host; outputs contiguous."""
+    fp32; rows [n_rows][R] 16-bit, device or pinned host; outputs contiguous.  4-bit rows hold
+    keys * 2^k_shift and values * 2^v_shift: raise them where entries lie below about 0.1."""
     T, H, D = (int(n) for n in q.shape)
     Hk = int(k.shape[1])
     a = c_qk_norm_rope_args()
@@ -563,7 +566,7 @@ def make_qk_norm_rope_args(q, k, v, positions, cos_sin, q_out, q_weight=None, k_
             raise EchoError("rows must be a CUDA tensor or pinned host memory")
         a.slot_map = _typed(slot_map, "slot_map", _INT, (T,))
         a.rows, a.n_rows = _typed(rows, "rows", (rows.dtype,)) if rows.is_cuda else rows.data_ptr(), int(rows.shape[0])
-    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a.dev_status, a.k_shift, a.v_shift = _typed(dev_status, "dev_status", _INT), int(k_shift), int(v_shift)
     a._keep = (q, k, v, positions, cos_sin, q_out, q_weight, k_weight, slot_map, rows, k_out, v_out, dev_status)
     return a
 
@@ -589,11 +592,12 @@ class BlockAttentionWorkspace:
 
 def make_block_attention_args(q, rows, table, ctx_len, n_kv_heads: int, scale: float, out, lse,
                               ws: BlockAttentionWorkspace, fmt: int = BLOCK_BF16, block_tokens: int = 64, sel=None,
-                              sinks: int = 0, window: int = 0, dev_status=None) -> c_block_attention_args:
+                              sinks: int = 0, window: int = 0, dev_status=None, k_shift: int = 0,
+                              v_shift: int = 0) -> c_block_attention_args:
     """Arguments of echo_block_attention (see include/echo.h).  q, out [B][n_q][n_heads][D]
     bf16; rows [n_rows][R] 16-bit; table (and sel) int32 [B][max_blocks] of block ids shared
     by the KV heads, or [B][n_kv_heads][max_blocks] of rows; ctx_len [B] int32; lse
-    [B][n_q][n_heads] fp32 or None."""
+    [B][n_q][n_heads] fp32 or None; k_shift, v_shift as the (4-bit) rows were written."""
     B, n_q, H, D = (int(n) for n in q.shape)
     if rows.dim() != 2 or rows.element_size() != 2:
         raise EchoError("rows must be 16-bit [n_rows][R]")
@@ -614,7 +618,7 @@ def make_block_attention_args(q, rows, table, ctx_len, n_kv_heads: int, scale: f
     a.lse = _typed(lse, "lse", _F32, (B, n_q, H))
     _typed(ws.buf, "workspace", (torch.uint8,))
     a.workspace, a.workspace_bytes = ws.base, ws.bytes
-    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a.dev_status, a.k_shift, a.v_shift = _typed(dev_status, "dev_status", _INT), int(k_shift), int(v_shift)
     a._keep = (q, rows, table, ctx_len, out, lse, ws, sel, dev_status)
     return a
 

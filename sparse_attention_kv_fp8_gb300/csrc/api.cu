@@ -168,7 +168,7 @@ int echo_selftest_wait_timeout(int32_t which, int32_t *dev_status, void *stream)
   return launch_wait_probe(which, dev_status, static_cast<cudaStream_t>(stream));
 }
 
-int32_t echo_version(void) { return (1 << 16) | 6; }
+int32_t echo_version(void) { return (1 << 16) | 7; }
 
 int64_t echo_metadata_bytes(int64_t n_h, int64_t n_g) {
   return static_cast<int64_t>(sizeof(int32_t)) * n_h +
@@ -397,6 +397,14 @@ static int check_block_rows(int32_t format, int32_t block_tokens, int32_t head_d
   return ECHO_OK;
 }
 
+// the powers of two that 4-bit rows are written and read with
+static int check_shifts(int32_t format, int32_t k_shift, int32_t v_shift) {
+  REQUIRE(format == ECHO_BLOCK_FP4 || (k_shift == 0 && v_shift == 0), "k_shift and v_shift are for 4-bit rows");
+  REQUIRE(k_shift >= -32 && k_shift <= 32 && v_shift >= -32 && v_shift <= 32, "k_shift and v_shift must be in [-32, 32] (got %d, %d)",
+          k_shift, v_shift);
+  return ECHO_OK;
+}
+
 int echo_block_row_elems(int32_t format, int32_t block_tokens, int32_t head_dim, int32_t *row_elems) {
   g_err[0] = 0;
   REQUIRE(row_elems, "row_elems is NULL");
@@ -438,6 +446,7 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *a, void *stream) {
   REQUIRE(std::isfinite(a->eps) && a->eps >= 0.f, "eps must be finite and >= 0");
   REQUIRE(a->interleaved == 0 || a->interleaved == 1, "interleaved must be 0 or 1");
   TRY(check_block_rows(a->format, a->slot_map ? a->block_tokens : echo::kSubTokens, a->head_dim));
+  TRY(check_shifts(a->format, a->k_shift, a->v_shift));
   REQUIRE(static_cast<long long>(a->T) * (a->n_heads + 2ll * a->n_kv_heads) * a->head_dim <= (1ll << 38), "call too large");
   if (a->T == 0) return ECHO_OK;
   REQUIRE(a->q && a->k && a->cos_sin && a->positions && a->q_out, "norm + rope pointer is NULL");
@@ -481,6 +490,8 @@ int echo_block_attention(const echo_block_attention_args *a, void *stream) {
   REQUIRE(a->sinks >= 0 && a->window >= 0 && a->sinks <= (1 << 30) && a->window <= (1 << 30), "sinks and window must be in [0, 2^30]");
   REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
   REQUIRE(std::isfinite(a->scale), "scale must be finite");
+  TRY(check_shifts(a->format, a->k_shift, a->v_shift));
+  REQUIRE(std::fabs(std::ldexp(static_cast<double>(a->scale), -a->k_shift)) < 1e38, "scale * 2^-k_shift must be finite");
   REQUIRE(a->n_heads <= 65536, "too many heads");
   REQUIRE(static_cast<long long>(a->B) * a->n_q * a->n_heads <= (1ll << 31) - 1, "B * n_q * n_heads too large");
   // (a CTA counts its share of all sub-blocks in 31 bits)

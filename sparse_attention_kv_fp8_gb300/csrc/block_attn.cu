@@ -73,7 +73,8 @@ struct BlockAttnParams {
   int32_t B, n_q, n_heads, n_kv, group;  // group: query heads per KV head
   int32_t mgroups;                   // row groups of a KV head (the kernel's kRows each)
   int32_t sinks, window;
-  float scale_log2;                  // |scale| log2 e
+  float scale_log2;                  // |scale| log2 e, over the keys' power of two
+  float v_scale;                     // one over the values' power of two
   uint32_t q_sign;                   // 0x80008000 for a negative scale
   uint16_t *out;
   float *lse;
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
         } else {
           const int64_t oh = row_index(cur, row);
           if (oh >= 0) {
-            const float inv = v.y > 0.f ? 1.f / v.y : v.y;  // (a NaN sum stays one)
+            const float inv = v.y > 0.f ? P.v_scale / v.y : v.y;  // (a NaN sum stays one)
             *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
             *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
             if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y);
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
         sum += v[r].y * f;
         y.x += x[r].x * f, y.y += x[r].y * f, y.z += x[r].z * f, y.w += x[r].w * f;
       }
-      const float inv = sum > 0.f ? 1.f / sum : sum;
+      const float inv = sum > 0.f ? P.v_scale / sum : sum;
       *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
           make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
       if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum);
@@ -1007,7 +1008,7 @@ __global__ void __launch_bounds__(BaComb<D, kPair>::kThreads) block_attn_combine
   }
   const int j = rq / P.group;
   const int64_t oh = (static_cast<int64_t>(tail.x) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
-  const float inv = sum > 0.f ? 1.f / sum : sum;
+  const float inv = sum > 0.f ? P.v_scale / sum : sum;
   *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
       make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
   if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum);
@@ -1159,7 +1160,8 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   // (48 rows as 24 + 24, not 32 + 16: 12 requests of up to 20000 tokens in 4 bits 200 -> 151 us)
   const int mrows = ((rows + P.mgroups - 1) / P.mgroups + 7) / 8 * 8;
   P.sinks = a->sinks, P.window = a->window;
-  P.scale_log2 = std::fabs(a->scale) * 1.4426950408889634f;
+  P.scale_log2 = std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift);
+  P.v_scale = std::ldexp(1.f, -a->v_shift);
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
   P.out = a->out, P.lse = a->lse;
   P.status = a->dev_status;

@@ -11,6 +11,8 @@
 // reaches here (0.87; 8-byte accesses and 32 warps an SM: with one 16-byte load per lane, the
 // partners shuffled between lanes and 16 warps it was 180 us); 8191 tokens x 40 heads of 64
 // into a 4-bit cache 19.8 us (0.69; first loads and tail), a decode step's tokens 3 us (latency).
+#include <cmath>
+
 #include "block_rows.cuh"
 
 namespace echo {
@@ -31,6 +33,7 @@ struct RopeParams {
   const int32_t *slot_map;
   uint16_t *rows;
   int32_t n_rows, format, bs;
+  float k_up, v_up, k_down, v_down;    // 4-bit rows: 2^shift of keys and values, and the inverse
   int64_t row_elems;
   int32_t span, kv_span;               // heads of a warp: q, and k or v
   int32_t q_chunks, k_chunks, chunks;  // warps per token group: of q, of k (and of v), in all
@@ -63,15 +66,16 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
 // borders between scales (5 bits) likewise.  A product with the reciprocal, off by 2^-22,
 // rounded to fp16 (11 bits), is the border itself in the first case and stays on its side in
 // the second, and the hardware's round-half-to-even then decides as the definition does.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t &scale) {
+// Taken times a power of two `up`, which moves the scale alone.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float up, uint32_t &scale) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
   amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-  scale = e4m3_from_half(__float2half_rn(amax * (1.f / 6.f)));
+  scale = e4m3_from_half(__float2half_rn(amax * (up * (1.f / 6.f))));
   const uint32_t sh = e4m3x2_to_half2(scale);
   const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffff)));
-  const float r = s > 0.f ? __fdividef(1.f, s) : 0.f;
+  const float r = s > 0.f ? __fdividef(up, s) : 0.f;
   float y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -81,8 +85,9 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t &sca
   return e2m1x8_from_float(y);
 }
 
-// the values 8 codes stand for, as bf16 (exact: a code has 2 significant bits, a scale 4)
-__device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t scale) {
+// the values 8 codes stand for, times a power of two, as bf16 (exact: a code has 2 significant
+// bits, a scale 4)
+__device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t scale, float down) {
   uint32_t h[4];
   e2m1x8_to_half2(codes, h);
   const uint32_t s2 = e4m3x2_to_half2(scale | (scale << 8));
@@ -93,7 +98,13 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t scale) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p));
     x[2 * i] = f.x, x[2 * i + 1] = f.y;
   }
-  return pack_bf16x8(x);
+  const uint4 u = pack_bf16x8(x);
+  const __nv_bfloat162 d = __floats2bfloat162_rn(down, down);
+  auto mul = [&](uint32_t w) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w), d);
+    return *reinterpret_cast<const uint32_t *>(&y);
+  };
+  return make_uint4(mul(u.x), mul(u.y), mul(u.z), mul(u.w));
 }
 
 // Kinds of heads, in the order of a token's chunks; a warp works on one kind.
@@ -310,12 +321,13 @@ __device__ __forceinline__ void rope_rows(const RopeParams &P, const RopeDst &W,
       if (fp4) {             // (every lane: the scale is a shuffle)
         float x[8];
         unpack_bf16x8(o, x);
-        codes = quantise8(x, scale);
+        codes = quantise8(x, is_v ? P.v_up : P.k_up, scale);
       }
       if (!W.in || h + u >= h1) continue;
       uint16_t *out = is_v ? P.v_out : P.k_out;
       if (out) {
-        *reinterpret_cast<uint4 *>(out + (W.t * P.n_kv_heads + h + u) * D + d0) = fp4 ? dequantise8(codes, scale) : o;
+        *reinterpret_cast<uint4 *>(out + (W.t * P.n_kv_heads + h + u) * D + d0) =
+            fp4 ? dequantise8(codes, scale, is_v ? P.v_down : P.k_down) : o;
       }
       uint16_t *row = W.row(h + u, l == 0);
       if (!row) continue;
@@ -426,6 +438,8 @@ int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream) {
   P.slot_map = a->slot_map, P.rows = a->rows, P.n_rows = a->n_rows;
   P.format = a->format, P.bs = a->block_tokens;
   P.row_elems = echo::block_row_elems(a->format, a->block_tokens, a->head_dim);
+  P.k_up = std::ldexp(1.f, a->k_shift), P.v_up = std::ldexp(1.f, a->v_shift);
+  P.k_down = std::ldexp(1.f, -a->k_shift), P.v_down = std::ldexp(1.f, -a->v_shift);
   P.status = a->dev_status;
   // value heads have work only when something takes them
   const bool values = a->v && (a->slot_map || a->v_out);
