@@ -600,8 +600,10 @@ int echo_qk_norm_rope(const echo_qk_norm_rope_args *args, void *stream);
  * ceil(n_q * n_heads / n_kv_heads / 32) * max_blocks * block_tokens / 16 below 2^37.  Launches 1 kernel, or 2 when
  * contexts are cut into pieces (the second merges their partial results): the choice goes by
  * B, the heads and how long a context may be (max_blocks, window), not by the contexts, so a
- * captured call serves any contexts.  The kernel depends on format, head_dim, n_q * n_heads /
- * n_kv_heads, B and max_blocks: make one call of a kind outside capture first.
+ * captured call serves any contexts.  The first call that takes some form of the kernel sets
+ * it up, which belongs outside capture; the form goes by all sizes of a call (format, head_dim,
+ * block_tokens, max_blocks, B, n_q, n_heads, n_kv_heads, sinks, window, whether sel is given):
+ * make the same call, whatever its contexts, once before it is captured.
  */
 typedef struct echo_block_attention_args {
     const uint16_t *q;

@@ -3,10 +3,12 @@
 //
 // For the M = n_q * n_heads / n_kv_heads query rows that share KV head h of request b:
 //   x_p = scale * q . k_p,   out = sum_p 2^(x_p log2 e - m) v_p / l,   one pass over p
-// with the running maximum m and sum l of each row.  K and V are read once from HBM, which
-// is the bound: 4 D bytes a token and KV head in bf16, 18 D / 16 in 4 bits, against
-// 4 M D flops (M is 1 to 32, so the legacy-size matrix instructions below are never the
-// limit; a 128-row tcgen05 tile would be 7/8 padding or more).
+// with the running maximum m and sum l of each row.  K and V are read once for up to 32 rows
+// (row groups of 32 beyond that read them once each), 4 D bytes a token and KV head in bf16,
+// 18 D / 16 in 4 bits, against 4 M D flops.  In bf16 that is the bound.  4-bit rows are bound
+// by instructions, and from 16 rows on by the registers that the output takes: a tcgen05.mma
+// with tokens, then dims, as its 128 rows and the query rows as its columns would leave both
+// to tensor memory; that kernel is not written.
 //
 // sm_103a design.
 //   Transposed products: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, tokens (then
@@ -720,6 +722,10 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
           }
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
+          // (4-bit rows: one fp16 term.  Its 2^-11 of a weight takes the outputs' distance to 64
+          // bits from 1.661e-3, all of it their rounding to bf16, to 1.670e-3; a second term would
+          // give that back for 8 registers and twice the value product: 16 x 32768 tokens 93 -> 100
+          // us, 8 x 131072 with 16 rows 212 -> 257 us)
           const uint32_t a = pack2<F16>(p0, p1), b = pack2<F16>(p2, p3);
           pb[u][nt][0] = movm_t(a);
           pb[u][nt][1] = movm_t(b);

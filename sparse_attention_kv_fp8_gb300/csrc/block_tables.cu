@@ -12,10 +12,10 @@
 // sums stay in shared memory) and then takes its share of the blocks and of the list, so
 // no CTA waits for another.  A stack entry at or above `count` is read where it comes from
 // (the shrinking request's table), never from the stack the same launch is writing.
-// Bound by latency: 64 decoding requests 2.8 us (lengths, sums, search, id, store, an entry
-// per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed
-// step with a list of 2^20 entries 7.6 us (8 MB of stores would take 1.3 us; the search and
-// the divisions of 608 CTAs are most of it).
+// Bound by latency: 64 decoding requests 2.7 us (lengths, sums, search, id, store, an entry
+// per thread; four in a row per thread took 3.3 us more), 256 requests in a mixed step with a
+// list of 2^20 entries 7.6 us, of which the launch and the sums take 3.2, the list's stores (8
+// MB) and the moved blocks 2.2 to 2.9, and the searches and the table's look-ups the rest.
 #include <algorithm>
 
 #include "block_rows.cuh"

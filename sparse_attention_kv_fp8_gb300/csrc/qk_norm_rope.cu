@@ -10,7 +10,7 @@
 // 16384 tokens x (64 + 8 + 8) heads of 128 in 117 us, 5.8 TB/s of the 6.67 TB/s that a copy
 // reaches here (0.87; 8-byte accesses and 32 warps an SM: with one 16-byte load per lane, the
 // partners shuffled between lanes and 16 warps it was 180 us); 8191 tokens x 40 heads of 64
-// into a 4-bit cache 19.8 us (0.69; first loads and tail), a decode step's tokens 3 us (latency).
+// into a 4-bit cache 19.7 us (0.69; first loads and tail), a decode step's tokens 3 us (latency).
 #include <cmath>
 
 #include "block_rows.cuh"
@@ -416,8 +416,10 @@ static cudaError_t launch_rope_dim(const echo::RopeParams &P, bool values, cudaS
   if (warps <= 4096) return launch_rope<D, 1, kInter>(P, values, 1, 1, stream);
   // Long runs want 8 and more KV heads: beside a warp's 16 query heads others would have 2 (16 + 4
   // heads of 128, 8 and 4 against 16 and 8: 7311 tokens into 4-bit rows 24.2 / 31.0, 16000 into
-  // bf16 rows 42.3 / 44.5).  4-bit rows: batches of 4 spill where the quantisation stands, and
-  // long runs of batches of 2 win sooner (2 of 8 and 4, 2 of 16 and 8, 4 of 16 and 8: 64000 warps
+  // bf16 rows 42.3 / 44.5).  The kernels with batches of 4 spill 148 to 176 bytes a thread (the
+  // format is a run-time branch: those of bf16 rows hold the quantisation too, and win all the
+  // same, as above), those with batches of 2 up to 24, and 4-bit rows win with long runs of
+  // batches of 2 sooner (2 of 8 and 4, 2 of 16 and 8, 4 of 16 and 8: 64000 warps
   // 18.9 / 18.6 / 18.0, 81920 20.7 / 19.8 / 23.2, 201340 50.5 / 47.4 / 53.4).
   const bool fp4 = P.format == ECHO_BLOCK_FP4;
   if (P.n_kv_heads < 8 || warps <= (fp4 ? 65536 : 163840)) return launch_rope<D, 2, kInter>(P, values, 8, 4, stream);
