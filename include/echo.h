@@ -627,6 +627,189 @@ typedef struct echo_block_attention_args {
 int echo_block_attention_workspace_bytes(int32_t rows_per_kv_head, int32_t head_dim, size_t *bytes);
 int echo_block_attention(const echo_block_attention_args *args, void *stream);
 
+/*
+ * Block-sparse attention: summaries of blocks, a bound on the scores that a query can have in
+ * each, and the blocks of the best bounds.  A table is given as to echo_block_attention:
+ * [B][max_blocks] block ids shared by the KV heads (table_heads == 1) or
+ * [B][n_kv_heads][max_blocks] rows (table_heads == n_kv_heads); a negative entry is a block
+ * that is not held, one outside the rows counts as such and sets ECHO_DEV_BAD_INDEX, as does a
+ * length above max_blocks * block_tokens, which is clamped.
+ *
+ * echo_block_summary: the smallest and the largest entry of the keys of a cache row, per dim,
+ * over the tokens that its request holds.  Request b went from old_len[b] to new_len[b] tokens
+ * (either way); the blocks that lost or gained a token and still have one are summed up anew,
+ * the others' summaries stay.  A block in the tables of several requests has to be as full in
+ * each that changed.
+ *   rows     [n_rows][R] cache rows of `format`, 16-byte aligned
+ *   old_len  [B] int32 device, optional (NULL: 0, all blocks);  new_len [B] int32 device
+ *   summary  [n_rows][2][head_dim] bf16 device, 16-byte aligned: minima, then maxima (a NaN
+ *            among a dim's keys gives NaN); exact, of the keys as the rows hold them without
+ *            2^k_shift
+ * Limits: B <= 16384, max_blocks * block_tokens below 2^31 - 1024, B * max_blocks below 2^30.
+ * Launches 1 kernel.
+ */
+typedef struct echo_block_summary_args {
+    const uint16_t *rows;
+    int32_t n_rows, format, block_tokens, head_dim;
+    const int32_t *table;
+    int32_t table_heads, max_blocks;
+    const int32_t *old_len;
+    const int32_t *new_len;
+    int32_t B, n_kv_heads;
+    uint16_t *summary;
+    int32_t k_shift;
+    int32_t *dev_status;
+} echo_block_summary_args;
+
+int echo_block_summary(const echo_block_summary_args *args, void *stream);
+
+/*
+ * echo_block_scores: for query token j of request b, which sees len = ctx_len[b] - (n_q - 1 - j)
+ * tokens, KV head h and each of its ceil(len / block_tokens) blocks i
+ *   scores[b][j][h][i] = max over h's query heads g of sum_d max(x_d lo_d, x_d hi_d),  x = scale * q_g,
+ * at least the score of every token of the block (up to the rounding of fp32 sums); -inf for a
+ * block that is not held.  Other entries of `scores` are left as they were.  A summary that
+ * is not finite gives no particular score.
+ *   q        [B][n_q][n_heads][head_dim] bf16 device, 16-byte aligned
+ *   summary  as echo_block_summary wrote it
+ *   ctx_len  [B] int32 device
+ *   scores   [B][n_q][n_kv_heads][max_blocks] fp32 device
+ * Limits: max_blocks * block_tokens below 2^31 - 1024, B * n_kv_heads * (max_blocks / 64 + 1)
+ * and B * n_q * n_heads below 2^31.  Launches 1 kernel.
+ */
+typedef struct echo_block_scores_args {
+    const uint16_t *q;
+    const uint16_t *summary;
+    int32_t n_rows, block_tokens, head_dim;
+    const int32_t *table;
+    int32_t table_heads, max_blocks;
+    const int32_t *ctx_len;
+    int32_t B, n_q, n_heads, n_kv_heads;
+    float scale;
+    float *scores;
+    int32_t *dev_status;
+} echo_block_scores_args;
+
+int echo_block_scores(const echo_block_scores_args *args, void *stream);
+
+/*
+ * echo_block_select: the k best blocks of each query token and KV head, of the
+ * ceil(len / block_tokens) it sees (len as above): the `first` first and the `last` last ones
+ * always, then by score (a NaN comes last), ties to the lower block; blocks that are not held
+ * are left out (with a table).
+ *   scores   [B][n_q][n_kv_heads][max_blocks] fp32 device
+ *   sel      [B][n_q][n_kv_heads][k] int32 device: block indices, ascending, then -1
+ *   table    optional;  sel_rows [B][n_q][n_kv_heads][k] int32 device, optional (with a table):
+ *            the blocks' rows, -1 beside -1
+ *   len_out  [B][n_q] int32 device, optional: len (at least 0)
+ * echo_block_attention reads them with the queries folded into the requests: B * n_q requests of
+ * one query token, table = sel_rows, sel, table_heads = n_kv_heads, max_blocks = k, ctx_len =
+ * len_out.  With n_q == 1, sel is a selection for echo_prefetch_recall over a pool of block rows.
+ * Limits: k >= 1, 0 <= first, last, first + last <= k, max_blocks <= 49152, B * n_q * n_kv_heads
+ * below 2^31.  Launches 1 kernel.
+ */
+typedef struct echo_block_select_args {
+    const float *scores;
+    const int32_t *ctx_len;
+    int32_t B, n_q, n_kv_heads, block_tokens;
+    int32_t k, first, last;
+    const int32_t *table;
+    int32_t table_heads, max_blocks;
+    int32_t *sel;
+    int32_t *sel_rows;
+    int32_t *len_out;
+    int32_t *dev_status;
+} echo_block_select_args;
+
+int echo_block_select(const echo_block_select_args *args, void *stream);
+
+/*
+ * The softmax weight that cached tokens gather, and eviction by it.
+ *
+ * echo_block_weights: with the log-sum-exp that the attention over the same rows returned, for
+ * token p < ctx_len[b] of request b and KV head h
+ *   acc_out[b][h][p] = decay * acc[b][h][p] + sum over query tokens j that see p (p < len, as
+ *                      above) and h's query heads g of exp(scale * q . k_p - lse[b][j][g])
+ * where acc counts as 0 for p >= old_len[b] (tokens that are new) and the sum is 0 for tokens of
+ * blocks that are not held.  Other entries are left as they were.  A row with lse = -inf (it saw
+ * nothing) adds nothing.  acc_out may be acc.
+ *   q, rows, table, ctx_len, scale, k_shift   as to echo_block_attention (no sel, no window)
+ *   lse      [B][n_q][n_heads] fp32 device
+ *   acc, acc_out [B][n_kv_heads][max_blocks * block_tokens] fp32 device; acc is optional (NULL:
+ *            all 0, old_len must be NULL too);  old_len [B] int32 device, optional (NULL: ctx_len)
+ * Sums are fp32; ECHO_BLOCK_FP4 takes the queries to fp16 as echo_block_attention does.
+ * Limits: n_q * n_heads / n_kv_heads <= 1024, B * n_q * n_heads below 2^31, max_blocks *
+ * block_tokens below 2^31 - 1024, B * n_kv_heads * (max_blocks * block_tokens / 128 + 1) below
+ * 2^31.  Launches 1 kernel.
+ */
+typedef struct echo_block_weights_args {
+    const uint16_t *q;
+    const uint16_t *rows;
+    int32_t n_rows, format, block_tokens, head_dim;
+    const int32_t *table;
+    int32_t table_heads, max_blocks;
+    const int32_t *ctx_len;
+    const int32_t *old_len;
+    int32_t B, n_q, n_heads, n_kv_heads;
+    float scale;
+    const float *lse;
+    const float *acc;
+    float *acc_out;
+    float decay;
+    int32_t k_shift;
+    int32_t *dev_status;
+} echo_block_weights_args;
+
+int echo_block_weights(const echo_block_weights_args *args, void *stream);
+
+/*
+ * echo_block_evict: a request whose len[b] tokens exceed `keep` is cut to `keep`, each KV head on
+ * its own: the tokens of the first `sinks` slots and of the last `recent` positions stay, then
+ * the heaviest by acc (a NaN is the lightest), ties to the lower slot.  Tokens that stay keep
+ * their slots below `keep`; those at or above it move, in order, into the slots that fell free.
+ * Attention without a window does not mind the order of a cache.
+ *   rows     [n_rows][R] cache rows of `format`, 16-byte aligned: keys and values move as they are
+ *   len      [B] int32 device: tokens held (clamped as above);  len_out [B] int32 device, another
+ *            address: min(len, keep).  echo_block_tables from len to len_out then returns the
+ *            blocks that are no longer needed (before any of them is appended to)
+ *   acc, acc_out [B][n_kv_heads][max_blocks * block_tokens] fp32 device: weights by slot before and
+ *            after; entries past len_out are left as they were.  acc_out may be acc
+ *   pos, pos_out optional, together with pos_len and next_pos, needed for recent > 0; laid out as
+ *            acc, int32: the position of each slot's token.  pos is read below pos_len[b]; the
+ *            slots from there up to len[b] hold the newest tokens, the last of them at position
+ *            next_pos[b] - 1.  pos_out may be pos
+ * With acc_out and pos_out apart from acc and pos a call that is repeated on the same inputs gives
+ * the same outputs.  A token of a block that is not held, or whose row is outside the rows, is
+ * not moved, with ECHO_DEV_BAD_INDEX.
+ *   workspace  device, 256-byte aligned, echo_block_evict_workspace_bytes() bytes; one workspace
+ *            serves calls that run one after another
+ * Limits: keep >= 1, 0 <= sinks, recent, sinks + recent <= keep, max_blocks * block_tokens below
+ * 2^31 - 1024, B * n_kv_heads below 2^26.  Launches 1 kernel, or 2 where more than 256 tokens of
+ * a request and KV head may move.
+ */
+typedef struct echo_block_evict_args {
+    uint16_t *rows;
+    int32_t n_rows, format, block_tokens, head_dim;
+    const int32_t *table;
+    int32_t table_heads, max_blocks;
+    const int32_t *len;
+    int32_t *len_out;
+    int32_t B, n_kv_heads;
+    int32_t keep, sinks, recent;
+    const float *acc;
+    float *acc_out;
+    const int32_t *pos;
+    int32_t *pos_out;
+    const int32_t *pos_len;
+    const int32_t *next_pos;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *dev_status;
+} echo_block_evict_args;
+
+int echo_block_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t keep, size_t *bytes);
+int echo_block_evict(const echo_block_evict_args *args, void *stream);
+
 /* Stages of echo_decode_step, in order (timing events are recorded before each
    stage and after the last).  The EMA is computed by the recall's last kernel, so
    the ECHO_STAGE_EMA interval is empty; the constant is kept for the event layout. */
@@ -785,7 +968,9 @@ const char *echo_last_error_string(void);
    1.2: echo_prefill_indexer_score, echo_ema_update_strided, n_q up to 65536 in
    top-k and recall; 1.3: echo_sparse_mla_decode; 1.4: echo_pool.row_elems,
    echo_stage.flags; 1.5: echo_pool_validate, echo_pool_validate_host; 1.6: block rows,
-   echo_block_tables, echo_qk_norm_rope, echo_block_attention; 1.7: k_shift, v_shift). */
+   echo_block_tables, echo_qk_norm_rope, echo_block_attention; 1.7: k_shift, v_shift;
+   1.8: echo_block_summary, echo_block_scores, echo_block_select, echo_block_weights,
+   echo_block_evict). */
 int32_t echo_version(void);
 
 /* Storage law of the metadata arrays of one pool (section 5.1): 4*n_h + 13*n_g. */

@@ -110,6 +110,42 @@ class c_block_attention_args(ctypes.Structure):
                 ("k_shift", _I32), ("v_shift", _I32)]
 
 
+class c_block_summary_args(ctypes.Structure):
+    _fields_ = [("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32), ("head_dim", _I32),
+                ("table", _P), ("table_heads", _I32), ("max_blocks", _I32), ("old_len", _P), ("new_len", _P),
+                ("B", _I32), ("n_kv_heads", _I32), ("summary", _P), ("k_shift", _I32), ("dev_status", _P)]
+
+
+class c_block_scores_args(ctypes.Structure):
+    _fields_ = [("q", _P), ("summary", _P), ("n_rows", _I32), ("block_tokens", _I32), ("head_dim", _I32),
+                ("table", _P), ("table_heads", _I32), ("max_blocks", _I32), ("ctx_len", _P), ("B", _I32),
+                ("n_q", _I32), ("n_heads", _I32), ("n_kv_heads", _I32), ("scale", ctypes.c_float), ("scores", _P),
+                ("dev_status", _P)]
+
+
+class c_block_select_args(ctypes.Structure):
+    _fields_ = [("scores", _P), ("ctx_len", _P), ("B", _I32), ("n_q", _I32), ("n_kv_heads", _I32),
+                ("block_tokens", _I32), ("k", _I32), ("first", _I32), ("last", _I32), ("table", _P),
+                ("table_heads", _I32), ("max_blocks", _I32), ("sel", _P), ("sel_rows", _P), ("len_out", _P),
+                ("dev_status", _P)]
+
+
+class c_block_weights_args(ctypes.Structure):
+    _fields_ = [("q", _P), ("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32),
+                ("head_dim", _I32), ("table", _P), ("table_heads", _I32), ("max_blocks", _I32), ("ctx_len", _P),
+                ("old_len", _P), ("B", _I32), ("n_q", _I32), ("n_heads", _I32), ("n_kv_heads", _I32),
+                ("scale", ctypes.c_float), ("lse", _P), ("acc", _P), ("acc_out", _P), ("decay", ctypes.c_float),
+                ("k_shift", _I32), ("dev_status", _P)]
+
+
+class c_block_evict_args(ctypes.Structure):
+    _fields_ = [("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32), ("head_dim", _I32),
+                ("table", _P), ("table_heads", _I32), ("max_blocks", _I32), ("len", _P), ("len_out", _P), ("B", _I32),
+                ("n_kv_heads", _I32), ("keep", _I32), ("sinks", _I32), ("recent", _I32), ("acc", _P), ("acc_out", _P),
+                ("pos", _P), ("pos_out", _P), ("pos_len", _P), ("next_pos", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("dev_status", _P)]
+
+
 _lib = None
 
 
@@ -148,6 +184,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "echo_qk_norm_rope": ([ctypes.POINTER(c_qk_norm_rope_args), _P], S),
         "echo_block_attention_workspace_bytes": ([_I32, _I32, ctypes.POINTER(ctypes.c_size_t)], S),
         "echo_block_attention": ([ctypes.POINTER(c_block_attention_args), _P], S),
+        "echo_block_summary": ([ctypes.POINTER(c_block_summary_args), _P], S),
+        "echo_block_scores": ([ctypes.POINTER(c_block_scores_args), _P], S),
+        "echo_block_select": ([ctypes.POINTER(c_block_select_args), _P], S),
+        "echo_block_weights": ([ctypes.POINTER(c_block_weights_args), _P], S),
+        "echo_block_evict_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)], S),
+        "echo_block_evict": ([ctypes.POINTER(c_block_evict_args), _P], S),
         "echo_decode_step": ([ctypes.POINTER(c_step_args), _P], S),
         "echo_decode_step_host": ([ctypes.POINTER(c_step_args), _P, _P, _P, _I32], S),
         "echo_step_graph_create": ([ctypes.POINTER(c_step_args), ctypes.POINTER(_P)], S),
@@ -626,6 +668,166 @@ def make_block_attention_args(q, rows, table, ctx_len, n_kv_heads: int, scale: f
 def echo_block_attention(args: c_block_attention_args, stream=None):
     """Decode attention over block rows."""
     _check((_lib or load_library()).echo_block_attention(ctypes.byref(args), _stream(stream)), "echo_block_attention")
+
+
+def _table_arg(a, table, B: int, n_kv_heads: int, name: str = "table"):
+    """Sets table, table_heads and max_blocks: [B][max_blocks] ids or [B][n_kv_heads][max_blocks] rows."""
+    a.table = _typed(table, name, _INT, (B, None) if table.dim() == 2 else (B, int(n_kv_heads), None))
+    a.table_heads, a.max_blocks = 1 if table.dim() == 2 else int(n_kv_heads), int(table.shape[-1])
+
+
+def _rows_arg(a, rows, fmt: int, block_tokens: int, head_dim: int):
+    """Sets rows, n_rows, format, block_tokens and head_dim."""
+    if rows.dim() != 2 or rows.element_size() != 2:
+        raise EchoError("rows must be 16-bit [n_rows][R]")
+    R = block_row_elems(fmt, block_tokens, head_dim)
+    if int(rows.shape[1]) != R:
+        raise EchoError(f"rows have {rows.shape[1]} elements, blocks of {block_tokens} tokens need {R}")
+    a.rows, a.n_rows = _typed(rows, "rows", (rows.dtype,)), int(rows.shape[0])
+    a.format, a.block_tokens, a.head_dim = int(fmt), int(block_tokens), int(head_dim)
+
+
+def make_block_summary_args(rows, table, new_len, n_kv_heads: int, summary, old_len=None, fmt: int = BLOCK_BF16,
+                            block_tokens: int = 64, k_shift: int = 0, dev_status=None) -> c_block_summary_args:
+    """Arguments of echo_block_summary (see include/echo.h).  rows [n_rows][R] 16-bit; table int32
+    [B][max_blocks] of block ids or [B][n_kv_heads][max_blocks] of rows; old_len, new_len [B]
+    int32; summary [n_rows][2][D] bf16."""
+    B = int(new_len.shape[0])
+    a = c_block_summary_args()
+    if summary.dim() != 3:
+        raise EchoError("summary must be [n_rows][2][head_dim]")
+    _rows_arg(a, rows, fmt, block_tokens, int(summary.shape[2]))
+    _table_arg(a, table, B, n_kv_heads)
+    a.old_len, a.new_len = _typed(old_len, "old_len", _INT, (B,)), _typed(new_len, "new_len", _INT, (B,))
+    a.B, a.n_kv_heads = B, int(n_kv_heads)
+    a.summary = _typed(summary, "summary", _BF16, (a.n_rows, 2, a.head_dim))
+    a.k_shift, a.dev_status = int(k_shift), _typed(dev_status, "dev_status", _INT)
+    a._keep = (rows, table, new_len, summary, old_len, dev_status)
+    return a
+
+
+def echo_block_summary(args: c_block_summary_args, stream=None):
+    """Smallest and largest keys of the blocks that changed."""
+    _check((_lib or load_library()).echo_block_summary(ctypes.byref(args), _stream(stream)), "echo_block_summary")
+
+
+def make_block_scores_args(q, summary, table, ctx_len, n_kv_heads: int, scale: float, scores, block_tokens: int = 64,
+                           dev_status=None) -> c_block_scores_args:
+    """Arguments of echo_block_scores (see include/echo.h).  q [B][n_q][n_heads][D] bf16; summary
+    [n_rows][2][D] bf16; table as above; ctx_len [B] int32; scores
+    [B][n_q][n_kv_heads][max_blocks] fp32."""
+    B, n_q, H, D = (int(n) for n in q.shape)
+    a = c_block_scores_args()
+    a.q, a.summary = _typed(q, "q", _BF16, (B, n_q, H, D)), _typed(summary, "summary", _BF16, (None, 2, D))
+    a.n_rows, a.block_tokens, a.head_dim = int(summary.shape[0]), int(block_tokens), D
+    _table_arg(a, table, B, n_kv_heads)
+    a.ctx_len = _typed(ctx_len, "ctx_len", _INT, (B,))
+    a.B, a.n_q, a.n_heads, a.n_kv_heads, a.scale = B, n_q, H, int(n_kv_heads), float(scale)
+    a.scores = _typed(scores, "scores", _F32, (B, n_q, int(n_kv_heads), a.max_blocks))
+    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a._keep = (q, summary, table, ctx_len, scores, dev_status)
+    return a
+
+
+def echo_block_scores(args: c_block_scores_args, stream=None):
+    """A bound on the scores that each query can have in each block."""
+    _check((_lib or load_library()).echo_block_scores(ctypes.byref(args), _stream(stream)), "echo_block_scores")
+
+
+def make_block_select_args(scores, ctx_len, sel, block_tokens: int = 64, first: int = 0, last: int = 0, table=None,
+                           sel_rows=None, len_out=None, dev_status=None) -> c_block_select_args:
+    """Arguments of echo_block_select (see include/echo.h).  scores [B][n_q][n_kv_heads][max_blocks]
+    fp32; ctx_len [B], sel and sel_rows [B][n_q][n_kv_heads][k], len_out [B][n_q] int32; table as
+    above or None."""
+    B, n_q, Hk, n = (int(x) for x in scores.shape)
+    a = c_block_select_args()
+    a.scores, a.ctx_len = _typed(scores, "scores", _F32, (B, n_q, Hk, n)), _typed(ctx_len, "ctx_len", _INT, (B,))
+    a.B, a.n_q, a.n_kv_heads, a.block_tokens = B, n_q, Hk, int(block_tokens)
+    a.table, a.table_heads, a.max_blocks = None, 1, n
+    if table is not None:
+        _table_arg(a, table, B, Hk)
+        if a.max_blocks != n:
+            raise EchoError(f"table has {a.max_blocks} blocks, scores have {n}")
+    a.sel = _typed(sel, "sel", _INT, (B, n_q, Hk, None))
+    a.k, a.first, a.last = int(sel.shape[3]), int(first), int(last)
+    a.sel_rows = _typed(sel_rows, "sel_rows", _INT, tuple(sel.shape))
+    a.len_out = _typed(len_out, "len_out", _INT, (B, n_q))
+    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a._keep = (scores, ctx_len, sel, table, sel_rows, len_out, dev_status)
+    return a
+
+
+def echo_block_select(args: c_block_select_args, stream=None):
+    """The k best blocks of each query token and KV head."""
+    _check((_lib or load_library()).echo_block_select(ctypes.byref(args), _stream(stream)), "echo_block_select")
+
+
+def make_block_weights_args(q, rows, table, ctx_len, n_kv_heads: int, scale: float, lse, acc, acc_out, old_len=None,
+                            decay: float = 1.0, fmt: int = BLOCK_BF16, block_tokens: int = 64, k_shift: int = 0,
+                            dev_status=None) -> c_block_weights_args:
+    """Arguments of echo_block_weights (see include/echo.h).  q, rows, table, ctx_len as to
+    make_block_attention_args, lse [B][n_q][n_heads] fp32 as it returned it; acc (or None) and
+    acc_out [B][n_kv_heads][max_blocks * block_tokens] fp32; old_len [B] int32 or None."""
+    B, n_q, H, D = (int(n) for n in q.shape)
+    a = c_block_weights_args()
+    a.q = _typed(q, "q", _BF16, (B, n_q, H, D))
+    _rows_arg(a, rows, fmt, block_tokens, D)
+    _table_arg(a, table, B, n_kv_heads)
+    a.ctx_len, a.old_len = _typed(ctx_len, "ctx_len", _INT, (B,)), _typed(old_len, "old_len", _INT, (B,))
+    a.B, a.n_q, a.n_heads, a.n_kv_heads, a.scale = B, n_q, H, int(n_kv_heads), float(scale)
+    shape = (B, int(n_kv_heads), a.max_blocks * a.block_tokens)
+    a.lse, a.acc = _typed(lse, "lse", _F32, (B, n_q, H)), _typed(acc, "acc", _F32, shape)
+    a.acc_out, a.decay = _typed(acc_out, "acc_out", _F32, shape), float(decay)
+    a.k_shift, a.dev_status = int(k_shift), _typed(dev_status, "dev_status", _INT)
+    a._keep = (q, rows, table, ctx_len, lse, acc, acc_out, old_len, dev_status)
+    return a
+
+
+def echo_block_weights(args: c_block_weights_args, stream=None):
+    """The softmax weight that cached tokens gather."""
+    _check((_lib or load_library()).echo_block_weights(ctypes.byref(args), _stream(stream)), "echo_block_weights")
+
+
+class BlockEvictWorkspace:
+    """Scratch of echo_block_evict for B requests.  Serves calls that run one after another: two
+    streams, or two graphs that may be replayed at once, need one each."""
+
+    def __init__(self, B: int, n_kv_heads: int, keep: int, device="cuda"):
+        n = ctypes.c_size_t()
+        _check(load_library().echo_block_evict_workspace_bytes(B, n_kv_heads, keep, ctypes.byref(n)),
+               "echo_block_evict_workspace_bytes")
+        self.buf = torch.empty(n.value + 256, dtype=torch.uint8, device=device)
+        self.base = (self.buf.data_ptr() + 255) & ~255
+        self.bytes = n.value
+
+
+def make_block_evict_args(rows, table, length, len_out, n_kv_heads: int, keep: int, acc, acc_out,
+                          ws: BlockEvictWorkspace, sinks: int = 0, recent: int = 0, pos=None, pos_out=None, pos_len=None,
+                          next_pos=None, fmt: int = BLOCK_BF16, block_tokens: int = 64,
+                          dev_status=None) -> c_block_evict_args:
+    """Arguments of echo_block_evict (see include/echo.h).  length, len_out, pos_len, next_pos [B]
+    int32; acc, acc_out fp32 and pos, pos_out int32 [B][n_kv_heads][max_blocks * block_tokens]."""
+    B = int(length.shape[0])
+    a = c_block_evict_args()
+    R, bs = int(rows.shape[-1]), int(block_tokens)
+    D = R * 16 // (9 * bs) if fmt == BLOCK_FP4 and bs > 0 else R // (2 * bs) if bs > 0 else 0
+    _rows_arg(a, rows, fmt, block_tokens, D)
+    _table_arg(a, table, B, n_kv_heads)
+    a.len, a.len_out = _typed(length, "length", _INT, (B,)), _typed(len_out, "len_out", _INT, (B,))
+    a.B, a.n_kv_heads, a.keep, a.sinks, a.recent = B, int(n_kv_heads), int(keep), int(sinks), int(recent)
+    shape = (B, int(n_kv_heads), a.max_blocks * a.block_tokens)
+    a.acc, a.acc_out = _typed(acc, "acc", _F32, shape), _typed(acc_out, "acc_out", _F32, shape)
+    a.pos, a.pos_out = _typed(pos, "pos", _INT, shape), _typed(pos_out, "pos_out", _INT, shape)
+    a.pos_len, a.next_pos = _typed(pos_len, "pos_len", _INT, (B,)), _typed(next_pos, "next_pos", _INT, (B,))
+    _typed(ws.buf, "workspace", (torch.uint8,))
+    a.workspace, a.workspace_bytes, a.dev_status = ws.base, ws.bytes, _typed(dev_status, "dev_status", _INT)
+    a._keep = (rows, table, length, len_out, acc, acc_out, ws, pos, pos_out, pos_len, next_pos, dev_status)
+    return a
+
+
+def echo_block_evict(args: c_block_evict_args, stream=None):
+    """Requests cut to the tokens that gathered the most weight."""
+    _check((_lib or load_library()).echo_block_evict(ctypes.byref(args), _stream(stream)), "echo_block_evict")
 
 
 class StepBuffers:

@@ -61,6 +61,12 @@ int launch_block_tables(const echo_block_tables_args *a, cudaStream_t stream);
 int launch_qk_norm_rope(const echo_qk_norm_rope_args *a, cudaStream_t stream);
 size_t block_attention_workspace_bytes(int32_t rows, int32_t head_dim);
 int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stream);
+int launch_block_summary(const echo_block_summary_args *a, cudaStream_t stream);
+int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream);
+int launch_block_select(const echo_block_select_args *a, cudaStream_t stream);
+int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream);
+size_t block_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t keep);
+int launch_block_evict(const echo_block_evict_args *a, cudaStream_t stream);
 int noalloc_workspace(int32_t n_g, int32_t rows, cudaStream_t stream, echo_workspace *out);
 int launch_validate(const echo_pool *p, const echo_stage *stage, int32_t *report, int32_t *status, cudaStream_t s);
 int validate_host(const echo_pool *p, const int32_t *reserve, int32_t reserve_len, int32_t *report);
@@ -168,7 +174,7 @@ int echo_selftest_wait_timeout(int32_t which, int32_t *dev_status, void *stream)
   return launch_wait_probe(which, dev_status, static_cast<cudaStream_t>(stream));
 }
 
-int32_t echo_version(void) { return (1 << 16) | 7; }
+int32_t echo_version(void) { return (1 << 16) | 8; }
 
 int64_t echo_metadata_bytes(int64_t n_h, int64_t n_g) {
   return static_cast<int64_t>(sizeof(int32_t)) * n_h +
@@ -506,6 +512,129 @@ int echo_block_attention(const echo_block_attention_args *a, void *stream) {
   REQUIRE(a->workspace_bytes >= block_attention_workspace_bytes(a->n_q * (a->n_heads / a->n_kv_heads), a->head_dim),
           "workspace smaller than echo_block_attention_workspace_bytes()");
   return launch_block_attention(a, static_cast<cudaStream_t>(stream));
+}
+
+// a table of B requests, shared by the KV heads or one per head
+static int check_block_table(int32_t table_heads, int32_t n_kv_heads, int32_t max_blocks, int32_t block_tokens) {
+  REQUIRE(n_kv_heads >= 1 && n_kv_heads <= 65536, "n_kv_heads must be in [1, 65536] (got %d)", n_kv_heads);
+  REQUIRE(table_heads == 1 || table_heads == n_kv_heads, "table_heads must be 1 or n_kv_heads (got %d)", table_heads);
+  REQUIRE(max_blocks >= 1 && block_tokens >= 1 && static_cast<long long>(max_blocks) * block_tokens <= (1ll << 31) - 1024,
+          "max_blocks * block_tokens must be positive and below 2^31 - 1024");
+  return ECHO_OK;
+}
+
+static int check_grouped_heads(int32_t B, int32_t n_q, int32_t n_heads, int32_t n_kv_heads) {
+  REQUIRE(B >= 0 && n_q >= 1, "bad sizes (B %d, n_q %d)", B, n_q);
+  REQUIRE(n_kv_heads >= 1 && n_heads >= 1 && n_heads % n_kv_heads == 0, "n_heads must be a multiple of n_kv_heads (got %d, %d)",
+          n_heads, n_kv_heads);
+  REQUIRE(n_heads <= 65536 && n_q <= 65536, "too many heads or query tokens");
+  REQUIRE(static_cast<long long>(B) * n_q <= ((1ll << 31) - 1) / n_heads, "B * n_q * n_heads too large");
+  return ECHO_OK;
+}
+
+int echo_block_summary(const echo_block_summary_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->B >= 0 && a->B <= 16384, "B must be in [0, 16384] (got %d)", a->B);
+  TRY(check_block_rows(a->format, a->block_tokens, a->head_dim));
+  TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
+  TRY(check_shifts(a->format, a->k_shift, 0));
+  REQUIRE(static_cast<long long>(a->B) * a->max_blocks < (1ll << 30), "B * max_blocks must be below 2^30");
+  REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->rows && a->table && a->new_len && a->summary, "block summary pointer is NULL");
+  REQUIRE(aligned(a->rows, 16) && aligned(a->summary, 16), "rows and summary must be 16-byte aligned");
+  return launch_block_summary(a, static_cast<cudaStream_t>(stream));
+}
+
+int echo_block_scores(const echo_block_scores_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  TRY(check_grouped_heads(a->B, a->n_q, a->n_heads, a->n_kv_heads));
+  REQUIRE(a->head_dim == 64 || a->head_dim == 128, "head_dim must be 64 or 128 (got %d)", a->head_dim);
+  TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
+  REQUIRE(static_cast<long long>(a->B) * a->n_kv_heads <= ((1ll << 31) - 1) / (a->max_blocks / 64 + 1),
+          "B * n_kv_heads * (max_blocks / 64 + 1) must be below 2^31");
+  REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
+  REQUIRE(std::isfinite(a->scale), "scale must be finite");
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->q && a->summary && a->table && a->ctx_len && a->scores, "block scores pointer is NULL");
+  REQUIRE(aligned(a->q, 16) && aligned(a->summary, 16), "q and summary must be 16-byte aligned");
+  return launch_block_scores(a, static_cast<cudaStream_t>(stream));
+}
+
+int echo_block_select(const echo_block_select_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->B >= 0 && a->n_q >= 1 && a->n_q <= 65536, "bad sizes (B %d, n_q %d)", a->B, a->n_q);
+  TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
+  REQUIRE(a->max_blocks <= 49152, "max_blocks must be at most 49152 (got %d)", a->max_blocks);
+  REQUIRE(a->k >= 1 && a->k <= (1 << 20), "k must be in [1, 2^20] (got %d)", a->k);
+  REQUIRE(a->first >= 0 && a->last >= 0 && static_cast<long long>(a->first) + a->last <= a->k,
+          "first and last must not be negative, their sum at most k (got %d, %d, k %d)", a->first, a->last, a->k);
+  REQUIRE(static_cast<long long>(a->B) * a->n_q <= ((1ll << 31) - 1) / a->n_kv_heads, "B * n_q * n_kv_heads too large");
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->scores && a->ctx_len && a->sel, "block select pointer is NULL");
+  REQUIRE(a->table || !a->sel_rows, "sel_rows needs a table");
+  REQUIRE(a->len_out != a->ctx_len, "len_out must not be ctx_len");
+  return launch_block_select(a, static_cast<cudaStream_t>(stream));
+}
+
+int echo_block_weights(const echo_block_weights_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  TRY(check_grouped_heads(a->B, a->n_q, a->n_heads, a->n_kv_heads));
+  REQUIRE(static_cast<long long>(a->n_q) * (a->n_heads / a->n_kv_heads) <= 1024, "n_q * n_heads / n_kv_heads must be at most 1024");
+  TRY(check_block_rows(a->format, a->block_tokens, a->head_dim));
+  TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
+  TRY(check_shifts(a->format, a->k_shift, 0));
+  REQUIRE(static_cast<long long>(a->B) * a->n_kv_heads <= ((1ll << 31) - 1) / (a->max_blocks * (a->block_tokens / echo::kSubTokens) / 8 + 1),
+          "B * n_kv_heads * (max_blocks * block_tokens / 128 + 1) must be below 2^31");
+  REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
+  REQUIRE(std::isfinite(a->scale) && std::isfinite(a->decay), "scale and decay must be finite");
+  REQUIRE(std::fabs(std::ldexp(static_cast<double>(a->scale), -a->k_shift)) < 1e38, "scale * 2^-k_shift must be finite");
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->q && a->rows && a->table && a->ctx_len && a->lse && a->acc_out, "block weights pointer is NULL");
+  REQUIRE(a->acc || !a->old_len, "old_len needs acc");
+  REQUIRE(aligned(a->q, 16) && aligned(a->rows, 16), "q and rows must be 16-byte aligned");
+  return launch_block_weights(a, static_cast<cudaStream_t>(stream));
+}
+
+static int check_evict_sizes(int32_t B, int32_t n_kv_heads, int32_t keep) {
+  REQUIRE(B >= 0 && n_kv_heads >= 1 && n_kv_heads <= 65536 && static_cast<long long>(B) * n_kv_heads < (1ll << 26),
+          "B * n_kv_heads must be in [0, 2^26) (got %d, %d)", B, n_kv_heads);
+  REQUIRE(keep >= 1, "keep must be >= 1 (got %d)", keep);
+  return ECHO_OK;
+}
+
+int echo_block_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t keep, size_t *bytes) {
+  g_err[0] = 0;
+  REQUIRE(bytes, "bytes is NULL");
+  TRY(check_evict_sizes(B, n_kv_heads, keep));
+  *bytes = block_evict_workspace_bytes(B, n_kv_heads, keep);
+  return ECHO_OK;
+}
+
+int echo_block_evict(const echo_block_evict_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  TRY(check_evict_sizes(a->B, a->n_kv_heads, a->keep));
+  TRY(check_block_rows(a->format, a->block_tokens, a->head_dim));
+  TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
+  REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
+  REQUIRE(a->sinks >= 0 && a->recent >= 0 && static_cast<long long>(a->sinks) + a->recent <= a->keep,
+          "sinks and recent must not be negative, their sum at most keep (got %d, %d, keep %d)", a->sinks, a->recent, a->keep);
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->rows && a->table && a->len && a->len_out && a->acc && a->acc_out && a->workspace, "block evict pointer is NULL");
+  REQUIRE(!a->pos == !a->pos_out && !a->pos == !a->pos_len && !a->pos == !a->next_pos, "pos, pos_out, pos_len and next_pos go together");
+  REQUIRE(a->pos || a->recent == 0, "recent needs pos");
+  REQUIRE(a->len_out != a->len && (!a->pos || (a->len_out != a->pos_len && a->len_out != a->next_pos)),
+          "len_out must not be one of the inputs");
+  REQUIRE(aligned(a->rows, 16), "rows must be 16-byte aligned");
+  REQUIRE(aligned(a->workspace, 256), "workspace must be 256-byte aligned");
+  REQUIRE(a->workspace_bytes >= block_evict_workspace_bytes(a->B, a->n_kv_heads, a->keep),
+          "workspace smaller than echo_block_evict_workspace_bytes()");
+  return launch_block_evict(a, static_cast<cudaStream_t>(stream));
 }
 
 int echo_prefill_indexer_score(const echo_prefill_args *a, void *stream) {

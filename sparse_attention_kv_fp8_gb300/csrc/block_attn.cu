@@ -49,7 +49,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "block_rows.cuh"
+#include "block_mma.cuh"
 #include "cluster_select.cuh"
 
 namespace echo {
@@ -181,24 +181,6 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // a shared-memory address of this CTA, in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
   uint32_t r;
@@ -209,14 +191,6 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
 __device__ __forceinline__ float ba_lse(float top, float sum) {
   return top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A place on the line of chunks, counted from the CTA's first chunk: the chunks start .. end
 // belong to row group hm (KV head * row groups + row group) of request b.
 struct LinePos {

@@ -1,0 +1,584 @@
+// block_evict.cu -- the softmax weight that each cached token gathers, and the eviction that
+// keeps the heaviest tokens of a request.
+//
+// Gathered weight of token p of (b, KV head h), over the call's query tokens j and the group's
+// heads g, with the log-sum-exp that the attention returned:
+//   acc'_p = decay * acc_p + sum_{j: p < len_j} sum_g exp(scale * q_jg . k_p - lse_jg)
+// One read of the keys (the values are not needed), 2 D bytes a token in bf16, against
+// 2 D flops and one exponential per query row.
+//
+// Eviction to `keep` tokens: the first `sinks` slots and the tokens of the last `recent`
+// positions stay, then the heaviest, ties to the lower slot.  Of n = len slots, those below
+// `keep` whose token goes are holes, and as many tokens at or above `keep` stay; the i-th hole
+// takes the i-th of them.  Sources lie at or above `keep`, targets below, so the moves need no
+// order, and a call that is repeated on the same inputs does the same again.
+//
+// sm_103a design.
+//   Weights: S^T = K Q^T with mma.m16n8k16, tokens as the 16 rows and query rows as the 8
+//     columns.  A contraction's dims may come in any order, so a lane reads 16 contiguous bytes
+//     of its token's key and feeds them as they are (4-bit rows: 16 bytes of codes, converted in
+//     place); keys go from memory to registers with nothing in between, two sub-blocks of 16
+//     tokens a warp at a time, the exponentials of a column summed over the quad.
+//   Eviction: a CTA per (b, h) finds the weight of the last token that stays, by passes over 256
+//     equal parts of the range that still holds it, and lists holes and movers in order; the
+//     moves follow in the same CTA when they are few, else in a second kernel over the whole GPU.
+#include <algorithm>
+#include <cmath>
+
+#include "block_mma.cuh"
+
+namespace echo {
+
+// ---------------------------------------------------------------------------
+// gathered weights
+// ---------------------------------------------------------------------------
+constexpr int kWtWarps = 4;
+constexpr int kWtCols = 64;   // query columns that a CTA lays out at a time
+
+struct WeightParams {
+  const uint16_t *q;
+  const uint8_t *rows;
+  int64_t row_bytes;
+  int32_t n_rows, bsub;
+  const int32_t *table;
+  int32_t table_heads, max_blocks;
+  const int32_t *ctx_len, *old_len;
+  int32_t n_q, n_heads, n_kv, group;
+  float scale_log2;            // |scale| log2 e, over the keys' power of two
+  uint32_t q_sign;
+  const float *lse, *acc;
+  float *acc_out;
+  float decay;
+  int32_t ctas, subs;          // CTAs of a (b, h), sub-blocks that a warp of one takes (even, at most 32)
+  int32_t *status;
+};
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const WeightParams P) {
+  constexpr bool F16 = FMT == ECHO_BLOCK_FP4;
+  constexpr int kStride = 2 * D + 64;               // bytes of a column; + 64: its quads on other banks
+  constexpr int kPieces = D / 32;                   // 16-byte pieces of a column's dims per lane
+  constexpr int kLoads = F16 ? 1 : kPieces;         // 16-byte loads of a token per lane (4 bits, D = 64: 8 bytes)
+  __shared__ __align__(16) uint8_t qs[kWtCols * kStride];
+  __shared__ float2 col[kWtCols];                   // scale and lse of a column, both times log2 e
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
+  const int pair = blockIdx.x / P.ctas, part = blockIdx.x - pair * P.ctas;
+  const int b = pair / P.n_kv, h = pair - b * P.n_kv;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int most = P.max_blocks * P.bsub * kSubTokens;
+  int len = P.ctx_len[b];
+  if (len > most) {
+    if (part == 0 && h == 0 && threadIdx.x == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
+    len = most;
+  }
+  const int nsub = (max(len, 0) + kSubTokens - 1) / kSubTokens;
+  const int first = part * kWtWarps * P.subs;
+  if (first >= nsub) return;
+  const int s0 = first + warp * P.subs, s1 = min(s0 + P.subs, nsub);
+  const int old = P.old_len ? min(max(P.old_len[b], 0), len) : P.acc ? len : 0;
+  const int rows_q = P.n_q * P.group;
+
+  // where this lane's sub-block of the warp's run lies
+  int64_t where = -1;
+  if (s0 + lane < s1) {
+    const int e = (s0 + lane) / P.bsub, in = s0 + lane - e * P.bsub;
+    const int32_t id = P.table[(static_cast<int64_t>(b) * P.table_heads + (P.table_heads > 1 ? h : 0)) * P.max_blocks + e];
+    const int64_t row = id < 0 ? -1 : P.table_heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
+    if (row >= P.n_rows) set_status(P.status, ECHO_DEV_BAD_INDEX);
+    else if (row >= 0) where = row * P.row_bytes + static_cast<int64_t>(in) * (F16 ? Fp4Sub<D>::kBytes : kSubTokens * D * 2);
+  }
+  const int64_t out0 = (static_cast<int64_t>(b) * P.n_kv + h) * most;
+
+  for (int c0 = 0; c0 < rows_q; c0 += kWtCols) {
+    const int nc = min(kWtCols, rows_q - c0), nc8 = (nc + 7) & ~7;
+    if (c0) __syncthreads();
+    // the queries as columns: piece 4 i + c holds what lane c of a quad feeds with its i-th piece
+    for (int i = warp; i < nc8; i += kWtWarps) {   // a column per warp
+      const int rq = c0 + i, j = rq / P.group;
+      const int64_t at = (static_cast<int64_t>(b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
+      const bool on = i < nc;
+      uint2 x = make_uint2(0u, 0u);               // dims 4 lane and up
+      if (on && lane < D / 4) x = *reinterpret_cast<const uint2 *>(P.q + at * D + 4 * lane);
+      float scale = P.scale_log2;
+      int piece;                                  // of this lane's dims
+      if constexpr (F16) {
+        // scaled by the power of two that brings the row's largest entry to [1, 2)
+        const float x0 = __uint_as_float(x.x << 16), x1 = __uint_as_float(x.x & 0xffff0000u);
+        const float x2 = __uint_as_float(x.y << 16), x3 = __uint_as_float(x.y & 0xffff0000u);
+        float m = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+        e = max(min(e, 126), -126);  // (zero rows, subnormal and infinite maxima)
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        x = make_uint2(pack2<true>(x0 * inv, x1 * inv), pack2<true>(x2 * inv, x3 * inv));
+        scale *= __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        const int c = 4 * lane / (D / 4), k = (4 * lane % (D / 4)) / 8;  // lane c reads dims c D / 4 and up
+        piece = 4 * k + c;
+      } else {
+        piece = lane / 2;                         // piece 4 i + c: dims 32 i + 8 c and up
+      }
+      x.x ^= P.q_sign, x.y ^= P.q_sign;
+      if (lane < D / 4) *reinterpret_cast<uint2 *>(qs + i * kStride + piece * 16 + (lane & 1) * 8) = x;
+      // (a row that saw nothing, lse = -inf, gives no weight)
+      const float lse = on && lane == 0 ? P.lse[at] : -INFINITY;
+      if (lane == 0) col[i] = make_float2(scale, lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f);
+    }
+    __syncthreads();
+    for (int s = s0; s < s1; s += 2) {
+      uint4 a[2][2][kLoads];      // sub-block, token r8 (+ 8)
+      uint32_t sc[2][2];
+      int64_t at[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        at[u] = __shfl_sync(~0u, where, s - s0 + u);  // (past the run: -1)
+        if (s + u >= s1) at[u] = -1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint8_t *src = P.rows + (at[u] < 0 ? 0 : at[u]);
+          const int tk = r8 + 8 * k;
+          sc[u][k] = 0;
+          if constexpr (F16) {
+            a[u][k][0] = make_uint4(0u, 0u, 0u, 0u);
+            if (at[u] >= 0) {
+              if constexpr (D == 128) {
+                a[u][k][0] = *reinterpret_cast<const uint4 *>(src + tk * (D / 2) + c4 * 16);
+                sc[u][k] = *reinterpret_cast<const uint16_t *>(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4 * 2);
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2 *>(src + tk * (D / 2) + c4 * 8);
+                a[u][k][0].x = y.x, a[u][k][0].y = y.y;
+                sc[u][k] = src[Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4];
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+              a[u][k][i] = at[u] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                     : *reinterpret_cast<const uint4 *>(src + tk * (2 * D) + i * 64 + c4 * 16);
+          }
+        }
+      }
+      // A fragments: piece i of a lane's dims in two steps of 16
+      uint32_t f[2][kPieces][2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if constexpr (F16) {
+              const uint32_t word[4] = {a[u][k][0].x, a[u][k][0].y, a[u][k][0].z, a[u][k][0].w};
+              uint32_t v[4];
+              e2m1x8_to_half2(word[i], v);
+              const uint32_t s2 = __byte_perm(e4m3x2_to_half2(sc[u][k]), 0, D == 128 && i >= 2 ? 0x3232 : 0x1010);
+              f[u][i][0][k] = hmul2(v[0], s2), f[u][i][0][2 + k] = hmul2(v[1], s2);
+              f[u][i][1][k] = hmul2(v[2], s2), f[u][i][1][2 + k] = hmul2(v[3], s2);
+            } else {
+              f[u][i][0][k] = a[u][k][i].x, f[u][i][0][2 + k] = a[u][k][i].y;
+              f[u][i][1][k] = a[u][k][i].z, f[u][i][1][2 + k] = a[u][k][i].w;
+            }
+          }
+      float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      // tokens that every query sees (the last n_q - 1 are looked at one by one)
+      const bool edge = (s + 2) * kSubTokens > len - (P.n_q - 1);
+      for (int cg = 0; cg < nc8; cg += 8) {
+        float x[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[u][k] = 0.f;
+        const uint8_t *qp = qs + (cg + r8) * kStride + c4 * 16;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const uint4 q = *reinterpret_cast<const uint4 *>(qp + i * 64);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            mma16816<F16>(x[u], f[u][i][0], q.x, q.y);
+            mma16816<F16>(x[u], f[u][i][1], q.z, q.w);
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int c = cg + 2 * c4 + p;
+          const float2 m = col[c];
+          const int seen = edge ? len - (P.n_q - 1 - min((c0 + c) / P.group, P.n_q - 1)) : 0x7fffffff;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float e = ex2(fmaf(x[u][p + 2 * k], m.x, -m.y));
+              w[u][k] += c < nc && (!edge || (s + u) * kSubTokens + r8 + 8 * k < seen) ? e : 0.f;
+            }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v = w[u][k];
+          v += __shfl_xor_sync(~0u, v, 1);
+          v += __shfl_xor_sync(~0u, v, 2);
+          const int p = (s + u) * kSubTokens + r8 + 8 * k;
+          if (c4 != 0 || s + u >= s1 || p >= len) continue;
+          if (at[u] < 0) v = 0.f;
+          float before;
+          if (c0) before = P.acc_out[out0 + p];  // (written by this thread)
+          else before = p < old ? P.acc[out0 + p] * P.decay : 0.f;
+          P.acc_out[out0 + p] = before + v;
+        }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// eviction
+// ---------------------------------------------------------------------------
+constexpr int kEvThreads = 512;
+constexpr int kEvBins = 256;
+constexpr int kEvStaged = 32768;      // tokens whose keys a CTA keeps in shared memory
+constexpr uint32_t kEvMust = 0xffffffffu;
+
+struct EvictParams {
+  uint8_t *rows;
+  int64_t row_bytes;
+  int32_t n_rows, bsub;
+  const int32_t *table;
+  int32_t table_heads, max_blocks, n_kv, B;
+  const int32_t *len;
+  int32_t *len_out;
+  int32_t keep, sinks, recent;
+  const float *acc;
+  float *acc_out;
+  const int32_t *pos, *pos_len, *next_pos;
+  int32_t *pos_out;
+  int32_t *moves;                     // [B * n_kv]
+  int2 *list;                         // [B * n_kv][keep] (from, to)
+  int32_t staged;                     // keys of a context fit in shared memory
+  int32_t move_here;                  // moves made by the CTA that lists them
+  int32_t move_ctas;
+  int32_t *status;
+};
+
+__device__ __forceinline__ int64_t ev_row(const EvictParams &P, int b, int h, int slot, int &off) {
+  const int bs = P.bsub * kSubTokens, e = slot / bs;
+  off = slot - e * bs;
+  const int32_t id = P.table[(static_cast<int64_t>(b) * P.table_heads + (P.table_heads > 1 ? h : 0)) * P.max_blocks + e];
+  return id < 0 ? -1 : P.table_heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
+}
+
+// One token's key and value from slot m.x to slot m.y, by a warp.
+template <int FMT, int D>
+__device__ __forceinline__ void move_token(const EvictParams &P, int b, int h, int2 m, int lane) {
+  int o0, o1;
+  const int64_t r0 = ev_row(P, b, h, m.x, o0), r1 = ev_row(P, b, h, m.y, o1);
+  if (r0 < 0 || r1 < 0 || r0 >= P.n_rows || r1 >= P.n_rows) {
+    if (lane == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
+    return;
+  }
+  const uint8_t *src = P.rows + r0 * P.row_bytes;
+  uint8_t *dst = P.rows + r1 * P.row_bytes;
+  if constexpr (FMT == ECHO_BLOCK_FP4) {
+    const int t0 = o0 % kSubTokens, t1 = o1 % kSubTokens;
+    src += (o0 / kSubTokens) * Fp4Sub<D>::kBytes, dst += (o1 / kSubTokens) * Fp4Sub<D>::kBytes;
+    if (lane < 8) {                 // a part of the value codes, D / 16 bytes
+      const uint8_t *s = src + Fp4Sub<D>::kValues + ((t0 >> 3) * 64 + lane * 8 + (t0 & 7)) * (D / 16);
+      uint8_t *d = dst + Fp4Sub<D>::kValues + ((t1 >> 3) * 64 + lane * 8 + (t1 & 7)) * (D / 16);
+      if constexpr (D == 128) *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(s);
+      else *reinterpret_cast<uint32_t *>(d) = *reinterpret_cast<const uint32_t *>(s);
+    } else if (lane < 8 + D / 16) { // a value scale, a byte
+      const int g = lane - 8;
+      dst[Fp4Sub<D>::kValueScales + (t1 >> 3) * (D / 2) + g * 8 + (t1 & 7)] =
+          src[Fp4Sub<D>::kValueScales + (t0 >> 3) * (D / 2) + g * 8 + (t0 & 7)];
+    } else if (lane < 16 + D / 32 && lane >= 16) {  // key codes
+      const int i = lane - 16;
+      *reinterpret_cast<uint4 *>(dst + t1 * (D / 2) + i * 16) = *reinterpret_cast<const uint4 *>(src + t0 * (D / 2) + i * 16);
+    } else if (lane == 31) {        // key scales
+      const uint8_t *s = src + Fp4Sub<D>::kKeyScales + t0 * (D / 16);
+      uint8_t *d = dst + Fp4Sub<D>::kKeyScales + t1 * (D / 16);
+      if constexpr (D == 128) *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(s);
+      else *reinterpret_cast<uint32_t *>(d) = *reinterpret_cast<const uint32_t *>(s);
+    }
+  } else {
+    constexpr int kHalf = D / 8;    // 16-byte pieces of a key
+    if (lane < 2 * kHalf) {
+      const int64_t v = lane < kHalf ? 0 : static_cast<int64_t>(P.bsub) * kSubTokens * D * 2;
+      const int i = lane < kHalf ? lane : lane - kHalf;
+      *reinterpret_cast<uint4 *>(dst + v + o1 * (2 * D) + i * 16) = *reinterpret_cast<const uint4 *>(src + v + o0 * (2 * D) + i * 16);
+    }
+  }
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kEvThreads) block_evict_kernel(const EvictParams P) {
+  constexpr int W = kEvThreads / 32;
+  extern __shared__ uint32_t ev_keys[];
+  __shared__ uint32_t hist[kEvBins];
+  __shared__ uint32_t red[3][W];
+  __shared__ uint32_t pick[3];
+  __shared__ uint32_t wcnt[2][W];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / P.n_kv, h = blockIdx.x - b * P.n_kv;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int most = P.max_blocks * P.bsub * kSubTokens;
+  int n = P.len[b];
+  if (n > most) {
+    if (h == 0 && tid == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
+    n = most;
+  }
+  n = max(n, 0);
+  const int end = min(n, P.keep);
+  if (h == 0 && tid == 0) P.len_out[b] = end;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * most;
+  const float *acc = P.acc + base;
+  const int32_t *pos = P.pos ? P.pos + base : nullptr;
+  float *acc_out = P.acc_out + base;
+  int32_t *pos_out = P.pos ? P.pos_out + base : nullptr;
+  const int known = P.pos ? min(max(P.pos_len[b], 0), n) : 0;
+  const int nxt = P.pos ? P.next_pos[b] : 0;
+  auto pos_of = [&](int i) { return i < known ? pos[i] : nxt - n + i; };
+
+  if (n <= P.keep) {
+    for (int i = tid; i < n; i += kEvThreads) {
+      acc_out[i] = acc[i];
+      if (pos_out) pos_out[i] = pos_of(i);
+    }
+    if (tid == 0) P.moves[blockIdx.x] = 0;
+    return;
+  }
+
+  auto key_of = [&](int i) -> uint32_t {
+    if (i < P.sinks || (pos && pos_of(i) >= nxt - P.recent)) return kEvMust;
+    const float s = acc[i];
+    return s != s ? 1u : score_key(s);  // (a weight that is NaN goes first)
+  };
+  uint32_t lo = kEvMust, hi = 0, n_must = 0;
+  for (int i = tid; i < n; i += kEvThreads) {
+    const uint32_t key = key_of(i);
+    if (P.staged) ev_keys[i] = key;
+    if (key == kEvMust) ++n_must;
+    else lo = min(lo, key), hi = max(hi, key);
+  }
+  n_must = __reduce_add_sync(~0u, n_must), lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
+  if (lane == 0) red[0][warp] = n_must, red[1][warp] = lo, red[2][warp] = hi;
+  __syncthreads();
+  n_must = hi = 0, lo = kEvMust;
+#pragma unroll
+  for (int w = 0; w < W; ++w) n_must += red[0][w], lo = min(lo, red[1][w]), hi = max(hi, red[2][w]);
+  auto key_at = [&](int i) -> uint32_t { return P.staged ? ev_keys[i] : key_of(i); };
+
+  // ----- the key above which all stay, and how many of its equals (n > keep: some go) -----
+  uint32_t thr = kEvMust - 1, need = 0;
+  if (n_must > static_cast<uint32_t>(P.keep)) {  // (more recent positions than their number: the first slots of them)
+    thr = kEvMust, need = P.keep;
+  } else {
+    uint32_t want = P.keep - n_must;
+    while (want) {  // the want-th largest of the keys in [lo, hi]
+      const int shift = max(0, 24 - __clz(hi - lo));
+      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += kEvThreads) {
+        const uint32_t key = key_at(i);
+        if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> shift], 1u);
+      }
+      __syncthreads();
+      if (warp == 0) {  // lane l holds bins 255 - 8 l .. 248 - 8 l
+        uint32_t c[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = hist[kEvBins - 1 - 8 * lane - i], sum += c[i];
+        uint32_t upto = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t x = __shfl_up_sync(~0u, upto, d);
+          if (lane >= d) upto += x;
+        }
+        uint32_t above = upto - sum;
+        if (above < want && upto >= want) {
+          int i = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i == k && above + c[k] < want) above += c[k], i = k + 1;
+          pick[0] = kEvBins - 1 - 8 * lane - i;
+          pick[1] = above;
+          pick[2] = pick_reg(c, i);
+        }
+      }
+      __syncthreads();
+      const uint32_t bin = pick[0], in = pick[2];
+      want -= pick[1];
+      lo += bin << shift;
+      const uint32_t width = (1u << shift) - 1;
+      hi = hi - lo > width ? lo + width : hi;
+      if (in == want) {
+        thr = lo - 1;
+        break;
+      }
+      if (shift == 0) {
+        thr = lo, need = want;
+        break;
+      }
+    }
+  }
+
+  // ----- holes and movers in order -----
+  // A thread takes a run of slots (an odd number: no bank conflicts); equals that stay, then holes and movers, are counted over the
+  // runs.  Movers and holes are as many.
+  const int per = (n + kEvThreads - 1) / kEvThreads | 1, i0 = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(n))), i1 = min(i0 + per, n);
+  auto scan = [&](uint32_t mine, int which) -> uint32_t {  // exclusive sum over the threads
+    uint32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) wcnt[which][warp] = upto;
+    __syncthreads();
+    uint32_t before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += wcnt[which][w];
+    return before;
+  };
+  uint32_t eq = 0;
+  for (int i = i0; i < i1; ++i) eq += key_at(i) == thr;
+  const uint32_t eq0 = scan(eq, 0);
+  auto walk = [&](auto &&hole, auto &&mover) {
+    uint32_t e = eq0;
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t key = key_at(i);
+      const bool stays = key > thr || (key == thr && e < need);
+      e += key == thr;
+      if (i < P.keep) {
+        if (!stays) hole(i);
+      } else if (stays) {
+        mover(i);
+      }
+    }
+  };
+  uint32_t holes = 0, movers = 0;
+  walk([&](int) { ++holes; }, [&](int) { ++movers; });
+  uint32_t hole_at = scan(holes, 1);
+  __syncthreads();
+  uint32_t mover_at = scan(movers, 0);
+  int2 *list = P.list + static_cast<int64_t>(blockIdx.x) * P.keep;
+  walk([&](int i) { list[hole_at++].y = i; }, [&](int i) { list[mover_at++].x = i; });
+  __syncthreads();
+  uint32_t count = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) count += wcnt[0][w];
+  if (tid == 0) P.moves[blockIdx.x] = count;
+
+  // ----- weights and positions: those that keep their slot, then those that move -----
+  // (in place the first pass writes what is there)
+  for (int i = tid; i < end; i += kEvThreads) {
+    acc_out[i] = acc[i];
+    if (pos_out) pos_out[i] = pos_of(i);
+  }
+  __syncthreads();
+  for (uint32_t i = tid; i < count; i += kEvThreads) {
+    const int2 m = list[i];
+    acc_out[m.y] = acc[m.x];
+    if (pos_out) pos_out[m.y] = pos_of(m.x);
+  }
+  if (P.move_here)
+    for (uint32_t i = warp; i < count; i += W) move_token<FMT, D>(P, b, h, list[i], lane);
+}
+
+constexpr int kMvWarps = 8;
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kMvWarps * 32) block_move_kernel(const EvictParams P) {
+  const int pair = blockIdx.x / P.move_ctas, part = blockIdx.x - pair * P.move_ctas;
+  const int b = pair / P.n_kv, h = pair - b * P.n_kv;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int count = P.moves[pair];
+  const int2 *list = P.list + static_cast<int64_t>(pair) * P.keep;
+  for (int i = part * kMvWarps + (threadIdx.x >> 5); i < count; i += P.move_ctas * kMvWarps)
+    move_token<FMT, D>(P, b, h, list[i], threadIdx.x & 31);
+}
+
+}  // namespace echo
+
+namespace echo_host {
+
+static int evict_sms(int *sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block eviction device");
+}
+
+int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream) {
+  echo::WeightParams P{};
+  P.q = a->q, P.rows = reinterpret_cast<const uint8_t *>(a->rows);
+  P.row_bytes = 2 * echo::block_row_elems(a->format, a->block_tokens, a->head_dim);
+  P.n_rows = a->n_rows, P.bsub = a->block_tokens / echo::kSubTokens;
+  P.table = a->table, P.table_heads = a->table_heads, P.max_blocks = a->max_blocks;
+  P.ctx_len = a->ctx_len, P.old_len = a->old_len;
+  P.n_q = a->n_q, P.n_heads = a->n_heads, P.n_kv = a->n_kv_heads, P.group = a->n_heads / a->n_kv_heads;
+  P.scale_log2 = std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift);
+  P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
+  P.lse = a->lse, P.acc = a->acc, P.acc_out = a->acc_out, P.decay = a->decay;
+  P.status = a->dev_status;
+  int sms = 0;
+  if (int rr = evict_sms(&sms)) return rr;
+  const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads;
+  const int64_t nsub = static_cast<int64_t>(a->max_blocks) * P.bsub;
+  // two sub-blocks a warp, or more where every SM still has several CTAs
+  P.subs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, nsub * pairs / (2 * echo::kWtWarps * 24ll * sms))) * 2);
+  P.ctas = static_cast<int>((nsub + echo::kWtWarps * P.subs - 1) / (echo::kWtWarps * P.subs));
+  const dim3 grid(static_cast<unsigned>(P.ctas * pairs)), block(echo::kWtWarps * 32);
+  cudaError_t e;
+  if (a->format == ECHO_BLOCK_FP4)
+    e = a->head_dim == 128 ? launch_pdl(echo::block_weights_kernel<ECHO_BLOCK_FP4, 128>, grid, block, 0, stream, P)
+                           : launch_pdl(echo::block_weights_kernel<ECHO_BLOCK_FP4, 64>, grid, block, 0, stream, P);
+  else
+    e = a->head_dim == 128 ? launch_pdl(echo::block_weights_kernel<ECHO_BLOCK_BF16, 128>, grid, block, 0, stream, P)
+                           : launch_pdl(echo::block_weights_kernel<ECHO_BLOCK_BF16, 64>, grid, block, 0, stream, P);
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block weights launch");
+}
+
+size_t block_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t keep) {
+  const size_t pairs = static_cast<size_t>(B) * n_kv_heads;
+  return (pairs * 4 + 255) / 256 * 256 + pairs * keep * sizeof(int2);
+}
+
+template <int FMT, int D>
+static int go_evict(echo::EvictParams P, cudaStream_t stream) {
+  static std::atomic<bool> attr[kMaxDevices];
+  const int64_t pairs = static_cast<int64_t>(P.B) * P.n_kv;
+  const int64_t most = static_cast<int64_t>(P.max_blocks) * P.bsub * echo::kSubTokens;
+  P.staged = most <= echo::kEvStaged;
+  const int smem = P.staged ? static_cast<int>(most) * 4 : 0;
+  if (smem > 40960)
+    if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
+  int sms = 0;
+  if (int rr = evict_sms(&sms)) return rr;
+  const int64_t moves = std::max<int64_t>(0, std::min<int64_t>(P.keep, most - P.keep));
+  P.move_here = moves <= 256;
+  P.move_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((moves + 31) / 32, 16ll * sms / pairs)));
+  cudaError_t e = launch_pdl(echo::block_evict_kernel<FMT, D>, dim3(static_cast<unsigned>(pairs)), dim3(echo::kEvThreads), smem, stream, P);
+  if (e == cudaSuccess && !P.move_here)
+    e = launch_pdl(echo::block_move_kernel<FMT, D>, dim3(static_cast<unsigned>(pairs * P.move_ctas)), dim3(echo::kMvWarps * 32), 0, stream, P);
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block eviction launch");
+}
+
+int launch_block_evict(const echo_block_evict_args *a, cudaStream_t stream) {
+  echo::EvictParams P{};
+  P.rows = reinterpret_cast<uint8_t *>(a->rows);
+  P.row_bytes = 2 * echo::block_row_elems(a->format, a->block_tokens, a->head_dim);
+  P.n_rows = a->n_rows, P.bsub = a->block_tokens / echo::kSubTokens;
+  P.table = a->table, P.table_heads = a->table_heads, P.max_blocks = a->max_blocks, P.n_kv = a->n_kv_heads, P.B = a->B;
+  P.len = a->len, P.len_out = a->len_out;
+  P.keep = a->keep, P.sinks = a->sinks, P.recent = a->recent;
+  P.acc = a->acc, P.acc_out = a->acc_out;
+  P.pos = a->pos, P.pos_len = a->pos_len, P.next_pos = a->next_pos, P.pos_out = a->pos_out;
+  P.moves = static_cast<int32_t *>(a->workspace);
+  P.list = reinterpret_cast<int2 *>(static_cast<uint8_t *>(a->workspace) + (static_cast<size_t>(a->B) * a->n_kv_heads * 4 + 255) / 256 * 256);
+  P.status = a->dev_status;
+  if (a->format == ECHO_BLOCK_FP4)
+    return a->head_dim == 128 ? go_evict<ECHO_BLOCK_FP4, 128>(P, stream) : go_evict<ECHO_BLOCK_FP4, 64>(P, stream);
+  return a->head_dim == 128 ? go_evict<ECHO_BLOCK_BF16, 128>(P, stream) : go_evict<ECHO_BLOCK_BF16, 64>(P, stream);
+}
+
+}  // namespace echo_host
