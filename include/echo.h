@@ -810,6 +810,58 @@ typedef struct echo_block_evict_args {
 int echo_block_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t keep, size_t *bytes);
 int echo_block_evict(const echo_block_evict_args *args, void *stream);
 
+/*
+ * Decode attention of requests that share a prefix (a system prompt, a document, the prompt of
+ * several samples): the prefix is read once for all query rows of a group, on the tensor cores,
+ * instead of once per request.  Requests group_start[g] .. group_start[g + 1] - 1 see the
+ * prefix_len[g] tokens of prefix g, all of them with every query token, and after it their own
+ * tokens: as to echo_block_attention without a window, query j of request b sees the first
+ * ctx_len[b] - (n_q - 1 - j) tokens of table[b].  Requests outside all groups have no prefix.
+ *   out = sum_p softmax(s)_p v_p and lse = log sum_p exp(s_p) over both; no token: 0 and -inf.
+ *   q, rows, table, table_heads, max_blocks, ctx_len, scale, k_shift, v_shift, out, lse   as to
+ *            echo_block_attention; table and ctx_len may be NULL together: no own tokens
+ *   prefix_table  int32 device, [n_groups][max_prefix_blocks] block ids shared by the KV heads
+ *            (prefix_heads == 1) or [n_groups][n_kv_heads][max_prefix_blocks] rows; a negative
+ *            entry is a block that is not held, one outside the rows also sets
+ *            ECHO_DEV_BAD_INDEX
+ *   prefix_len    [n_groups] int32 device, any length (0: none; it may end inside a block); above
+ *            max_prefix_blocks * block_tokens it is clamped with ECHO_DEV_BAD_INDEX
+ *   group_start   [n_groups + 1] int32 device, ascending, from 0 to B at most; a value that is not
+ *            sets ECHO_DEV_BAD_INDEX, and the outputs of the requests around it are unspecified
+ *   workspace device, 256-byte aligned, echo_prefix_attention_workspace_bytes() bytes; one workspace
+ *            serves calls that run one after another
+ * Prefix tokens past its length may hold any bytes.  Scores, the softmax and all sums are fp32; the
+ * prefix's softmax weights enter its value product in 16 bits (bf16, with ECHO_BLOCK_FP4 fp16; the
+ * tensor cores' operand type), the own tokens' as in echo_block_attention.
+ * Limits: those of echo_block_attention, n_groups in [1, 65536], n_groups * n_kv_heads *
+ * max_prefix_blocks below 2^31.  Launches 2 kernels, with own tokens 3 or 4; the first call that takes
+ * some form of them sets it up, outside capture, as with echo_block_attention.
+ */
+typedef struct echo_prefix_attention_args {
+    const uint16_t *q;
+    const uint16_t *rows;
+    int32_t n_rows, format, block_tokens, head_dim;
+    const int32_t *prefix_table;
+    const int32_t *prefix_len;
+    const int32_t *group_start;
+    int32_t n_groups, prefix_heads, max_prefix_blocks;
+    const int32_t *table;
+    int32_t table_heads, max_blocks;
+    const int32_t *ctx_len;
+    int32_t B, n_q, n_heads, n_kv_heads;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *dev_status;
+    int32_t k_shift, v_shift;
+} echo_prefix_attention_args;
+
+int echo_prefix_attention_workspace_bytes(int32_t B, int32_t n_q, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                          size_t *bytes);
+int echo_prefix_attention(const echo_prefix_attention_args *args, void *stream);
+
 /* Stages of echo_decode_step, in order (timing events are recorded before each
    stage and after the last).  The EMA is computed by the recall's last kernel, so
    the ECHO_STAGE_EMA interval is empty; the constant is kept for the event layout. */
@@ -970,7 +1022,7 @@ const char *echo_last_error_string(void);
    echo_stage.flags; 1.5: echo_pool_validate, echo_pool_validate_host; 1.6: block rows,
    echo_block_tables, echo_qk_norm_rope, echo_block_attention; 1.7: k_shift, v_shift;
    1.8: echo_block_summary, echo_block_scores, echo_block_select, echo_block_weights,
-   echo_block_evict). */
+   echo_block_evict, echo_prefix_attention). */
 int32_t echo_version(void);
 
 /* Storage law of the metadata arrays of one pool (section 5.1): 4*n_h + 13*n_g. */

@@ -146,6 +146,15 @@ class c_block_evict_args(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("dev_status", _P)]
 
 
+class c_prefix_attention_args(ctypes.Structure):
+    _fields_ = [("q", _P), ("rows", _P), ("n_rows", _I32), ("format", _I32), ("block_tokens", _I32),
+                ("head_dim", _I32), ("prefix_table", _P), ("prefix_len", _P), ("group_start", _P), ("n_groups", _I32),
+                ("prefix_heads", _I32), ("max_prefix_blocks", _I32), ("table", _P), ("table_heads", _I32),
+                ("max_blocks", _I32), ("ctx_len", _P), ("B", _I32), ("n_q", _I32), ("n_heads", _I32),
+                ("n_kv_heads", _I32), ("scale", ctypes.c_float), ("out", _P), ("lse", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("dev_status", _P), ("k_shift", _I32), ("v_shift", _I32)]
+
+
 _lib = None
 
 
@@ -190,6 +199,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "echo_block_weights": ([ctypes.POINTER(c_block_weights_args), _P], S),
         "echo_block_evict_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)], S),
         "echo_block_evict": ([ctypes.POINTER(c_block_evict_args), _P], S),
+        "echo_prefix_attention_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)], S),
+        "echo_prefix_attention": ([ctypes.POINTER(c_prefix_attention_args), _P], S),
         "echo_decode_step": ([ctypes.POINTER(c_step_args), _P], S),
         "echo_decode_step_host": ([ctypes.POINTER(c_step_args), _P, _P, _P, _I32], S),
         "echo_step_graph_create": ([ctypes.POINTER(c_step_args), ctypes.POINTER(_P)], S),
@@ -828,6 +839,58 @@ def make_block_evict_args(rows, table, length, len_out, n_kv_heads: int, keep: i
 def echo_block_evict(args: c_block_evict_args, stream=None):
     """Requests cut to the tokens that gathered the most weight."""
     _check((_lib or load_library()).echo_block_evict(ctypes.byref(args), _stream(stream)), "echo_block_evict")
+
+
+class PrefixAttentionWorkspace:
+    """Scratch of echo_prefix_attention for B requests (any prefixes and contexts).  Serves calls
+    that run one after another: two streams, or two graphs that may be replayed at once, need one
+    each."""
+
+    def __init__(self, B: int, n_q: int, n_heads: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        n = ctypes.c_size_t()
+        _check(load_library().echo_prefix_attention_workspace_bytes(B, n_q, n_heads, n_kv_heads, head_dim,
+                                                                    ctypes.byref(n)),
+               "echo_prefix_attention_workspace_bytes")
+        self.buf = torch.empty(n.value + 256, dtype=torch.uint8, device=device)
+        self.base = (self.buf.data_ptr() + 255) & ~255
+        self.bytes = n.value
+
+
+def make_prefix_attention_args(q, rows, prefix_table, prefix_len, group_start, table, ctx_len, n_kv_heads: int,
+                               scale: float, out, lse, ws: PrefixAttentionWorkspace, fmt: int = BLOCK_BF16,
+                               block_tokens: int = 64, dev_status=None, k_shift: int = 0,
+                               v_shift: int = 0) -> c_prefix_attention_args:
+    """Arguments of echo_prefix_attention (see include/echo.h).  q, rows, table, ctx_len, out and lse
+    as to make_block_attention_args (table and ctx_len None: no own tokens); prefix_table int32
+    [n_groups][max_prefix_blocks] of block ids or [n_groups][n_kv_heads][max_prefix_blocks] of
+    rows; prefix_len [n_groups], group_start [n_groups + 1] int32."""
+    B, n_q, H, D = (int(n) for n in q.shape)
+    a = c_prefix_attention_args()
+    a.q = _typed(q, "q", _BF16, (B, n_q, H, D))
+    _rows_arg(a, rows, fmt, block_tokens, D)
+    G = int(prefix_len.shape[0])
+    shape = (G, None) if prefix_table.dim() == 2 else (G, int(n_kv_heads), None)
+    a.prefix_table = _typed(prefix_table, "prefix_table", _INT, shape)
+    a.prefix_len = _typed(prefix_len, "prefix_len", _INT, (G,))
+    a.group_start = _typed(group_start, "group_start", _INT, (G + 1,))
+    a.n_groups, a.max_prefix_blocks = G, int(prefix_table.shape[-1])
+    a.prefix_heads = 1 if prefix_table.dim() == 2 else int(n_kv_heads)
+    a.table, a.table_heads, a.max_blocks = None, 1, 1
+    if table is not None:
+        _table_arg(a, table, B, n_kv_heads)
+    a.ctx_len = _typed(ctx_len, "ctx_len", _INT, (B,))
+    a.B, a.n_q, a.n_heads, a.n_kv_heads, a.scale = B, n_q, H, int(n_kv_heads), float(scale)
+    a.out, a.lse = _typed(out, "out", _BF16, (B, n_q, H, D)), _typed(lse, "lse", _F32, (B, n_q, H))
+    _typed(ws.buf, "workspace", (torch.uint8,))
+    a.workspace, a.workspace_bytes = ws.base, ws.bytes
+    a.dev_status, a.k_shift, a.v_shift = _typed(dev_status, "dev_status", _INT), int(k_shift), int(v_shift)
+    a._keep = (q, rows, prefix_table, prefix_len, group_start, table, ctx_len, out, lse, ws, dev_status)
+    return a
+
+
+def echo_prefix_attention(args: c_prefix_attention_args, stream=None):
+    """Decode attention of requests that share a prefix."""
+    _check((_lib or load_library()).echo_prefix_attention(ctypes.byref(args), _stream(stream)), "echo_prefix_attention")
 
 
 class StepBuffers:

@@ -67,6 +67,8 @@ int launch_block_select(const echo_block_select_args *a, cudaStream_t stream);
 int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream);
 size_t block_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t keep);
 int launch_block_evict(const echo_block_evict_args *a, cudaStream_t stream);
+size_t prefix_attention_workspace_bytes(int32_t B, int32_t n_q, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t stream);
 int noalloc_workspace(int32_t n_g, int32_t rows, cudaStream_t stream, echo_workspace *out);
 int launch_validate(const echo_pool *p, const echo_stage *stage, int32_t *report, int32_t *status, cudaStream_t s);
 int validate_host(const echo_pool *p, const int32_t *reserve, int32_t reserve_len, int32_t *report);
@@ -482,9 +484,8 @@ int echo_block_attention_workspace_bytes(int32_t rows_per_kv_head, int32_t head_
   return ECHO_OK;
 }
 
-int echo_block_attention(const echo_block_attention_args *a, void *stream) {
-  g_err[0] = 0;
-  REQUIRE(a, "args is NULL");
+// the sizes of an attention over block tables
+static int check_block_attention(const echo_block_attention_args *a) {
   REQUIRE(a->B >= 0 && a->n_q >= 1 && a->n_q <= 64, "bad sizes (B %d, n_q %d)", a->B, a->n_q);
   REQUIRE(a->n_kv_heads >= 1 && a->n_heads >= 1 && a->n_heads % a->n_kv_heads == 0,
           "n_heads must be a multiple of n_kv_heads (got %d, %d)", a->n_heads, a->n_kv_heads);
@@ -504,6 +505,13 @@ int echo_block_attention(const echo_block_attention_args *a, void *stream) {
   const long long groups = (static_cast<long long>(a->n_q) * (a->n_heads / a->n_kv_heads) + 31) / 32;
   REQUIRE(a->B * groups * a->n_kv_heads * a->max_blocks * (a->block_tokens / echo::kSubTokens) < (1ll << 37),
           "contexts too large: B * n_kv_heads * row groups * max_blocks * block_tokens / 16 must be below 2^37");
+  return ECHO_OK;
+}
+
+int echo_block_attention(const echo_block_attention_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  TRY(check_block_attention(a));
   if (a->B == 0) return ECHO_OK;
   REQUIRE(a->q && a->rows && a->table && a->ctx_len && a->out && a->workspace, "block attention pointer is NULL");
   REQUIRE(aligned(a->q, 16) && aligned(a->rows, 16) && aligned(a->out, 16), "q, rows and out must be 16-byte aligned");
@@ -635,6 +643,45 @@ int echo_block_evict(const echo_block_evict_args *a, void *stream) {
   REQUIRE(a->workspace_bytes >= block_evict_workspace_bytes(a->B, a->n_kv_heads, a->keep),
           "workspace smaller than echo_block_evict_workspace_bytes()");
   return launch_block_evict(a, static_cast<cudaStream_t>(stream));
+}
+
+int echo_prefix_attention_workspace_bytes(int32_t B, int32_t n_q, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                          size_t *bytes) {
+  g_err[0] = 0;
+  REQUIRE(bytes, "bytes is NULL");
+  TRY(check_grouped_heads(B, n_q, n_heads, n_kv_heads));
+  REQUIRE(static_cast<long long>(n_q) * (n_heads / n_kv_heads) <= 1024, "n_q * n_heads / n_kv_heads must be at most 1024");
+  REQUIRE(head_dim == 64 || head_dim == 128, "head_dim must be 64 or 128 (got %d)", head_dim);
+  *bytes = prefix_attention_workspace_bytes(B, n_q, n_heads, n_kv_heads, head_dim);
+  return ECHO_OK;
+}
+
+int echo_prefix_attention(const echo_prefix_attention_args *a, void *stream) {
+  g_err[0] = 0;
+  REQUIRE(a, "args is NULL");
+  echo_block_attention_args own{};
+  own.n_rows = a->n_rows, own.format = a->format, own.block_tokens = a->block_tokens, own.head_dim = a->head_dim;
+  own.table_heads = a->table ? a->table_heads : 1, own.max_blocks = a->table ? a->max_blocks : 1;
+  own.B = a->B, own.n_q = a->n_q, own.n_heads = a->n_heads, own.n_kv_heads = a->n_kv_heads, own.scale = a->scale;
+  own.k_shift = a->k_shift, own.v_shift = a->v_shift;
+  TRY(check_block_attention(&own));
+  REQUIRE(a->n_groups >= 1 && a->n_groups <= 65536, "n_groups must be in [1, 65536] (got %d)", a->n_groups);
+  REQUIRE(a->prefix_heads == 1 || a->prefix_heads == a->n_kv_heads, "prefix_heads must be 1 or n_kv_heads (got %d)", a->prefix_heads);
+  REQUIRE(a->max_prefix_blocks >= 1 && static_cast<long long>(a->max_prefix_blocks) * a->block_tokens <= (1ll << 31) - 1024,
+          "max_prefix_blocks * block_tokens must be positive and below 2^31 - 1024");
+  REQUIRE(static_cast<long long>(a->n_groups) * a->n_kv_heads <= ((1ll << 31) - 1) / a->max_prefix_blocks,
+          "n_groups * n_kv_heads * max_prefix_blocks must be below 2^31");
+  REQUIRE(a->n_rows <= (1 << 30), "n_rows must be at most 2^30");
+  if (a->B == 0) return ECHO_OK;
+  REQUIRE(a->q && a->rows && a->prefix_table && a->prefix_len && a->group_start && a->out && a->workspace,
+          "prefix attention pointer is NULL");
+  REQUIRE(!a->table == !a->ctx_len, "table and ctx_len go together");
+  REQUIRE(aligned(a->q, 16) && aligned(a->rows, 16) && aligned(a->out, 16), "q, rows and out must be 16-byte aligned");
+  REQUIRE(a->out != a->q, "out must not be q");
+  REQUIRE(aligned(a->workspace, 256), "workspace must be 256-byte aligned");
+  REQUIRE(a->workspace_bytes >= prefix_attention_workspace_bytes(a->B, a->n_q, a->n_heads, a->n_kv_heads, a->head_dim),
+          "workspace smaller than echo_prefix_attention_workspace_bytes()");
+  return launch_prefix_attention(a, static_cast<cudaStream_t>(stream));
 }
 
 int echo_prefill_indexer_score(const echo_prefill_args *a, void *stream) {

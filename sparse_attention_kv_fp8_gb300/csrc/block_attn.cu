@@ -79,6 +79,7 @@ struct BlockAttnParams {
   float v_scale;                     // one over the values' power of two
   uint32_t q_sign;                   // 0x80008000 for a negative scale
   uint16_t *out;
+  float *out32;                      // instead of out: the result in fp32, for a merge with other tokens'
   float *lse;
   int32_t cluster;                   // CTAs of a (b, h, row group), a cluster; 0: the line is cut
   float *part_o;                     // [2 * grid][rows][D]
@@ -338,8 +339,12 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
       if (P.by_pair)
         for (int i = threadIdx.x; i < heads; i += C::kThreads) P.tail[b * heads + i] = make_int4(0, 0, 0, 0);
       const int64_t o0 = static_cast<int64_t>(b) * P.n_q * P.n_heads;
-      for (int i = threadIdx.x; i < P.n_q * P.n_heads * (D / 8); i += C::kThreads)
-        reinterpret_cast<uint4 *>(P.out + o0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (P.out32)
+        for (int i = threadIdx.x; i < P.n_q * P.n_heads * (D / 4); i += C::kThreads)
+          reinterpret_cast<float4 *>(P.out32 + o0 * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        for (int i = threadIdx.x; i < P.n_q * P.n_heads * (D / 8); i += C::kThreads)
+          reinterpret_cast<uint4 *>(P.out + o0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
       if (P.lse)
         for (int i = threadIdx.x; i < P.n_q * P.n_heads; i += C::kThreads) P.lse[o0 + i] = -INFINITY;
     }
@@ -864,8 +869,13 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
           const int64_t oh = row_index(cur, row);
           if (oh >= 0) {
             const float inv = v.y > 0.f ? P.v_scale / v.y : v.y;  // (a NaN sum stays one)
-            *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
-            *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
+            if (P.out32) {
+              *reinterpret_cast<float2 *>(P.out32 + oh * D + d0) = make_float2(a.x * inv, a.y * inv);
+              *reinterpret_cast<float2 *>(P.out32 + oh * D + d1) = make_float2(b.x * inv, b.y * inv);
+            } else {
+              *reinterpret_cast<uint32_t *>(P.out + oh * D + d0) = pack2<false>(a.x * inv, a.y * inv);
+              *reinterpret_cast<uint32_t *>(P.out + oh * D + d1) = pack2<false>(b.x * inv, b.y * inv);
+            }
             if (k == 0 && hf == 0 && P.lse) P.lse[oh] = ba_lse(v.x, v.y);
           }
         }
@@ -914,8 +924,11 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
         y.x += x[r].x * f, y.y += x[r].y * f, y.z += x[r].z * f, y.w += x[r].w * f;
       }
       const float inv = sum > 0.f ? P.v_scale / sum : sum;
-      *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
-          make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
+      if (P.out32)
+        *reinterpret_cast<float4 *>(P.out32 + oh * D + d) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      else
+        *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
+            make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
       if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum);
     }
     cluster_arrive();  // (no CTA's shared memory goes while another reads it)
@@ -989,8 +1002,11 @@ __global__ void __launch_bounds__(BaComb<D, kPair>::kThreads) block_attn_combine
   const int j = rq / P.group;
   const int64_t oh = (static_cast<int64_t>(tail.x) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
   const float inv = sum > 0.f ? P.v_scale / sum : sum;
-  *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
-      make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
+  if (P.out32)
+    *reinterpret_cast<float4 *>(P.out32 + oh * D + d) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(P.out + oh * D + d) =
+        make_uint2(pack2<false>(y.x * inv, y.y * inv), pack2<false>(y.z * inv, y.w * inv));
   if (d == 0 && P.lse) P.lse[oh] = ba_lse(top, sum);
 }
 
@@ -1124,7 +1140,7 @@ static int ba_go(const echo::BlockAttnParams &P, int64_t pairs, int64_t most, in
   return Wide::launch(P, share <= cut && share <= 4 * extra ? cs : 0, pairs, sms, stream);
 }
 
-int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stream) {
+static int launch_block_attention(const echo_block_attention_args *a, float *out32, cudaStream_t stream) {
   echo::BlockAttnParams P{};
   P.q = a->q, P.rows = a->rows;
   P.row_bytes = 2 * echo::block_row_elems(a->format, a->block_tokens, a->head_dim);
@@ -1143,7 +1159,7 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   P.scale_log2 = std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift);
   P.v_scale = std::ldexp(1.f, -a->v_shift);
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
-  P.out = a->out, P.lse = a->lse;
+  P.out = a->out, P.out32 = out32, P.lse = a->lse;
   P.status = a->dev_status;
   const int pad = ba_row_pad(rows < echo::kBaMaxRows ? rows : echo::kBaMaxRows);
   P.tail = reinterpret_cast<int4 *>(a->workspace);
@@ -1181,6 +1197,15 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
 #undef BA_PICK
 #undef BA_SHAPE
 #undef BA_GO
+}
+
+int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stream) {
+  return launch_block_attention(a, nullptr, stream);
+}
+
+// the same with the result in fp32 (16-byte aligned, [B][n_q][n_heads][head_dim]) instead of a->out
+int launch_block_attention_f32(const echo_block_attention_args *a, float *out, cudaStream_t stream) {
+  return launch_block_attention(a, out, stream);
 }
 
 }  // namespace echo_host

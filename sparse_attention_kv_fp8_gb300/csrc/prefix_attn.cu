@@ -1,0 +1,973 @@
+// prefix_attn.cu -- decode attention of requests that share a prefix: the prefix's keys and
+// values are read once for all query rows of a group, as tensor-core tiles of 256 rows.
+//
+// For query row r of a request of group g (prefix tokens P_g, own tokens O_b):
+//   x_p = scale * q_r . k_p,   out = sum_{P_g and O_b} 2^(x_p log2 e - m) v_p / l.
+// A softmax over two sets of tokens is the merge of the two softmaxes by their maxima and sums,
+// so the prefix goes through this kernel, the own tokens through the kernel of
+// echo_block_attention (with its result left in fp32), and a last kernel merges the two.
+// 4 D flops per query row and token against 4 D bytes per token and KV head (bf16): from
+// about 280 rows a KV head on the tensor cores are the bound, below it HBM.
+//
+// sm_103a design.
+//   A CTA holds the queries of a tile of up to 256 rows (two sub-tiles of 128) in shared memory
+//     and walks over chunks of 128 prefix tokens:  S = Q K^T (tcgen05.mma, M = 128 rows, N = 128
+//     tokens) into tensor memory, softmax by a warpgroup per sub-tile (a thread per row), P back
+//     into the tensor memory that S took (16 bit, half its columns), O += P V with P as the
+//     tensor-memory operand and V read along the tokens.  While one sub-tile's warpgroup is at
+//     its softmax, the tensor cores work for the other; one thread issues all products, which
+//     run in the order of their issue, so S may overwrite the P that the product before it read.
+//   Blocks come by TMA, a box per run of tokens inside a block, into a ring of key and value
+//     tiles in the 128-byte swizzle.  4-bit rows come as they are (one bulk copy per sub-block of
+//     16 tokens) and eight warps convert them, exactly, to fp16 tiles.
+//   Lazy maximum as in the decode kernel: O is rescaled (in tensor memory) only when a score
+//     exceeds its row's maximum by 2^8.
+//   All chunks of all (group, KV head, row tile) form one line, cut into equal pieces by the
+//     lengths on the device, one per CTA.  Each (tile, piece) leaves its maxima, sums and O in
+//     fp32: pieces that begin with a tile in a row per query row, the others in a slot per CTA.
+//     The merge kernel takes them in order, so results do not depend on timing.
+#include <algorithm>
+#include <cmath>
+
+#include "block_mma.cuh"
+
+namespace echo {
+
+constexpr int kPxChunk = 128;         // prefix tokens of a step
+constexpr int kPxRows = 256;          // query rows of a CTA's tile (two sub-tiles)
+constexpr int kPxMaxGrid = 160;
+constexpr float kPxLazy = 8.f;        // log2 of how far a score may exceed its row's maximum
+constexpr float kPxLift = 7.f;        // fp16 weights are kept 2^7 up (their subnormals begin 2^-21 below the maximum)
+constexpr float kPxNone = -3.4028234664e38f;
+
+struct PrefixParams {
+  const uint16_t *q;
+  const uint8_t *rows;
+  int64_t row_bytes;
+  int32_t n_rows, bs, box;            // box: tokens of a TMA box, a divisor of bs
+  const int32_t *table;               // [n_groups][heads][max_blocks]
+  int32_t heads, max_blocks;
+  const int32_t *len, *start;         // [n_groups], [n_groups + 1]
+  int32_t n_groups;
+  int32_t B, n_q, n_heads, n_kv, group;
+  float scale_log2;                   // |scale| log2 e, over the keys' power of two
+  float v_scale;                      // one over the values' power of two
+  uint32_t q_sign;
+  float *first_o;                     // [B n_q n_heads][D]: pieces that begin with their tile
+  float2 *first_ml;
+  float *rest_o;                      // [kPxMaxGrid][kPxRows][D]: of a CTA's first piece otherwise
+  float2 *rest_ml;
+  const float *own_o, *own_lse;       // [B n_q n_heads][D], or NULL
+  uint16_t *out;
+  float *lse;
+  int32_t grid;
+  int32_t *status;
+};
+
+// ---------------------------------------------------------------------------
+// the line of chunks
+// ---------------------------------------------------------------------------
+struct PxGroup {
+  int b0, rows;       // first request, query rows of a KV head
+  int len, tiles, chunks;
+};
+
+__device__ __forceinline__ PxGroup px_group(const PrefixParams &P, int g, bool report) {
+  PxGroup x;
+  const int s0 = P.start[g], s1 = P.start[g + 1];
+  x.b0 = min(max(s0, 0), P.B);
+  const int b1 = min(max(s1, x.b0), P.B);
+  x.rows = (b1 - x.b0) * P.n_q * P.group;
+  const int most = P.max_blocks * P.bs, n = P.len[g];
+  x.len = min(max(n, 0), most);
+  if (report && (n > most || s0 < 0 || s1 > P.B || s1 < s0)) set_status(P.status, ECHO_DEV_BAD_INDEX);
+  x.tiles = (x.rows + kPxRows - 1) / kPxRows;
+  x.chunks = (x.len + kPxChunk - 1) / kPxChunk;
+  return x;
+}
+__device__ __forceinline__ int64_t px_units(const PrefixParams &P, const PxGroup &x) {
+  return static_cast<int64_t>(P.n_kv) * x.tiles * x.chunks;
+}
+
+// One CTA's place on the line: the piece of tile (g, h, t) from chunk c on, n chunks long.
+struct PxLine {
+  int g, h, t, c, n;
+  PxGroup x;
+  int64_t left;       // chunks of this CTA's share from c on
+
+  __device__ __forceinline__ void piece() { n = static_cast<int>(min(static_cast<int64_t>(x.chunks - c), left)); }
+
+  // the first piece (by a whole warp)
+  __device__ __forceinline__ bool begin(const PrefixParams &P, bool report) {
+    const int lane = threadIdx.x & 31;
+    const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
+    int64_t mine = 0;
+    for (int i = g0; i < g1; ++i) mine += px_units(P, px_group(P, i, report));
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += y;
+    }
+    const int64_t total = __shfl_sync(~0u, upto, 31);
+    const int64_t per = (total + P.grid - 1) / P.grid, u0 = per * blockIdx.x;
+    if (u0 >= total) return false;
+    left = min(per, total - u0);
+    int at = 0, off_tile = 0, off_chunk = 0;
+    const bool own = u0 >= upto - mine && u0 < upto;
+    if (own) {
+      int64_t u = upto - mine;
+      for (at = g0;; ++at) {
+        const PxGroup y = px_group(P, at, false);
+        const int64_t k = px_units(P, y);
+        if (u0 < u + k) {
+          off_tile = static_cast<int>((u0 - u) / y.chunks);
+          off_chunk = static_cast<int>((u0 - u) % y.chunks);
+          break;
+        }
+        u += k;
+      }
+    }
+    const int src = __ffs(__ballot_sync(~0u, own)) - 1;
+    g = __shfl_sync(~0u, at, src);
+    const int tile = __shfl_sync(~0u, off_tile, src);
+    c = __shfl_sync(~0u, off_chunk, src);
+    x = px_group(P, g, false);
+    h = tile / x.tiles, t = tile - h * x.tiles;
+    piece();
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const PrefixParams &P) {
+    left -= n;
+    if (left <= 0) return false;
+    c = 0;            // (a piece ends with its tile or with the share)
+    if (++t == x.tiles) {
+      t = 0;
+      if (++h == P.n_kv) {
+        h = 0;
+        do {
+          x = px_group(P, ++g, false);
+        } while (x.tiles == 0 || x.chunks == 0);  // (chunks are left: there is such a group)
+      }
+    }
+    piece();
+    return true;
+  }
+
+  // rows of sub-tile s
+  __device__ __forceinline__ int sub_rows(int s) const { return min(max(x.rows - t * kPxRows - s * 128, 0), 128); }
+};
+
+// the cache row of a prefix token (a token below the prefix's length), -1: not held
+__device__ __forceinline__ int64_t px_row(const PrefixParams &P, int g, int h, int token, int &off, bool report) {
+  const int e = token / P.bs;
+  off = token - e * P.bs;
+  const int32_t id = P.table[(static_cast<int64_t>(g) * P.heads + (P.heads > 1 ? h : 0)) * P.max_blocks + e];
+  if (id < 0) return -1;
+  const int64_t row = P.heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
+  if (row < P.n_rows) return row;
+  if (report) set_status(P.status, ECHO_DEV_BAD_INDEX);
+  return -1;
+}
+
+// (b, query token, head) of row r of a tile's group
+__device__ __forceinline__ int64_t px_out_row(const PrefixParams &P, const PxLine &L, int r) {
+  const int per = P.n_q * P.group, b = r / per, rq = r - b * per, j = rq / P.group;
+  return (static_cast<int64_t>(L.x.b0 + b) * P.n_q + j) * P.n_heads + L.h * P.group + rq - j * P.group;
+}
+
+// ---------------------------------------------------------------------------
+// tensor-core helpers (beside those of echo_common.cuh)
+// ---------------------------------------------------------------------------
+__host__ __device__ constexpr uint32_t px_idesc(bool f16, int N, int b_mn) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (128u >> 4 << 24);
+}
+// MN-major operand in the 128-byte swizzle: groups of 64 elements along N `lbo` bytes apart, groups
+// of 8 rows along K 1024 bytes apart
+__device__ __forceinline__ uint64_t px_mn_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+__device__ __forceinline__ void px_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(acc)
+               : "memory");
+}
+__device__ __forceinline__ void px_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(acc)
+               : "memory");
+}
+__device__ __forceinline__ void px_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void px_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void px_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void px_tma(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void px_bulk(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void px_store8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+               "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+// a wait without the abort flag, for what is in flight when a kernel gives up
+__device__ __forceinline__ void px_drain(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < kWaitLimitNs) {
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <int FMT, int D>
+struct PxCfg {
+  static constexpr bool kFp4 = FMT == ECHO_BLOCK_FP4;
+  static constexpr uint32_t kBlock = 128 * 128;             // 128 rows or tokens of 64 dims
+  static constexpr uint32_t kTile = kBlock * (D / 64);      // of all dims
+  static constexpr int kSlots = kFp4 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 9;  // ring of key and value tiles
+  static constexpr int kRaw = kFp4 ? 3 : 0;                 // stages of 4-bit chunks
+  static constexpr uint32_t kRawBytes = 8 * 18 * D;
+  static constexpr int kConvWarps = kFp4 ? 8 : 0;
+  static constexpr int kThreads = 32 * (8 + 2 + kConvWarps);
+  static constexpr uint32_t kOffQ = 0, kOffRing = 2 * kTile, kOffRaw = kOffRing + kSlots * kTile;
+  static constexpr uint32_t kOffCtl = kOffRaw + kRaw * kRawBytes;
+};
+
+struct PxCtl {
+  uint64_t kv_full[9], kv_empty[9], raw_full[3], raw_empty[3];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain;
+  uint32_t held[9];       // sub-blocks of 16 tokens that a value tile holds, a bit each
+  uint32_t tmem;
+  int abort;
+};
+
+// which of a chunk's sub-blocks of 16 tokens are held (by a warp; bits 0-7)
+__device__ __forceinline__ uint32_t px_held(const PrefixParams &P, int g, int h, int len, int chunk) {
+  const int lane = threadIdx.x & 31, token = chunk * kPxChunk + lane * kSubTokens;
+  int off;
+  const bool on = lane < kPxChunk / kSubTokens && token < len && px_row(P, g, h, token, off, false) >= 0;
+  return __ballot_sync(~0u, on);
+}
+// tokens 32 w .. 32 w + 31 of a chunk: held and below the length
+__device__ __forceinline__ uint32_t px_seen(uint32_t held, int w, int tokens) {
+  const uint32_t two = held >> (2 * w);
+  const int n = tokens - 32 * w;
+  return ((two & 1 ? 0xffffu : 0u) | (two & 2 ? 0xffff0000u : 0u)) & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1);
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap map, const PrefixParams P) {
+  using C = PxCfg<FMT, D>;
+  constexpr bool F16 = C::kFp4;
+  constexpr float kLift = F16 ? kPxLift : 0.f;
+  constexpr uint32_t kIdescS = px_idesc(F16, kPxChunk, 0), kIdescO = px_idesc(F16, D, 1);
+  extern __shared__ uint8_t px_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(px_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  PxCtl *ctl = reinterpret_cast<PxCtl *>(smem + C::kOffCtl);
+  float *qscale = reinterpret_cast<float *>(ctl + 1);   // [kPxRows] (4-bit rows)
+  const uint32_t q_at = smem_u32(smem + C::kOffQ), ring = smem_u32(smem + C::kOffRing);
+  volatile int *abort = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&ctl->kv_full[i], F16 ? C::kConvWarps : 1);
+      mbar_init(&ctl->kv_empty[i], 1);
+    }
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&ctl->raw_full[i], 1);
+      mbar_init(&ctl->raw_empty[i], C::kConvWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->q_full[s], 4);
+      mbar_init(&ctl->s_full[s], 1);
+      mbar_init(&ctl->p_full[s], 4);
+      mbar_init(&ctl->o_full[s], 1);
+      mbar_init(&ctl->o_free[s], 4);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;   // S of the sub-tiles at columns 0 and 128, O at 256 and 256 + D
+  pdl_wait();
+  pdl_launch_dependents();
+
+  PxLine L;
+  const bool any = L.begin(P, blockIdx.x == 0 && warp == 0);
+  if (any && warp < 8) {
+    // ===================== softmax: a warpgroup per sub-tile, a thread per row =====================
+    const int s = warp >> 2, w4 = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t s_at = tmem + s * 128 + lanes, o_at = tmem + 256 + s * D + lanes;
+    uint32_t ph_s = 0, ph_o = 0;
+    bool ok = true, active = L.sub_rows(s) > 0;
+
+    // the queries of this warp's rows: D / 8 lanes a row, 16 bytes each
+    auto load_q = [&]() {
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+      const int n = L.sub_rows(s), d8 = lane % kLanes;
+      for (int r0 = 0; r0 < 32; r0 += 4 * kPer) {
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = w4 * 32 + r0 + u * kPer + lane / kLanes;
+          x[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < n) x[u] = *reinterpret_cast<const uint4 *>(P.q + px_out_row(P, L, L.t * kPxRows + s * 128 + r) * D + d8 * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = w4 * 32 + r0 + u * kPer + lane / kLanes;
+          uint32_t v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          if constexpr (F16) {  // scaled by the power of two that brings the row's largest entry to [1, 2)
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xffff0000u))));
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+            int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+            e = max(min(e, 126), -126);  // (zero rows, subnormal and infinite maxima)
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = pack2<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
+            if (d8 == 0) qscale[s * 128 + r] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          }
+          uint8_t *dst = smem + C::kOffQ + s * C::kTile + (d8 >> 3) * C::kBlock + r * 128 + (((d8 & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0] ^ P.q_sign, v[1] ^ P.q_sign, v[2] ^ P.q_sign, v[3] ^ P.q_sign);
+        }
+      }
+      px_fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full[s]);
+    };
+
+    if (active) load_q();
+    for (bool more = true; more && ok;) {
+      const PxLine cur = L;
+      const bool rows = active && w4 * 32 < cur.sub_rows(s);   // of this warp
+      const float c = P.scale_log2 * (F16 && active ? qscale[s * 128 + w4 * 32 + lane] : 1.f);
+      float m = kPxNone, l = 0.f;
+      uint32_t held = active ? px_held(P, cur.g, cur.h, cur.x.len, cur.c) : 0u;
+      for (int i = 0; active && i < cur.n; ++i) {
+        const uint32_t held_now = held;
+        if (i + 1 < cur.n) held = px_held(P, cur.g, cur.h, cur.x.len, cur.c + i + 1);
+        if (!mbar_wait(&ctl->s_full[s], ph_s, abort, P.status)) {
+          ok = false;
+          break;
+        }
+        ph_s ^= 1;
+        tc_fence_after();
+        if (rows) {
+          const int tokens = cur.x.len - (cur.c + i) * kPxChunk;
+          const bool edge = held_now != 0xffu || tokens < kPxChunk;
+          float top = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < 4; b += 2) {
+            float v[2][32];
+            tmem_ld_32x32b_x32(s_at + b * 32, v[0]);
+            tmem_ld_32x32b_x32(s_at + b * 32 + 32, v[1]);
+            tmem_wait_ld();
+            reg_fence_32(v[0]);
+            reg_fence_32(v[1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (edge) {
+                const uint32_t seen = px_seen(held_now, b + u, tokens);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) top = fmaxf(top, seen >> k & 1 ? v[u][k] : -INFINITY);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) top = fmaxf(top, v[u][k]);
+              }
+            }
+          }
+          const float x = top == -INFINITY ? kPxNone : fmaf(top, c, -kLift);
+          if (i == 0) {
+            m = x;
+          } else if (__any_sync(~0u, x - m > kPxLazy)) {
+            const float up = fmaxf(m, x), f = ex2(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b) {
+              uint32_t o[16];
+              asm volatile(
+                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
+                    "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                  : "r"(o_at + b * 16)
+                  : "memory");
+              asm volatile("tcgen05.wait::ld.sync.aligned;"
+                           : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7]),
+                             "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]), "+r"(o[13]), "+r"(o[14]), "+r"(o[15])
+                           :
+                           : "memory");
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              px_st16(o_at + b * 16, o);
+            }
+          }
+          const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            float v[32];
+            tmem_ld_32x32b_x32(s_at + b * 32, v);
+            tmem_wait_ld();
+            reg_fence_32(v);
+            const uint32_t seen = edge ? px_seen(held_now, b, tokens) : ~0u;
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 y = __ffma2_rn(make_float2(v[2 * k], v[2 * k + 1]), c2, m2);
+              float2 e = make_float2(ex2(y.x), ex2(y.y));
+              if (edge) e.x = seen >> (2 * k) & 1 ? e.x : 0.f, e.y = seen >> (2 * k + 1) & 1 ? e.y : 0.f;
+              sum = __fadd2_rn(sum, e);
+              // (one 16-bit term: 2^-9 (2^-12 in 4 bits) of a weight at most, of random sign; a second
+              // term would cost half as many products again)
+              p[k] = pack2<F16>(e.x, e.y);
+            }
+            px_st16(s_at + b * 16, p);
+          }
+          l += sum.x + sum.y;
+          px_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full[s]);
+      }
+      if (!ok) break;
+      // every product with the queries is done: the next piece's go in
+      more = L.next(P);
+      const bool was = active;
+      active = more && L.sub_rows(s) > 0;
+      if (active) load_q();
+      if (!was) continue;
+      if (!mbar_wait(&ctl->o_full[s], ph_o, abort, P.status)) {
+        ok = false;
+        break;
+      }
+      ph_o ^= 1;
+      tc_fence_after();
+      if (rows) {
+        const int r = s * 128 + w4 * 32 + lane;
+        const bool valid = w4 * 32 + lane < cur.sub_rows(s);
+        const int64_t at = cur.c == 0 ? (valid ? px_out_row(P, cur, cur.t * kPxRows + r) : 0)
+                                      : static_cast<int64_t>(blockIdx.x) * kPxRows + r;
+        float *dst = (cur.c == 0 ? P.first_o : P.rest_o) + at * D;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+          float v[32];
+          tmem_ld_32x32b_x32(o_at + b * 32, v);
+          tmem_wait_ld();
+          reg_fence_32(v);
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) px_store8(dst + b * 32 + k, v + k);
+          }
+        }
+        if (valid) (cur.c == 0 ? P.first_ml : P.rest_ml)[at] = make_float2(m == kPxNone && l == 0.f ? -INFINITY : m, l);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->o_free[s]);
+    }
+  } else if (any && warp == 8) {
+    // ===================== producer =====================
+    int k = 0;        // tiles (bf16) or chunks (4 bits) asked for
+    bool ok = true;
+    for (bool more = true; more && ok; more = ok && L.next(P)) {
+      for (int i = 0; i < L.n && ok; ++i) {
+        const int base = (L.c + i) * kPxChunk;
+        if constexpr (F16) {
+          const int st = k % C::kRaw, token = base + lane * kSubTokens;
+          int off = 0;
+          const int64_t row = lane < 8 && token < L.x.len ? px_row(P, L.g, L.h, token, off, true) : -1;
+          const uint32_t held = __ballot_sync(~0u, row >= 0);
+          if (k >= C::kRaw && !mbar_wait(&ctl->raw_empty[st], (k / C::kRaw - 1) & 1, abort, P.status)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->raw_full[st], __popc(held) * 18 * D);
+          __syncwarp();
+          if (row >= 0)
+            px_bulk(smem_u32(smem + C::kOffRaw) + st * C::kRawBytes + lane * 18 * D,
+                    P.rows + row * P.row_bytes + (off / kSubTokens) * Fp4Sub<D>::kBytes, 18 * D, &ctl->raw_full[st]);
+          ++k;
+        } else {
+          const int boxes = kPxChunk / P.box, token = base + lane * P.box;
+          int off = 0;
+          const int64_t row = lane < boxes && token < L.x.len ? px_row(P, L.g, L.h, token, off, true) : -1;
+          const uint32_t held = __ballot_sync(~0u, row >= 0);
+          uint32_t subs = 0;   // the same by 16 tokens
+          for (int x = 0; x < 8; ++x) subs |= (held >> (x * kSubTokens / P.box) & 1) << x;
+#pragma unroll
+          for (int v = 0; v < 2; ++v, ++k) {
+            const int st = k % C::kSlots;
+            if (k >= C::kSlots && !mbar_wait(&ctl->kv_empty[st], (k / C::kSlots - 1) & 1, abort, P.status)) {
+              ok = false;
+              break;
+            }
+            __syncwarp();
+            if (lane == 0) {
+              ctl->held[st] = subs;
+              mbar_arrive_expect_tx(&ctl->kv_full[st], __popc(held) * P.box * 2 * D);
+            }
+            __syncwarp();
+            if (row >= 0) {
+#pragma unroll
+              for (int hb = 0; hb < D / 64; ++hb)
+                px_tma(ring + st * C::kTile + hb * C::kBlock + lane * P.box * 128, &map, &ctl->kv_full[st], hb * 64, off,
+                       static_cast<int>(2 * row + v));
+            }
+          }
+        }
+      }
+    }
+    if (*abort) {  // let every copy this warp started land before the CTA exits
+      constexpr int kDepth = F16 ? (C::kRaw ? C::kRaw : 1) : C::kSlots;
+      for (int j = max(k - kDepth, 0); j < k; ++j) px_drain(F16 ? &ctl->raw_full[j % kDepth] : &ctl->kv_full[j % kDepth], (j / kDepth) & 1);
+    }
+  } else if (any && warp == 9) {
+    // ===================== tensor-core issuer =====================
+    uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_free[2] = {1, 1};  // (O is free at first)
+    int k = 0;        // tiles taken from the ring
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = ok && mbar_wait(bar, parity, abort, P.status);
+      ok = __all_sync(~0u, ok);
+      return ok;
+    };
+    auto full = [&](int tile) { return wait(&ctl->kv_full[tile % C::kSlots], (tile / C::kSlots) & 1); };
+    auto slot = [&](int tile) { return ring + (tile % C::kSlots) * C::kTile; };
+    auto scores = [&](int s, int tile) {     // S of sub-tile s
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t a = q_at + s * C::kTile, b = slot(tile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * C::kBlock + (kk & 3) * 32;
+          px_mma_ss(tmem + s * 128, kmajor_sw128_desc(a + o), kmajor_sw128_desc(b + o), kIdescS, kk > 0);
+        }
+        mma_commit(&ctl->s_full[s]);
+      }
+    };
+    auto values = [&](int s, int tile, bool more) {  // O of sub-tile s
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t b = slot(tile);
+#pragma unroll
+        for (int kk = 0; kk < kPxChunk / 16; ++kk)
+          px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8, px_mn_desc(b + kk * 16 * 128, C::kBlock), kIdescO, more || kk > 0);
+      }
+    };
+    auto release = [&](int tile) {
+      if (lane == 0) mma_commit(&ctl->kv_empty[tile % C::kSlots]);
+    };
+    for (bool more = true; more && ok; more = ok && L.next(P)) {
+      const bool two = L.sub_rows(1) > 0;
+      if (!full(k)) break;
+      for (int s = 0; s < (two ? 2 : 1); ++s) {
+        if (!wait(&ctl->q_full[s], ph_q[s])) break;
+        ph_q[s] ^= 1;
+        scores(s, k);
+      }
+      if (!ok) break;
+      release(k);
+      for (int i = 0; i < L.n && ok; ++i, k += 2) {
+        const bool last = i + 1 == L.n;
+        if (!full(k + 1)) break;
+        if constexpr (!F16) {
+          // values that no query sees are zeros (a weight of zero times NaN is NaN)
+          const uint32_t held = ctl->held[(k + 1) % C::kSlots];
+          const int tokens = L.x.len - (L.c + i) * kPxChunk;
+          if (held != 0xffu || tokens < kPxChunk) {
+            uint8_t *v = smem + C::kOffRing + ((k + 1) % C::kSlots) * C::kTile;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if (!(px_seen(held, w, tokens) >> lane & 1))
+                for (int x = 0; x < static_cast<int>(C::kTile / C::kBlock) * 8; ++x)
+                  *reinterpret_cast<uint4 *>(v + (x >> 3) * C::kBlock + (w * 32 + lane) * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            px_fence_smem();
+            __syncwarp();
+          }
+        }
+        if (!last && !full(k + 2)) break;
+        for (int s = 0; s < (two ? 2 : 1); ++s) {
+          if (!wait(&ctl->p_full[s], ph_p[s])) break;
+          ph_p[s] ^= 1;
+          if (i == 0) {
+            if (!wait(&ctl->o_free[s], ph_free[s])) break;
+            ph_free[s] ^= 1;
+          }
+          values(s, k + 1, i > 0);
+          if (s == (two ? 1 : 0)) release(k + 1);
+          if (last) {
+            if (lane == 0) mma_commit(&ctl->o_full[s]);
+          } else {
+            scores(s, k + 2);
+            if (s == (two ? 1 : 0)) release(k + 2);
+          }
+        }
+      }
+    }
+    if (!ok) {  // no product may run on when the tensor memory goes
+      if (lane == 0) {
+        mma_commit(&ctl->drain);
+        px_drain(&ctl->drain, 0);
+      }
+    }
+    __syncwarp();
+  } else if (F16 && any) {
+    // ===================== 4-bit rows to fp16 tiles: a warp per sub-block, a lane per (token, half of the dims) ====
+    constexpr int kWords = D / 16;      // 8-code words of a lane
+    const int sub = warp - 10, tk = lane & 15, hf = lane >> 4;
+    int k = 0;
+    bool ok = true;
+    auto store = [&](uint8_t *tile, const uint32_t (&h)[kWords][4], bool on) {
+      const int r = sub * kSubTokens + tk;
+      uint8_t *dst = tile + (D == 128 ? hf * C::kBlock : 0u) + r * 128;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int piece = D == 128 ? i : hf * kWords + i;
+        *reinterpret_cast<uint4 *>(dst + ((piece ^ (r & 7)) << 4)) = on ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto convert = [&](const uint32_t (&w)[kWords], const uint32_t (&sc)[kWords / 2], uint32_t (&h)[kWords][4]) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t s2 = __byte_perm(e4m3x2_to_half2(sc[i / 2]), 0, 0x1010);
+        e2m1x8_to_half2(w[i], h[i]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) h[i][v] = hmul2(h[i][v], s2);
+      }
+    };
+    for (bool more = true; more && ok; more = ok && L.next(P)) {
+      uint32_t held = px_held(P, L.g, L.h, L.x.len, L.c);
+      for (int i = 0; i < L.n && ok; ++i, ++k) {
+        const uint32_t held_now = held;
+        if (i + 1 < L.n) held = px_held(P, L.g, L.h, L.x.len, L.c + i + 1);
+        const int st = k % C::kRaw, token = (L.c + i) * kPxChunk + sub * kSubTokens + tk;
+        const bool on = (held_now >> sub & 1) && token < L.x.len;
+        if (!mbar_wait(&ctl->raw_full[st], (k / C::kRaw) & 1, abort, P.status)) {
+          ok = false;
+          break;
+        }
+        const uint8_t *src = smem + C::kOffRaw + st * C::kRawBytes + sub * 18 * D;
+        uint32_t w[kWords], sc[kWords / 2], h[kWords][4];
+        // keys: codes [16][D / 2], scales [16][D / 16]
+#pragma unroll
+        for (int x = 0; x < kWords / 4; ++x) {
+          const uint4 y = *reinterpret_cast<const uint4 *>(src + tk * (D / 2) + hf * (D / 4) + x * 16);
+          w[4 * x] = y.x, w[4 * x + 1] = y.y, w[4 * x + 2] = y.z, w[4 * x + 3] = y.w;
+        }
+#pragma unroll
+        for (int x = 0; x < kWords / 2; ++x) sc[x] = src[Fp4Sub<D>::kKeyScales + tk * (D / 16) + hf * (D / 32) + x];
+        convert(w, sc, h);
+        // values: codes [2][8][8 tokens][D / 16], scales [2][D / 16][8 tokens]
+        const uint8_t *vc = src + Fp4Sub<D>::kValues + (tk >> 3) * (4 * D) + (hf * 4 * 8 + (tk & 7)) * (D / 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if constexpr (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2 *>(vc + x * 8 * (D / 16));
+            w[2 * x] = y.x, w[2 * x + 1] = y.y;
+          } else {
+            w[x] = *reinterpret_cast<const uint32_t *>(vc + x * 8 * (D / 16));
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kWords / 2; ++x)
+          sc[x] = src[Fp4Sub<D>::kValueScales + (tk >> 3) * (D / 2) + (hf * (D / 32) + x) * 8 + (tk & 7)];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->raw_empty[st]);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int tile = 2 * k + v, sl = tile % C::kSlots;
+          if (tile >= C::kSlots && !mbar_wait(&ctl->kv_empty[sl], (tile / C::kSlots - 1) & 1, abort, P.status)) {
+            ok = false;
+            break;
+          }
+          if (v) convert(w, sc, h);
+          store(smem + C::kOffRing + sl * C::kTile, h, on);
+          px_fence_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->kv_full[sl]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge: a warp per query row
+// ---------------------------------------------------------------------------
+constexpr int kPxMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const PrefixParams P) {
+  constexpr int kPer = D / 32;      // dims of a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kPxMergeWarps + warp, rows = static_cast<int64_t>(P.B) * P.n_q * P.n_heads;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (row >= rows) return;
+  const int head = static_cast<int>(row % P.n_heads);
+  const int64_t bj = row / P.n_heads;
+  const int b = static_cast<int>(bj / P.n_q), j = static_cast<int>(bj - static_cast<int64_t>(b) * P.n_q), h = head / P.group;
+
+  // where the row's tile lies on the line
+  const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
+  int64_t mine = 0, u = 0;
+  int chunks = 0, tiles = 0, r = 0;
+  bool own = false;
+  for (int g = g0; g < g1; ++g) {
+    const PxGroup x = px_group(P, g, false);
+    const int per = P.n_q * P.group;
+    if (!own && x.chunks > 0 && b >= x.b0 && b < x.b0 + x.rows / per)
+      own = true, u = mine, chunks = x.chunks, tiles = x.tiles, r = (b - x.b0) * per + j * P.group + head - h * P.group;
+    mine += px_units(P, x);
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += y;
+  }
+  const int64_t total = __shfl_sync(~0u, upto, 31);
+  u += upto - mine;
+  const uint32_t who = __ballot_sync(~0u, own);
+  int first = 0, pieces = 0;        // the tile's first CTA and how many pieces it has
+  if (who) {
+    const int src = __ffs(who) - 1;
+    u = __shfl_sync(~0u, u, src);
+    chunks = __shfl_sync(~0u, chunks, src), tiles = __shfl_sync(~0u, tiles, src), r = __shfl_sync(~0u, r, src);
+    const int64_t per = (total + P.grid - 1) / P.grid;
+    u += (static_cast<int64_t>(h) * tiles + r / kPxRows) * chunks;
+    first = static_cast<int>(u / per);
+    pieces = static_cast<int>((u + chunks - 1) / per) - first + 1;
+    r %= kPxRows;
+  }
+
+  float top = -INFINITY, sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  auto part = [&](int p, float2 &ml, const float *&o) {
+    const int64_t at = p == 0 ? row : static_cast<int64_t>(first + p) * kPxRows + r;
+    ml = (p == 0 ? P.first_ml : P.rest_ml)[at];
+    o = (p == 0 ? P.first_o : P.rest_o) + at * D + lane * kPer;
+  };
+  constexpr int kAhead = 4;
+  for (int p0 = 0; p0 < pieces; p0 += kAhead) {
+    float2 ml[kAhead];
+    float x[kAhead][kPer];
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      ml[p] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) x[p][k] = 0.f;
+      if (p0 + p < pieces) {
+        const float *o;
+        part(p0 + p, ml[p], o);
+        if constexpr (kPer == 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(o);
+          x[p][0] = y.x, x[p][1] = y.y, x[p][2] = y.z, x[p][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2 *>(o);
+          x[p][0] = y.x, x[p][1] = y.y;
+        }
+      }
+    }
+    float up = top;
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) up = fmaxf(up, ml[p].x);
+    const float f = top == -INFINITY ? 0.f : ex2(top - up);
+    sum *= f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] *= f;
+    top = up;
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      if (ml[p].x == -INFINITY) continue;  // (nothing seen; a sum that is NaN has a maximum all the same)
+      const float e = ex2(ml[p].x - top);
+      sum = fmaf(ml[p].y, e, sum);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(x[p][k], e, acc[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] *= P.v_scale;
+  if (P.own_o) {                    // divided by its sum already: weight 2^lse, sum 1
+    const float lse = P.own_lse[row] * 1.4426950408889634f;
+    if (lse != -INFINITY) {
+      const float up = fmaxf(top, lse), f = top == -INFINITY ? 0.f : ex2(top - up), e = ex2(lse - up);
+      top = up;
+      sum = fmaf(sum, f, e);
+      const float *o = P.own_o + row * D + lane * kPer;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(o[k], e, acc[k] * f);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum;  // (a NaN sum stays one)
+  uint32_t *dst = reinterpret_cast<uint32_t *>(P.out + row * D + lane * kPer);
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k) dst[k] = pack2<false>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  if (P.lse && lane == 0) P.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+}
+
+}  // namespace echo
+
+namespace echo_host {
+
+size_t block_attention_workspace_bytes(int32_t rows, int32_t head_dim);
+int launch_block_attention_f32(const echo_block_attention_args *a, float *out, cudaStream_t stream);
+
+// workspace: pieces that begin with a tile | pieces that do not | the own tokens' results | the
+// decode kernel's own workspace
+struct PxSpace {
+  size_t first_ml, rest_o, rest_ml, own_o, own_lse, own_ws, end;
+};
+static PxSpace px_space(int64_t rows, int32_t rows_per_kv_head, int32_t head_dim) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  PxSpace s;
+  s.first_ml = up(static_cast<size_t>(rows) * head_dim * 4);
+  s.rest_o = s.first_ml + up(static_cast<size_t>(rows) * 8);
+  s.rest_ml = s.rest_o + up(static_cast<size_t>(echo::kPxMaxGrid) * echo::kPxRows * head_dim * 4);
+  s.own_o = s.rest_ml + up(static_cast<size_t>(echo::kPxMaxGrid) * echo::kPxRows * 8);
+  s.own_lse = s.own_o + up(static_cast<size_t>(rows) * head_dim * 4);
+  s.own_ws = s.own_lse + up(static_cast<size_t>(rows) * 4);
+  s.end = s.own_ws + up(block_attention_workspace_bytes(rows_per_kv_head, head_dim));
+  return s;
+}
+
+size_t prefix_attention_workspace_bytes(int32_t B, int32_t n_q, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+  return px_space(static_cast<int64_t>(B) * n_q * n_heads, n_q * (n_heads / n_kv_heads), head_dim).end;
+}
+
+typedef CUresult (*PFN_encodeTiledX)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                     const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// keys and values of bf16 rows as [2 n_rows][block_tokens][head_dim], boxes of `box` tokens and 64 dims
+static int px_map(const echo::PrefixParams &P, int D, CUtensorMap *map) {
+  static std::atomic<PFN_encodeTiledX> known{nullptr};
+  PFN_encodeTiledX enc = known.load(std::memory_order_acquire);
+  if (!enc) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      set_error("cuTensorMapEncodeTiled unavailable from the driver");
+      return ECHO_ECUDA;
+    }
+    enc = reinterpret_cast<PFN_encodeTiledX>(p);
+    known.store(enc, std::memory_order_release);
+  }
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(P.bs), 2 * static_cast<cuuint64_t>(P.n_rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(P.bs) * D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(P.box), 1}, es[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t *>(P.rows), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("tensor map for rows failed (CUresult %d)", static_cast<int>(r));
+    return ECHO_ECUDA;
+  }
+  return ECHO_OK;
+}
+
+template <int FMT, int D>
+static int go_prefix(const echo::PrefixParams &P, cudaStream_t stream) {
+  using C = echo::PxCfg<FMT, D>;
+  constexpr int kSmem = C::kOffCtl + sizeof(echo::PxCtl) + (C::kFp4 ? echo::kPxRows * 4 : 0) + 1024;
+  static_assert(kSmem <= 232448, "prefix attention: shared memory of one CTA");
+  static std::atomic<bool> attr[kMaxDevices];
+  if (int rr = smem_limit_once(attr, echo::prefix_attn_kernel<FMT, D>, kSmem, "prefix attention smem attribute")) return rr;
+  CUtensorMap map{};
+  if (!C::kFp4)
+    if (int rr = px_map(P, D, &map)) return rr;
+  cudaError_t e = launch_pdl(echo::prefix_attn_kernel<FMT, D>, dim3(P.grid), dim3(C::kThreads), kSmem, stream, map, P);
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "prefix attention launch");
+}
+
+int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix attention device");
+  const int64_t rows = static_cast<int64_t>(a->B) * a->n_q * a->n_heads;
+  const PxSpace s = px_space(rows, a->n_q * (a->n_heads / a->n_kv_heads), a->head_dim);
+  uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+  echo::PrefixParams P{};
+  P.q = a->q, P.rows = reinterpret_cast<const uint8_t *>(a->rows);
+  P.row_bytes = 2 * echo::block_row_elems(a->format, a->block_tokens, a->head_dim);
+  P.n_rows = a->n_rows, P.bs = a->block_tokens;
+  for (P.box = 128; a->block_tokens % P.box; P.box /= 2) {
+  }
+  P.table = a->prefix_table, P.heads = a->prefix_heads, P.max_blocks = a->max_prefix_blocks;
+  P.len = a->prefix_len, P.start = a->group_start, P.n_groups = a->n_groups;
+  P.B = a->B, P.n_q = a->n_q, P.n_heads = a->n_heads, P.n_kv = a->n_kv_heads, P.group = a->n_heads / a->n_kv_heads;
+  P.scale_log2 = std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift);
+  P.v_scale = std::ldexp(1.f, -a->v_shift);
+  P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
+  P.first_o = reinterpret_cast<float *>(ws), P.first_ml = reinterpret_cast<float2 *>(ws + s.first_ml);
+  P.rest_o = reinterpret_cast<float *>(ws + s.rest_o), P.rest_ml = reinterpret_cast<float2 *>(ws + s.rest_ml);
+  P.out = a->out, P.lse = a->lse, P.status = a->dev_status;
+  P.grid = std::min(sms, echo::kPxMaxGrid);
+  if (a->table) P.own_o = reinterpret_cast<float *>(ws + s.own_o), P.own_lse = reinterpret_cast<float *>(ws + s.own_lse);
+
+  int r;
+  if (a->format == ECHO_BLOCK_FP4) r = a->head_dim == 128 ? go_prefix<ECHO_BLOCK_FP4, 128>(P, stream) : go_prefix<ECHO_BLOCK_FP4, 64>(P, stream);
+  else r = a->head_dim == 128 ? go_prefix<ECHO_BLOCK_BF16, 128>(P, stream) : go_prefix<ECHO_BLOCK_BF16, 64>(P, stream);
+  if (r) return r;
+  if (a->table) {
+    echo_block_attention_args o{};
+    o.q = a->q, o.rows = a->rows, o.n_rows = a->n_rows, o.format = a->format, o.block_tokens = a->block_tokens, o.head_dim = a->head_dim;
+    o.table = a->table, o.table_heads = a->table_heads, o.max_blocks = a->max_blocks, o.ctx_len = a->ctx_len;
+    o.B = a->B, o.n_q = a->n_q, o.n_heads = a->n_heads, o.n_kv_heads = a->n_kv_heads, o.scale = a->scale;
+    o.lse = reinterpret_cast<float *>(ws + s.own_lse), o.workspace = ws + s.own_ws, o.dev_status = a->dev_status;
+    o.k_shift = a->k_shift, o.v_shift = a->v_shift;
+    if (int rr = launch_block_attention_f32(&o, reinterpret_cast<float *>(ws + s.own_o), stream)) return rr;
+  }
+  const dim3 grid(static_cast<unsigned>((rows + echo::kPxMergeWarps - 1) / echo::kPxMergeWarps)), block(echo::kPxMergeWarps * 32);
+  e = a->head_dim == 128 ? launch_pdl(echo::prefix_merge_kernel<128>, grid, block, 0, stream, P)
+                         : launch_pdl(echo::prefix_merge_kernel<64>, grid, block, 0, stream, P);
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "prefix attention merge launch");
+}
+
+}  // namespace echo_host
