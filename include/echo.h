@@ -833,8 +833,9 @@ int echo_block_evict(const echo_block_evict_args *args, void *stream);
  * Prefix tokens past its length may hold any bytes.  Scores, the softmax and all sums are fp32; the
  * prefix's softmax weights enter its value product in 16 bits (bf16, with ECHO_BLOCK_FP4 fp16; the
  * tensor cores' operand type), the own tokens' as in echo_block_attention.
- * Limits: those of echo_block_attention, n_groups in [1, 65536], n_groups * n_kv_heads *
- * max_prefix_blocks below 2^31.  Launches 2 kernels, with own tokens 3 or 4; the first call that takes
+ * Limits: those of echo_block_attention, n_groups in [1, 65536], n_rows at most 2^30, n_groups *
+ * n_kv_heads * max_prefix_blocks below 2^31, (B * n_q * n_heads / n_kv_heads / 256 + n_groups) *
+ * n_kv_heads * (max_prefix_blocks * block_tokens / 128 + 1) below 2^31 - 1024.  Launches 2 kernels, with own tokens 3 or 4; the first call that takes
  * some form of them sets it up, outside capture, as with echo_block_attention.
  */
 typedef struct echo_prefix_attention_args {

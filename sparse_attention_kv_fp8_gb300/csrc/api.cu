@@ -672,6 +672,11 @@ int echo_prefix_attention(const echo_prefix_attention_args *a, void *stream) {
   REQUIRE(static_cast<long long>(a->n_groups) * a->n_kv_heads <= ((1ll << 31) - 1) / a->max_prefix_blocks,
           "n_groups * n_kv_heads * max_prefix_blocks must be below 2^31");
   REQUIRE(a->n_rows <= (1 << 30), "n_rows must be at most 2^30");
+  // (the line of all tiles' chunks is counted in 31 bits)
+  const long long tiles = (static_cast<long long>(a->B) * a->n_q * (a->n_heads / a->n_kv_heads) / 256 + a->n_groups) * a->n_kv_heads;
+  REQUIRE(tiles < ((1ll << 31) - 1024) / (static_cast<long long>(a->max_prefix_blocks) * a->block_tokens / 128 + 1),
+          "prefixes too large: (B * n_q * n_heads / n_kv_heads / 256 + n_groups) * n_kv_heads * (max_prefix_blocks * block_tokens / 128 + 1) "
+          "must be below 2^31 - 1024");
   if (a->B == 0) return ECHO_OK;
   REQUIRE(a->q && a->rows && a->prefix_table && a->prefix_len && a->group_start && a->out && a->workspace,
           "prefix attention pointer is NULL");

@@ -78,6 +78,7 @@ struct BlockAttnParams {
   float scale_log2;                  // |scale| log2 e, over the keys' power of two
   float v_scale;                     // one over the values' power of two
   uint32_t q_sign;                   // 0x80008000 for a negative scale
+  int32_t beside;                    // runs beside the kernel before it, which it does not read, and ends after it
   uint16_t *out;
   float *out32;                      // instead of out: the result in fp32, for a merge with other tokens'
   float *lse;
@@ -287,7 +288,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   float2 *fin = reinterpret_cast<float2 *>(ba_smem + C::kOffFin);     // [kRows]
   const int heads = P.n_kv * P.mgroups;
   pdl_launch_dependents();  // (what follows waits for this grid's end all the same)
-  pdl_wait();
+  if (!P.beside) pdl_wait();
+  else __threadfence();     // (the kernel before began after its own wait: what came before that is there)
 
   // ===== this CTA's range of the line: chunks 0 .. n_chunks from its first =====
   LinePos cur;
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     const int64_t g0 = per * blockIdx.x;
     if (g0 >= total) {
       if (threadIdx.x == 0 && !P.by_pair) P.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (P.beside) pdl_wait();
       return;
     }
     n_chunks = static_cast<int>(min(total - g0, per));
@@ -934,6 +937,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     cluster_arrive();  // (no CTA's shared memory goes while another reads it)
     cluster_wait();
   }
+  if (P.beside) pdl_wait();
 }
 
 // Merge of the pieces of each (b, hm) that was cut: block (i, y) takes row y of the i-th one
@@ -1159,7 +1163,7 @@ static int launch_block_attention(const echo_block_attention_args *a, float *out
   P.scale_log2 = std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift);
   P.v_scale = std::ldexp(1.f, -a->v_shift);
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
-  P.out = a->out, P.out32 = out32, P.lse = a->lse;
+  P.out = a->out, P.out32 = out32, P.beside = out32 != nullptr, P.lse = a->lse;
   P.status = a->dev_status;
   const int pad = ba_row_pad(rows < echo::kBaMaxRows ? rows : echo::kBaMaxRows);
   P.tail = reinterpret_cast<int4 *>(a->workspace);
@@ -1203,7 +1207,9 @@ int launch_block_attention(const echo_block_attention_args *a, cudaStream_t stre
   return launch_block_attention(a, nullptr, stream);
 }
 
-// the same with the result in fp32 (16-byte aligned, [B][n_q][n_heads][head_dim]) instead of a->out
+// the same with the result in fp32 (16-byte aligned, [B][n_q][n_heads][head_dim]) instead of a->out, beside
+// the kernel before it on the stream: one that waits for what came before it, then lets its dependents start,
+// and that shares no output with this one
 int launch_block_attention_f32(const echo_block_attention_args *a, float *out, cudaStream_t stream) {
   return launch_block_attention(a, out, stream);
 }

@@ -31,6 +31,8 @@
 
 #include "block_mma.cuh"
 
+ECHO_TRACE_UNIT(prefix_attn)
+
 namespace echo {
 
 constexpr int kPxChunk = 128;         // prefix tokens of a step
@@ -85,55 +87,110 @@ __device__ __forceinline__ PxGroup px_group(const PrefixParams &P, int g, bool r
   x.chunks = (x.len + kPxChunk - 1) / kPxChunk;
   return x;
 }
-__device__ __forceinline__ int64_t px_units(const PrefixParams &P, const PxGroup &x) {
-  return static_cast<int64_t>(P.n_kv) * x.tiles * x.chunks;
+// (below 2^31 over all groups: the host checks the sizes)
+__device__ __forceinline__ int px_units(const PrefixParams &P, const PxGroup &x) { return P.n_kv * x.tiles * x.chunks; }
+
+// exclusive sum over the lanes of a warp, and the total
+__device__ __forceinline__ int px_scan(int mine, int &total) {
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(~0u, upto, d);
+    if ((threadIdx.x & 31) >= d) upto += y;
+  }
+  total = __shfl_sync(~0u, upto, 31);
+  return upto - mine;
 }
 
-// One CTA's place on the line: the piece of tile (g, h, t) from chunk c on, n chunks long.
+// How the tiles are cut.  Whole: every tile of group g into ceil(chunks / whole) equal pieces, one
+// per CTA, the row tiles of a KV head beside one another, so that they read the same blocks at the
+// same time.  Otherwise (whole == 0): the line of all chunks into shares of `per`, one per CTA, which may
+// begin and end inside a tile.  A CTA that changes tiles takes as long as kPxChange chunks more, so
+// whole pieces are taken where they are no longer than a share by more.
+constexpr int kPxChange = 5;
+constexpr int kPxFewGroups = 8;       // (more groups: their tiles are not tried)
+
+struct PxPlan {
+  int whole, per, total;
+};
+
+__device__ __forceinline__ PxPlan px_plan(const PrefixParams &P, int total) {  // (by a whole warp)
+  PxPlan x{0, 0, total};
+  x.per = static_cast<int>((static_cast<uint32_t>(total) + P.grid - 1) / static_cast<uint32_t>(P.grid));
+  if (total == 0 || P.n_groups > kPxFewGroups) return x;
+  const int lane = threadIdx.x & 31, len = x.per + lane;
+  int64_t pieces = 0;
+  for (int g = 0; g < P.n_groups; ++g) {
+    const PxGroup y = px_group(P, g, false);
+    pieces += static_cast<int64_t>(P.n_kv) * y.tiles * ((static_cast<uint32_t>(y.chunks) + len - 1) / static_cast<uint32_t>(len));
+  }
+  const uint32_t fits = __ballot_sync(~0u, lane <= kPxChange && pieces <= P.grid);
+  if (fits) x.whole = x.per + __ffs(fits) - 1;
+  return x;
+}
+// pieces of a tile, and their length
+__device__ __forceinline__ int px_pieces(const PxPlan &x, const PxGroup &y, int &len) {
+  const int n = (y.chunks + x.whole - 1) / x.whole;
+  len = n ? (y.chunks + n - 1) / n : 0;
+  return n;
+}
+
+// One CTA's place: the piece of tile (g, h, t) from chunk c on, n chunks long.
 struct PxLine {
   int g, h, t, c, n;
   PxGroup x;
-  int64_t left;       // chunks of this CTA's share from c on
+  int left;       // chunks of this CTA's share from c on
 
-  __device__ __forceinline__ void piece() { n = static_cast<int>(min(static_cast<int64_t>(x.chunks - c), left)); }
+  __device__ __forceinline__ void piece() { n = min(x.chunks - c, left); }
 
   // the first piece (by a whole warp)
   __device__ __forceinline__ bool begin(const PrefixParams &P, bool report) {
     const int lane = threadIdx.x & 31;
     const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
-    int64_t mine = 0;
+    int mine = 0, total;
     for (int i = g0; i < g1; ++i) mine += px_units(P, px_group(P, i, report));
-    int64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, upto, d);
-      if (lane >= d) upto += y;
-    }
-    const int64_t total = __shfl_sync(~0u, upto, 31);
-    const int64_t per = (total + P.grid - 1) / P.grid, u0 = per * blockIdx.x;
-    if (u0 >= total) return false;
-    left = min(per, total - u0);
-    int at = 0, off_tile = 0, off_chunk = 0;
-    const bool own = u0 >= upto - mine && u0 < upto;
-    if (own) {
-      int64_t u = upto - mine;
-      for (at = g0;; ++at) {
-        const PxGroup y = px_group(P, at, false);
-        const int64_t k = px_units(P, y);
-        if (u0 < u + k) {
-          off_tile = static_cast<int>((u0 - u) / y.chunks);
-          off_chunk = static_cast<int>((u0 - u) % y.chunks);
-          break;
+    const int before = px_scan(mine, total);
+    const PxPlan plan = px_plan(P, total);
+    if (plan.whole) {
+      int at = blockIdx.x;
+      for (g = 0; g < P.n_groups; ++g) {
+        x = px_group(P, g, false);
+        int len;
+        const int pieces = px_pieces(plan, x, len), all = P.n_kv * x.tiles * pieces;
+        if (at >= all) {
+          at -= all;
+          continue;
         }
+        const int row = at / x.tiles;      // (KV head, piece)
+        t = at - row * x.tiles;
+        h = row / pieces;
+        c = (row - h * pieces) * len;
+        left = n = min(len, x.chunks - c);
+        return true;
+      }
+      return false;
+    }
+    if (static_cast<int64_t>(plan.per) * blockIdx.x >= total) return false;
+    const int u0 = plan.per * blockIdx.x;
+    left = min(plan.per, total - u0);
+    int at = 0, off = 0;
+    const bool own = u0 >= before && u0 < before + mine;
+    if (own) {
+      int u = before;
+      for (at = g0;; ++at) {
+        const int k = px_units(P, px_group(P, at, false));
+        if (u0 < u + k) break;
         u += k;
       }
+      off = u0 - u;
     }
     const int src = __ffs(__ballot_sync(~0u, own)) - 1;
     g = __shfl_sync(~0u, at, src);
-    const int tile = __shfl_sync(~0u, off_tile, src);
-    c = __shfl_sync(~0u, off_chunk, src);
+    off = __shfl_sync(~0u, off, src);
     x = px_group(P, g, false);
-    h = tile / x.tiles, t = tile - h * x.tiles;
+    const uint32_t tile = static_cast<uint32_t>(off) / static_cast<uint32_t>(x.chunks);
+    c = off - tile * x.chunks;
+    h = tile / static_cast<uint32_t>(x.tiles), t = tile - h * x.tiles;
     piece();
     return true;
   }
@@ -161,7 +218,7 @@ struct PxLine {
 
 // the cache row of a prefix token (a token below the prefix's length), -1: not held
 __device__ __forceinline__ int64_t px_row(const PrefixParams &P, int g, int h, int token, int &off, bool report) {
-  const int e = token / P.bs;
+  const uint32_t e = static_cast<uint32_t>(token) / static_cast<uint32_t>(P.bs);
   off = token - e * P.bs;
   const int32_t id = P.table[(static_cast<int64_t>(g) * P.heads + (P.heads > 1 ? h : 0)) * P.max_blocks + e];
   if (id < 0) return -1;
@@ -173,7 +230,7 @@ __device__ __forceinline__ int64_t px_row(const PrefixParams &P, int g, int h, i
 
 // (b, query token, head) of row r of a tile's group
 __device__ __forceinline__ int64_t px_out_row(const PrefixParams &P, const PxLine &L, int r) {
-  const int per = P.n_q * P.group, b = r / per, rq = r - b * per, j = rq / P.group;
+  const uint32_t per = P.n_q * P.group, b = static_cast<uint32_t>(r) / per, rq = r - b * per, j = rq / static_cast<uint32_t>(P.group);
   return (static_cast<int64_t>(L.x.b0 + b) * P.n_q + j) * P.n_heads + L.h * P.group + rq - j * P.group;
 }
 
@@ -207,6 +264,14 @@ __device__ __forceinline__ void px_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+template <int N>
+__device__ __forceinline__ void px_more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void px_fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void px_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void px_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void px_tma(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
@@ -224,6 +289,11 @@ __device__ __forceinline__ void px_store8(float *p, const float *v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
                "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+__device__ __forceinline__ float px_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // a wait without the abort flag, for what is in flight when a kernel gives up
 __device__ __forceinline__ void px_drain(uint64_t *bar, uint32_t parity) {
@@ -243,27 +313,30 @@ struct PxCfg {
   static constexpr int kSlots = kFp4 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 9;  // ring of key and value tiles
   static constexpr int kRaw = kFp4 ? 3 : 0;                 // stages of 4-bit chunks
   static constexpr uint32_t kRawBytes = 8 * 18 * D;
-  static constexpr int kConvWarps = kFp4 ? 8 : 0;
-  static constexpr int kThreads = 32 * (8 + 2 + kConvWarps);
+  static constexpr int kConvWarps = kFp4 ? 4 : 0;
+  // Warpgroups: two of softmax, one of the producer and the issuer (and two idle warps), one that
+  // converts.  A launch gives every thread the same registers (168 of 384 threads, 128 of 512);
+  // they are handed over to the softmax, which keeps a row of 128 scores.
+  static constexpr int kThreads = 32 * (12 + kConvWarps);
+  static constexpr int kRegs = kFp4 ? 128 : 168, kRegsSoft = kFp4 ? 176 : 208, kRegsLoad = kFp4 ? 80 : 88, kRegsConv = kFp4 ? 80 : 0;
+  static_assert(2 * kRegsSoft + kRegsLoad + kRegsConv <= kRegs * kThreads / 128, "registers of the launch");
   static constexpr uint32_t kOffQ = 0, kOffRing = 2 * kTile, kOffRaw = kOffRing + kSlots * kTile;
   static constexpr uint32_t kOffCtl = kOffRaw + kRaw * kRawBytes;
 };
 
+// Chunks whose `held` is kept: the producer is at most kSlots chunks ahead of the issuer, the
+// softmax at most two behind it.
+constexpr int kPxHeld = 16;
+
 struct PxCtl {
   uint64_t kv_full[9], kv_empty[9], raw_full[3], raw_empty[3];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain;
-  uint32_t held[9];       // sub-blocks of 16 tokens that a value tile holds, a bit each
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], o_free[2], drain, fix;  // (p: half the tokens each)
+  uint32_t held[kPxHeld]; // which sub-blocks of 16 tokens of a chunk are held, a bit each
   uint32_t tmem;
   int abort;
+  PxLine line[8];         // a softmax warp's place, which it does not need in registers meanwhile
 };
 
-// which of a chunk's sub-blocks of 16 tokens are held (by a warp; bits 0-7)
-__device__ __forceinline__ uint32_t px_held(const PrefixParams &P, int g, int h, int len, int chunk) {
-  const int lane = threadIdx.x & 31, token = chunk * kPxChunk + lane * kSubTokens;
-  int off;
-  const bool on = lane < kPxChunk / kSubTokens && token < len && px_row(P, g, h, token, off, false) >= 0;
-  return __ballot_sync(~0u, on);
-}
 // tokens 32 w .. 32 w + 31 of a chunk: held and below the length
 __device__ __forceinline__ uint32_t px_seen(uint32_t held, int w, int tokens) {
   const uint32_t two = held >> (2 * w);
@@ -286,6 +359,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
   volatile int *abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  ECHO_TRACE_MARK(0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&ctl->kv_full[i], F16 ? C::kConvWarps : 1);
@@ -297,12 +371,14 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->q_full[s], 4);
-      mbar_init(&ctl->s_full[s], 1);
-      mbar_init(&ctl->p_full[s], 4);
+      mbar_init(&ctl->s_full[s], 2);   // the products, and the issuer (for `held`)
+      mbar_init(&ctl->p_full[s][0], 4);
+      mbar_init(&ctl->p_full[s][1], 4);
       mbar_init(&ctl->o_full[s], 1);
       mbar_init(&ctl->o_free[s], 4);
     }
     mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->fix, 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -314,33 +390,41 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;   // S of the sub-tiles at columns 0 and 128, O at 256 and 256 + D
+  ECHO_TRACE_MARK(1);
   pdl_wait();
   pdl_launch_dependents();
+  ECHO_TRACE_MARK(2);
 
   PxLine L;
   const bool any = L.begin(P, blockIdx.x == 0 && warp == 0);
-  if (any && warp < 8) {
+  ECHO_TRACE_MARK(3);
+  if (warp < 8) {
+    px_more_regs<C::kRegsSoft>();
+    if (any) {
     // ===================== softmax: a warpgroup per sub-tile, a thread per row =====================
     const int s = warp >> 2, w4 = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t s_at = tmem + s * 128 + lanes, o_at = tmem + 256 + s * D + lanes;
     uint32_t ph_s = 0, ph_o = 0;
+    int done = 0;       // chunks of the pieces before
     bool ok = true, active = L.sub_rows(s) > 0;
 
     // the queries of this warp's rows: D / 8 lanes a row, 16 bytes each
     auto load_q = [&]() {
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes;
-      const int n = L.sub_rows(s), d8 = lane % kLanes;
-      for (int r0 = 0; r0 < 32; r0 += 4 * kPer) {
-        uint4 x[4];
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 8;
+      const int n = L.sub_rows(s), d8 = lane % kLanes, mine = w4 * 32 + lane;
+      const int64_t at = mine < n ? px_out_row(P, L, L.t * kPxRows + s * 128 + mine) : -1;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += kAhead * kPer) {
+        uint4 x[kAhead];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = w4 * 32 + r0 + u * kPer + lane / kLanes;
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t from = __shfl_sync(~0u, at, r0 + u * kPer + lane / kLanes);
           x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < n) x[u] = *reinterpret_cast<const uint4 *>(P.q + px_out_row(P, L, L.t * kPxRows + s * 128 + r) * D + d8 * 8);
+          if (from >= 0) x[u] = *reinterpret_cast<const uint4 *>(P.q + from * D + d8 * 8);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
           const int r = w4 * 32 + r0 + u * kPer + lane / kLanes;
           uint32_t v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
           if constexpr (F16) {  // scaled by the power of two that brings the row's largest entry to [1, 2)
@@ -368,53 +452,75 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
     };
 
     if (active) load_q();
+    ECHO_TRACE_MARK(4);
     for (bool more = true; more && ok;) {
-      const PxLine cur = L;
-      const bool rows = active && w4 * 32 < cur.sub_rows(s);   // of this warp
+      const int n = L.n, len0 = L.x.len - L.c * kPxChunk;  // (tokens from the piece's first on)
+      const bool rows = active && w4 * 32 < L.sub_rows(s);  // of this warp
+      if (lane == 0) ctl->line[warp] = L;
+      __syncwarp();
       const float c = P.scale_log2 * (F16 && active ? qscale[s * 128 + w4 * 32 + lane] : 1.f);
       float m = kPxNone, l = 0.f;
-      uint32_t held = active ? px_held(P, cur.g, cur.h, cur.x.len, cur.c) : 0u;
-      for (int i = 0; active && i < cur.n; ++i) {
-        const uint32_t held_now = held;
-        if (i + 1 < cur.n) held = px_held(P, cur.g, cur.h, cur.x.len, cur.c + i + 1);
+      for (int i = 0; active && i < n; ++i) {
         if (!mbar_wait(&ctl->s_full[s], ph_s, abort, P.status)) {
           ok = false;
           break;
         }
         ph_s ^= 1;
         tc_fence_after();
+        if (i < 6) ECHO_TRACE_MARK(5 + 2 * i);
         if (rows) {
-          const int tokens = cur.x.len - (cur.c + i) * kPxChunk;
-          const bool edge = held_now != 0xffu || tokens < kPxChunk;
-          float top = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < 4; b += 2) {
-            float v[2][32];
-            tmem_ld_32x32b_x32(s_at + b * 32, v[0]);
-            tmem_ld_32x32b_x32(s_at + b * 32 + 32, v[1]);
-            tmem_wait_ld();
-            reg_fence_32(v[0]);
-            reg_fence_32(v[1]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (edge) {
-                const uint32_t seen = px_seen(held_now, b + u, tokens);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) top = fmaxf(top, seen >> k & 1 ? v[u][k] : -INFINITY);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) top = fmaxf(top, v[u][k]);
-              }
-            }
+          const uint32_t held = ctl->held[(done + i) % kPxHeld];
+          const int tokens = len0 - i * kPxChunk;
+          if (held != 0xffu || tokens < kPxChunk) {  // scores of tokens that are not there (rare: a loop)
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w)
+              for (uint32_t no = ~px_seen(held, w, tokens); no; no &= no - 1)
+                asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(s_at + w * 32 + __ffs(no) - 1), "r"(0xff800000u)
+                             : "memory");
+            px_wait_st();
           }
-          const float x = top == -INFINITY ? kPxNone : fmaf(top, c, -kLift);
-          if (i == 0) {
-            m = x;
-          } else if (__any_sync(~0u, x - m > kPxLazy)) {
+          float v[4][32];      // S of the row
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(s_at + b * 32, v[b]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) reg_fence_32(v[b]);
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) tops[x] = px_max3(tops[x], v[b][k + 2 * x], v[b][k + 2 * x + 1]);
+          const float2 c2 = make_float2(c, c);
+          float2 sums[2];
+          uint32_t p[16];
+          // weights of 32 tokens.  (One 16-bit term: 2^-9 (2^-12 in 4 bits) of a weight at most, of random
+          // sign; a second term would cost half as many products again)
+          auto weights = [&](int b) {
+            const float2 m2 = make_float2(-m, -m);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 y = __ffma2_rn(make_float2(v[b][2 * k], v[b][2 * k + 1]), c2, m2);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              sums[k & 1] = __fadd2_rn(sums[k & 1], e);
+              p[k] = pack2<F16>(e.x, e.y);
+            }
+          };
+          // The first quarter of the weights is worked out with the maximum as it was, beside the search for
+          // the new one, which seldom is far above it; if it is (and with a piece's first chunk) again.
+          for (bool again = false;; again = true) {
+            sums[0] = sums[1] = make_float2(0.f, 0.f);
+            weights(0);
+            if (again) break;
+            const float top = fmaxf(px_max3(tops[0], tops[1], tops[2]), tops[3]);
+            const float x = top == -INFINITY ? kPxNone : fmaf(top, c, -kLift);
+            if (!__any_sync(~0u, i == 0 || x - m > kPxLazy)) break;
             const float up = fmaxf(m, x), f = ex2(m - up);
             m = up;
             l *= f;
-#pragma unroll
+            if (i == 0) continue;
+#pragma unroll 1
             for (int b = 0; b < D / 16; ++b) {
               uint32_t o[16];
               asm volatile(
@@ -433,55 +539,52 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
               px_st16(o_at + b * 16, o);
             }
           }
-          const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float v[32];
-            tmem_ld_32x32b_x32(s_at + b * 32, v);
-            tmem_wait_ld();
-            reg_fence_32(v);
-            const uint32_t seen = edge ? px_seen(held_now, b, tokens) : ~0u;
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 y = __ffma2_rn(make_float2(v[2 * k], v[2 * k + 1]), c2, m2);
-              float2 e = make_float2(ex2(y.x), ex2(y.y));
-              if (edge) e.x = seen >> (2 * k) & 1 ? e.x : 0.f, e.y = seen >> (2 * k + 1) & 1 ? e.y : 0.f;
-              sum = __fadd2_rn(sum, e);
-              // (one 16-bit term: 2^-9 (2^-12 in 4 bits) of a weight at most, of random sign; a second
-              // term would cost half as many products again)
-              p[k] = pack2<F16>(e.x, e.y);
-            }
-            px_st16(s_at + b * 16, p);
-          }
-          l += sum.x + sum.y;
+          px_st16(s_at, p);
+          weights(1);
+          px_st16(s_at + 16, p);
           px_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->p_full[s][0]);
+          weights(2);
+          px_st16(s_at + 32, p);
+          weights(3);
+          px_st16(s_at + 48, p);
+          l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+          px_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&ctl->p_full[s][0]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[s]);
+        if (lane == 0) mbar_arrive(&ctl->p_full[s][1]);
+        if (i < 6) ECHO_TRACE_MARK(6 + 2 * i);
       }
       if (!ok) break;
+      done += n;
+      L = ctl->line[warp];
+      // where this row's part goes
+      const bool valid = w4 * 32 + lane < L.sub_rows(s), head = L.c == 0;
+      const int64_t to = head ? (valid ? px_out_row(P, L, L.t * kPxRows + s * 128 + w4 * 32 + lane) : 0)
+                              : static_cast<int64_t>(blockIdx.x) * kPxRows + s * 128 + w4 * 32 + lane;
+      __syncwarp();
       // every product with the queries is done: the next piece's go in
       more = L.next(P);
       const bool was = active;
       active = more && L.sub_rows(s) > 0;
       if (active) load_q();
       if (!was) continue;
+      ECHO_TRACE_MARK(20);
       if (!mbar_wait(&ctl->o_full[s], ph_o, abort, P.status)) {
         ok = false;
         break;
       }
       ph_o ^= 1;
       tc_fence_after();
+      ECHO_TRACE_MARK(21);
       if (rows) {
-        const int r = s * 128 + w4 * 32 + lane;
-        const bool valid = w4 * 32 + lane < cur.sub_rows(s);
-        const int64_t at = cur.c == 0 ? (valid ? px_out_row(P, cur, cur.t * kPxRows + r) : 0)
-                                      : static_cast<int64_t>(blockIdx.x) * kPxRows + r;
-        float *dst = (cur.c == 0 ? P.first_o : P.rest_o) + at * D;
-#pragma unroll
+        float *dst = (head ? P.first_o : P.rest_o) + to * D;
+#pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
           float v[32];
           tmem_ld_32x32b_x32(o_at + b * 32, v);
@@ -492,241 +595,269 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
             for (int k = 0; k < 32; k += 8) px_store8(dst + b * 32 + k, v + k);
           }
         }
-        if (valid) (cur.c == 0 ? P.first_ml : P.rest_ml)[at] = make_float2(m == kPxNone && l == 0.f ? -INFINITY : m, l);
+        if (valid) (head ? P.first_ml : P.rest_ml)[to] = make_float2(m == kPxNone && l == 0.f ? -INFINITY : m, l);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->o_free[s]);
+      ECHO_TRACE_MARK(22);
     }
-  } else if (any && warp == 8) {
+    }
+  } else if (warp < 12) {
+    px_fewer_regs<C::kRegsLoad>();
+    if (any && warp == 8) {
     // ===================== producer =====================
-    int k = 0;        // tiles (bf16) or chunks (4 bits) asked for
+    const int boxes = F16 ? kPxChunk / kSubTokens : kPxChunk / P.box, box = F16 ? kSubTokens : P.box;
+    int k = 0, asked = 0;  // chunks, and (bf16) tiles, asked for
     bool ok = true;
-    for (bool more = true; more && ok; more = ok && L.next(P)) {
-      for (int i = 0; i < L.n && ok; ++i) {
-        const int base = (L.c + i) * kPxChunk;
+    // the row and offset of this lane's box of a chunk, looked up a chunk ahead
+    int off = 0;
+    int64_t row = -1;
+    uint32_t ph_fix = 0;
+    auto look_up = [&](int chunk) {
+      const int token = chunk * kPxChunk + lane * box;
+      row = lane < boxes && token < L.x.len ? px_row(P, L.g, L.h, token, off, true) : -1;
+    };
+    look_up(L.c);
+    for (bool more = true; more && ok;) {
+      const int n = L.n, c0 = L.c, len = L.x.len;
+      for (int i = 0; i < n && ok; ++i) {
+        const int64_t row_now = row;
+        const int off_now = off;
+        if (i + 1 < n) {
+          look_up(c0 + i + 1);
+        } else {
+          more = L.next(P);
+          if (more) look_up(L.c);
+        }
+        const uint32_t held = __ballot_sync(~0u, row_now >= 0);
         if constexpr (F16) {
-          const int st = k % C::kRaw, token = base + lane * kSubTokens;
-          int off = 0;
-          const int64_t row = lane < 8 && token < L.x.len ? px_row(P, L.g, L.h, token, off, true) : -1;
-          const uint32_t held = __ballot_sync(~0u, row >= 0);
+          const int st = k % C::kRaw;
           if (k >= C::kRaw && !mbar_wait(&ctl->raw_empty[st], (k / C::kRaw - 1) & 1, abort, P.status)) {
             ok = false;
             break;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->raw_full[st], __popc(held) * 18 * D);
+          if (lane == 0) {
+            ctl->held[k % kPxHeld] = held;
+            mbar_arrive_expect_tx(&ctl->raw_full[st], __popc(held) * 18 * D);
+          }
           __syncwarp();
-          if (row >= 0)
+          if (row_now >= 0)
             px_bulk(smem_u32(smem + C::kOffRaw) + st * C::kRawBytes + lane * 18 * D,
-                    P.rows + row * P.row_bytes + (off / kSubTokens) * Fp4Sub<D>::kBytes, 18 * D, &ctl->raw_full[st]);
-          ++k;
+                    P.rows + row_now * P.row_bytes + (off_now / kSubTokens) * Fp4Sub<D>::kBytes, 18 * D, &ctl->raw_full[st]);
         } else {
-          const int boxes = kPxChunk / P.box, token = base + lane * P.box;
-          int off = 0;
-          const int64_t row = lane < boxes && token < L.x.len ? px_row(P, L.g, L.h, token, off, true) : -1;
-          const uint32_t held = __ballot_sync(~0u, row >= 0);
-          uint32_t subs = 0;   // the same by 16 tokens
-          for (int x = 0; x < 8; ++x) subs |= (held >> (x * kSubTokens / P.box) & 1) << x;
+          uint32_t subs = held;   // the same by 16 tokens
+          if (box != kSubTokens) {
+            subs = 0;
 #pragma unroll
-          for (int v = 0; v < 2; ++v, ++k) {
-            const int st = k % C::kSlots;
-            if (k >= C::kSlots && !mbar_wait(&ctl->kv_empty[st], (k / C::kSlots - 1) & 1, abort, P.status)) {
+            for (int x = 0; x < 8; ++x) subs |= (held >> (x * kSubTokens / box) & 1) << x;
+          }
+          if (lane == 0) ctl->held[k % kPxHeld] = subs;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const int tile = 2 * k + v, st = tile % C::kSlots;
+            if (tile >= C::kSlots && !mbar_wait(&ctl->kv_empty[st], (tile / C::kSlots - 1) & 1, abort, P.status)) {
               ok = false;
               break;
             }
             __syncwarp();
-            if (lane == 0) {
-              ctl->held[st] = subs;
-              mbar_arrive_expect_tx(&ctl->kv_full[st], __popc(held) * P.box * 2 * D);
-            }
+            // values that no query sees have to be zeros (a weight of zero times NaN is NaN): the tile
+            // is waited for here, mended, and handed on
+            const int tokens = len - (c0 + i) * kPxChunk;
+            const bool mend = v == 1 && (subs != 0xffu || tokens < kPxChunk);
+            uint64_t *bar = mend ? &ctl->fix : &ctl->kv_full[st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(held) * box * 2 * D);
             __syncwarp();
-            if (row >= 0) {
+            if (row_now >= 0) {
 #pragma unroll
               for (int hb = 0; hb < D / 64; ++hb)
-                px_tma(ring + st * C::kTile + hb * C::kBlock + lane * P.box * 128, &map, &ctl->kv_full[st], hb * 64, off,
-                       static_cast<int>(2 * row + v));
+                px_tma(ring + st * C::kTile + hb * C::kBlock + lane * box * 128, &map, bar, hb * 64, off_now,
+                       static_cast<int>(2 * row_now + v));
             }
+            if (mend) {
+              if (!mbar_wait(&ctl->fix, ph_fix, abort, P.status)) {
+                px_drain(&ctl->fix, ph_fix);
+                ok = false;
+                break;
+              }
+              ph_fix ^= 1;
+              uint8_t *tile_at = smem + C::kOffRing + st * C::kTile;
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if (!(px_seen(subs, w, tokens) >> lane & 1))
+                  for (int x = 0; x < D / 8; ++x)
+                    *reinterpret_cast<uint4 *>(tile_at + (x >> 3) * C::kBlock + (w * 32 + lane) * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              px_fence_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
+            }
+            asked = tile + 1;
           }
         }
+        if (ok) ++k;
       }
     }
     if (*abort) {  // let every copy this warp started land before the CTA exits
       constexpr int kDepth = F16 ? (C::kRaw ? C::kRaw : 1) : C::kSlots;
-      for (int j = max(k - kDepth, 0); j < k; ++j) px_drain(F16 ? &ctl->raw_full[j % kDepth] : &ctl->kv_full[j % kDepth], (j / kDepth) & 1);
+      const int n = F16 ? k : asked;
+      for (int j = max(n - kDepth, 0); j < n; ++j) px_drain(F16 ? &ctl->raw_full[j % kDepth] : &ctl->kv_full[j % kDepth], (j / kDepth) & 1);
     }
-  } else if (any && warp == 9) {
-    // ===================== tensor-core issuer =====================
-    uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_free[2] = {1, 1};  // (O is free at first)
-    int k = 0;        // tiles taken from the ring
-    bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = ok && mbar_wait(bar, parity, abort, P.status);
-      ok = __all_sync(~0u, ok);
-      return ok;
-    };
-    auto full = [&](int tile) { return wait(&ctl->kv_full[tile % C::kSlots], (tile / C::kSlots) & 1); };
-    auto slot = [&](int tile) { return ring + (tile % C::kSlots) * C::kTile; };
-    auto scores = [&](int s, int tile) {     // S of sub-tile s
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t a = q_at + s * C::kTile, b = slot(tile);
+    } else if (any && warp == 9) {
+    // ===================== tensor-core issuer: one thread =====================
+    if (elect_one()) {
+      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_free[2] = {1, 1};  // (O is free at first)
+      int k = 0;        // tiles taken from the ring
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort, P.status); };
+      auto full = [&](int tile) { return wait(&ctl->kv_full[tile % C::kSlots], (tile / C::kSlots) & 1); };
+      auto scores = [&](int s, int tile) {     // S of sub-tile s
+        tc_fence_after();
+        const uint64_t a = kmajor_sw128_desc(q_at + s * C::kTile), b = kmajor_sw128_desc(ring + (tile % C::kSlots) * C::kTile);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * C::kBlock + (kk & 3) * 32;
-          px_mma_ss(tmem + s * 128, kmajor_sw128_desc(a + o), kmajor_sw128_desc(b + o), kIdescS, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) {  // (addresses in units of 16 bytes)
+          const uint32_t o = ((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4;
+          px_mma_ss(tmem + s * 128, a + o, b + o, kIdescS, kk > 0);
         }
         mma_commit(&ctl->s_full[s]);
-      }
-    };
-    auto values = [&](int s, int tile, bool more) {  // O of sub-tile s
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t b = slot(tile);
+        mbar_arrive(&ctl->s_full[s]);
+      };
+      auto values = [&](int s, int tile, int half, bool more) {  // O of sub-tile s, half the tokens
+        tc_fence_after();
+        const uint64_t b = px_mn_desc(ring + (tile % C::kSlots) * C::kTile, C::kBlock) + half * (64 * 128 >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kPxChunk / 16; ++kk)
-          px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8, px_mn_desc(b + kk * 16 * 128, C::kBlock), kIdescO, more || kk > 0);
-      }
-    };
-    auto release = [&](int tile) {
-      if (lane == 0) mma_commit(&ctl->kv_empty[tile % C::kSlots]);
-    };
-    for (bool more = true; more && ok; more = ok && L.next(P)) {
-      const bool two = L.sub_rows(1) > 0;
-      if (!full(k)) break;
-      for (int s = 0; s < (two ? 2 : 1); ++s) {
-        if (!wait(&ctl->q_full[s], ph_q[s])) break;
-        ph_q[s] ^= 1;
-        scores(s, k);
-      }
-      if (!ok) break;
-      release(k);
-      for (int i = 0; i < L.n && ok; ++i, k += 2) {
-        const bool last = i + 1 == L.n;
-        if (!full(k + 1)) break;
-        if constexpr (!F16) {
-          // values that no query sees are zeros (a weight of zero times NaN is NaN)
-          const uint32_t held = ctl->held[(k + 1) % C::kSlots];
-          const int tokens = L.x.len - (L.c + i) * kPxChunk;
-          if (held != 0xffu || tokens < kPxChunk) {
-            uint8_t *v = smem + C::kOffRing + ((k + 1) % C::kSlots) * C::kTile;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              if (!(px_seen(held, w, tokens) >> lane & 1))
-                for (int x = 0; x < static_cast<int>(C::kTile / C::kBlock) * 8; ++x)
-                  *reinterpret_cast<uint4 *>(v + (x >> 3) * C::kBlock + (w * 32 + lane) * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int kk = 0; kk < kPxChunk / 32; ++kk)
+          px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + half * 32 + kk * 8, b + (kk * 16 * 128 >> 4), kIdescO, more || kk > 0);
+      };
+      auto release = [&](int tile) { mma_commit(&ctl->kv_empty[tile % C::kSlots]); };
+      for (bool more = true; more && ok; more = ok && L.next(P)) {
+        const int subs = L.sub_rows(1) > 0 ? 2 : 1;
+        if (!full(k)) break;
+        for (int s = 0; s < subs; ++s) {
+          if (!wait(&ctl->q_full[s], ph_q[s])) break;
+          ph_q[s] ^= 1;
+          scores(s, k);
+        }
+        if (!ok) break;
+        release(k);
+        for (int i = 0; i < L.n && ok; ++i, k += 2) {
+          const bool last = i + 1 == L.n;
+          if (!full(k + 1) || (!last && !full(k + 2))) break;
+          for (int s = 0; s < subs; ++s) {
+            if (!wait(&ctl->p_full[s][0], ph_p[s])) break;
+            if (i == 0) {
+              if (!wait(&ctl->o_free[s], ph_free[s])) break;
+              ph_free[s] ^= 1;
             }
-            px_fence_smem();
-            __syncwarp();
-          }
-        }
-        if (!last && !full(k + 2)) break;
-        for (int s = 0; s < (two ? 2 : 1); ++s) {
-          if (!wait(&ctl->p_full[s], ph_p[s])) break;
-          ph_p[s] ^= 1;
-          if (i == 0) {
-            if (!wait(&ctl->o_free[s], ph_free[s])) break;
-            ph_free[s] ^= 1;
-          }
-          values(s, k + 1, i > 0);
-          if (s == (two ? 1 : 0)) release(k + 1);
-          if (last) {
-            if (lane == 0) mma_commit(&ctl->o_full[s]);
-          } else {
-            scores(s, k + 2);
-            if (s == (two ? 1 : 0)) release(k + 2);
+            values(s, k + 1, 0, i > 0);
+            if (!wait(&ctl->p_full[s][1], ph_p[s])) break;
+            ph_p[s] ^= 1;
+            values(s, k + 1, 1, true);
+            if (s == subs - 1) release(k + 1);
+            if (last) {
+              mma_commit(&ctl->o_full[s]);
+            } else {
+              scores(s, k + 2);
+              if (s == subs - 1) release(k + 2);
+            }
           }
         }
       }
-    }
-    if (!ok) {  // no product may run on when the tensor memory goes
-      if (lane == 0) {
+      if (!ok) {  // no product may run on when the tensor memory goes
         mma_commit(&ctl->drain);
         px_drain(&ctl->drain, 0);
       }
     }
-    __syncwarp();
-  } else if (F16 && any) {
-    // ===================== 4-bit rows to fp16 tiles: a warp per sub-block, a lane per (token, half of the dims) ====
+    }
+  } else if constexpr (F16) {
+    px_fewer_regs<C::kRegsConv>();
+    if (any) {
+    // ===================== 4-bit rows to fp16 tiles: two sub-blocks a warp, a lane per (token, half of the dims) ====
     constexpr int kWords = D / 16;      // 8-code words of a lane
-    const int sub = warp - 10, tk = lane & 15, hf = lane >> 4;
+    const int tk = lane & 15, hf = lane >> 4;
     int k = 0;
     bool ok = true;
-    auto store = [&](uint8_t *tile, const uint32_t (&h)[kWords][4], bool on) {
+    // one sub-block's keys or values as rows of a tile
+    auto convert = [&](uint8_t *tile, int sub, const uint32_t (&w)[kWords], const uint32_t (&sc)[kWords / 2], bool on) {
       const int r = sub * kSubTokens + tk;
       uint8_t *dst = tile + (D == 128 ? hf * C::kBlock : 0u) + r * 128;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const int piece = D == 128 ? i : hf * kWords + i;
-        *reinterpret_cast<uint4 *>(dst + ((piece ^ (r & 7)) << 4)) = on ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    auto convert = [&](const uint32_t (&w)[kWords], const uint32_t (&sc)[kWords / 2], uint32_t (&h)[kWords][4]) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
         const uint32_t s2 = __byte_perm(e4m3x2_to_half2(sc[i / 2]), 0, 0x1010);
-        e2m1x8_to_half2(w[i], h[i]);
+        uint32_t h[4];
+        e2m1x8_to_half2(w[i], h);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) h[i][v] = hmul2(h[i][v], s2);
+        for (int v = 0; v < 4; ++v) h[v] = on ? hmul2(h[v], s2) : 0u;
+        const int piece = D == 128 ? i : hf * kWords + i;
+        *reinterpret_cast<uint4 *>(dst + ((piece ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
     };
     for (bool more = true; more && ok; more = ok && L.next(P)) {
-      uint32_t held = px_held(P, L.g, L.h, L.x.len, L.c);
       for (int i = 0; i < L.n && ok; ++i, ++k) {
-        const uint32_t held_now = held;
-        if (i + 1 < L.n) held = px_held(P, L.g, L.h, L.x.len, L.c + i + 1);
-        const int st = k % C::kRaw, token = (L.c + i) * kPxChunk + sub * kSubTokens + tk;
-        const bool on = (held_now >> sub & 1) && token < L.x.len;
+        const int st = k % C::kRaw, tokens = L.x.len - (L.c + i) * kPxChunk;
         if (!mbar_wait(&ctl->raw_full[st], (k / C::kRaw) & 1, abort, P.status)) {
           ok = false;
           break;
         }
-        const uint8_t *src = smem + C::kOffRaw + st * C::kRawBytes + sub * 18 * D;
-        uint32_t w[kWords], sc[kWords / 2], h[kWords][4];
-        // keys: codes [16][D / 2], scales [16][D / 16]
+        const uint32_t held = ctl->held[k % kPxHeld];
+        const uint8_t *src = smem + C::kOffRaw + st * C::kRawBytes;
 #pragma unroll
-        for (int x = 0; x < kWords / 4; ++x) {
-          const uint4 y = *reinterpret_cast<const uint4 *>(src + tk * (D / 2) + hf * (D / 4) + x * 16);
-          w[4 * x] = y.x, w[4 * x + 1] = y.y, w[4 * x + 2] = y.z, w[4 * x + 3] = y.w;
-        }
+        for (int v = 0; v < 2; ++v) {    // keys, then values
+          uint32_t w[2][kWords], sc[2][kWords / 2];
 #pragma unroll
-        for (int x = 0; x < kWords / 2; ++x) sc[x] = src[Fp4Sub<D>::kKeyScales + tk * (D / 16) + hf * (D / 32) + x];
-        convert(w, sc, h);
-        // values: codes [2][8][8 tokens][D / 16], scales [2][D / 16][8 tokens]
-        const uint8_t *vc = src + Fp4Sub<D>::kValues + (tk >> 3) * (4 * D) + (hf * 4 * 8 + (tk & 7)) * (D / 16);
+          for (int u = 0; u < 2; ++u) {
+            const uint8_t *from = src + ((warp - 12) * 2 + u) * 18 * D;
+            if (v == 0) {                // codes [16][D / 2], scales [16][D / 16]
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if constexpr (D == 128) {
-            const uint2 y = *reinterpret_cast<const uint2 *>(vc + x * 8 * (D / 16));
-            w[2 * x] = y.x, w[2 * x + 1] = y.y;
-          } else {
-            w[x] = *reinterpret_cast<const uint32_t *>(vc + x * 8 * (D / 16));
+              for (int x = 0; x < kWords / 4; ++x) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(from + tk * (D / 2) + hf * (D / 4) + x * 16);
+                w[u][4 * x] = y.x, w[u][4 * x + 1] = y.y, w[u][4 * x + 2] = y.z, w[u][4 * x + 3] = y.w;
+              }
+#pragma unroll
+              for (int x = 0; x < kWords / 2; ++x) sc[u][x] = from[Fp4Sub<D>::kKeyScales + tk * (D / 16) + hf * (D / 32) + x];
+            } else {                     // codes [2][8][8 tokens][D / 16], scales [2][D / 16][8 tokens]
+              const uint8_t *vc = from + Fp4Sub<D>::kValues + (tk >> 3) * (4 * D) + (hf * 4 * 8 + (tk & 7)) * (D / 16);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                if constexpr (D == 128) {
+                  const uint2 y = *reinterpret_cast<const uint2 *>(vc + x * 8 * (D / 16));
+                  w[u][2 * x] = y.x, w[u][2 * x + 1] = y.y;
+                } else {
+                  w[u][x] = *reinterpret_cast<const uint32_t *>(vc + x * 8 * (D / 16));
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < kWords / 2; ++x)
+                sc[u][x] = from[Fp4Sub<D>::kValueScales + (tk >> 3) * (D / 2) + (hf * (D / 32) + x) * 8 + (tk & 7)];
+            }
           }
-        }
-#pragma unroll
-        for (int x = 0; x < kWords / 2; ++x)
-          sc[x] = src[Fp4Sub<D>::kValueScales + (tk >> 3) * (D / 2) + (hf * (D / 32) + x) * 8 + (tk & 7)];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->raw_empty[st]);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
+          if (v == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->raw_empty[st]);
+          }
           const int tile = 2 * k + v, sl = tile % C::kSlots;
           if (tile >= C::kSlots && !mbar_wait(&ctl->kv_empty[sl], (tile / C::kSlots - 1) & 1, abort, P.status)) {
             ok = false;
             break;
           }
-          if (v) convert(w, sc, h);
-          store(smem + C::kOffRing + sl * C::kTile, h, on);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int sub = (warp - 12) * 2 + u;
+            convert(smem + C::kOffRing + sl * C::kTile, sub, w[u], sc[u], (held >> sub & 1) && sub * kSubTokens + tk < tokens);
+          }
           px_fence_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->kv_full[sl]);
         }
       }
     }
+    }
   }
 
   tc_fence_before();
   __syncthreads();
+  ECHO_TRACE_MARK(23);
+  ECHO_TRACE_LAST(24);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -745,54 +876,77 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kPxMergeWarps + warp, rows = static_cast<int64_t>(P.B) * P.n_q * P.n_heads;
   pdl_launch_dependents();
   pdl_wait();
+  ECHO_TRACE_FIRST(25);
   if (row >= rows) return;
-  const int head = static_cast<int>(row % P.n_heads);
-  const int64_t bj = row / P.n_heads;
-  const int b = static_cast<int>(bj / P.n_q), j = static_cast<int>(bj - static_cast<int64_t>(b) * P.n_q), h = head / P.group;
+  // what every row may need is under way while its tile is looked for
+  auto load = [&](const float *o, float (&x)[kPer]) {
+    if constexpr (kPer == 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(o);
+      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2 *>(o);
+      x[0] = y.x, x[1] = y.y;
+    }
+  };
+  float own_x[kPer], first_x[kPer], own_lse = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) own_x[k] = 0.f;
+  const float2 first_ml = P.first_ml[row];
+  load(P.first_o + row * D + lane * kPer, first_x);
+  if (P.own_o) {
+    own_lse = P.own_lse[row];
+    load(P.own_o + row * D + lane * kPer, own_x);
+  }
+  const uint32_t bj = static_cast<uint32_t>(row) / static_cast<uint32_t>(P.n_heads), head = static_cast<uint32_t>(row) - bj * P.n_heads;
+  const int b = bj / static_cast<uint32_t>(P.n_q), j = bj - b * P.n_q, h = head / static_cast<uint32_t>(P.group);
 
   // where the row's tile lies on the line
   const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
-  int64_t mine = 0, u = 0;
-  int chunks = 0, tiles = 0, r = 0;
-  bool own = false;
+  int mine = 0, u = 0, total, at = -1, r = 0;
   for (int g = g0; g < g1; ++g) {
     const PxGroup x = px_group(P, g, false);
-    const int per = P.n_q * P.group;
-    if (!own && x.chunks > 0 && b >= x.b0 && b < x.b0 + x.rows / per)
-      own = true, u = mine, chunks = x.chunks, tiles = x.tiles, r = (b - x.b0) * per + j * P.group + head - h * P.group;
+    const int in = (b - x.b0) * P.n_q * P.group;   // (rows of a request outside the group are not below x.rows)
+    if (at < 0 && x.chunks > 0 && b >= x.b0 && in < x.rows) at = g, u = mine, r = in + j * P.group + head - h * P.group;
     mine += px_units(P, x);
   }
-  int64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(~0u, upto, d);
-    if (lane >= d) upto += y;
-  }
-  const int64_t total = __shfl_sync(~0u, upto, 31);
-  u += upto - mine;
-  const uint32_t who = __ballot_sync(~0u, own);
-  int first = 0, pieces = 0;        // the tile's first CTA and how many pieces it has
+  u += px_scan(mine, total);
+  const PxPlan plan = px_plan(P, total);
+  const uint32_t who = __ballot_sync(~0u, at >= 0);
+  int first = 0, pieces = 0, step = 1;   // the tile's first CTA, how many pieces it has, their CTAs' distance
   if (who) {
     const int src = __ffs(who) - 1;
+    at = __shfl_sync(~0u, at, src);
     u = __shfl_sync(~0u, u, src);
-    chunks = __shfl_sync(~0u, chunks, src), tiles = __shfl_sync(~0u, tiles, src), r = __shfl_sync(~0u, r, src);
-    const int64_t per = (total + P.grid - 1) / P.grid;
-    u += (static_cast<int64_t>(h) * tiles + r / kPxRows) * chunks;
-    first = static_cast<int>(u / per);
-    pieces = static_cast<int>((u + chunks - 1) / per) - first + 1;
+    r = __shfl_sync(~0u, r, src);
+    const PxGroup x = px_group(P, at, false);
+    const int tile = r / kPxRows;
+    if (plan.whole) {
+      int len;
+      for (int g = 0; g < at; ++g) {
+        const PxGroup y = px_group(P, g, false);
+        first += P.n_kv * y.tiles * px_pieces(plan, y, len);
+      }
+      pieces = px_pieces(plan, x, len);
+      first += h * pieces * x.tiles + tile;
+      step = x.tiles;
+    } else {
+      u += (h * x.tiles + tile) * x.chunks;
+      first = u / plan.per;
+      pieces = (u + x.chunks - 1) / plan.per - first + 1;
+    }
     r %= kPxRows;
   }
 
   float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  auto part = [&](int p, float2 &ml, const float *&o) {
-    const int64_t at = p == 0 ? row : static_cast<int64_t>(first + p) * kPxRows + r;
-    ml = (p == 0 ? P.first_ml : P.rest_ml)[at];
-    o = (p == 0 ? P.first_o : P.rest_o) + at * D + lane * kPer;
-  };
+  if (pieces > 0 && first_ml.x != -INFINITY) {
+    top = first_ml.x, sum = first_ml.y;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = first_x[k];
+  }
   constexpr int kAhead = 4;
-  for (int p0 = 0; p0 < pieces; p0 += kAhead) {
+  for (int p0 = 1; p0 < pieces; p0 += kAhead) {
     float2 ml[kAhead];
     float x[kAhead][kPer];
 #pragma unroll
@@ -801,15 +955,9 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
       for (int k = 0; k < kPer; ++k) x[p][k] = 0.f;
       if (p0 + p < pieces) {
-        const float *o;
-        part(p0 + p, ml[p], o);
-        if constexpr (kPer == 4) {
-          const float4 y = *reinterpret_cast<const float4 *>(o);
-          x[p][0] = y.x, x[p][1] = y.y, x[p][2] = y.z, x[p][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2 *>(o);
-          x[p][0] = y.x, x[p][1] = y.y;
-        }
+        const int64_t from = static_cast<int64_t>(first + (p0 + p) * step) * kPxRows + r;
+        ml[p] = P.rest_ml[from];
+        load(P.rest_o + from * D + lane * kPer, x[p]);
       }
     }
     float up = top;
@@ -832,14 +980,13 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] *= P.v_scale;
   if (P.own_o) {                    // divided by its sum already: weight 2^lse, sum 1
-    const float lse = P.own_lse[row] * 1.4426950408889634f;
+    const float lse = own_lse * 1.4426950408889634f;
     if (lse != -INFINITY) {
       const float up = fmaxf(top, lse), f = top == -INFINITY ? 0.f : ex2(top - up), e = ex2(lse - up);
       top = up;
       sum = fmaf(sum, f, e);
-      const float *o = P.own_o + row * D + lane * kPer;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(o[k], e, acc[k] * f);
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(own_x[k], e, acc[k] * f);
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : sum;  // (a NaN sum stays one)
@@ -847,6 +994,7 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
   for (int k = 0; k < kPer / 2; ++k) dst[k] = pack2<false>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   if (P.lse && lane == 0) P.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+  ECHO_TRACE_LAST(26);
 }
 
 }  // namespace echo
@@ -918,6 +1066,18 @@ static int go_prefix(const echo::PrefixParams &P, cudaStream_t stream) {
   static_assert(kSmem <= 232448, "prefix attention: shared memory of one CTA");
   static std::atomic<bool> attr[kMaxDevices];
   if (int rr = smem_limit_once(attr, echo::prefix_attn_kernel<FMT, D>, kSmem, "prefix attention smem attribute")) return rr;
+  // (the warpgroups' shares have to fit what the launch gets: a build that needs fewer registers is refused)
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, echo::prefix_attn_kernel<FMT, D>);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix attention attributes");
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < C::kRegs) {
+    set_error("prefix attention was built with %d registers, its warpgroups need %d", regs.load(), C::kRegs);
+    return ECHO_ENOTSUP;
+  }
   CUtensorMap map{};
   if (!C::kFp4)
     if (int rr = px_map(P, D, &map)) return rr;
@@ -942,7 +1102,8 @@ int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t st
   P.table = a->prefix_table, P.heads = a->prefix_heads, P.max_blocks = a->max_prefix_blocks;
   P.len = a->prefix_len, P.start = a->group_start, P.n_groups = a->n_groups;
   P.B = a->B, P.n_q = a->n_q, P.n_heads = a->n_heads, P.n_kv = a->n_kv_heads, P.group = a->n_heads / a->n_kv_heads;
-  P.scale_log2 = std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift);
+  // (not zero: it has to leave a masked score's infinity what it is)
+  P.scale_log2 = std::max(std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift), 1e-37f);
   P.v_scale = std::ldexp(1.f, -a->v_shift);
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
   P.first_o = reinterpret_cast<float *>(ws), P.first_ml = reinterpret_cast<float2 *>(ws + s.first_ml);
