@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     const int64_t g0 = per * blockIdx.x;
     if (g0 >= total) {
       if (threadIdx.x == 0 && !P.by_pair) P.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
-      if (P.beside) pdl_wait();
+      if (P.beside && blockIdx.x == 0) pdl_wait();
       return;
     }
     n_chunks = static_cast<int>(min(total - g0, per));
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
     cluster_arrive();  // (no CTA's shared memory goes while another reads it)
     cluster_wait();
   }
-  if (P.beside) pdl_wait();
+  if (P.beside && blockIdx.x == 0) pdl_wait();  // (one CTA keeps the grid from ending first, the others make room)
 }
 
 // Merge of the pieces of each (b, hm) that was cut: block (i, y) takes row y of the i-th one

@@ -31,7 +31,6 @@
 
 #include "block_mma.cuh"
 
-ECHO_TRACE_UNIT(prefix_attn)
 
 namespace echo {
 
@@ -247,15 +246,25 @@ __device__ __forceinline__ uint64_t px_mn_desc(uint32_t addr, uint32_t lbo) {
   return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16 |
          static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
 }
-__device__ __forceinline__ void px_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-               "l"(a), "l"(b), "r"(idesc), "r"(acc)
-               : "memory");
+// A descriptor's upper half is the same for all of an operand's steps: the lower one (addresses in
+// units of 16 bytes) is what a step changes.
+struct PxDesc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit PxDesc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+};
+__device__ __forceinline__ void px_mma_ss(uint32_t d, const PxDesc &a, const PxDesc &b, uint32_t step, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a.lo + step), "r"(a.hi), "r"(b.lo + step), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
 }
-__device__ __forceinline__ void px_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-               "r"(a), "l"(b), "r"(idesc), "r"(acc)
-               : "memory");
+__device__ __forceinline__ void px_mma_ts(uint32_t d, uint32_t a, const PxDesc &b, uint32_t step, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b.lo + step), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
 }
 __device__ __forceinline__ void px_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -295,6 +304,14 @@ __device__ __forceinline__ float px_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// mbar_wait() without a look at the clock before the wait has become a long one: reading it takes
+// longer than most waits here
+__device__ __forceinline__ bool px_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, status);
+}
 // a wait without the abort flag, for what is in flight when a kernel gives up
 __device__ __forceinline__ void px_drain(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -315,9 +332,12 @@ struct PxCfg {
   static constexpr uint32_t kRawBytes = 8 * 18 * D;
   static constexpr int kConvWarps = kFp4 ? 4 : 0;
   // Warpgroups: two of softmax, one of the producer and the issuer (and two idle warps), one that
-  // converts.  A launch gives every thread the same registers (168 of 384 threads, 128 of 512);
-  // they are handed over to the softmax, which keeps a row of 128 scores.
-  static constexpr int kThreads = 32 * (12 + kConvWarps);
+  // converts.  A launch gives every thread the same registers (168 of 384 threads, 128 of 512); they
+  // are handed over to the softmax, whose threads keep a row of 128 scores.  (Two threads a row, 64
+  // scores each, meet for the maximum in every chunk: 70 us where one takes 65, with half the row
+  // each still 0.75 us a chunk.)
+  static constexpr int kLoadWarp = 8, kConvWarp = 12;
+  static constexpr int kThreads = 32 * (kConvWarp + kConvWarps);
   static constexpr int kRegs = kFp4 ? 128 : 168, kRegsSoft = kFp4 ? 176 : 208, kRegsLoad = kFp4 ? 80 : 88, kRegsConv = kFp4 ? 80 : 0;
   static_assert(2 * kRegsSoft + kRegsLoad + kRegsConv <= kRegs * kThreads / 128, "registers of the launch");
   static constexpr uint32_t kOffQ = 0, kOffRing = 2 * kTile, kOffRaw = kOffRing + kSlots * kTile;
@@ -359,7 +379,6 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
   volatile int *abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  ECHO_TRACE_MARK(0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&ctl->kv_full[i], F16 ? C::kConvWarps : 1);
@@ -382,7 +401,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
     ctl->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == C::kLoadWarp + 1) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
@@ -390,15 +409,12 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;   // S of the sub-tiles at columns 0 and 128, O at 256 and 256 + D
-  ECHO_TRACE_MARK(1);
   pdl_wait();
   pdl_launch_dependents();
-  ECHO_TRACE_MARK(2);
 
   PxLine L;
   const bool any = L.begin(P, blockIdx.x == 0 && warp == 0);
-  ECHO_TRACE_MARK(3);
-  if (warp < 8) {
+  if (warp < C::kLoadWarp) {
     px_more_regs<C::kRegsSoft>();
     if (any) {
     // ===================== softmax: a warpgroup per sub-tile, a thread per row =====================
@@ -409,23 +425,22 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
     int done = 0;       // chunks of the pieces before
     bool ok = true, active = L.sub_rows(s) > 0;
 
-    // the queries of this warp's rows: D / 8 lanes a row, 16 bytes each
+    // the queries of this warp's 32 rows: D / 8 lanes a row, 16 bytes each
     auto load_q = [&]() {
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 8;
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 32 / kPer;
       const int n = L.sub_rows(s), d8 = lane % kLanes, mine = w4 * 32 + lane;
       const int64_t at = mine < n ? px_out_row(P, L, L.t * kPxRows + s * 128 + mine) : -1;
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += kAhead * kPer) {
+      {
         uint4 x[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int64_t from = __shfl_sync(~0u, at, r0 + u * kPer + lane / kLanes);
+          const int64_t from = __shfl_sync(~0u, at, u * kPer + lane / kLanes);
           x[u] = make_uint4(0u, 0u, 0u, 0u);
           if (from >= 0) x[u] = *reinterpret_cast<const uint4 *>(P.q + from * D + d8 * 8);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int r = w4 * 32 + r0 + u * kPer + lane / kLanes;
+          const int r = w4 * 32 + u * kPer + lane / kLanes;
           uint32_t v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
           if constexpr (F16) {  // scaled by the power of two that brings the row's largest entry to [1, 2)
             float m = 0.f;
@@ -452,7 +467,6 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
     };
 
     if (active) load_q();
-    ECHO_TRACE_MARK(4);
     for (bool more = true; more && ok;) {
       const int n = L.n, len0 = L.x.len - L.c * kPxChunk;  // (tokens from the piece's first on)
       const bool rows = active && w4 * 32 < L.sub_rows(s);  // of this warp
@@ -461,13 +475,12 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
       const float c = P.scale_log2 * (F16 && active ? qscale[s * 128 + w4 * 32 + lane] : 1.f);
       float m = kPxNone, l = 0.f;
       for (int i = 0; active && i < n; ++i) {
-        if (!mbar_wait(&ctl->s_full[s], ph_s, abort, P.status)) {
+        if (!px_wait(&ctl->s_full[s], ph_s, abort, P.status)) {
           ok = false;
           break;
         }
         ph_s ^= 1;
         tc_fence_after();
-        if (i < 6) ECHO_TRACE_MARK(5 + 2 * i);
         if (rows) {
           const uint32_t held = ctl->held[(done + i) % kPxHeld];
           const int tokens = len0 - i * kPxChunk;
@@ -507,37 +520,41 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
               p[k] = pack2<F16>(e.x, e.y);
             }
           };
-          // The first quarter of the weights is worked out with the maximum as it was, beside the search for
-          // the new one, which seldom is far above it; if it is (and with a piece's first chunk) again.
-          for (bool again = false;; again = true) {
-            sums[0] = sums[1] = make_float2(0.f, 0.f);
-            weights(0);
-            if (again) break;
-            const float top = fmaxf(px_max3(tops[0], tops[1], tops[2]), tops[3]);
-            const float x = top == -INFINITY ? kPxNone : fmaf(top, c, -kLift);
-            if (!__any_sync(~0u, i == 0 || x - m > kPxLazy)) break;
+          // The first weights are worked out with the maximum as it was, beside the search for the new
+          // one, which seldom is far above it; if it is (and with a piece's first chunk) again.
+          sums[0] = sums[1] = make_float2(0.f, 0.f);
+          weights(0);
+          const float top = fmaxf(px_max3(tops[0], tops[1], tops[2]), tops[3]);
+          const float x = top == -INFINITY ? kPxNone : fmaf(top, c, -kLift);
+          if (__any_sync(~0u, i == 0 || x - m > kPxLazy)) {
             const float up = fmaxf(m, x), f = ex2(m - up);
             m = up;
             l *= f;
-            if (i == 0) continue;
+            if (i > 0) {
 #pragma unroll 1
-            for (int b = 0; b < D / 16; ++b) {
-              uint32_t o[16];
-              asm volatile(
-                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
-                    "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                  : "r"(o_at + b * 16)
-                  : "memory");
-              asm volatile("tcgen05.wait::ld.sync.aligned;"
-                           : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7]),
-                             "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]), "+r"(o[13]), "+r"(o[14]), "+r"(o[15])
-                           :
-                           : "memory");
+              for (int b = 0; b < D / 16; ++b) {
+                uint32_t o[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
+                      "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                    : "r"(o_at + b * 16)
+                    : "memory");
+                asm volatile("tcgen05.wait::ld.sync.aligned;"
+                             : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7]),
+                               "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]), "+r"(o[13]), "+r"(o[14]), "+r"(o[15])
+                             :
+                             : "memory");
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              px_st16(o_at + b * 16, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                px_st16(o_at + b * 16, o);
+              }
             }
+            tmem_ld_32x32b_x32(s_at, v[0]);  // (read once more: registers are short)
+            tmem_wait_ld();
+            reg_fence_32(v[0]);
+            sums[0] = sums[1] = make_float2(0.f, 0.f);
+            weights(0);
           }
           px_st16(s_at, p);
           weights(1);
@@ -558,7 +575,6 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->p_full[s][1]);
-        if (i < 6) ECHO_TRACE_MARK(6 + 2 * i);
       }
       if (!ok) break;
       done += n;
@@ -574,14 +590,12 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
       active = more && L.sub_rows(s) > 0;
       if (active) load_q();
       if (!was) continue;
-      ECHO_TRACE_MARK(20);
-      if (!mbar_wait(&ctl->o_full[s], ph_o, abort, P.status)) {
+      if (!px_wait(&ctl->o_full[s], ph_o, abort, P.status)) {
         ok = false;
         break;
       }
       ph_o ^= 1;
       tc_fence_after();
-      ECHO_TRACE_MARK(21);
       if (rows) {
         float *dst = (head ? P.first_o : P.rest_o) + to * D;
 #pragma unroll 1
@@ -600,12 +614,11 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->o_free[s]);
-      ECHO_TRACE_MARK(22);
     }
     }
-  } else if (warp < 12) {
+  } else if (warp < C::kConvWarp) {
     px_fewer_regs<C::kRegsLoad>();
-    if (any && warp == 8) {
+    if (any && warp == C::kLoadWarp) {
     // ===================== producer =====================
     const int boxes = F16 ? kPxChunk / kSubTokens : kPxChunk / P.box, box = F16 ? kSubTokens : P.box;
     int k = 0, asked = 0;  // chunks, and (bf16) tiles, asked for
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
         const uint32_t held = __ballot_sync(~0u, row_now >= 0);
         if constexpr (F16) {
           const int st = k % C::kRaw;
-          if (k >= C::kRaw && !mbar_wait(&ctl->raw_empty[st], (k / C::kRaw - 1) & 1, abort, P.status)) {
+          if (k >= C::kRaw && !px_wait(&ctl->raw_empty[st], (k / C::kRaw - 1) & 1, abort, P.status)) {
             ok = false;
             break;
           }
@@ -657,7 +670,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int tile = 2 * k + v, st = tile % C::kSlots;
-            if (tile >= C::kSlots && !mbar_wait(&ctl->kv_empty[st], (tile / C::kSlots - 1) & 1, abort, P.status)) {
+            if (tile >= C::kSlots && !px_wait(&ctl->kv_empty[st], (tile / C::kSlots - 1) & 1, abort, P.status)) {
               ok = false;
               break;
             }
@@ -676,7 +689,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
                        static_cast<int>(2 * row_now + v));
             }
             if (mend) {
-              if (!mbar_wait(&ctl->fix, ph_fix, abort, P.status)) {
+              if (!px_wait(&ctl->fix, ph_fix, abort, P.status)) {
                 px_drain(&ctl->fix, ph_fix);
                 ok = false;
                 break;
@@ -703,31 +716,29 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
       const int n = F16 ? k : asked;
       for (int j = max(n - kDepth, 0); j < n; ++j) px_drain(F16 ? &ctl->raw_full[j % kDepth] : &ctl->kv_full[j % kDepth], (j / kDepth) & 1);
     }
-    } else if (any && warp == 9) {
+    } else if (any && warp == C::kLoadWarp + 1) {
     // ===================== tensor-core issuer: one thread =====================
     if (elect_one()) {
       uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_free[2] = {1, 1};  // (O is free at first)
       int k = 0;        // tiles taken from the ring
       bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort, P.status); };
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && px_wait(bar, parity, abort, P.status); };
       auto full = [&](int tile) { return wait(&ctl->kv_full[tile % C::kSlots], (tile / C::kSlots) & 1); };
       auto scores = [&](int s, int tile) {     // S of sub-tile s
         tc_fence_after();
-        const uint64_t a = kmajor_sw128_desc(q_at + s * C::kTile), b = kmajor_sw128_desc(ring + (tile % C::kSlots) * C::kTile);
+        const PxDesc a(kmajor_sw128_desc(q_at + s * C::kTile)), b(kmajor_sw128_desc(ring + (tile % C::kSlots) * C::kTile));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {  // (addresses in units of 16 bytes)
-          const uint32_t o = ((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4;
-          px_mma_ss(tmem + s * 128, a + o, b + o, kIdescS, kk > 0);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          px_mma_ss(tmem + s * 128, a, b, ((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4, kIdescS, kk > 0);
         mma_commit(&ctl->s_full[s]);
         mbar_arrive(&ctl->s_full[s]);
       };
       auto values = [&](int s, int tile, int half, bool more) {  // O of sub-tile s, half the tokens
         tc_fence_after();
-        const uint64_t b = px_mn_desc(ring + (tile % C::kSlots) * C::kTile, C::kBlock) + half * (64 * 128 >> 4);
+        const PxDesc b(px_mn_desc(ring + (tile % C::kSlots) * C::kTile, C::kBlock));
 #pragma unroll
         for (int kk = 0; kk < kPxChunk / 32; ++kk)
-          px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + half * 32 + kk * 8, b + (kk * 16 * 128 >> 4), kIdescO, more || kk > 0);
+          px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + half * 32 + kk * 8, b, (half * 64 + kk * 16) * 128 >> 4, kIdescO, more || kk > 0);
       };
       auto release = [&](int tile) { mma_commit(&ctl->kv_empty[tile % C::kSlots]); };
       for (bool more = true; more && ok; more = ok && L.next(P)) {
@@ -795,7 +806,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
     for (bool more = true; more && ok; more = ok && L.next(P)) {
       for (int i = 0; i < L.n && ok; ++i, ++k) {
         const int st = k % C::kRaw, tokens = L.x.len - (L.c + i) * kPxChunk;
-        if (!mbar_wait(&ctl->raw_full[st], (k / C::kRaw) & 1, abort, P.status)) {
+        if (!px_wait(&ctl->raw_full[st], (k / C::kRaw) & 1, abort, P.status)) {
           ok = false;
           break;
         }
@@ -806,7 +817,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
           uint32_t w[2][kWords], sc[2][kWords / 2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint8_t *from = src + ((warp - 12) * 2 + u) * 18 * D;
+            const uint8_t *from = src + ((warp - C::kConvWarp) * 2 + u) * 18 * D;
             if (v == 0) {                // codes [16][D / 2], scales [16][D / 16]
 #pragma unroll
               for (int x = 0; x < kWords / 4; ++x) {
@@ -836,13 +847,13 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
             if (lane == 0) mbar_arrive(&ctl->raw_empty[st]);
           }
           const int tile = 2 * k + v, sl = tile % C::kSlots;
-          if (tile >= C::kSlots && !mbar_wait(&ctl->kv_empty[sl], (tile / C::kSlots - 1) & 1, abort, P.status)) {
+          if (tile >= C::kSlots && !px_wait(&ctl->kv_empty[sl], (tile / C::kSlots - 1) & 1, abort, P.status)) {
             ok = false;
             break;
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int sub = (warp - 12) * 2 + u;
+            const int sub = (warp - C::kConvWarp) * 2 + u;
             convert(smem + C::kOffRing + sl * C::kTile, sub, w[u], sc[u], (held >> sub & 1) && sub * kSubTokens + tk < tokens);
           }
           px_fence_smem();
@@ -856,9 +867,7 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  ECHO_TRACE_MARK(23);
-  ECHO_TRACE_LAST(24);
-  if (warp == 9) {
+  if (warp == C::kLoadWarp + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -876,7 +885,6 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kPxMergeWarps + warp, rows = static_cast<int64_t>(P.B) * P.n_q * P.n_heads;
   pdl_launch_dependents();
   pdl_wait();
-  ECHO_TRACE_FIRST(25);
   if (row >= rows) return;
   // what every row may need is under way while its tile is looked for
   auto load = [&](const float *o, float (&x)[kPer]) {
@@ -945,7 +953,7 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = first_x[k];
   }
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   for (int p0 = 1; p0 < pieces; p0 += kAhead) {
     float2 ml[kAhead];
     float x[kAhead][kPer];
@@ -994,7 +1002,6 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
   for (int k = 0; k < kPer / 2; ++k) dst[k] = pack2<false>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   if (P.lse && lane == 0) P.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
-  ECHO_TRACE_LAST(26);
 }
 
 }  // namespace echo
