@@ -705,7 +705,7 @@ int echo_block_scores(const echo_block_scores_args *args, void *stream);
  * echo_block_attention reads them with the queries folded into the requests: B * n_q requests of
  * one query token, table = sel_rows, sel, table_heads = n_kv_heads, max_blocks = k, ctx_len =
  * len_out.  With n_q == 1, sel is a selection for echo_prefetch_recall over a pool of block rows.
- * Limits: k >= 1, 0 <= first, last, first + last <= k, max_blocks <= 49152, B * n_q * n_kv_heads
+ * Limits: k >= 1, 0 <= first, last, first + last <= k, max_blocks <= 32768, B * n_q * n_kv_heads
  * below 2^31.  Launches 1 kernel.
  */
 typedef struct echo_block_select_args {

@@ -576,7 +576,7 @@ int echo_block_select(const echo_block_select_args *a, void *stream) {
   REQUIRE(a, "args is NULL");
   REQUIRE(a->B >= 0 && a->n_q >= 1 && a->n_q <= 65536, "bad sizes (B %d, n_q %d)", a->B, a->n_q);
   TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
-  REQUIRE(a->max_blocks <= 49152, "max_blocks must be at most 49152 (got %d)", a->max_blocks);
+  REQUIRE(a->max_blocks <= 32768, "max_blocks must be at most 32768 (got %d)", a->max_blocks);
   REQUIRE(a->k >= 1 && a->k <= (1 << 20), "k must be in [1, 2^20] (got %d)", a->k);
   REQUIRE(a->first >= 0 && a->last >= 0 && static_cast<long long>(a->first) + a->last <= a->k,
           "first and last must not be negative, their sum at most k (got %d, %d, k %d)", a->first, a->last, a->k);

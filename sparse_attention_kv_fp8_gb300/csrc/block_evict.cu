@@ -19,13 +19,14 @@
 //     of its token's key and feeds them as they are (4-bit rows: 16 bytes of codes, converted in
 //     place); keys go from memory to registers with nothing in between, two sub-blocks of 16
 //     tokens a warp at a time, the exponentials of a column summed over the quad.
-//   Eviction: a CTA per (b, h) finds the weight of the last token that stays, by passes over 256
-//     equal parts of the range that still holds it, and lists holes and movers in order; the
+//   Eviction: a CTA per (b, h) finds the weight of the last token that stays from counts over the
+//     range of the weights (block_pick.cuh), and lists holes and movers in order; the
 //     moves follow in the same CTA when they are few, else in a second kernel over the whole GPU.
 #include <algorithm>
 #include <cmath>
 
 #include "block_mma.cuh"
+#include "block_pick.cuh"
 
 namespace echo {
 
@@ -90,8 +91,45 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
   }
   const int64_t out0 = (static_cast<int64_t>(b) * P.n_kv + h) * most;
 
+  // two sub-blocks: tokens r8 and r8 + 8 of each
+  uint4 a[2][2][kLoads];
+  uint32_t sc[2][2];
+  bool held[2];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      int64_t at = __shfl_sync(~0u, where, (s - s0 + u) & 31);
+      if (s + u >= s1) at = -1;
+      held[u] = at >= 0;
+      const uint8_t *src = P.rows + (at < 0 ? 0 : at);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int tk = r8 + 8 * k;
+        sc[u][k] = 0;
+        if constexpr (F16) {
+          a[u][k][0] = make_uint4(0u, 0u, 0u, 0u);
+          if (at >= 0) {
+            if constexpr (D == 128) {
+              a[u][k][0] = *reinterpret_cast<const uint4 *>(src + tk * (D / 2) + c4 * 16);
+              sc[u][k] = *reinterpret_cast<const uint16_t *>(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4 * 2);
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2 *>(src + tk * (D / 2) + c4 * 8);
+              a[u][k][0].x = y.x, a[u][k][0].y = y.y;
+              sc[u][k] = src[Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i)
+            a[u][k][i] = at < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(src + tk * (2 * D) + i * 64 + c4 * 16);
+        }
+      }
+    }
+  };
+
   for (int c0 = 0; c0 < rows_q; c0 += kWtCols) {
     const int nc = min(kWtCols, rows_q - c0), nc8 = (nc + 7) & ~7;
+    if (s0 < s1) load(s0);   // (under way while the queries are laid out)
     if (c0) __syncthreads();
     // the queries as columns: piece 4 i + c holds what lane c of a quad feeds with its i-th piece
     for (int i = warp; i < nc8; i += kWtWarps) {   // a column per warp
@@ -127,63 +165,27 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
     }
     __syncthreads();
     for (int s = s0; s < s1; s += 2) {
-      uint4 a[2][2][kLoads];      // sub-block, token r8 (+ 8)
-      uint32_t sc[2][2];
-      int64_t at[2];
+      const bool held_now[2] = {held[0], held[1]};
+      // 4 bits: the A fragments, piece i of a lane's dims in two steps of 16 (bf16: as they were loaded)
+      uint32_t f[F16 ? 2 : 1][F16 ? kPieces : 1][2][4];
+      if constexpr (F16) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        at[u] = __shfl_sync(~0u, where, s - s0 + u);  // (past the run: -1)
-        if (s + u >= s1) at[u] = -1;
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint8_t *src = P.rows + (at[u] < 0 ? 0 : at[u]);
-          const int tk = r8 + 8 * k;
-          sc[u][k] = 0;
-          if constexpr (F16) {
-            a[u][k][0] = make_uint4(0u, 0u, 0u, 0u);
-            if (at[u] >= 0) {
-              if constexpr (D == 128) {
-                a[u][k][0] = *reinterpret_cast<const uint4 *>(src + tk * (D / 2) + c4 * 16);
-                sc[u][k] = *reinterpret_cast<const uint16_t *>(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4 * 2);
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2 *>(src + tk * (D / 2) + c4 * 8);
-                a[u][k][0].x = y.x, a[u][k][0].y = y.y;
-                sc[u][k] = src[Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4];
-              }
-            }
-          } else {
+          for (int i = 0; i < kPieces; ++i)
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-              a[u][k][i] = at[u] < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                     : *reinterpret_cast<const uint4 *>(src + tk * (2 * D) + i * 64 + c4 * 16);
-          }
-        }
-      }
-      // A fragments: piece i of a lane's dims in two steps of 16
-      uint32_t f[2][kPieces][2][4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if constexpr (F16) {
+            for (int k = 0; k < 2; ++k) {
               const uint32_t word[4] = {a[u][k][0].x, a[u][k][0].y, a[u][k][0].z, a[u][k][0].w};
               uint32_t v[4];
               e2m1x8_to_half2(word[i], v);
               const uint32_t s2 = __byte_perm(e4m3x2_to_half2(sc[u][k]), 0, D == 128 && i >= 2 ? 0x3232 : 0x1010);
               f[u][i][0][k] = hmul2(v[0], s2), f[u][i][0][2 + k] = hmul2(v[1], s2);
               f[u][i][1][k] = hmul2(v[2], s2), f[u][i][1][2 + k] = hmul2(v[3], s2);
-            } else {
-              f[u][i][0][k] = a[u][k][i].x, f[u][i][0][2 + k] = a[u][k][i].y;
-              f[u][i][1][k] = a[u][k][i].z, f[u][i][1][2 + k] = a[u][k][i].w;
             }
-          }
-      float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-      // tokens that every query sees (the last n_q - 1 are looked at one by one)
-      const bool edge = (s + 2) * kSubTokens > len - (P.n_q - 1);
-      for (int cg = 0; cg < nc8; cg += 8) {
-        float x[2][4];
+        if (s + 2 < s1) load(s + 2);   // (the registers are free)
+      }
+      float x[2][4], w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      auto products = [&](int cg) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -194,10 +196,21 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
           const uint4 q = *reinterpret_cast<const uint4 *>(qp + i * 64);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            mma16816<F16>(x[u], f[u][i][0], q.x, q.y);
-            mma16816<F16>(x[u], f[u][i][1], q.z, q.w);
+            if constexpr (F16) {
+              mma16816<true>(x[u], f[u][i][0], q.x, q.y);
+              mma16816<true>(x[u], f[u][i][1], q.z, q.w);
+            } else {
+              const uint32_t y[4] = {a[u][0][i].x, a[u][1][i].x, a[u][0][i].y, a[u][1][i].y};
+              const uint32_t z[4] = {a[u][0][i].z, a[u][1][i].z, a[u][0][i].w, a[u][1][i].w};
+              mma16816<false>(x[u], y, q.x, q.y);
+              mma16816<false>(x[u], z, q.z, q.w);
+            }
           }
         }
+      };
+      // tokens that every query sees (the last n_q - 1 are looked at one by one)
+      const bool edge = (s + 2) * kSubTokens > len - (P.n_q - 1);
+      auto weights = [&](int cg) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const int c = cg + 2 * c4 + p;
@@ -211,7 +224,14 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
               w[u][k] += c < nc && (!edge || (s + u) * kSubTokens + r8 + 8 * k < seen) ? e : 0.f;
             }
         }
+      };
+      for (int cg = 0; cg + 8 < nc8; cg += 8) {
+        products(cg);
+        weights(cg);
       }
+      products(nc8 - 8);
+      if (!F16 && s + 2 < s1) load(s + 2);   // (now the keys' registers are free)
+      weights(nc8 - 8);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -221,7 +241,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
           v += __shfl_xor_sync(~0u, v, 2);
           const int p = (s + u) * kSubTokens + r8 + 8 * k;
           if (c4 != 0 || s + u >= s1 || p >= len) continue;
-          if (at[u] < 0) v = 0.f;
+          if (!held_now[u]) v = 0.f;
           float before;
           if (c0) before = P.acc_out[out0 + p];  // (written by this thread)
           else before = p < old ? P.acc[out0 + p] * P.decay : 0.f;
@@ -234,10 +254,8 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
 // ---------------------------------------------------------------------------
 // eviction
 // ---------------------------------------------------------------------------
-constexpr int kEvThreads = 512;
-constexpr int kEvBins = 256;
+constexpr int kEvAhead = 8;           // slots a thread has under way
 constexpr int kEvStaged = 32768;      // tokens whose keys a CTA keeps in shared memory
-constexpr uint32_t kEvMust = 0xffffffffu;
 
 struct EvictParams {
   uint8_t *rows;
@@ -309,13 +327,11 @@ __device__ __forceinline__ void move_token(const EvictParams &P, int b, int h, i
   }
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kEvThreads) block_evict_kernel(const EvictParams P) {
-  constexpr int W = kEvThreads / 32;
+template <int FMT, int D, int T>
+__global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
+  constexpr int W = T / 32;
   extern __shared__ uint32_t ev_keys[];
-  __shared__ uint32_t hist[kEvBins];
-  __shared__ uint32_t red[3][W];
-  __shared__ uint32_t pick[3];
+  __shared__ PickSpace<W> S;
   __shared__ uint32_t wcnt[2][W];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / P.n_kv, h = blockIdx.x - b * P.n_kv;
@@ -339,92 +355,83 @@ __global__ void __launch_bounds__(kEvThreads) block_evict_kernel(const EvictPara
   const int nxt = P.pos ? P.next_pos[b] : 0;
   auto pos_of = [&](int i) { return i < known ? pos[i] : nxt - n + i; };
 
-  if (n <= P.keep) {
-    for (int i = tid; i < n; i += kEvThreads) {
-      acc_out[i] = acc[i];
-      if (pos_out) pos_out[i] = pos_of(i);
+  // weights and positions of slots [0, upto) as they are, loads ahead of the stores (which may go to
+  // the same memory)
+  auto copy = [&](int upto) {
+    for (int i0 = tid; i0 < upto; i0 += kEvAhead * T) {
+      float x[kEvAhead];
+      int y[kEvAhead];
+#pragma unroll
+      for (int r = 0; r < kEvAhead; ++r) {
+        const int i = i0 + r * T;
+        x[r] = i < upto ? acc[i] : 0.f;
+        y[r] = pos_out && i < upto ? pos_of(i) : 0;
+      }
+#pragma unroll
+      for (int r = 0; r < kEvAhead; ++r) {
+        const int i = i0 + r * T;
+        if (i < upto) {
+          acc_out[i] = x[r];
+          if (pos_out) pos_out[i] = y[r];
+        }
+      }
     }
+  };
+  if (n <= P.keep) {
+    copy(n);
     if (tid == 0) P.moves[blockIdx.x] = 0;
     return;
   }
 
-  auto key_of = [&](int i) -> uint32_t {
-    if (i < P.sinks || (pos && pos_of(i) >= nxt - P.recent)) return kEvMust;
-    const float s = acc[i];
+  auto make_key = [&](int i, float s, int at) -> uint32_t {
+    if (i < P.sinks || (pos && at >= nxt - P.recent)) return kMustKey;
     return s != s ? 1u : score_key(s);  // (a weight that is NaN goes first)
   };
-  uint32_t lo = kEvMust, hi = 0, n_must = 0;
-  for (int i = tid; i < n; i += kEvThreads) {
-    const uint32_t key = key_of(i);
-    if (P.staged) ev_keys[i] = key;
-    if (key == kEvMust) ++n_must;
-    else lo = min(lo, key), hi = max(hi, key);
-  }
-  n_must = __reduce_add_sync(~0u, n_must), lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
-  if (lane == 0) red[0][warp] = n_must, red[1][warp] = lo, red[2][warp] = hi;
-  __syncthreads();
-  n_must = hi = 0, lo = kEvMust;
+  auto key_of = [&](int i) { return make_key(i, acc[i], pos ? pos_of(i) : 0); };
+  const uint32_t zero = score_key(0.f);
+  uint32_t lo = kMustKey, hi = 0, n_must = 0;   // (of the weights above zero)
+  for (int i0 = tid; i0 < n; i0 += kEvAhead * T) {
+    float x[kEvAhead];
+    int y[kEvAhead];
 #pragma unroll
-  for (int w = 0; w < W; ++w) n_must += red[0][w], lo = min(lo, red[1][w]), hi = max(hi, red[2][w]);
+    for (int r = 0; r < kEvAhead; ++r) {
+      const int i = min(i0 + r * T, n - 1);
+      x[r] = acc[i];
+      y[r] = pos ? pos[i] : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < kEvAhead; ++r) {
+      const int i = i0 + r * T;
+      if (i >= n) break;
+      const uint32_t key = make_key(i, x[r], i < known ? y[r] : nxt - n + i);
+      if (P.staged) ev_keys[i] = key;
+      if (key == kMustKey) ++n_must;
+      else if (key > zero) lo = min(lo, key), hi = max(hi, key);
+    }
+  }
+  n_must = pick_sum(S, n_must, 0), lo = pick_min(S, lo, 1), hi = ~pick_min(S, ~hi, 0);
   auto key_at = [&](int i) -> uint32_t { return P.staged ? ev_keys[i] : key_of(i); };
 
   // ----- the key above which all stay, and how many of its equals (n > keep: some go) -----
-  uint32_t thr = kEvMust - 1, need = 0;
+  uint32_t thr = kMustKey - 1, need = 0;
   if (n_must > static_cast<uint32_t>(P.keep)) {  // (more recent positions than their number: the first slots of them)
-    thr = kEvMust, need = P.keep;
-  } else {
-    uint32_t want = P.keep - n_must;
-    while (want) {  // the want-th largest of the keys in [lo, hi]
-      const int shift = max(0, 24 - __clz(hi - lo));
-      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kEvThreads) {
-        const uint32_t key = key_at(i);
-        if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> shift], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) {  // lane l holds bins 255 - 8 l .. 248 - 8 l
-        uint32_t c[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = hist[kEvBins - 1 - 8 * lane - i], sum += c[i];
-        uint32_t upto = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t x = __shfl_up_sync(~0u, upto, d);
-          if (lane >= d) upto += x;
-        }
-        uint32_t above = upto - sum;
-        if (above < want && upto >= want) {
-          int i = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i == k && above + c[k] < want) above += c[k], i = k + 1;
-          pick[0] = kEvBins - 1 - 8 * lane - i;
-          pick[1] = above;
-          pick[2] = pick_reg(c, i);
-        }
-      }
-      __syncthreads();
-      const uint32_t bin = pick[0], in = pick[2];
-      want -= pick[1];
-      lo += bin << shift;
-      const uint32_t width = (1u << shift) - 1;
-      hi = hi - lo > width ? lo + width : hi;
-      if (in == want) {
-        thr = lo - 1;
-        break;
-      }
-      if (shift == 0) {
-        thr = lo, need = want;
-        break;
-      }
-    }
+    thr = kMustKey, need = P.keep;
+  } else if (n_must < static_cast<uint32_t>(P.keep)) {
+    // 256 equal parts of the keys' range (a weight's exponent and leading bits) above zero
+    const int shift = hi > lo ? max(0, 24 - __clz(hi - lo)) : 0;
+    auto bin = [&](int, uint32_t k) { return k <= lo ? 0 : static_cast<int>(min((k - lo) >> shift, kPickBins - 1u)); };
+    auto each = [&](auto &&f) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += T) f(0, key_at(i));
+    };
+    pick_kth(S, P.keep - n_must, each, bin, bin, thr, need);
   }
+  __syncthreads();
 
   // ----- holes and movers in order -----
   // A thread takes a run of slots (an odd number: no bank conflicts); equals that stay, then holes and movers, are counted over the
   // runs.  Movers and holes are as many.
-  const int per = (n + kEvThreads - 1) / kEvThreads | 1, i0 = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(n))), i1 = min(i0 + per, n);
+  const int per = (n + T - 1) / T | 1, i0 = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(n))), i1 = min(i0 + per, n);
   auto scan = [&](uint32_t mine, int which) -> uint32_t {  // exclusive sum over the threads
     uint32_t upto = mine;
 #pragma unroll
@@ -469,12 +476,9 @@ __global__ void __launch_bounds__(kEvThreads) block_evict_kernel(const EvictPara
 
   // ----- weights and positions: those that keep their slot, then those that move -----
   // (in place the first pass writes what is there)
-  for (int i = tid; i < end; i += kEvThreads) {
-    acc_out[i] = acc[i];
-    if (pos_out) pos_out[i] = pos_of(i);
-  }
+  copy(end);
   __syncthreads();
-  for (uint32_t i = tid; i < count; i += kEvThreads) {
+  for (uint32_t i = tid; i < count; i += T) {
     const int2 m = list[i];
     acc_out[m.y] = acc[m.x];
     if (pos_out) pos_out[m.y] = pos_of(m.x);
@@ -550,14 +554,17 @@ static int go_evict(echo::EvictParams P, cudaStream_t stream) {
   const int64_t most = static_cast<int64_t>(P.max_blocks) * P.bsub * echo::kSubTokens;
   P.staged = most <= echo::kEvStaged;
   const int smem = P.staged ? static_cast<int>(most) * 4 : 0;
+  // (threads by the slots a pair may have: 512 CTAs' worth of either is on the device at once)
+  const bool wide = most > 8192;
   if (smem > 40960)
-    if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
+    if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D, 1024>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
   int sms = 0;
   if (int rr = evict_sms(&sms)) return rr;
   const int64_t moves = std::max<int64_t>(0, std::min<int64_t>(P.keep, most - P.keep));
   P.move_here = moves <= 256;
   P.move_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((moves + 31) / 32, 16ll * sms / pairs)));
-  cudaError_t e = launch_pdl(echo::block_evict_kernel<FMT, D>, dim3(static_cast<unsigned>(pairs)), dim3(echo::kEvThreads), smem, stream, P);
+  cudaError_t e = wide ? launch_pdl(echo::block_evict_kernel<FMT, D, 1024>, dim3(static_cast<unsigned>(pairs)), dim3(1024), smem, stream, P)
+                       : launch_pdl(echo::block_evict_kernel<FMT, D, 512>, dim3(static_cast<unsigned>(pairs)), dim3(512), smem, stream, P);
   if (e == cudaSuccess && !P.move_here)
     e = launch_pdl(echo::block_move_kernel<FMT, D>, dim3(static_cast<unsigned>(pairs * P.move_ctas)), dim3(echo::kMvWarps * 32), 0, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block eviction launch");

@@ -1,0 +1,140 @@
+// block_pick.cuh -- the want-th largest of a set of keys that a warp or a block holds, for the
+// selections over block scores and over gathered weights.
+//
+// One pass counts the keys in 256 parts of their range, and the part that holds the want-th largest is
+// found from the counts.  Its keys, a few as a rule, are gathered and ranked against one another; more
+// than 32 are settled by halving their range.  (Halving the whole range takes up to 31 passes: a row of
+// 1024 block scores 19 us, 8 prompts of 32768 weights 102 us in all.)
+#pragma once
+
+#include "block_rows.cuh"
+
+namespace echo {
+
+constexpr int kPickBins = 256;
+constexpr uint32_t kMustKey = 0xffffffffu;  // a key that is always taken; 0: one that may not be
+
+// Scratch of a group of W warps.
+template <int W>
+struct PickSpace {
+  uint32_t hist[kPickBins];
+  uint32_t red[2][W];
+  uint32_t pick[3];
+  uint32_t few[32], n_few;
+};
+
+template <int W>
+__device__ __forceinline__ void pick_sync() {
+  if constexpr (W > 1) __syncthreads();
+  else __syncwarp();
+}
+
+// sum over the group (turn: 0 and 1 by turns, so that one barrier does)
+template <int W>
+__device__ __forceinline__ uint32_t pick_sum(PickSpace<W> &S, uint32_t x, int turn) {
+  x = __reduce_add_sync(~0u, x);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) S.red[turn][threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) x += S.red[turn][w];
+  }
+  return x;
+}
+template <int W>
+__device__ __forceinline__ uint32_t pick_min(PickSpace<W> &S, uint32_t x, int turn) {
+  x = __reduce_min_sync(~0u, x);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) S.red[turn][threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = S.red[turn][0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) x = min(x, S.red[turn][w]);
+  }
+  return x;
+}
+
+// thr and need such that the keys above thr, and the first `need` that equal it, are the `want`
+// largest (0 < want < their number) of the keys other than 0 and kMustKey.  each(f) calls f(r, key) on
+// each key of the thread, r its number; bin(r, key) in [0, kPickBins) does not fall as the key grows, and
+// again(r, key) gives the same once bin() was asked.
+template <int W, class Each, class Bin, class Again>
+__device__ __forceinline__ void pick_kth(PickSpace<W> &S, uint32_t want, Each &&each, Bin &&bin, Again &&again, uint32_t &thr,
+                                         uint32_t &need) {
+  const int lane = threadIdx.x & 31, tid = W > 1 ? threadIdx.x : lane;
+  for (int i = tid; i < kPickBins; i += W * 32) S.hist[i] = 0;
+  if (tid == 0) S.n_few = 0;
+  pick_sync<W>();
+  each([&](int r, uint32_t key) {
+    if (key != 0 && key != kMustKey) atomicAdd(&S.hist[bin(r, key)], 1u);
+  });
+  pick_sync<W>();
+  if (W == 1 || threadIdx.x < 32) {  // lane l holds bins 255 - 8 l .. 248 - 8 l
+    uint32_t n[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = S.hist[kPickBins - 1 - 8 * lane - i], sum += n[i];
+    uint32_t upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += x;
+    }
+    uint32_t above = upto - sum;
+    if (above < want && upto >= want) {
+      int i = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i == k && above + n[k] < want) above += n[k], i = k + 1;
+      S.pick[0] = kPickBins - 1 - 8 * lane - i, S.pick[1] = above, S.pick[2] = pick_reg(n, i);
+    }
+  }
+  pick_sync<W>();
+  const int part = S.pick[0];
+  const uint32_t in = S.pick[2];
+  want -= S.pick[1];
+  auto member = [&](int r, uint32_t key) { return key != 0 && key != kMustKey && again(r, key) == part; };
+  if (in <= 32) {
+    each([&](int r, uint32_t key) {
+      if (member(r, key)) S.few[atomicAdd(&S.n_few, 1u)] = key;
+    });
+    pick_sync<W>();
+    const uint32_t mine = lane < in ? S.few[lane] : 0u;   // (any order: only counts come of it)
+    uint32_t above = 0, equal = 0;
+    for (int i = 0; i < in; ++i) {
+      const uint32_t x = __shfl_sync(~0u, mine, i);
+      above += x > mine, equal += x == mine;
+    }
+    const int src = __ffs(__ballot_sync(~0u, lane < in && above < want && above + equal >= want)) - 1;
+    thr = __shfl_sync(~0u, mine, src);
+    need = want - __shfl_sync(~0u, above, src);
+    return;
+  }
+  uint32_t lo = kMustKey, hi = 0;   // the part's keys
+  each([&](int r, uint32_t key) {
+    if (member(r, key)) lo = min(lo, key), hi = max(hi, key);
+  });
+  lo = pick_min(S, lo, 0);
+  hi = ~pick_min(S, ~hi, 1);
+  // of the keys in [lo, hi], more than `want` (or all) lie above `below`, above_hi < want above `top`
+  uint32_t below = lo - 1, top = hi, above_hi = 0, mid = lo;   // (many equal to the lowest: seen at once)
+  need = 0;
+  for (int turn = 0;; turn ^= 1) {
+    if (top - below == 1) {    // equal keys: the first of them
+      thr = top, need = want - above_hi;
+      return;
+    }
+    uint32_t c = 0;
+    each([&](int, uint32_t key) { c += key > mid && key <= hi; });
+    c = pick_sum(S, c, turn);
+    if (c == want) {
+      thr = mid;
+      return;
+    }
+    if (c > want) below = mid;
+    else top = mid, above_hi = c;
+    mid = below + (top - below) / 2;
+  }
+}
+
+}  // namespace echo

@@ -19,13 +19,14 @@
 //     as they are: a warp has the 16 summaries (8 KB) in registers after one round of loads, with
 //     no shared memory.  The 8 columns are the heads of one query token, or of several where a
 //     group has fewer, so the maximum over a group stays within a quad.
-//   Selection: a CTA per (query, KV head) with its keys in shared memory.  Radix passes over the
-//     range that still holds the k-th best, 256 equal parts of it at a time, and one ordered
-//     pass over the blocks that writes those above it and the first of its equals.
+//   Selection: a warp per (query, KV head) up to 1024 blocks, up to 32 warps beyond, with the keys in
+//     registers.  The k-th best is found from counts over the range of the scores (block_pick.cuh), then
+//     one ordered pass writes those above it and the first of its equals.
 #include <algorithm>
 #include <cmath>
 
 #include "block_mma.cuh"
+#include "block_pick.cuh"
 
 namespace echo {
 
@@ -252,8 +253,33 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   const int first = part * (kScoreWarps * 16) * P.tiles;
   if (first >= blocks) return;
 
+  // summaries of blocks r8 and r8 + 8 of a tile; their rows are looked up a tile ahead
+  uint4 a[2][kChunks];
+  int64_t row[2];
+  bool there[2];
+  auto look_up = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = first + (t * kScoreWarps + warp) * 16 + r8 + 8 * k;
+      row[k] = t < P.tiles && e < blocks ? P.tab.row(b, h, e) : -1;
+    }
+  };
+  auto load = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (row[k] >= P.n_rows) set_status(P.status, ECHO_DEV_BAD_INDEX);
+      there[k] = row[k] >= 0 && row[k] < P.n_rows;
+      const uint8_t *src = P.summary + (there[k] ? row[k] : 0) * (4 * D) + c4 * 16;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) a[k][i] = there[k] ? *reinterpret_cast<const uint4 *>(src + i * 64) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    look_up(t + 1);
+  };
+
   for (int c0 = 0; c0 < P.cols; c0 += P.chunk) {
     const int nc = min(P.chunk, P.cols - c0);
+    look_up(0);
+    load(0);     // (under way while the queries are laid out)
     if (c0) __syncthreads();
     // [q-, q+] of the columns; a group's last head fills its padding (a maximum does not mind)
     for (int i = threadIdx.x; i < nc * (D / 8); i += kScoreWarps * 32) {
@@ -279,19 +305,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
     for (int t = 0; t < P.tiles; ++t) {
       const int e0 = first + (t * kScoreWarps + warp) * 16;
       if (e0 >= blocks) break;
-      uint4 a[2][kChunks];
-      bool held[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int e = e0 + r8 + 8 * k;
-        const int64_t row = e < blocks ? P.tab.row(b, h, e) : -1;
-        held[k] = row >= 0 && row < P.n_rows;
-        if (row >= P.n_rows) set_status(P.status, ECHO_DEV_BAD_INDEX);
-        const uint8_t *src = P.summary + (held[k] ? row : 0) * (4 * D) + c4 * 16;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-          a[k][i] = held[k] ? *reinterpret_cast<const uint4 *>(src + i * 64) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      const bool held[2] = {there[0], there[1]};
       float best[2][2];  // of column parity and block
 #pragma unroll
       for (int k = 0; k < 4; ++k) best[k >> 1][k & 1] = -INFINITY;
@@ -305,6 +319,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
           mma16816<false>(acc, x, q.x, q.y);
           mma16816<false>(acc, y, q.z, q.w);
         }
+        if (cg + 8 >= nc) load(t + 1);   // (the registers are free)
         // acc[p + 2 k]: column 2 c4 + p of block k.  One value per (query token, block)
         const int cc = c0 + cg + 2 * c4;
         if (P.pad_log2 == 0) {
@@ -352,155 +367,140 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 // ---------------------------------------------------------------------------
 // selection
 // ---------------------------------------------------------------------------
-constexpr uint32_t kMustKey = 0xffffffffu;  // a block that is always taken; 0: one that may not be
-constexpr int kSelBins = 256;
+constexpr int kSelRows = 4;                 // rows of a CTA that takes one per warp
 
 struct SelectParams {
   const float *scores;
   const int32_t *ctx_len;
+  int64_t n;          // rows: (query, KV head)
   int32_t n_q, bs, k, first, last;
-  BlockTable tab;  // (table: optional)
+  BlockTable tab;     // (table: optional)
   int32_t *sel, *sel_rows, *len_out;
   int32_t *status;
 };
 
-template <int T>
-__global__ void __launch_bounds__(T) block_select_kernel(const SelectParams P) {
-  constexpr int W = T / 32;
-  extern __shared__ uint32_t sel_smem[];
-  __shared__ uint32_t hist[kSelBins];
-  __shared__ uint32_t red[4][W];
-  __shared__ uint32_t pick[3];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t row = blockIdx.x;
-  const int bj = static_cast<int>(row / P.tab.n_kv), h = static_cast<int>(row - static_cast<int64_t>(bj) * P.tab.n_kv);
-  const int b = bj / P.n_q, j = bj - b * P.n_q;
+// W warps a row (one: kSelRows rows a CTA), R keys a thread
+template <int W, int R>
+__global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_kernel(const SelectParams P) {
+  __shared__ PickSpace<W> space[W == 1 ? kSelRows : 1];
+  __shared__ uint32_t cnt[W > 1 ? R * W : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = W == 1 ? lane : threadIdx.x;
+  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * kSelRows + warp : blockIdx.x;
+  PickSpace<W> &S = space[W == 1 ? warp : 0];
   pdl_launch_dependents();
   pdl_wait();
+  if (row >= P.n) return;
+  const int bj = static_cast<int>(row / P.tab.n_kv), h = static_cast<int>(row - static_cast<int64_t>(bj) * P.tab.n_kv);
+  const int b = bj / P.n_q, j = bj - b * P.n_q;
+  const float *src = P.scores + row * P.tab.max_blocks;
   const int ctx = held_len(P.ctx_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, P.status, j == 0 && h == 0 && tid == 0);
   const int len = max(ctx - (P.n_q - 1 - j), 0), nb = (len + P.bs - 1) / P.bs;
   if (P.len_out && h == 0 && tid == 0) P.len_out[bj] = len;
-  uint32_t *keys = sel_smem;                        // [max_blocks]
-  uint32_t *cnt = sel_smem + P.tab.max_blocks;      // [ceil(max_blocks / T) * W]
-  const float *src = P.scores + row * P.tab.max_blocks;
 
-  uint32_t n_ok = 0, n_must = 0, lo = kMustKey, hi = 0;
-  for (int i = tid; i < nb; i += T) {
-    uint32_t key;
-    if (P.tab.table && P.tab.row(b, h, i) < 0) key = 0;
-    else if (i < P.first || i >= nb - P.last) key = kMustKey;
-    else {
-      const float s = src[i];
-      key = s != s ? 1u : score_key(s);  // (a score that is NaN comes last)
-    }
-    keys[i] = key;
-    n_ok += key != 0, n_must += key == kMustKey;
-    if (key != 0 && key != kMustKey) lo = min(lo, key), hi = max(hi, key);
-  }
-  n_ok = __reduce_add_sync(~0u, n_ok), n_must = __reduce_add_sync(~0u, n_must);
-  lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
-  if (lane == 0) red[0][warp] = n_ok, red[1][warp] = n_must, red[2][warp] = lo, red[3][warp] = hi;
-  __syncthreads();
-  n_ok = n_must = hi = 0, lo = kMustKey;
+  // keys of blocks tid, tid + 32 W, ..., and what the row has
+  uint32_t key[R], n_ok = 0, n_must = 0;
+  float lo = INFINITY, hi = -INFINITY;  // of the finite scores
+  const int32_t *ids = P.tab.table ? P.tab.table + (static_cast<int64_t>(b) * P.tab.heads + (P.tab.heads > 1 ? h : 0)) * P.tab.max_blocks : nullptr;
+  {
+    float score[R];
+    int32_t id[R];
 #pragma unroll
-  for (int w = 0; w < W; ++w) n_ok += red[0][w], n_must += red[1][w], lo = min(lo, red[2][w]), hi = max(hi, red[3][w]);
+    for (int r = 0; r < R; ++r) {
+      // (volatile, and a block that is there in any case: all loads are then made before the first use,
+      // not one by one where the branches below want them, 78 us for 8000 rows of 1024 blocks)
+      const int i = min(r * W * 32 + tid, max(nb - 1, 0));
+      score[r] = 0.f, id[r] = 0;
+      if (r * W * 32 < nb) {
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(score[r]) : "l"(src + i));
+        if (ids) asm volatile("ld.global.s32 %0, [%1];" : "=r"(id[r]) : "l"(ids + i));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * W * 32 + tid;
+      key[r] = i < P.first || i >= nb - P.last ? kMustKey : score[r] != score[r] ? 1u : score_key(score[r]);  // (a NaN comes last)
+      if (i >= nb || id[r] < 0) key[r] = 0;
+      n_ok += key[r] != 0, n_must += key[r] == kMustKey;
+      if (key[r] != 0 && key[r] != kMustKey && fabsf(score[r]) < INFINITY) lo = fminf(lo, score[r]), hi = fmaxf(hi, score[r]);
+    }
+  }
+  n_ok = pick_sum(S, n_ok, 0), n_must = pick_sum(S, n_must, 1);
 
   // ----- the key above which all are taken, and how many of its equals -----
   uint32_t thr = 0, need = 0;
   if (n_ok > static_cast<uint32_t>(P.k)) {
-    uint32_t want = P.k - n_must;  // (first + last <= k)
+    const uint32_t want = P.k - n_must;  // (first + last <= k)
     thr = kMustKey - 1;
-    while (want) {  // the want-th largest of the keys in [lo, hi]
-      const uint32_t span = hi - lo;
-      const int shift = max(0, 24 - __clz(span));
-      for (int i = tid; i < kSelBins; i += T) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < nb; i += T) {
-        const uint32_t key = keys[i];
-        if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> shift], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) {  // lane l holds bins 255 - 8 l .. 248 - 8 l
-        uint32_t n[8], sum = 0;
+    if (want) {
+      lo = key_score(pick_min(S, score_key(lo), 0)), hi = key_score(~pick_min(S, ~score_key(hi), 1));
+      // 256 equal parts of the scores' range; a score that is not finite goes to an end (NaN: 0)
+      const float step = hi > lo ? kPickBins / (hi - lo) : 0.f;
+      uint32_t bins[(R + 3) / 4];       // of the thread's keys, a byte each
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = hist[kSelBins - 1 - 8 * lane - i], sum += n[i];
-        uint32_t upto = sum;
+      for (int r = 0; r < (R + 3) / 4; ++r) bins[r] = 0;
+      auto bin = [&](int r, uint32_t k) {
+        const float at = k == 1u ? 0.f : (key_score(k) - lo) * step;
+        const uint32_t x = static_cast<uint32_t>(fminf(fmaxf(at, 0.f), kPickBins - 1.f));
+        bins[r / 4] |= x << (r % 4 * 8);
+        return static_cast<int>(x);
+      };
+      auto again = [&](int r, uint32_t) { return static_cast<int>(bins[r / 4] >> (r % 4 * 8) & 255u); };
+      auto each = [&](auto &&f) {
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t x = __shfl_up_sync(~0u, upto, d);
-          if (lane >= d) upto += x;
-        }
-        uint32_t above = upto - sum;
-        if (above < want && upto >= want) {
-          int i = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i == k && above + n[k] < want) above += n[k], i = k + 1;
-          pick[0] = kSelBins - 1 - 8 * lane - i;
-          pick[1] = above;
-          pick[2] = pick_reg(n, i);
-        }
-      }
-      __syncthreads();
-      const uint32_t bin = pick[0], in = pick[2];
-      want -= pick[1];
-      lo += bin << shift;
-      const uint32_t width = (1u << shift) - 1;
-      hi = hi - lo > width ? lo + width : hi;
-      if (in == want) {          // the whole part
-        thr = lo - 1;
-        break;
-      }
-      if (shift == 0) {          // equal keys: the first of them
-        thr = lo, need = want;
-        break;
-      }
+        for (int r = 0; r < R; ++r) f(r, key[r]);
+      };
+      pick_kth(S, want, each, bin, again, thr, need);
     }
   }
 
   // ----- the blocks in order -----
-  const int rounds = (nb + T - 1) / T;
-  for (int r = 0; r < rounds; ++r) {
-    const int i = r * T + tid;
-    const uint32_t key = i < nb ? keys[i] : 0u;
-    const uint32_t gt = __ballot_sync(~0u, key > thr), eq = __ballot_sync(~0u, key == thr && key != 0);
-    if (lane == 0) cnt[r * W + warp] = __popc(gt) | __popc(eq) << 16;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t base = 0;
-    for (int r = 0; r < rounds * W; r += 32) {
-      const uint32_t x = r + lane < rounds * W ? cnt[r + lane] : 0u;
-      uint32_t upto = x;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, upto, d);
-        if (lane >= d) upto += y;
-      }
-      if (r + lane < rounds * W) cnt[r + lane] = base + upto - x;
-      base += __shfl_sync(~0u, upto, 31);
-    }
-    if (lane == 0) pick[0] = (base & 0xffffu) + min(base >> 16, need);
-  }
-  __syncthreads();
   int32_t *sel = P.sel + row * P.k, *rows = P.sel_rows ? P.sel_rows + row * P.k : nullptr;
-  for (int r = 0; r < rounds; ++r) {
-    const int i = r * T + tid;
-    const uint32_t key = i < nb ? keys[i] : 0u;
-    const bool gt = key > thr, eq = key == thr && key != 0;
-    const uint32_t below = (1u << lane) - 1, c = cnt[r * W + warp];
-    const uint32_t g = (c & 0xffffu) + __popc(__ballot_sync(~0u, gt) & below);
-    const uint32_t q = (c >> 16) + __popc(__ballot_sync(~0u, eq) & below);
-    if (gt || (eq && q < need)) {
-      const uint32_t at = g + min(q, need);
-      sel[at] = i;
-      if (rows) rows[at] = static_cast<int32_t>(P.tab.row(b, h, i));
+  const uint32_t before = (1u << lane) - 1;
+  uint32_t taken;     // above the threshold, and equal to it (upper half)
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t gt = __ballot_sync(~0u, key[r] > thr), eq = __ballot_sync(~0u, key[r] == thr && key[r] != 0);
+      if (lane == 0) cnt[r * W + warp] = __popc(gt) | __popc(eq) << 16;
     }
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t base = 0;
+      for (int r = 0; r < R * W; r += 32) {
+        const uint32_t x = cnt[r + lane];
+        uint32_t upto = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(~0u, upto, d);
+          if (lane >= d) upto += y;
+        }
+        cnt[r + lane] = base + upto - x;
+        base += __shfl_sync(~0u, upto, 31);
+      }
+      if (lane == 0) S.pick[0] = base;
+    }
+    __syncthreads();
+    taken = S.pick[0];
+  } else {
+    taken = 0;
   }
-  for (int i = pick[0] + tid; i < P.k; i += T) {
-    sel[i] = -1;
-    if (rows) rows[i] = -1;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool is_gt = key[r] > thr, is_eq = key[r] == thr && key[r] != 0;
+    const uint32_t gt = __ballot_sync(~0u, is_gt), eq = __ballot_sync(~0u, is_eq);
+    if ((gt | eq) == 0) continue;
+    const uint32_t c = W > 1 ? cnt[W > 1 ? r * W + warp : 0] : taken;
+    const uint32_t q = (c >> 16) + __popc(eq & before);
+    if (is_gt || (is_eq && q < need)) {
+      sel[(c & 0xffffu) + __popc(gt & before) + min(q, need)] = r * W * 32 + tid;
+    }
+    if constexpr (W == 1) taken += __popc(gt) | __popc(eq) << 16;
   }
+  const int n = (taken & 0xffffu) + min(taken >> 16, need);
+  for (int i = n + tid; i < P.k; i += W * 32) sel[i] = -1;
+  if (!rows) return;
+  pick_sync<W>();     // (the list is read back: looked up one by one above, each row would wait for its id)
+  for (int i = tid; i < P.k; i += W * 32) rows[i] = i < n ? static_cast<int32_t>(P.tab.row(b, h, sel[i])) : -1;
 }
 
 }  // namespace echo
@@ -523,7 +523,7 @@ static int go_summary(const echo::SummaryParams &P, cudaStream_t stream) {
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
   const int64_t most = static_cast<int64_t>(P.B) * P.tab.max_blocks * P.tab.n_kv;
-  const int64_t grid = std::min<int64_t>(most, static_cast<int64_t>(sms) * 12);
+  const int64_t grid = std::min<int64_t>(most, static_cast<int64_t>(sms) * 16);
   cudaError_t e = launch_pdl(echo::block_summary_kernel<FMT, D>, dim3(static_cast<unsigned>(grid)), dim3(echo::kSumThreads), smem, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block summary launch");
 }
@@ -562,7 +562,7 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   // a tile per warp, or more where that still leaves every SM several CTAs
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads, per_cta = echo::kScoreWarps * 16;
   const int64_t ctas = (a->max_blocks + per_cta - 1) / per_cta;
-  P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ctas, ctas * pairs / (16 * sms))));
+  P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas * pairs / (6 * sms))));
   P.ctas = static_cast<int>((ctas + P.tiles - 1) / P.tiles);
   const dim3 grid(static_cast<unsigned>(P.ctas * pairs));
   cudaError_t e = a->head_dim == 128 ? launch_pdl(echo::block_scores_kernel<128>, grid, dim3(echo::kScoreWarps * 32), 0, stream, P)
@@ -570,26 +570,29 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block scores launch");
 }
 
-template <int T>
-static int go_select(const echo::SelectParams &P, int64_t rows, cudaStream_t stream) {
-  static std::atomic<bool> attr[kMaxDevices];
-  const int64_t smem = (P.tab.max_blocks + (static_cast<int64_t>(P.tab.max_blocks) + T - 1) / T * (T / 32)) * 4;
-  if (smem > 40960)
-    if (int rr = smem_limit_once(attr, echo::block_select_kernel<T>, 212992, "block selection smem attribute")) return rr;
-  cudaError_t e = launch_pdl(echo::block_select_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(T), static_cast<size_t>(smem), stream, P);
+template <int W, int R>
+static int go_select(const echo::SelectParams &P, cudaStream_t stream) {
+  const int64_t ctas = W == 1 ? (P.n + echo::kSelRows - 1) / echo::kSelRows : P.n;
+  cudaError_t e = launch_pdl(echo::block_select_kernel<W, R>, dim3(static_cast<unsigned>(ctas)), dim3(W == 1 ? echo::kSelRows * 32 : W * 32), 0,
+                             stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block selection launch");
 }
 
 int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   echo::SelectParams P{};
   P.scores = a->scores, P.ctx_len = a->ctx_len;
+  P.n = static_cast<int64_t>(a->B) * a->n_q * a->n_kv_heads;
   P.n_q = a->n_q, P.bs = a->block_tokens, P.k = a->k, P.first = a->first, P.last = a->last;
   P.tab = {a->table, a->table_heads, a->max_blocks, a->n_kv_heads};
   P.sel = a->sel, P.sel_rows = a->sel_rows, P.len_out = a->len_out, P.status = a->dev_status;
-  const int64_t rows = static_cast<int64_t>(a->B) * a->n_q * a->n_kv_heads;
-  if (a->max_blocks <= 1024) return go_select<128>(P, rows, stream);
-  if (a->max_blocks <= 8192) return go_select<256>(P, rows, stream);
-  return go_select<1024>(P, rows, stream);
+  // the keys of a row in the registers of as few warps as hold them
+  // (few rows: 8 warps each, which have less to go through one after another)
+  int sms = 0;
+  if (int rr = sm_count(&sms)) return rr;
+  if (a->max_blocks <= 256) return go_select<1, 8>(P, stream);
+  if (a->max_blocks <= 1024) return P.n <= 4 * sms ? go_select<8, 4>(P, stream) : go_select<1, 32>(P, stream);
+  if (a->max_blocks <= 4096) return go_select<8, 16>(P, stream);
+  return go_select<32, 32>(P, stream);
 }
 
 }  // namespace echo_host
