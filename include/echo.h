@@ -695,7 +695,7 @@ int echo_block_scores(const echo_block_scores_args *args, void *stream);
 /*
  * echo_block_select: the k best blocks of each query token and KV head, of the
  * ceil(len / block_tokens) it sees (len as above): the `first` first and the `last` last ones
- * always, then by score (a NaN comes last), ties to the lower block; blocks that are not held
+ * always, then by score (a NaN counts as -inf), ties to the lower block; blocks that are not held
  * are left out (with a table).
  *   scores   [B][n_q][n_kv_heads][max_blocks] fp32 device
  *   sel      [B][n_q][n_kv_heads][k] int32 device: block indices, ascending, then -1

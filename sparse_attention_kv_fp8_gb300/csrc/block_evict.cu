@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
           a[u][k][0] = make_uint4(0u, 0u, 0u, 0u);
           if (at >= 0) {
             if constexpr (D == 128) {
-              a[u][k][0] = *reinterpret_cast<const uint4 *>(src + tk * (D / 2) + c4 * 16);
+              a[u][k][0] = load16_here(src + tk * (D / 2) + c4 * 16);
               sc[u][k] = *reinterpret_cast<const uint16_t *>(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4 * 2);
             } else {
               const uint2 y = *reinterpret_cast<const uint2 *>(src + tk * (D / 2) + c4 * 8);
@@ -120,8 +120,10 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i)
-            a[u][k][i] = at < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(src + tk * (2 * D) + i * 64 + c4 * 16);
+          for (int i = 0; i < kLoads; ++i) {
+            a[u][k][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (at >= 0) a[u][k][i] = load16_here(src + tk * (2 * D) + i * 64 + c4 * 16);
+          }
         }
       }
     }
@@ -254,6 +256,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
 // ---------------------------------------------------------------------------
 // eviction
 // ---------------------------------------------------------------------------
+constexpr uint32_t kMustKey = 0xffffffffu;  // of a token that stays in any case
 constexpr int kEvAhead = 8;           // slots a thread has under way
 constexpr int kEvStaged = 32768;      // tokens whose keys a CTA keeps in shared memory
 
@@ -419,12 +422,12 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
   } else if (n_must < static_cast<uint32_t>(P.keep)) {
     // 256 equal parts of the keys' range (a weight's exponent and leading bits) above zero
     const int shift = hi > lo ? max(0, 24 - __clz(hi - lo)) : 0;
-    auto bin = [&](int, uint32_t k) { return k <= lo ? 0 : static_cast<int>(min((k - lo) >> shift, kPickBins - 1u)); };
+    auto bin = [&](uint32_t k) { return k <= lo ? 0 : static_cast<int>(min((k - lo) >> shift, kPickBins - 1u)); };
     auto each = [&](auto &&f) {
 #pragma unroll 4
-      for (int i = tid; i < n; i += T) f(0, key_at(i));
+      for (int i = tid; i < n; i += T) f(key_at(i));
     };
-    pick_kth(S, P.keep - n_must, each, bin, bin, thr, need);
+    pick_kth(S, P.keep - n_must, each, [](uint32_t k) { return k != kMustKey; }, bin, [](uint32_t k) { return k; }, thr, need);
   }
   __syncthreads();
 

@@ -12,7 +12,6 @@
 namespace echo {
 
 constexpr int kPickBins = 256;
-constexpr uint32_t kMustKey = 0xffffffffu;  // a key that is always taken; 0: one that may not be
 
 // Scratch of a group of W warps.
 template <int W>
@@ -55,19 +54,19 @@ __device__ __forceinline__ uint32_t pick_min(PickSpace<W> &S, uint32_t x, int tu
   return x;
 }
 
-// thr and need such that the keys above thr, and the first `need` that equal it, are the `want`
-// largest (0 < want < their number) of the keys other than 0 and kMustKey.  each(f) calls f(r, key) on
-// each key of the thread, r its number; bin(r, key) in [0, kPickBins) does not fall as the key grows, and
-// again(r, key) gives the same once bin() was asked.
-template <int W, class Each, class Bin, class Again>
-__device__ __forceinline__ void pick_kth(PickSpace<W> &S, uint32_t want, Each &&each, Bin &&bin, Again &&again, uint32_t &thr,
-                                         uint32_t &need) {
+// thr and need such that the keys whose ord() lies above thr, and the first `need` whose ord() is thr,
+// are the `want` largest (0 < want < their number) of the keys that count.  each(f) calls f on each key of
+// the thread; counts(key): whether it is one of them; ord(key) orders them as whole numbers above 0;
+// bin(key) in [0, kPickBins) does not fall as ord(key) grows.
+template <int W, class Each, class Counts, class Bin, class Ord>
+__device__ __forceinline__ void pick_kth(PickSpace<W> &S, uint32_t want, Each &&each, Counts &&counts, Bin &&bin, Ord &&ord,
+                                         uint32_t &thr, uint32_t &need) {
   const int lane = threadIdx.x & 31, tid = W > 1 ? threadIdx.x : lane;
   for (int i = tid; i < kPickBins; i += W * 32) S.hist[i] = 0;
   if (tid == 0) S.n_few = 0;
   pick_sync<W>();
-  each([&](int r, uint32_t key) {
-    if (key != 0 && key != kMustKey) atomicAdd(&S.hist[bin(r, key)], 1u);
+  each([&](auto key) {
+    if (counts(key)) atomicAdd(&S.hist[bin(key)], 1u);
   });
   pick_sync<W>();
   if (W == 1 || threadIdx.x < 32) {  // lane l holds bins 255 - 8 l .. 248 - 8 l
@@ -93,10 +92,9 @@ __device__ __forceinline__ void pick_kth(PickSpace<W> &S, uint32_t want, Each &&
   const int part = S.pick[0];
   const uint32_t in = S.pick[2];
   want -= S.pick[1];
-  auto member = [&](int r, uint32_t key) { return key != 0 && key != kMustKey && again(r, key) == part; };
   if (in <= 32) {
-    each([&](int r, uint32_t key) {
-      if (member(r, key)) S.few[atomicAdd(&S.n_few, 1u)] = key;
+    each([&](auto key) {
+      if (bin(key) == part && counts(key)) S.few[atomicAdd(&S.n_few, 1u)] = ord(key);
     });
     pick_sync<W>();
     const uint32_t mine = lane < in ? S.few[lane] : 0u;   // (any order: only counts come of it)
@@ -110,9 +108,9 @@ __device__ __forceinline__ void pick_kth(PickSpace<W> &S, uint32_t want, Each &&
     need = want - __shfl_sync(~0u, above, src);
     return;
   }
-  uint32_t lo = kMustKey, hi = 0;   // the part's keys
-  each([&](int r, uint32_t key) {
-    if (member(r, key)) lo = min(lo, key), hi = max(hi, key);
+  uint32_t lo = ~0u, hi = 0;   // the part's keys
+  each([&](auto key) {
+    if (bin(key) == part && counts(key)) lo = min(lo, ord(key)), hi = max(hi, ord(key));
   });
   lo = pick_min(S, lo, 0);
   hi = ~pick_min(S, ~hi, 1);
@@ -125,7 +123,7 @@ __device__ __forceinline__ void pick_kth(PickSpace<W> &S, uint32_t want, Each &&
       return;
     }
     uint32_t c = 0;
-    each([&](int, uint32_t key) { c += key > mid && key <= hi; });
+    each([&](auto key) { c += counts(key) && ord(key) > mid && ord(key) <= hi; });
     c = pick_sum(S, c, turn);
     if (c == want) {
       thr = mid;

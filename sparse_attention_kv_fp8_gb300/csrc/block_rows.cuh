@@ -67,6 +67,14 @@ __device__ __forceinline__ uint32_t e4m3_from_half(__half x) {
   return r & 0xffu;
 }
 
+// 16 bytes, loaded where this stands: a plain load may be moved down to its first use, where one of
+// several that should be under way at once then waits for the one before
+__device__ __forceinline__ uint4 load16_here(const void *p) {
+  uint4 x;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

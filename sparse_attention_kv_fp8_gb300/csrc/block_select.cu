@@ -157,10 +157,10 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
         const int tk = min(t + r * kTokens + t0, n - 1);
         if constexpr (kFp4) {
           const uint8_t *sub = src + (tk / kSubTokens) * Fp4Sub<D>::kBytes;
-          x[r] = *reinterpret_cast<const uint4 *>(sub + (tk % kSubTokens) * (D / 2) + c * 16);
+          x[r] = load16_here(sub + (tk % kSubTokens) * (D / 2) + c * 16);
           sc[r] = *reinterpret_cast<const uint16_t *>(sub + Fp4Sub<D>::kKeyScales + (tk % kSubTokens) * (D / 16) + c * 2);
         } else {
-          x[r] = *reinterpret_cast<const uint4 *>(src + tk * (2 * D) + c * 16);
+          x[r] = load16_here(src + tk * (2 * D) + c * 16);
         }
       }
 #pragma unroll
@@ -271,7 +271,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
       there[k] = row[k] >= 0 && row[k] < P.n_rows;
       const uint8_t *src = P.summary + (there[k] ? row[k] : 0) * (4 * D) + c4 * 16;
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) a[k][i] = there[k] ? *reinterpret_cast<const uint4 *>(src + i * 64) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kChunks; ++i) {
+        a[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (there[k]) a[k][i] = load16_here(src + i * 64);
+      }
     }
     look_up(t + 1);
   };
@@ -397,12 +400,12 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   const int len = max(ctx - (P.n_q - 1 - j), 0), nb = (len + P.bs - 1) / P.bs;
   if (P.len_out && h == 0 && tid == 0) P.len_out[bj] = len;
 
-  // keys of blocks tid, tid + 32 W, ..., and what the row has
-  uint32_t key[R], n_ok = 0, n_must = 0;
-  float lo = INFINITY, hi = -INFINITY;  // of the finite scores
+  // Scores of blocks tid, tid + 32 W, ...; NaN: not to be chosen by its score (a block that is not there
+  // or not held, or one of `must`, which is taken in any case); a score that is NaN becomes -inf
+  float score[R], lo = INFINITY, hi = -INFINITY;  // (range of the finite ones)
+  uint32_t must = 0, n_ok = 0;
   const int32_t *ids = P.tab.table ? P.tab.table + (static_cast<int64_t>(b) * P.tab.heads + (P.tab.heads > 1 ? h : 0)) * P.tab.max_blocks : nullptr;
   {
-    float score[R];
     int32_t id[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -418,39 +421,37 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int i = r * W * 32 + tid;
-      key[r] = i < P.first || i >= nb - P.last ? kMustKey : score[r] != score[r] ? 1u : score_key(score[r]);  // (a NaN comes last)
-      if (i >= nb || id[r] < 0) key[r] = 0;
-      n_ok += key[r] != 0, n_must += key[r] == kMustKey;
-      if (key[r] != 0 && key[r] != kMustKey && fabsf(score[r]) < INFINITY) lo = fminf(lo, score[r]), hi = fmaxf(hi, score[r]);
+      const bool there = i < nb && id[r] >= 0, always = there && (i < P.first || i >= nb - P.last);
+      float s = score[r] == score[r] ? score[r] : -INFINITY;
+      must |= always ? 1u << r : 0u;
+      s = there && !always ? s : NAN;
+      n_ok += s == s;
+      if (fabsf(s) < INFINITY) lo = fminf(lo, s), hi = fmaxf(hi, s);
+      score[r] = s;
     }
   }
-  n_ok = pick_sum(S, n_ok, 0), n_must = pick_sum(S, n_must, 1);
+  static_assert(R <= 32, "a bit of `must` each");
+  n_ok = pick_sum(S, n_ok, 0);
+  const uint32_t n_must = pick_sum(S, __popc(must), 1);
 
-  // ----- the key above which all are taken, and how many of its equals -----
-  uint32_t thr = 0, need = 0;
-  if (n_ok > static_cast<uint32_t>(P.k)) {
-    const uint32_t want = P.k - n_must;  // (first + last <= k)
-    thr = kMustKey - 1;
-    if (want) {
-      lo = key_score(pick_min(S, score_key(lo), 0)), hi = key_score(~pick_min(S, ~score_key(hi), 1));
-      // 256 equal parts of the scores' range; a score that is not finite goes to an end (NaN: 0)
-      const float step = hi > lo ? kPickBins / (hi - lo) : 0.f;
-      uint32_t bins[(R + 3) / 4];       // of the thread's keys, a byte each
+  // ----- the score above which all are taken, and how many of its equals -----
+  const uint32_t want = P.k - n_must;  // (first + last <= k)
+  float thr = -INFINITY;
+  uint32_t need = ~0u >> 1;            // (all of them)
+  if (want == 0) {
+    thr = INFINITY, need = 0;
+  } else if (n_ok > want) {
+    lo = key_score(pick_min(S, score_key(lo), 0)), hi = key_score(~pick_min(S, ~score_key(hi), 1));
+    // 256 equal parts of the scores' range; an infinite score goes to an end
+    const float step = hi > lo ? fminf(kPickBins / (hi - lo), 3e38f) : 0.f, from = -lo * step;
+    auto each = [&](auto &&f) {
 #pragma unroll
-      for (int r = 0; r < (R + 3) / 4; ++r) bins[r] = 0;
-      auto bin = [&](int r, uint32_t k) {
-        const float at = k == 1u ? 0.f : (key_score(k) - lo) * step;
-        const uint32_t x = static_cast<uint32_t>(fminf(fmaxf(at, 0.f), kPickBins - 1.f));
-        bins[r / 4] |= x << (r % 4 * 8);
-        return static_cast<int>(x);
-      };
-      auto again = [&](int r, uint32_t) { return static_cast<int>(bins[r / 4] >> (r % 4 * 8) & 255u); };
-      auto each = [&](auto &&f) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) f(r, key[r]);
-      };
-      pick_kth(S, want, each, bin, again, thr, need);
-    }
+      for (int r = 0; r < R; ++r) f(score[r]);
+    };
+    auto bin = [&](float s) { return static_cast<int>(min(__float2uint_rz(fmaf(s, step, from)), kPickBins - 1u)); };
+    uint32_t key;
+    pick_kth(S, want, each, [](float s) { return s == s; }, bin, [](float s) { return score_key(s); }, key, need);
+    thr = key_score(key);
   }
 
   // ----- the blocks in order -----
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   if constexpr (W > 1) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t gt = __ballot_sync(~0u, key[r] > thr), eq = __ballot_sync(~0u, key[r] == thr && key[r] != 0);
+      const uint32_t gt = __ballot_sync(~0u, score[r] > thr || must >> r & 1), eq = __ballot_sync(~0u, score[r] == thr);
       if (lane == 0) cnt[r * W + warp] = __popc(gt) | __popc(eq) << 16;
     }
     __syncthreads();
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const bool is_gt = key[r] > thr, is_eq = key[r] == thr && key[r] != 0;
+    const bool is_gt = score[r] > thr || must >> r & 1, is_eq = score[r] == thr;
     const uint32_t gt = __ballot_sync(~0u, is_gt), eq = __ballot_sync(~0u, is_eq);
     if ((gt | eq) == 0) continue;
     const uint32_t c = W > 1 ? cnt[W > 1 ? r * W + warp : 0] : taken;
@@ -590,7 +591,7 @@ int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
   if (a->max_blocks <= 256) return go_select<1, 8>(P, stream);
-  if (a->max_blocks <= 1024) return P.n <= 4 * sms ? go_select<8, 4>(P, stream) : go_select<1, 32>(P, stream);
+  if (a->max_blocks <= 1024) return P.n <= 4 * sms ? go_select<8, 4>(P, stream) : go_select<4, 8>(P, stream);
   if (a->max_blocks <= 4096) return go_select<8, 16>(P, stream);
   return go_select<32, 32>(P, stream);
 }
