@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
 // eviction
 // ---------------------------------------------------------------------------
 constexpr uint32_t kMustKey = 0xffffffffu;  // of a token that stays in any case
+constexpr int kEvBins = 2048;          // parts of the weights' range
 constexpr int kEvAhead = 8;           // slots a thread has under way
 constexpr int kEvStaged = 32768;      // tokens whose keys a CTA keeps in shared memory
 
@@ -334,7 +335,7 @@ template <int FMT, int D, int T>
 __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
   constexpr int W = T / 32;
   extern __shared__ uint32_t ev_keys[];
-  __shared__ PickSpace<W> S;
+  __shared__ PickSpace<W, kEvBins> S;
   __shared__ uint32_t wcnt[2][W];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / P.n_kv, h = blockIdx.x - b * P.n_kv;
@@ -399,8 +400,9 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
 #pragma unroll
     for (int r = 0; r < kEvAhead; ++r) {
       const int i = min(i0 + r * T, n - 1);
-      x[r] = acc[i];
-      y[r] = pos ? pos[i] : 0;
+      y[r] = 0;
+      asm volatile("ld.global.f32 %0, [%1];" : "=f"(x[r]) : "l"(acc + i));   // (all under way at once)
+      if (pos) asm volatile("ld.global.s32 %0, [%1];" : "=r"(y[r]) : "l"(pos + i));
     }
 #pragma unroll
     for (int r = 0; r < kEvAhead; ++r) {
@@ -417,17 +419,18 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
 
   // ----- the key above which all stay, and how many of its equals (n > keep: some go) -----
   uint32_t thr = kMustKey - 1, need = 0;
+  bool all_equal = false;    // all that equal thr stay
   if (n_must > static_cast<uint32_t>(P.keep)) {  // (more recent positions than their number: the first slots of them)
     thr = kMustKey, need = P.keep;
   } else if (n_must < static_cast<uint32_t>(P.keep)) {
-    // 256 equal parts of the keys' range (a weight's exponent and leading bits) above zero
-    const int shift = hi > lo ? max(0, 24 - __clz(hi - lo)) : 0;
-    auto bin = [&](uint32_t k) { return k <= lo ? 0 : static_cast<int>(min((k - lo) >> shift, kPickBins - 1u)); };
+    // equal parts of the keys' range (a weight's exponent and leading bits) above zero
+    const int shift = hi > lo ? max(0, 21 - __clz(hi - lo)) : 0;
+    auto bin = [&](uint32_t k) { return k <= lo ? 0 : static_cast<int>(min((k - lo) >> shift, kEvBins - 1u)); };
     auto each = [&](auto &&f) {
 #pragma unroll 4
       for (int i = tid; i < n; i += T) f(key_at(i));
     };
-    pick_kth(S, P.keep - n_must, each, [](uint32_t k) { return k != kMustKey; }, bin, [](uint32_t k) { return k; }, thr, need);
+    all_equal = pick_kth(S, P.keep - n_must, each, [](uint32_t k) { return k != kMustKey; }, bin, [](uint32_t k) { return k; }, thr, need);
   }
   __syncthreads();
 
@@ -448,29 +451,44 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
     for (int w = 0; w < warp; ++w) before += wcnt[which][w];
     return before;
   };
-  uint32_t eq = 0;
-  for (int i = i0; i < i1; ++i) eq += key_at(i) == thr;
-  const uint32_t eq0 = scan(eq, 0);
-  auto walk = [&](auto &&hole, auto &&mover) {
-    uint32_t e = eq0;
-    for (int i = i0; i < i1; ++i) {
+  uint32_t eq0 = 0;
+  if (!all_equal) {
+    uint32_t eq = 0;
+    for (int i = i0; i < i1; ++i) eq += key_at(i) == thr;
+    eq0 = scan(eq, 0);
+  }
+  // f(i, whether it stays) for each slot of the run
+  auto walk = [&](int from, int to, auto &&f) {
+    for (int i = from; i < to; ++i) {
       const uint32_t key = key_at(i);
-      const bool stays = key > thr || (key == thr && e < need);
-      e += key == thr;
-      if (i < P.keep) {
-        if (!stays) hole(i);
-      } else if (stays) {
-        mover(i);
-      }
+      f(i, key > thr || (key == thr && (all_equal || eq0 < need)));
+      eq0 += key == thr;
     }
   };
+  // (as bits, 64 slots of a run at a time: all of it where keys are in shared memory)
   uint32_t holes = 0, movers = 0;
-  walk([&](int) { ++holes; }, [&](int) { ++movers; });
+  const uint32_t eq_first = eq0;
+  uint64_t marks = 0;       // of the first 64 slots: a hole, or a mover
+  walk(i0, i1, [&](int i, bool stays) {
+    const bool mark = stays == (i >= P.keep);
+    if (mark && i - i0 < 64) marks |= 1ull << (i - i0);
+    holes += mark && i < P.keep, movers += mark && i >= P.keep;
+  });
   uint32_t hole_at = scan(holes, 1);
   __syncthreads();
   uint32_t mover_at = scan(movers, 0);
   int2 *list = P.list + static_cast<int64_t>(blockIdx.x) * P.keep;
-  walk([&](int i) { list[hole_at++].y = i; }, [&](int i) { list[mover_at++].x = i; });
+  auto note = [&](int i) {
+    if (i < P.keep) list[hole_at++].y = i;
+    else list[mover_at++].x = i;
+  };
+  for (; marks; marks &= marks - 1) note(i0 + __ffsll(marks) - 1);
+  if (i1 - i0 > 64) {       // (longer runs: looked at once more)
+    eq0 = eq_first;
+    walk(i0, i1, [&](int i, bool stays) {
+      if (i - i0 >= 64 && stays == (i >= P.keep)) note(i);
+    });
+  }
   __syncthreads();
   uint32_t count = 0;
 #pragma unroll

@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 // ---------------------------------------------------------------------------
 // selection
 // ---------------------------------------------------------------------------
+constexpr int kSelBins = 256;               // parts of a row's range of scores
 constexpr int kSelRows = 4;                 // rows of a CTA that takes one per warp
 
 struct SelectParams {
@@ -385,11 +386,11 @@ struct SelectParams {
 // W warps a row (one: kSelRows rows a CTA), R keys a thread
 template <int W, int R>
 __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_kernel(const SelectParams P) {
-  __shared__ PickSpace<W> space[W == 1 ? kSelRows : 1];
+  __shared__ PickSpace<W, kSelBins> space[W == 1 ? kSelRows : 1];
   __shared__ uint32_t cnt[W > 1 ? R * W : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = W == 1 ? lane : threadIdx.x;
   const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * kSelRows + warp : blockIdx.x;
-  PickSpace<W> &S = space[W == 1 ? warp : 0];
+  auto &S = space[W == 1 ? warp : 0];
   pdl_launch_dependents();
   pdl_wait();
   if (row >= P.n) return;
@@ -443,12 +444,12 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   } else if (n_ok > want) {
     lo = key_score(pick_min(S, score_key(lo), 0)), hi = key_score(~pick_min(S, ~score_key(hi), 1));
     // 256 equal parts of the scores' range; an infinite score goes to an end
-    const float step = hi > lo ? fminf(kPickBins / (hi - lo), 3e38f) : 0.f, from = -lo * step;
+    const float step = hi > lo ? fminf(kSelBins / (hi - lo), 3e38f) : 0.f, from = -lo * step;
     auto each = [&](auto &&f) {
 #pragma unroll
       for (int r = 0; r < R; ++r) f(score[r]);
     };
-    auto bin = [&](float s) { return static_cast<int>(min(__float2uint_rz(fmaf(s, step, from)), kPickBins - 1u)); };
+    auto bin = [&](float s) { return static_cast<int>(min(__float2uint_rz(fmaf(s, step, from)), kSelBins - 1u)); };
     uint32_t key;
     pick_kth(S, want, each, [](float s) { return s == s; }, bin, [](float s) { return score_key(s); }, key, need);
     thr = key_score(key);
