@@ -289,44 +289,79 @@ __device__ __forceinline__ int64_t ev_row(const EvictParams &P, int b, int h, in
   return id < 0 ? -1 : P.table_heads > 1 ? id : static_cast<int64_t>(id) * P.n_kv + h;
 }
 
-// One token's key and value from slot m.x to slot m.y, by a warp.
+// The keys and values of tokens list[first] .. list[first + 7] (of `count`) from slot x to slot y, by a
+// warp: a lane looks up a token's places, then all loads are under way before the first store.
+constexpr int kMoveAhead = 8;
+
 template <int FMT, int D>
-__device__ __forceinline__ void move_token(const EvictParams &P, int b, int h, int2 m, int lane) {
-  int o0, o1;
-  const int64_t r0 = ev_row(P, b, h, m.x, o0), r1 = ev_row(P, b, h, m.y, o1);
-  if (r0 < 0 || r1 < 0 || r0 >= P.n_rows || r1 >= P.n_rows) {
-    if (lane == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
-    return;
+__device__ __forceinline__ void move_tokens(const EvictParams &P, int b, int h, const int2 *list, int first, int count, int lane) {
+  constexpr bool kFp4 = FMT == ECHO_BLOCK_FP4;
+  // bytes from the start of `rows` to the token's key (bf16) or to its sub-block (4 bits; the token in
+  // the lowest 4 bits, which are zeros otherwise), -1: not to be moved
+  int64_t from = -1, to = -1;
+  if (lane < kMoveAhead && first + lane < count) {
+    const int2 m = list[first + lane];
+    int o0, o1;
+    const int64_t r0 = ev_row(P, b, h, m.x, o0), r1 = ev_row(P, b, h, m.y, o1);
+    if (r0 < 0 || r1 < 0 || r0 >= P.n_rows || r1 >= P.n_rows) {
+      set_status(P.status, ECHO_DEV_BAD_INDEX);
+    } else if constexpr (kFp4) {
+      from = r0 * P.row_bytes + o0 / kSubTokens * Fp4Sub<D>::kBytes + o0 % kSubTokens;
+      to = r1 * P.row_bytes + o1 / kSubTokens * Fp4Sub<D>::kBytes + o1 % kSubTokens;
+    } else {
+      from = r0 * P.row_bytes + o0 * (2 * D);
+      to = r1 * P.row_bytes + o1 * (2 * D);
+    }
   }
-  const uint8_t *src = P.rows + r0 * P.row_bytes;
-  uint8_t *dst = P.rows + r1 * P.row_bytes;
-  if constexpr (FMT == ECHO_BLOCK_FP4) {
-    const int t0 = o0 % kSubTokens, t1 = o1 % kSubTokens;
-    src += (o0 / kSubTokens) * Fp4Sub<D>::kBytes, dst += (o1 / kSubTokens) * Fp4Sub<D>::kBytes;
-    if (lane < 8) {                 // a part of the value codes, D / 16 bytes
-      const uint8_t *s = src + Fp4Sub<D>::kValues + ((t0 >> 3) * 64 + lane * 8 + (t0 & 7)) * (D / 16);
-      uint8_t *d = dst + Fp4Sub<D>::kValues + ((t1 >> 3) * 64 + lane * 8 + (t1 & 7)) * (D / 16);
-      if constexpr (D == 128) *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(s);
-      else *reinterpret_cast<uint32_t *>(d) = *reinterpret_cast<const uint32_t *>(s);
-    } else if (lane < 8 + D / 16) { // a value scale, a byte
-      const int g = lane - 8;
-      dst[Fp4Sub<D>::kValueScales + (t1 >> 3) * (D / 2) + g * 8 + (t1 & 7)] =
-          src[Fp4Sub<D>::kValueScales + (t0 >> 3) * (D / 2) + g * 8 + (t0 & 7)];
-    } else if (lane < 16 + D / 32 && lane >= 16) {  // key codes
-      const int i = lane - 16;
-      *reinterpret_cast<uint4 *>(dst + t1 * (D / 2) + i * 16) = *reinterpret_cast<const uint4 *>(src + t0 * (D / 2) + i * 16);
-    } else if (lane == 31) {        // key scales
-      const uint8_t *s = src + Fp4Sub<D>::kKeyScales + t0 * (D / 16);
-      uint8_t *d = dst + Fp4Sub<D>::kKeyScales + t1 * (D / 16);
-      if constexpr (D == 128) *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(s);
-      else *reinterpret_cast<uint32_t *>(d) = *reinterpret_cast<const uint32_t *>(s);
+  if constexpr (kFp4) {
+    static_assert(Fp4Sub<D>::kBytes % 16 == 0, "a token's number fits under a sub-block's place");
+    // lanes 0-7: a part of the value codes each, D / 16 bytes; from 8: a value scale each; from 16: key
+    // codes, 16 bytes each; 31: the key scales
+    auto place = [&](int64_t at) -> uint8_t * {
+      const int t = static_cast<int>(at & 15);
+      uint8_t *sub = P.rows + (at - t);
+      if (lane < 8) return sub + Fp4Sub<D>::kValues + ((t >> 3) * 64 + lane * 8 + (t & 7)) * (D / 16);
+      if (lane < 16) return sub + Fp4Sub<D>::kValueScales + (t >> 3) * (D / 2) + (lane - 8) * 8 + (t & 7);
+      if (lane < 31) return sub + t * (D / 2) + (lane - 16) * 16;
+      return sub + Fp4Sub<D>::kKeyScales + t * (D / 16);
+    };
+    const bool bytes16 = lane >= 16 && lane < 16 + D / 32, scale = lane >= 8 && lane < 8 + D / 16, part = lane < 8 || lane == 31;
+    uint4 x[kMoveAhead];
+#pragma unroll
+    for (int u = 0; u < kMoveAhead; ++u) {
+      const int64_t at = __shfl_sync(~0u, from, u);
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at < 0) continue;
+      const uint8_t *s = place(at);
+      if (bytes16) x[u] = *reinterpret_cast<const uint4 *>(s);
+      else if (scale) x[u].x = *s;
+      else if (part && D == 128) *reinterpret_cast<uint2 *>(&x[u]) = *reinterpret_cast<const uint2 *>(s);
+      else if (part) x[u].x = *reinterpret_cast<const uint32_t *>(s);
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveAhead; ++u) {
+      const int64_t at = __shfl_sync(~0u, to, u);
+      if (at < 0) continue;
+      uint8_t *d = place(at);
+      if (bytes16) *reinterpret_cast<uint4 *>(d) = x[u];
+      else if (scale) *d = static_cast<uint8_t>(x[u].x);
+      else if (part && D == 128) *reinterpret_cast<uint2 *>(d) = make_uint2(x[u].x, x[u].y);
+      else if (part) *reinterpret_cast<uint32_t *>(d) = x[u].x;
     }
   } else {
     constexpr int kHalf = D / 8;    // 16-byte pieces of a key
-    if (lane < 2 * kHalf) {
-      const int64_t v = lane < kHalf ? 0 : static_cast<int64_t>(P.bsub) * kSubTokens * D * 2;
-      const int i = lane < kHalf ? lane : lane - kHalf;
-      *reinterpret_cast<uint4 *>(dst + v + o1 * (2 * D) + i * 16) = *reinterpret_cast<const uint4 *>(src + v + o0 * (2 * D) + i * 16);
+    const int64_t piece = lane < kHalf ? lane * 16 : static_cast<int64_t>(P.bsub) * kSubTokens * D * 2 + (lane - kHalf) * 16;
+    uint4 x[kMoveAhead];
+#pragma unroll
+    for (int u = 0; u < kMoveAhead; ++u) {
+      const int64_t at = __shfl_sync(~0u, from, u);
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at >= 0 && lane < 2 * kHalf) x[u] = load16_here(P.rows + at + piece);
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveAhead; ++u) {
+      const int64_t at = __shfl_sync(~0u, to, u);
+      if (at >= 0 && lane < 2 * kHalf) *reinterpret_cast<uint4 *>(P.rows + at + piece) = x[u];
     }
   }
 }
@@ -505,7 +540,7 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
     if (pos_out) pos_out[m.y] = pos_of(m.x);
   }
   if (P.move_here)
-    for (uint32_t i = warp; i < count; i += W) move_token<FMT, D>(P, b, h, list[i], lane);
+    for (int i = warp * kMoveAhead; i < static_cast<int>(count); i += W * kMoveAhead) move_tokens<FMT, D>(P, b, h, list, i, count, lane);
 }
 
 constexpr int kMvWarps = 8;
@@ -518,8 +553,8 @@ __global__ void __launch_bounds__(kMvWarps * 32) block_move_kernel(const EvictPa
   pdl_wait();
   const int count = P.moves[pair];
   const int2 *list = P.list + static_cast<int64_t>(pair) * P.keep;
-  for (int i = part * kMvWarps + (threadIdx.x >> 5); i < count; i += P.move_ctas * kMvWarps)
-    move_token<FMT, D>(P, b, h, list[i], threadIdx.x & 31);
+  for (int i = (part * kMvWarps + (threadIdx.x >> 5)) * kMoveAhead; i < count; i += P.move_ctas * kMvWarps * kMoveAhead)
+    move_tokens<FMT, D>(P, b, h, list, i, count, threadIdx.x & 31);
 }
 
 }  // namespace echo
@@ -583,7 +618,7 @@ static int go_evict(echo::EvictParams P, cudaStream_t stream) {
   if (int rr = evict_sms(&sms)) return rr;
   const int64_t moves = std::max<int64_t>(0, std::min<int64_t>(P.keep, most - P.keep));
   P.move_here = moves <= 256;
-  P.move_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((moves + 31) / 32, 16ll * sms / pairs)));
+  P.move_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((moves + 63) / 64, 8ll * sms / pairs)));
   cudaError_t e = wide ? launch_pdl(echo::block_evict_kernel<FMT, D, 1024>, dim3(static_cast<unsigned>(pairs)), dim3(1024), smem, stream, P)
                        : launch_pdl(echo::block_evict_kernel<FMT, D, 512>, dim3(static_cast<unsigned>(pairs)), dim3(512), smem, stream, P);
   if (e == cudaSuccess && !P.move_here)
