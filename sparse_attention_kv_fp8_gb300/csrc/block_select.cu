@@ -131,7 +131,12 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
   const int64_t units = static_cast<int64_t>(sum_cu[P.B]) * P.tab.n_kv;
 
   const int t0 = tid / kLanes, c = tid % kLanes;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  // where a (block, KV head) lies and how many tokens it has; row -1: past the end, or not there
+  int64_t row = -1, next_row = -1;
+  int n = 0, next_n = 0;
+  auto look_up = [&](int64_t u) {
+    next_row = -1;
+    if (u >= units) return;
     const int line = static_cast<int>(u / P.tab.n_kv), h = static_cast<int>(u - static_cast<int64_t>(line) * P.tab.n_kv);
     int b = 0, end = P.B;
     while (end - b > 1) {
@@ -140,11 +145,18 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
       else end = mid;
     }
     const int e = redone(P, b, false).x + line - sum_cu[b];
-    const int64_t row = P.tab.row(b, h, e);
-    if (row >= P.n_rows && tid == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
-    if (row < 0 || row >= P.n_rows) continue;  // (the same for the whole CTA)
-    // tokens of the block (rounds past the last one read it again: a minimum does not mind)
-    const int n = min(P.bs, held_len(P.new_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, nullptr, false) - e * P.bs);
+    next_row = P.tab.row(b, h, e);
+    next_n = min(P.bs, held_len(P.new_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, nullptr, false) - e * P.bs);
+  };
+  look_up(blockIdx.x);
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    row = next_row, n = next_n;
+    if (row < 0 || row >= P.n_rows) {  // (the same for the whole CTA)
+      if (row >= 0 && tid == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
+      look_up(u + gridDim.x);
+      continue;
+    }
+    // (rounds past the last token read it again: a minimum does not mind)
     const uint8_t *src = P.rows + row * P.row_bytes;
     uint32_t lo[kWords], hi[kWords];
 #pragma unroll
@@ -163,6 +175,7 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
           x[r] = load16_here(src + tk * (2 * D) + c * 16);
         }
       }
+      if (t == 0) look_up(u + gridDim.x);  // (while the loads are under way)
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
         const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
@@ -243,8 +256,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   constexpr int kChunks = D / 16;           // 16-byte pieces of a summary row that a lane holds
   __shared__ __align__(16) uint8_t qs[kScoreCols * kStride];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
-  const int pair = blockIdx.x / P.ctas, part = blockIdx.x - pair * P.ctas;
-  const int b = pair / P.tab.n_kv, h = pair - b * P.tab.n_kv;
+  // (the KV heads of the same blocks beside one another: their rows are neighbours in memory)
+  const int bp = blockIdx.x / P.tab.n_kv, h = blockIdx.x - bp * P.tab.n_kv;
+  const int b = bp / P.ctas, part = bp - b * P.ctas;
   pdl_launch_dependents();
   pdl_wait();
   const int len = held_len(P.ctx_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, P.status,
