@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
             a[u][k][i] = make_uint4(0u, 0u, 0u, 0u);
-            if (at >= 0) a[u][k][i] = load16_here(src + tk * (2 * D) + i * 64 + c4 * 16);
+            if (at >= 0) a[u][k][i] = load16_here(src + tk * (2 * D) + (i / 2 * 8 + c4 * 2 + i % 2) * 16);
           }
         }
       }
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
     const int nc = min(kWtCols, rows_q - c0), nc8 = (nc + 7) & ~7;
     if (s0 < s1) load(s0);   // (under way while the queries are laid out)
     if (c0) __syncthreads();
-    // the queries as columns: piece 4 i + c holds what lane c of a quad feeds with its i-th piece
+    // the queries as columns: piece 4 i + c holds what lane c of a quad feeds with its i-th piece.
     for (int i = warp; i < nc8; i += kWtWarps) {   // a column per warp
       const int rq = c0 + i, j = rq / P.group;
       const int64_t at = (static_cast<int64_t>(b) * P.n_q + j) * P.n_heads + h * P.group + rq - j * P.group;
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
         const int c = 4 * lane / (D / 4), k = (4 * lane % (D / 4)) / 8;  // lane c reads dims c D / 4 and up
         piece = 4 * k + c;
       } else {
-        piece = lane / 2;                         // piece 4 i + c: dims 32 i + 8 c and up
+        const int d8 = lane / 2;                  // lane c reads 32 bytes (a sector) of every 128, in two pieces
+        piece = 4 * (d8 / 8 * 2 + d8 % 2) + d8 % 8 / 2;
       }
       x.x ^= P.q_sign, x.y ^= P.q_sign;
       if (lane < D / 4) *reinterpret_cast<uint2 *>(qs + i * kStride + piece * 16 + (lane & 1) * 8) = x;
@@ -585,7 +586,7 @@ int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream) 
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads;
   const int64_t nsub = static_cast<int64_t>(a->max_blocks) * P.bsub;
   // two sub-blocks a warp, or more where every SM still has several CTAs
-  P.subs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, nsub * pairs / (2 * echo::kWtWarps * 24ll * sms))) * 2);
+  P.subs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, nsub * pairs / (2 * echo::kWtWarps * 48ll * sms))) * 2);
   P.ctas = static_cast<int>((nsub + echo::kWtWarps * P.subs - 1) / (echo::kWtWarps * P.subs));
   const dim3 grid(static_cast<unsigned>(P.ctas * pairs)), block(echo::kWtWarps * 32);
   cudaError_t e;

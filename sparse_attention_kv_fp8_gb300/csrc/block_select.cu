@@ -283,11 +283,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
     for (int k = 0; k < 2; ++k) {
       if (row[k] >= P.n_rows) set_status(P.status, ECHO_DEV_BAD_INDEX);
       there[k] = row[k] >= 0 && row[k] < P.n_rows;
-      const uint8_t *src = P.summary + (there[k] ? row[k] : 0) * (4 * D) + c4 * 16;
+      const uint8_t *src = P.summary + (there[k] ? row[k] : 0) * (4 * D) + c4 * 32;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         a[k][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (there[k]) a[k][i] = load16_here(src + i * 64);
+        if (there[k]) a[k][i] = load16_here(src + i / 2 * 128 + i % 2 * 16);
       }
     }
     look_up(t + 1);
@@ -315,8 +315,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
         const uint32_t neg = ((w[k] >> 15) & 0x10001u) * 0xffffu;  // all ones in the halves below zero
         n[k] = w[k] & neg, w[k] &= ~neg;
       }
-      *reinterpret_cast<uint4 *>(qs + col * kStride + d8 * 16) = make_uint4(n[0], n[1], n[2], n[3]);
-      *reinterpret_cast<uint4 *>(qs + col * kStride + 2 * D + d8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      // piece 4 i + c is what lane c of a quad feeds with its i-th: it reads 32 bytes (a sector) of every 128
+      uint8_t *dst = qs + col * kStride + (4 * (d8 / 8 * 2 + d8 % 2) + d8 % 8 / 2) * 16;
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(n[0], n[1], n[2], n[3]);
+      *reinterpret_cast<uint4 *>(dst + 2 * D) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncthreads();
     for (int t = 0; t < P.tiles; ++t) {
@@ -578,7 +580,7 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   // a tile per warp, or more where that still leaves every SM several CTAs
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads, per_cta = echo::kScoreWarps * 16;
   const int64_t ctas = (a->max_blocks + per_cta - 1) / per_cta;
-  P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas * pairs / (6 * sms))));
+  P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas * pairs / (12 * sms))));
   P.ctas = static_cast<int>((ctas + P.tiles - 1) / P.tiles);
   const dim3 grid(static_cast<unsigned>(P.ctas * pairs));
   cudaError_t e = a->head_dim == 128 ? launch_pdl(echo::block_scores_kernel<128>, grid, dim3(echo::kScoreWarps * 32), 0, stream, P)
