@@ -427,20 +427,21 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
 
     // the queries of this warp's 32 rows: D / 8 lanes a row, 16 bytes each
     auto load_q = [&]() {
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 32 / kPer;
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 8;
       const int n = L.sub_rows(s), d8 = lane % kLanes, mine = w4 * 32 + lane;
       const int64_t at = mine < n ? px_out_row(P, L, L.t * kPxRows + s * 128 + mine) : -1;
-      {
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += kAhead * kPer) {
         uint4 x[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int64_t from = __shfl_sync(~0u, at, u * kPer + lane / kLanes);
+          const int64_t from = __shfl_sync(~0u, at, r0 + u * kPer + lane / kLanes);
           x[u] = make_uint4(0u, 0u, 0u, 0u);
           if (from >= 0) x[u] = *reinterpret_cast<const uint4 *>(P.q + from * D + d8 * 8);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int r = w4 * 32 + u * kPer + lane / kLanes;
+          const int r = w4 * 32 + r0 + u * kPer + lane / kLanes;
           uint32_t v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
           if constexpr (F16) {  // scaled by the power of two that brings the row's largest entry to [1, 2)
             float m = 0.f;
@@ -961,7 +962,7 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = first_x[k];
   }
-  constexpr int kAhead = RW > 1 ? 6 : 8;
+  constexpr int kAhead = RW > 1 ? 6 : 4;
   for (int p0 = 1 + mine_of; p0 < pieces; p0 += kAhead * RW) {   // pieces p0, p0 + RW, ...
     float2 ml[kAhead];
     float x[kAhead][kPer];
