@@ -613,7 +613,7 @@ static int go_evict(echo::EvictParams P, cudaStream_t stream) {
   const int smem = P.staged ? static_cast<int>(most) * 4 : 0;
   // (threads by the slots a pair may have: 512 CTAs' worth of either is on the device at once)
   const bool wide = most > 8192;
-  if (smem > 40960)
+  if (smem > 32768)   // (beside 9 KB of its own)
     if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D, 1024>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
   int sms = 0;
   if (int rr = evict_sms(&sms)) return rr;

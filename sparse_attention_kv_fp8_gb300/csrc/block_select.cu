@@ -95,10 +95,12 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
   constexpr bool kFp4 = FMT == ECHO_BLOCK_FP4;
   constexpr int kWords = kFp4 ? 16 : 4;               // pairs of dims that a thread holds
   constexpr int kLanes = D / (2 * kWords);            // threads of a token
-  constexpr int kTokens = kSumThreads / kLanes;       // tokens a round
-  constexpr int kRounds = kFp4 ? 2 : 8;               // rounds of loads in flight
+  constexpr int kTeam = kFp4 ? 32 : kSumThreads;      // threads of a block: a warp has 64 4-bit keys in flight
+  constexpr int kTeams = kSumThreads / kTeam;
+  constexpr int kTokens = kTeam / kLanes;             // tokens a round
+  constexpr int kRounds = 8;                          // rounds of loads in flight
   extern __shared__ int32_t sum_cu[];                 // [B + 1] exclusive sums of the redone blocks
-  __shared__ uint32_t part[4][2][D / 2];
+  __shared__ uint32_t part[kFp4 ? 1 : 4][2][D / 2];
   __shared__ int32_t wsum[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
   __syncthreads();
   const int64_t units = static_cast<int64_t>(sum_cu[P.B]) * P.tab.n_kv;
 
-  const int t0 = tid / kLanes, c = tid % kLanes;
+  const int t0 = tid % kTeam / kLanes, c = tid % kLanes;
   // where a (block, KV head) lies and how many tokens it has; row -1: past the end, or not there
   int64_t row = -1, next_row = -1;
   int n = 0, next_n = 0;
@@ -148,12 +150,13 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
     next_row = P.tab.row(b, h, e);
     next_n = min(P.bs, held_len(P.new_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, nullptr, false) - e * P.bs);
   };
-  look_up(blockIdx.x);
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kTeams + tid / kTeam, stride = static_cast<int64_t>(gridDim.x) * kTeams;
+  look_up(u0);
+  for (int64_t u = u0; u < units; u += stride) {
     row = next_row, n = next_n;
-    if (row < 0 || row >= P.n_rows) {  // (the same for the whole CTA)
-      if (row >= 0 && tid == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
-      look_up(u + gridDim.x);
+    if (row < 0 || row >= P.n_rows) {  // (the same for the whole team)
+      if (row >= 0 && tid % kTeam == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
+      look_up(u + stride);
       continue;
     }
     // (rounds past the last token read it again: a minimum does not mind)
@@ -168,16 +171,18 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
       for (int r = 0; r < kRounds; ++r) {
         const int tk = min(t + r * kTokens + t0, n - 1);
         if constexpr (kFp4) {
+          if (t + r * kTokens >= n) break;
           const uint8_t *sub = src + (tk / kSubTokens) * Fp4Sub<D>::kBytes;
           x[r] = load16_here(sub + (tk % kSubTokens) * (D / 2) + c * 16);
-          sc[r] = *reinterpret_cast<const uint16_t *>(sub + Fp4Sub<D>::kKeyScales + (tk % kSubTokens) * (D / 16) + c * 2);
+          sc[r] = load2_here(sub + Fp4Sub<D>::kKeyScales + (tk % kSubTokens) * (D / 16) + c * 2);
         } else {
           x[r] = load16_here(src + tk * (2 * D) + c * 16);
         }
       }
-      if (t == 0) look_up(u + gridDim.x);  // (while the loads are under way)
+      if (t == 0) look_up(u + stride);  // (while the loads are under way)
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
+        if (kFp4 && t + r * kTokens >= n) break;
         const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
         if constexpr (kFp4) {
           const uint32_t s2 = e4m3x2_to_half2(sc[r]);
@@ -199,30 +204,59 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
         }
       }
     }
+    if constexpr (kFp4) {
+      // Joined over the lanes of the same dims, each of which hands half of its words over and keeps the
+      // other: minima, and maxima as minima of what is less, first (28 shuffles a lane, not 96).  What is
+      // left are D / 32 words from word `at` on: one store.
+      constexpr int kLeft = 32 / kTokens;
+      const uint32_t flip = lane & 16 ? 0x80008000u : 0u;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i)
-#pragma unroll
-      for (int d = kLanes; d < 32; d <<= 1) {
-        lo[i] = min2<FMT>(lo[i], __shfl_xor_sync(~0u, lo[i], d));
-        hi[i] = max2<FMT>(hi[i], __shfl_xor_sync(~0u, hi[i], d));
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t less = hi[i] ^ 0x80008000u, give = lane & 16 ? lo[i] : less;
+        lo[i] = min2<FMT>(lane & 16 ? less : lo[i], __shfl_xor_sync(~0u, give, 16));
       }
-    if (lane < kLanes) {
+      int at = c * kWords;
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) part[warp][0][c * kWords + i] = lo[i], part[warp][1][c * kWords + i] = hi[i];
-    }
-    __syncthreads();
-    if (tid < D) {
-      const int m = tid / (D / 2), i = tid % (D / 2);
-      uint32_t v = part[0][m][i];
+      for (int d = 8, k = kWords / 2; d >= kLanes; d >>= 1, k >>= 1) {
 #pragma unroll
-      for (int w = 1; w < 4; ++w) v = m ? max2<FMT>(v, part[w][m][i]) : min2<FMT>(v, part[w][m][i]);
-      if constexpr (kFp4) {  // (6 significant bits: exact in bf16, a power of two less too)
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
-        v = pack2<false>(f.x * P.k_scale, f.y * P.k_scale);
+        for (int i = 0; i < k; ++i) {
+          const uint32_t give = lane & d ? lo[i] : lo[i + k];
+          lo[i] = min2<FMT>(lane & d ? lo[i + k] : lo[i], __shfl_xor_sync(~0u, give, d));
+        }
+        if (lane & d) at += k;
       }
-      P.summary[row * D + tid] = v;
+      uint32_t v[kLeft];
+#pragma unroll
+      for (int i = 0; i < kLeft; ++i) {  // (6 significant bits: exact in bf16, a power of two less too)
+        const uint32_t y = lo[i] ^ flip;
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+        v[i] = pack2<false>(f.x * P.k_scale, f.y * P.k_scale);
+      }
+      uint32_t *dst = P.summary + row * D + (lane & 16 ? D / 2 : 0) + at;
+      if constexpr (kLeft == 4) *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+      else *reinterpret_cast<uint2 *>(dst) = make_uint2(v[0], v[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int d = kLanes; d < 32; d <<= 1) {
+          lo[i] = min2<FMT>(lo[i], __shfl_xor_sync(~0u, lo[i], d));
+          hi[i] = max2<FMT>(hi[i], __shfl_xor_sync(~0u, hi[i], d));
+        }
+      if (lane < kLanes) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) part[warp][0][c * kWords + i] = lo[i], part[warp][1][c * kWords + i] = hi[i];
+      }
+      __syncthreads();
+      if (tid < D) {
+        const int m = tid / (D / 2), i = tid % (D / 2);
+        uint32_t v = part[0][m][i];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) v = m ? max2<FMT>(v, part[w][m][i]) : min2<FMT>(v, part[w][m][i]);
+        P.summary[row * D + tid] = v;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -243,7 +277,8 @@ struct ScoreParams {
   int32_t cols;           // columns of a KV head, a multiple of 8
   int32_t wide;           // columns of a query token where the group has more than 8 heads
   int32_t chunk;          // columns laid out at a time: whole query tokens if they fit
-  int32_t ctas, tiles;    // CTAs of a (b, h), 16-block tiles that a warp of one takes
+  int32_t ctas, tiles;    // CTAs along the blocks of a (b, h), 16-block tiles that a warp of one takes
+  int32_t parts, span;    // CTAs along its columns, columns that one takes (whole chunks)
   float scale;            // |scale|
   uint32_t q_sign;
   float *scores;
@@ -258,12 +293,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
   // (the KV heads of the same blocks beside one another: their rows are neighbours in memory)
   const int bp = blockIdx.x / P.tab.n_kv, h = blockIdx.x - bp * P.tab.n_kv;
-  const int b = bp / P.ctas, part = bp - b * P.ctas;
+  const int line = bp / P.parts, c_from = (bp - line * P.parts) * P.span;
+  const int b = line / P.ctas, part = line - b * P.ctas;
   pdl_launch_dependents();
   pdl_wait();
   const int len = held_len(P.ctx_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, P.status,
-                           part == 0 && h == 0 && threadIdx.x == 0);
-  const int blocks = (len + P.bs - 1) / P.bs;
+                           part == 0 && h == 0 && c_from == 0 && threadIdx.x == 0);
+  const int blocks = (len + P.bs - 1) / P.bs, c_end = min(c_from + P.span, P.cols);
   const int first = part * (kScoreWarps * 16) * P.tiles;
   if (first >= blocks) return;
 
@@ -293,11 +329,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
     look_up(t + 1);
   };
 
-  for (int c0 = 0; c0 < P.cols; c0 += P.chunk) {
-    const int nc = min(P.chunk, P.cols - c0);
+  for (int c0 = c_from; c0 < c_end; c0 += P.chunk) {
+    const int nc = min(P.chunk, c_end - c0);
     look_up(0);
     load(0);     // (under way while the queries are laid out)
-    if (c0) __syncthreads();
+    if (c0 != c_from) __syncthreads();
     // [q-, q+] of the columns; a group's last head fills its padding (a maximum does not mind)
     for (int i = threadIdx.x; i < nc * (D / 8); i += kScoreWarps * 32) {
       const int col = i / (D / 8), d8 = i % (D / 8), cc = c0 + col;
@@ -541,7 +577,8 @@ static int go_summary(const echo::SummaryParams &P, cudaStream_t stream) {
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
   const int64_t most = static_cast<int64_t>(P.B) * P.tab.max_blocks * P.tab.n_kv;
-  const int64_t grid = std::min<int64_t>(most, static_cast<int64_t>(sms) * 16);
+  const int64_t ctas = FMT == ECHO_BLOCK_FP4 ? (most + 3) / 4 : most;   // (4 bits: a warp per block)
+  const int64_t grid = std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 16);
   cudaError_t e = launch_pdl(echo::block_summary_kernel<FMT, D>, dim3(static_cast<unsigned>(grid)), dim3(echo::kSumThreads), smem, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block summary launch");
 }
@@ -582,7 +619,12 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   const int64_t ctas = (a->max_blocks + per_cta - 1) / per_cta;
   P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas * pairs / (12 * sms))));
   P.ctas = static_cast<int>((ctas + P.tiles - 1) / P.tiles);
-  const dim3 grid(static_cast<unsigned>(P.ctas * pairs));
+  // columns (a prompt's query tokens) over several CTAs where blocks and heads give the SMs too few; a
+  // token whose heads do not fit one chunk stays with one thread, which joins them
+  const int64_t chunks = (P.cols + P.chunk - 1) / P.chunk, want = (12ll * sms + P.ctas * pairs - 1) / (P.ctas * pairs);
+  const int64_t each = P.wide > echo::kScoreCols ? chunks : (chunks + std::min(chunks, want) - 1) / std::min(chunks, want);
+  P.span = static_cast<int>(each * P.chunk), P.parts = static_cast<int>((chunks + each - 1) / each);
+  const dim3 grid(static_cast<unsigned>(P.ctas * pairs * P.parts));
   cudaError_t e = a->head_dim == 128 ? launch_pdl(echo::block_scores_kernel<128>, grid, dim3(echo::kScoreWarps * 32), 0, stream, P)
                                      : launch_pdl(echo::block_scores_kernel<64>, grid, dim3(echo::kScoreWarps * 32), 0, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block scores launch");

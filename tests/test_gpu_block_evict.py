@@ -219,6 +219,12 @@ def test_evict_long(lens, keep, recent):
     run_evict(FP4, 64, 64, 1, lens, keep, sinks=2, recent=recent, seed=len(lens))
 
 
+@pytest.mark.parametrize("slots", [8192, 8256, 10048, 10112, 10240, 12288, 32768, 32832])
+def test_evict_at_the_edges_of_shared_memory(slots):
+    """Contexts whose keys, beside what the kernel holds in any case, take just under and over 48 KB of it."""
+    run_evict(BF16, 64, 64, 1, [slots], 300, sinks=4, recent=100, seed=9, twice=False)
+
+
 def test_evict_more_recent_positions_than_room():
     """Positions that repeat (a caller's mistake): more tokens are recent than may stay; the first slots do."""
     g = np.random.default_rng(8)

@@ -132,6 +132,12 @@ def test_scores_of_long_contexts_tables_per_head_and_scales():
     check_scores(64, 32, 4, 2, 1, [100], scale=0.0, seed=3)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,n_q", [(64, 8, 2, 150), (128, 12, 4, 70), (64, 32, 2, 40), (64, 2, 2, 300), (64, 70, 1, 5)])
+def test_scores_of_many_query_tokens(D, Hq, Hkv, n_q):
+    """Columns that are split over CTAs, of groups that fill a chunk and of those that do not."""
+    check_scores(D, 16, Hq, Hkv, n_q, [n_q, n_q - 3, 16 * 9 + 5], gaps=0.1, seed=n_q)
+
+
 def test_scores_bound_the_keys():
     """Every key's score is below its block's, up to the rounding of both."""
     g = np.random.default_rng(4)
