@@ -60,6 +60,8 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
   constexpr int kStride = 2 * D + 64;               // bytes of a column; + 64: its quads on other banks
   constexpr int kPieces = D / 32;                   // 16-byte pieces of a column's dims per lane
   constexpr int kLoads = F16 ? 1 : kPieces;         // 16-byte loads of a token per lane (4 bits, D = 64: 8 bytes)
+  constexpr int kU = F16 ? 1 : 2;                   // sub-blocks of a step
+  constexpr int kDeep = F16 ? 4 : 1;                // steps whose loads are under way
   __shared__ __align__(16) uint8_t qs[kWtCols * kStride];
   __shared__ float2 col[kWtCols];                   // scale and lse of a column, both times log2 e
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
@@ -91,13 +93,13 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
   }
   const int64_t out0 = (static_cast<int64_t>(b) * P.n_kv + h) * most;
 
-  // two sub-blocks: tokens r8 and r8 + 8 of each
-  uint4 a[2][2][kLoads];
-  uint32_t sc[2][2];
-  bool held[2];
-  auto load = [&](int s) {
+  // tokens r8 and r8 + 8 of each sub-block
+  uint4 a[kDeep][kU][2][kLoads];
+  uint32_t sc[kDeep][kU][2];
+  bool held[kDeep][kU];
+  auto load = [&](auto &a, auto &sc, auto &held, int s) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kU; ++u) {
       int64_t at = __shfl_sync(~0u, where, (s - s0 + u) & 31);
       if (s + u >= s1) at = -1;
       held[u] = at >= 0;
@@ -111,11 +113,11 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
           if (at >= 0) {
             if constexpr (D == 128) {
               a[u][k][0] = load16_here(src + tk * (D / 2) + c4 * 16);
-              sc[u][k] = *reinterpret_cast<const uint16_t *>(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4 * 2);
+              sc[u][k] = load2_here(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4 * 2);
             } else {
-              const uint2 y = *reinterpret_cast<const uint2 *>(src + tk * (D / 2) + c4 * 8);
+              const uint2 y = load8_here(src + tk * (D / 2) + c4 * 8);
               a[u][k][0].x = y.x, a[u][k][0].y = y.y;
-              sc[u][k] = src[Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4];
+              sc[u][k] = load1_here(src + Fp4Sub<D>::kKeyScales + tk * (D / 16) + c4);
             }
           }
         } else {
@@ -131,7 +133,9 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
 
   for (int c0 = 0; c0 < rows_q; c0 += kWtCols) {
     const int nc = min(kWtCols, rows_q - c0), nc8 = (nc + 7) & ~7;
-    if (s0 < s1) load(s0);   // (under way while the queries are laid out)
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+      if (s0 + d * kU < s1) load(a[d], sc[d], held[d], s0 + d * kU);   // (under way while the queries are laid out)
     if (c0) __syncthreads();
     // the queries as columns: piece 4 i + c holds what lane c of a quad feeds with its i-th piece.
     for (int i = warp; i < nc8; i += kWtWarps) {   // a column per warp
@@ -167,30 +171,39 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
       if (lane == 0) col[i] = make_float2(scale, lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f);
     }
     __syncthreads();
-    for (int s = s0; s < s1; s += 2) {
-      const bool held_now[2] = {held[0], held[1]};
+    for (int at = s0; at < s1; at += kU * kDeep)
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int s = at + d * kU;
+      if (s >= s1) break;
+      bool held_now[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) held_now[u] = held[d][u];
+      auto next = [&] {      // (the registers are free)
+        if (s + kU * kDeep < s1) load(a[d], sc[d], held[d], s + kU * kDeep);
+      };
       // 4 bits: the A fragments, piece i of a lane's dims in two steps of 16 (bf16: as they were loaded)
-      uint32_t f[F16 ? 2 : 1][F16 ? kPieces : 1][2][4];
+      uint32_t f[F16 ? kU : 1][F16 ? kPieces : 1][2][4];
       if constexpr (F16) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int i = 0; i < kPieces; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t word[4] = {a[u][k][0].x, a[u][k][0].y, a[u][k][0].z, a[u][k][0].w};
+              const uint32_t word[4] = {a[d][u][k][0].x, a[d][u][k][0].y, a[d][u][k][0].z, a[d][u][k][0].w};
               uint32_t v[4];
               e2m1x8_to_half2(word[i], v);
-              const uint32_t s2 = __byte_perm(e4m3x2_to_half2(sc[u][k]), 0, D == 128 && i >= 2 ? 0x3232 : 0x1010);
+              const uint32_t s2 = __byte_perm(e4m3x2_to_half2(sc[d][u][k]), 0, D == 128 && i >= 2 ? 0x3232 : 0x1010);
               f[u][i][0][k] = hmul2(v[0], s2), f[u][i][0][2 + k] = hmul2(v[1], s2);
               f[u][i][1][k] = hmul2(v[2], s2), f[u][i][1][2 + k] = hmul2(v[3], s2);
             }
-        if (s + 2 < s1) load(s + 2);   // (the registers are free)
+        next();
       }
-      float x[2][4], w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      float x[kU][4], w[kU][2] = {};
       auto products = [&](int cg) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[u][k] = 0.f;
         const uint8_t *qp = qs + (cg + r8) * kStride + c4 * 16;
@@ -198,13 +211,13 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
         for (int i = 0; i < kPieces; ++i) {
           const uint4 q = *reinterpret_cast<const uint4 *>(qp + i * 64);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < kU; ++u) {
             if constexpr (F16) {
               mma16816<true>(x[u], f[u][i][0], q.x, q.y);
               mma16816<true>(x[u], f[u][i][1], q.z, q.w);
             } else {
-              const uint32_t y[4] = {a[u][0][i].x, a[u][1][i].x, a[u][0][i].y, a[u][1][i].y};
-              const uint32_t z[4] = {a[u][0][i].z, a[u][1][i].z, a[u][0][i].w, a[u][1][i].w};
+              const uint32_t y[4] = {a[d][u][0][i].x, a[d][u][1][i].x, a[d][u][0][i].y, a[d][u][1][i].y};
+              const uint32_t z[4] = {a[d][u][0][i].z, a[d][u][1][i].z, a[d][u][0][i].w, a[d][u][1][i].w};
               mma16816<false>(x[u], y, q.x, q.y);
               mma16816<false>(x[u], z, q.z, q.w);
             }
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
         }
       };
       // tokens that every query sees (the last n_q - 1 are looked at one by one)
-      const bool edge = (s + 2) * kSubTokens > len - (P.n_q - 1);
+      const bool edge = (s + kU) * kSubTokens > len - (P.n_q - 1);
       auto weights = [&](int cg) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
           const float2 m = col[c];
           const int seen = edge ? len - (P.n_q - 1 - min((c0 + c) / P.group, P.n_q - 1)) : 0x7fffffff;
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < kU; ++u)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const float e = ex2(fmaf(x[u][p + 2 * k], m.x, -m.y));
@@ -233,10 +246,10 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
         weights(cg);
       }
       products(nc8 - 8);
-      if (!F16 && s + 2 < s1) load(s + 2);   // (now the keys' registers are free)
+      if (!F16) next();
       weights(nc8 - 8);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float v = w[u][k];
