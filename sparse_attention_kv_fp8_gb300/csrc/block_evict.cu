@@ -55,13 +55,15 @@ struct WeightParams {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const WeightParams P) {
+__global__ void __launch_bounds__(kWtWarps * 32, 4) block_weights_kernel(const WeightParams P) {
   constexpr bool F16 = FMT == ECHO_BLOCK_FP4;
   constexpr int kStride = 2 * D + 64;               // bytes of a column; + 64: its quads on other banks
   constexpr int kPieces = D / 32;                   // 16-byte pieces of a column's dims per lane
   constexpr int kLoads = F16 ? 1 : kPieces;         // 16-byte loads of a token per lane (4 bits, D = 64: 8 bytes)
   constexpr int kU = F16 ? 1 : 2;                   // sub-blocks of a step
   constexpr int kDeep = F16 ? 4 : 1;                // steps whose loads are under way
+  constexpr int kRun = kU * kDeep;                  // sub-blocks of a round of them
+  constexpr int kOut = kRun / 2;                    // tokens of a round per lane: lane, lane + 32, ...
   __shared__ __align__(16) uint8_t qs[kWtCols * kStride];
   __shared__ float2 col[kWtCols];                   // scale and lse of a column, both times log2 e
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
@@ -131,8 +133,21 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
     }
   };
 
+  // what the tokens of a round gathered before, a round ahead
+  float before[kOut], before_next[kOut];
+  const int end = min(len, s1 * kSubTokens);
+  auto load_before = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+      const int p = s * kSubTokens + 32 * i + lane;
+      before_next[i] = 0.f;
+      if (p < min(old, end)) asm volatile("ld.global.f32 %0, [%1];" : "=f"(before_next[i]) : "l"(P.acc + out0 + p));
+    }
+  };
+
   for (int c0 = 0; c0 < rows_q; c0 += kWtCols) {
     const int nc = min(kWtCols, rows_q - c0), nc8 = (nc + 7) & ~7;
+    if (c0 == 0) load_before(s0);
 #pragma unroll
     for (int d = 0; d < kDeep; ++d)
       if (s0 + d * kU < s1) load(a[d], sc[d], held[d], s0 + d * kU);   // (under way while the queries are laid out)
@@ -171,7 +186,11 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
       if (lane == 0) col[i] = make_float2(scale, lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f);
     }
     __syncthreads();
-    for (int at = s0; at < s1; at += kU * kDeep)
+    for (int at = s0; at < s1; at += kRun) {
+    float sum[kOut];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) sum[i] = 0.f, before[i] = before_next[i];
+    if (c0 == 0) load_before(at + kRun);
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
       const int s = at + d * kU;
@@ -248,21 +267,26 @@ __global__ void __launch_bounds__(kWtWarps * 32) block_weights_kernel(const Weig
       products(nc8 - 8);
       if (!F16) next();
       weights(nc8 - 8);
+      // the quad's sum of token r8 + 8 k goes to the lane of that token
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
+      for (int u = 0; u < kU; ++u) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float v = w[u][k];
-          v += __shfl_xor_sync(~0u, v, 1);
-          v += __shfl_xor_sync(~0u, v, 2);
-          const int p = (s + u) * kSubTokens + r8 + 8 * k;
-          if (c4 != 0 || s + u >= s1 || p >= len) continue;
-          if (!held_now[u]) v = 0.f;
-          float before;
-          if (c0) before = P.acc_out[out0 + p];  // (written by this thread)
-          else before = p < old ? P.acc[out0 + p] * P.decay : 0.f;
-          P.acc_out[out0 + p] = before + v;
+          w[u][k] += __shfl_xor_sync(~0u, w[u][k], 1);
+          w[u][k] += __shfl_xor_sync(~0u, w[u][k], 2);
+          w[u][k] = __shfl_sync(~0u, w[u][k], (lane & 7) * 4);
         }
+        const int i = d * kU + u;     // (sub-block of the round: tokens 16 i and up of it)
+        if (lane / 16 == i % 2 && held_now[u]) sum[i / 2] = lane & 8 ? w[u][1] : w[u][0];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+      const int p = at * kSubTokens + 32 * i + lane;
+      if (p >= end) continue;
+      // (a later chunk of columns adds to what this thread wrote for the one before)
+      P.acc_out[out0 + p] = (c0 ? P.acc_out[out0 + p] : before[i] * P.decay) + sum[i];
+    }
     }
   }
 }
@@ -599,7 +623,7 @@ int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream) 
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads;
   const int64_t nsub = static_cast<int64_t>(a->max_blocks) * P.bsub;
   // two sub-blocks a warp, or more where every SM still has several CTAs
-  P.subs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, nsub * pairs / (2 * echo::kWtWarps * 48ll * sms))) * 2);
+  P.subs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, nsub * pairs / (2 * echo::kWtWarps * 24ll * sms))) * 2);
   P.ctas = static_cast<int>((nsub + echo::kWtWarps * P.subs - 1) / (echo::kWtWarps * P.subs));
   const dim3 grid(static_cast<unsigned>(P.ctas * pairs)), block(echo::kWtWarps * 32);
   cudaError_t e;
