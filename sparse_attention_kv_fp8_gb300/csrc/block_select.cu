@@ -24,6 +24,7 @@
 //     one ordered pass writes those above it and the first of its equals.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "block_mma.cuh"
 #include "block_pick.cuh"
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
 // ---------------------------------------------------------------------------
 constexpr int kScoreWarps = 4;
 constexpr int kScoreCols = 64;  // query columns that a CTA lays out at a time
+constexpr int kScoreAhead = 4;  // 16-byte pieces of them that a thread has under way
 
 struct ScoreParams {
   const uint16_t *q;
@@ -273,7 +275,6 @@ struct ScoreParams {
   BlockTable tab;
   const int32_t *ctx_len;
   int32_t n_q, n_heads, group;
-  int32_t pad_log2;       // columns of a query token: 2^pad_log2, of which `group` or fewer differ
   int32_t cols;           // columns of a KV head, a multiple of 8
   int32_t wide;           // columns of a query token where the group has more than 8 heads
   int32_t chunk;          // columns laid out at a time: whole query tokens if they fit
@@ -285,8 +286,9 @@ struct ScoreParams {
   int32_t *status;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const ScoreParams P) {
+// PAD: a query token has 2^PAD columns, of which `group` or fewer differ; 4: P.wide columns
+template <int D, int PAD>
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(const ScoreParams P) {
   constexpr int kStride = 4 * D + 64;       // bytes of a column; + 64: its quads on other banks
   constexpr int kChunks = D / 16;           // 16-byte pieces of a summary row that a lane holds
   __shared__ __align__(16) uint8_t qs[kScoreCols * kStride];
@@ -331,39 +333,57 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 
   for (int c0 = c_from; c0 < c_end; c0 += P.chunk) {
     const int nc = min(P.chunk, c_end - c0);
-    look_up(0);
-    load(0);     // (under way while the queries are laid out)
+    if (c0 == c_from || P.tiles > 1) {   // (a single tile stays in the registers)
+      look_up(0);
+      load(0);     // (under way while the queries are laid out)
+    }
     if (c0 != c_from) __syncthreads();
     // [q-, q+] of the columns; a group's last head fills its padding (a maximum does not mind)
-    for (int i = threadIdx.x; i < nc * (D / 8); i += kScoreWarps * 32) {
-      const int col = i / (D / 8), d8 = i % (D / 8), cc = c0 + col;
-      int j, g;
-      if (P.pad_log2 <= 3) {
-        j = cc >> P.pad_log2, g = cc & ((1 << P.pad_log2) - 1);
-      } else {
-        j = cc / P.wide, g = cc - j * P.wide;
-      }
-      j = min(j, P.n_q - 1), g = min(g, P.group - 1);
-      uint4 x = *reinterpret_cast<const uint4 *>(P.q + ((static_cast<int64_t>(b) * P.n_q + j) * P.n_heads + h * P.group + g) * D + d8 * 8);
-      uint32_t w[4] = {x.x ^ P.q_sign, x.y ^ P.q_sign, x.z ^ P.q_sign, x.w ^ P.q_sign}, n[4];
+    for (int i0 = threadIdx.x; i0 < nc * (D / 8); i0 += kScoreAhead * kScoreWarps * 32) {
+      uint4 x[kScoreAhead];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t neg = ((w[k] >> 15) & 0x10001u) * 0xffffu;  // all ones in the halves below zero
-        n[k] = w[k] & neg, w[k] &= ~neg;
+      for (int r = 0; r < kScoreAhead; ++r) {
+        const int i = i0 + r * kScoreWarps * 32, cc = c0 + i / (D / 8);
+        if (i >= nc * (D / 8)) break;
+        int j, g;
+        if constexpr (PAD <= 3) {
+          j = cc >> PAD, g = cc & ((1 << PAD) - 1);
+        } else {
+          j = cc / P.wide, g = cc - j * P.wide;
+        }
+        j = min(j, P.n_q - 1), g = min(g, P.group - 1);
+        x[r] = load16_here(P.q + ((static_cast<int64_t>(b) * P.n_q + j) * P.n_heads + h * P.group + g) * D + i % (D / 8) * 8);
       }
-      // piece 4 i + c is what lane c of a quad feeds with its i-th: it reads 32 bytes (a sector) of every 128
-      uint8_t *dst = qs + col * kStride + (4 * (d8 / 8 * 2 + d8 % 2) + d8 % 8 / 2) * 16;
-      *reinterpret_cast<uint4 *>(dst) = make_uint4(n[0], n[1], n[2], n[3]);
-      *reinterpret_cast<uint4 *>(dst + 2 * D) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int r = 0; r < kScoreAhead; ++r) {
+        const int i = i0 + r * kScoreWarps * 32, col = i / (D / 8), d8 = i % (D / 8);
+        if (i >= nc * (D / 8)) break;
+        uint32_t w[4] = {x[r].x ^ P.q_sign, x[r].y ^ P.q_sign, x[r].z ^ P.q_sign, x[r].w ^ P.q_sign}, n[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t neg = ((w[k] >> 15) & 0x10001u) * 0xffffu;  // all ones in the halves below zero
+          n[k] = w[k] & neg, w[k] &= ~neg;
+        }
+        // piece 4 i + c is what lane c of a quad feeds with its i-th: it reads 32 bytes (a sector) of every 128
+        uint8_t *dst = qs + col * kStride + (4 * (d8 / 8 * 2 + d8 % 2) + d8 % 8 / 2) * 16;
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(n[0], n[1], n[2], n[3]);
+        *reinterpret_cast<uint4 *>(dst + 2 * D) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
     __syncthreads();
     for (int t = 0; t < P.tiles; ++t) {
       const int e0 = first + (t * kScoreWarps + warp) * 16;
       if (e0 >= blocks) break;
       const bool held[2] = {there[0], there[1]};
-      float best[2][2];  // of column parity and block
-#pragma unroll
-      for (int k = 0; k < 4; ++k) best[k >> 1][k & 1] = -INFINITY;
+      // the score of block r8 + 8 k of the tile for query token j, if the token sees the block's first one
+      auto put = [&](int j, int k, float v, bool more) {
+        const int e = e0 + r8 + 8 * k;
+        if (j >= P.n_q || e >= blocks || e * P.bs >= len - (P.n_q - 1 - j)) return;
+        float *dst = P.scores + ((static_cast<int64_t>(b) * P.n_q + j) * P.tab.n_kv + h) * P.tab.max_blocks + e;
+        v = (k ? held[1] : held[0]) ? v * P.scale : -INFINITY;
+        *dst = more ? fmaxf(v, *dst) : v;   // (more: heads of an earlier chunk, written by this thread)
+      };
+      float best[2] = {-INFINITY, -INFINITY};  // (PAD 4: of a token's columns so far)
       for (int cg = 0; cg < nc; cg += 8) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         const uint8_t *qp = qs + (cg + r8) * kStride + c4 * 16;
@@ -374,46 +394,34 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
           mma16816<false>(acc, x, q.x, q.y);
           mma16816<false>(acc, y, q.z, q.w);
         }
-        if (cg + 8 >= nc) load(t + 1);   // (the registers are free)
+        if (cg + 8 >= nc && t + 1 < P.tiles) load(t + 1);   // (the registers are free)
         // acc[p + 2 k]: column 2 c4 + p of block k.  One value per (query token, block)
-        const int cc = c0 + cg + 2 * c4;
-        if (P.pad_log2 == 0) {
+        if constexpr (PAD == 0) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) best[p][k] = acc[p + 2 * k];
+          for (int k = 0; k < 2; ++k) put(c0 + cg + 2 * c4, k, acc[2 * k], false), put(c0 + cg + 2 * c4 + 1, k, acc[1 + 2 * k], false);
         } else {
+          float v[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float v = fmaxf(acc[2 * k], acc[1 + 2 * k]);
-            if (P.pad_log2 >= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
-            if (P.pad_log2 >= 3) v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
-            best[0][k] = P.pad_log2 > 3 ? fmaxf(best[0][k], v) : v;
+            v[k] = fmaxf(acc[2 * k], acc[1 + 2 * k]);
+            if (PAD >= 2) v[k] = fmaxf(v[k], __shfl_xor_sync(~0u, v[k], 1));
+            if (PAD >= 3) v[k] = fmaxf(v[k], __shfl_xor_sync(~0u, v[k], 2));
+          }
+          if constexpr (PAD == 1) {
+            const int j = (c0 + cg + 2 * c4) >> 1;
+            put(j, 0, v[0], false), put(j, 1, v[1], false);
+          } else if constexpr (PAD <= 3) {   // (two lanes or four have them both: one writes each)
+            const int j = (c0 + cg + 2 * c4) >> PAD;
+            if (c4 % (1 << (PAD - 1)) < 2) put(j, c4 & 1, c4 & 1 ? v[1] : v[0], false);
+          } else {
+            best[0] = fmaxf(best[0], v[0]), best[1] = fmaxf(best[1], v[1]);
+            const int at = c0 + cg, j = at / P.wide;
+            if (at + 8 == (j + 1) * P.wide || cg + 8 == nc) {
+              if (c4 < 2) put(j, c4, c4 ? best[1] : best[0], j * P.wide < c0);
+              best[0] = best[1] = -INFINITY;
+            }
           }
         }
-        int j = cc >> P.pad_log2, n_out = P.pad_log2 ? 1 : 2;
-        bool write = (cc & ((1 << min(P.pad_log2, 3)) - 1) & ~1) == 0;
-        bool more = false;  // an earlier chunk had heads of this token too
-        if (P.pad_log2 > 3) {
-          const int at = c0 + cg;
-          j = at / P.wide;
-          write = at + 8 == (j + 1) * P.wide || cg + 8 == nc;
-          more = j * P.wide < c0;
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          if (!write || p >= n_out || j + p >= P.n_q || (P.pad_log2 > 3 && c4)) continue;
-          const int nb = (len - (P.n_q - 1 - j - p) + P.bs - 1) / P.bs;  // (may be negative: nothing)
-          float *dst = P.scores + ((static_cast<int64_t>(b) * P.n_q + j + p) * P.tab.n_kv + h) * P.tab.max_blocks;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (e0 + r8 + 8 * k < nb) {
-              float v = held[k] ? best[p][k] * P.scale : -INFINITY;
-              if (more) v = fmaxf(v, dst[e0 + r8 + 8 * k]);  // (written by this thread)
-              dst[e0 + r8 + 8 * k] = v;
-            }
-        }
-        if (P.pad_log2 > 3 && write) best[0][0] = best[0][1] = -INFINITY;
       }
     }
   }
@@ -605,11 +613,11 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   P.tab = {a->table, a->table_heads, a->max_blocks, a->n_kv_heads};
   P.ctx_len = a->ctx_len;
   P.n_q = a->n_q, P.n_heads = a->n_heads, P.group = a->n_heads / a->n_kv_heads;
-  P.pad_log2 = 0;
-  while ((1 << P.pad_log2) < P.group && P.pad_log2 <= 3) ++P.pad_log2;
+  int pad = 0;
+  while ((1 << pad) < P.group && pad <= 3) ++pad;
   P.wide = (P.group + 7) & ~7;
-  P.cols = P.pad_log2 > 3 ? P.n_q * P.wide : ((P.n_q << P.pad_log2) + 7) & ~7;
-  P.chunk = P.pad_log2 > 3 && P.wide <= echo::kScoreCols ? echo::kScoreCols / P.wide * P.wide : echo::kScoreCols;
+  P.cols = pad > 3 ? P.n_q * P.wide : ((P.n_q << pad) + 7) & ~7;
+  P.chunk = pad > 3 && P.wide <= echo::kScoreCols ? echo::kScoreCols / P.wide * P.wide : echo::kScoreCols;
   P.scale = std::fabs(a->scale), P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
   P.scores = a->scores, P.status = a->dev_status;
   int sms = 0;
@@ -625,8 +633,13 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   const int64_t each = P.wide > echo::kScoreCols ? chunks : (chunks + std::min(chunks, want) - 1) / std::min(chunks, want);
   P.span = static_cast<int>(each * P.chunk), P.parts = static_cast<int>((chunks + each - 1) / each);
   const dim3 grid(static_cast<unsigned>(P.ctas * pairs * P.parts));
-  cudaError_t e = a->head_dim == 128 ? launch_pdl(echo::block_scores_kernel<128>, grid, dim3(echo::kScoreWarps * 32), 0, stream, P)
-                                     : launch_pdl(echo::block_scores_kernel<64>, grid, dim3(echo::kScoreWarps * 32), 0, stream, P);
+  auto go = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    auto *kernel = pad == 0 ? echo::block_scores_kernel<D, 0> : pad == 1 ? echo::block_scores_kernel<D, 1>
+                 : pad == 2 ? echo::block_scores_kernel<D, 2> : pad == 3 ? echo::block_scores_kernel<D, 3> : echo::block_scores_kernel<D, 4>;
+    return launch_pdl(kernel, grid, dim3(echo::kScoreWarps * 32), 0, stream, P);
+  };
+  cudaError_t e = a->head_dim == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block scores launch");
 }
 
