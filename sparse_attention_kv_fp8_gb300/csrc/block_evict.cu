@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
     return s != s ? 1u : score_key(s);  // (a weight that is NaN goes first)
   };
   auto key_of = [&](int i) { return make_key(i, acc[i], pos ? pos_of(i) : 0); };
+  pick_clear(S);
   const uint32_t zero = score_key(0.f);
   uint32_t lo = kMustKey, hi = 0, n_must = 0;   // (of the weights above zero)
   for (int i0 = tid; i0 < n; i0 += kEvAhead * T) {
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
       else if (key > zero) lo = min(lo, key), hi = max(hi, key);
     }
   }
-  n_must = pick_sum(S, n_must, 0), lo = pick_min(S, lo, 1), hi = ~pick_min(S, ~hi, 0);
+  pick_stats(S, n_must, lo, hi);
   auto key_at = [&](int i) -> uint32_t { return P.staged ? ev_keys[i] : key_of(i); };
 
   // ----- the key above which all stay, and how many of its equals (n > keep: some go) -----

@@ -436,64 +436,84 @@ constexpr int kSelRows = 4;                 // rows of a CTA that takes one per 
 struct SelectParams {
   const float *scores;
   const int32_t *ctx_len;
-  int64_t n;          // rows: (query, KV head)
+  uint32_t n;         // rows: (query, KV head)
   int32_t n_q, bs, k, first, last;
   BlockTable tab;     // (table: optional)
   int32_t *sel, *sel_rows, *len_out;
+  int32_t vec;        // rows of `scores` and of the table lie on 16-byte boundaries
   int32_t *status;
 };
 
-// W warps a row (one: kSelRows rows a CTA), R keys a thread
+// W warps a row (one: kSelRows rows a CTA), R blocks a thread, one after another: the order within a
+// thread is then free, and one sum over the threads gives each its place in the list
 template <int W, int R>
 __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_kernel(const SelectParams P) {
   __shared__ PickSpace<W, kSelBins> space[W == 1 ? kSelRows : 1];
-  __shared__ uint32_t cnt[W > 1 ? R * W : 1];
+  __shared__ uint32_t cnt[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = W == 1 ? lane : threadIdx.x;
-  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * kSelRows + warp : blockIdx.x;
+  const uint32_t row = W == 1 ? blockIdx.x * kSelRows + warp : blockIdx.x;   // (rows: below 2^31)
   auto &S = space[W == 1 ? warp : 0];
   pdl_launch_dependents();
   pdl_wait();
   if (row >= P.n) return;
-  const int bj = static_cast<int>(row / P.tab.n_kv), h = static_cast<int>(row - static_cast<int64_t>(bj) * P.tab.n_kv);
-  const int b = bj / P.n_q, j = bj - b * P.n_q;
-  const float *src = P.scores + row * P.tab.max_blocks;
+  const int bj = row / static_cast<uint32_t>(P.tab.n_kv), h = row - bj * P.tab.n_kv;
+  const int b = static_cast<uint32_t>(bj) / static_cast<uint32_t>(P.n_q), j = bj - b * P.n_q;
+  const float *src = P.scores + static_cast<int64_t>(row) * P.tab.max_blocks;
   const int ctx = held_len(P.ctx_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, P.status, j == 0 && h == 0 && tid == 0);
-  const int len = max(ctx - (P.n_q - 1 - j), 0), nb = (len + P.bs - 1) / P.bs;
+  const int len = max(ctx - (P.n_q - 1 - j), 0), nb = static_cast<uint32_t>(len + P.bs - 1) / static_cast<uint32_t>(P.bs);
   if (P.len_out && h == 0 && tid == 0) P.len_out[bj] = len;
 
-  // Scores of blocks tid, tid + 32 W, ...; NaN: not to be chosen by its score (a block that is not there
-  // or not held, or one of `must`, which is taken in any case); a score that is NaN becomes -inf
+  // Scores of blocks i0 and up; NaN: not to be chosen by its score (a block that is not there or not held,
+  // or one of `must`, which is taken in any case); a score that is NaN becomes -inf
+  const int i0 = tid * R;
   float score[R], lo = INFINITY, hi = -INFINITY;  // (range of the finite ones)
-  uint32_t must = 0, n_ok = 0;
+  uint32_t must = 0, n_ok = 0, n_must;
+  pick_clear(S);
   const int32_t *ids = P.tab.table ? P.tab.table + (static_cast<int64_t>(b) * P.tab.heads + (P.tab.heads > 1 ? h : 0)) * P.tab.max_blocks : nullptr;
   {
+    // (all loads before the first use: one by one where the branches below want them they take 78 us for
+    // 8000 rows of 1024 blocks)
     int32_t id[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      // (volatile, and a block that is there in any case: all loads are then made before the first use,
-      // not one by one where the branches below want them, 78 us for 8000 rows of 1024 blocks)
-      const int i = min(r * W * 32 + tid, max(nb - 1, 0));
-      score[r] = 0.f, id[r] = 0;
-      if (r * W * 32 < nb) {
-        asm volatile("ld.global.f32 %0, [%1];" : "=f"(score[r]) : "l"(src + i));
-        if (ids) asm volatile("ld.global.s32 %0, [%1];" : "=r"(id[r]) : "l"(ids + i));
+    for (int r = 0; r < R; ++r) score[r] = 0.f, id[r] = 0;
+    if (P.vec) {
+#pragma unroll
+      for (int r = 0; r < R; r += 4) {
+        if (i0 + r >= nb) break;
+        const uint4 x = load16_here(src + i0 + r);
+        score[r] = __uint_as_float(x.x), score[r + 1] = __uint_as_float(x.y);
+        score[r + 2] = __uint_as_float(x.z), score[r + 3] = __uint_as_float(x.w);
+        if (ids) {
+          const uint4 y = load16_here(ids + i0 + r);
+          id[r] = y.x, id[r + 1] = y.y, id[r + 2] = y.z, id[r + 3] = y.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (i0 + r >= nb) break;
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(score[r]) : "l"(src + i0 + r));
+        if (ids) asm volatile("ld.global.s32 %0, [%1];" : "=r"(id[r]) : "l"(ids + i0 + r));
       }
     }
+    const uint32_t plain = max(nb - P.first - P.last, 0);   // blocks that are neither of the first nor of the last
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = r * W * 32 + tid;
-      const bool there = i < nb && id[r] >= 0, always = there && (i < P.first || i >= nb - P.last);
+      const bool there = i0 + r < nb && id[r] >= 0, by_score = static_cast<uint32_t>(i0 + r - P.first) < plain;
       float s = score[r] == score[r] ? score[r] : -INFINITY;
-      must |= always ? 1u << r : 0u;
-      s = there && !always ? s : NAN;
+      must |= there && !by_score ? 1u << r : 0u;
+      s = there && by_score ? s : NAN;
       n_ok += s == s;
       if (fabsf(s) < INFINITY) lo = fminf(lo, s), hi = fmaxf(hi, s);
       score[r] = s;
     }
   }
   static_assert(R <= 32, "a bit of `must` each");
-  n_ok = pick_sum(S, n_ok, 0);
-  const uint32_t n_must = pick_sum(S, __popc(must), 1);
+  {  // (counts of 32768 at most: both in one word)
+    uint32_t both = n_ok | __popc(must) << 16, k0 = score_key(lo), k1 = score_key(hi);
+    pick_stats(S, both, k0, k1);
+    n_ok = both & 0xffffu, n_must = both >> 16, lo = key_score(k0), hi = key_score(k1);
+  }
 
   // ----- the score above which all are taken, and how many of its equals -----
   const uint32_t want = P.k - n_must;  // (first + last <= k)
@@ -502,7 +522,6 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   if (want == 0) {
     thr = INFINITY, need = 0;
   } else if (n_ok > want) {
-    lo = key_score(pick_min(S, score_key(lo), 0)), hi = key_score(~pick_min(S, ~score_key(hi), 1));
     // 256 equal parts of the scores' range; an infinite score goes to an end
     const float step = hi > lo ? fminf(kSelBins / (hi - lo), 3e38f) : 0.f, from = -lo * step;
     auto each = [&](auto &&f) {
@@ -516,53 +535,41 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   }
 
   // ----- the blocks in order -----
-  int32_t *sel = P.sel + row * P.k, *rows = P.sel_rows ? P.sel_rows + row * P.k : nullptr;
-  const uint32_t before = (1u << lane) - 1;
-  uint32_t taken;     // above the threshold, and equal to it (upper half)
-  if constexpr (W > 1) {
+  int32_t *sel = P.sel + static_cast<int64_t>(row) * P.k, *rows = P.sel_rows ? P.sel_rows + static_cast<int64_t>(row) * P.k : nullptr;
+  uint32_t gt = must, eq = 0;   // above the threshold, and equal to it
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t gt = __ballot_sync(~0u, score[r] > thr || must >> r & 1), eq = __ballot_sync(~0u, score[r] == thr);
-      if (lane == 0) cnt[r * W + warp] = __popc(gt) | __popc(eq) << 16;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t base = 0;
-      for (int r = 0; r < R * W; r += 32) {
-        const uint32_t x = cnt[r + lane];
-        uint32_t upto = x;
+  for (int r = 0; r < R; ++r) gt |= score[r] > thr ? 1u << r : 0u, eq |= score[r] == thr ? 1u << r : 0u;
+  const uint32_t mine = __popc(gt) | __popc(eq) << 16;
+  uint32_t at = mine, taken;     // of the blocks before the thread's, and of all
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t y = __shfl_up_sync(~0u, upto, d);
-          if (lane >= d) upto += y;
-        }
-        cnt[r + lane] = base + upto - x;
-        base += __shfl_sync(~0u, upto, 31);
-      }
-      if (lane == 0) S.pick[0] = base;
-    }
-    __syncthreads();
-    taken = S.pick[0];
-  } else {
-    taken = 0;
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t x = __shfl_up_sync(~0u, at, d);
+    if (lane >= d) at += x;
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const bool is_gt = score[r] > thr || must >> r & 1, is_eq = score[r] == thr;
-    const uint32_t gt = __ballot_sync(~0u, is_gt), eq = __ballot_sync(~0u, is_eq);
-    if ((gt | eq) == 0) continue;
-    const uint32_t c = W > 1 ? cnt[W > 1 ? r * W + warp : 0] : taken;
-    const uint32_t q = (c >> 16) + __popc(eq & before);
-    if (is_gt || (is_eq && q < need)) {
-      sel[(c & 0xffffu) + __popc(gt & before) + min(q, need)] = r * W * 32 + tid;
+  if constexpr (W > 1) {
+    if (lane == 31) cnt[warp] = at;
+    __syncthreads();
+    const uint32_t x = lane < W ? cnt[lane % W] : 0u;
+    at += __reduce_add_sync(~0u, lane < warp ? x : 0u), taken = __reduce_add_sync(~0u, x);
+  } else {
+    taken = __shfl_sync(~0u, at, 31);
+  }
+  at -= mine;
+  for (uint32_t m = gt | eq; m; m &= m - 1) {
+    const int r = __ffs(m) - 1;
+    const bool equal = eq >> r & 1;
+    const uint32_t q = at >> 16, to = (at & 0xffffu) + min(q, need);
+    if (!equal || q < need) {
+      sel[to] = i0 + r;
+      if (rows) rows[to] = P.tab.heads > 1 ? ids[i0 + r] : ids[i0 + r] * P.tab.n_kv + h;
     }
-    if constexpr (W == 1) taken += __popc(gt) | __popc(eq) << 16;
+    at += equal ? 0x10000u : 1u;
   }
   const int n = (taken & 0xffffu) + min(taken >> 16, need);
-  for (int i = n + tid; i < P.k; i += W * 32) sel[i] = -1;
-  if (!rows) return;
-  pick_sync<W>();     // (the list is read back: looked up one by one above, each row would wait for its id)
-  for (int i = tid; i < P.k; i += W * 32) rows[i] = i < n ? static_cast<int32_t>(P.tab.row(b, h, sel[i])) : -1;
+  for (int i = n + tid; i < P.k; i += W * 32) {
+    sel[i] = -1;
+    if (rows) rows[i] = -1;
+  }
 }
 
 }  // namespace echo
@@ -645,8 +652,8 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
 
 template <int W, int R>
 static int go_select(const echo::SelectParams &P, cudaStream_t stream) {
-  const int64_t ctas = W == 1 ? (P.n + echo::kSelRows - 1) / echo::kSelRows : P.n;
-  cudaError_t e = launch_pdl(echo::block_select_kernel<W, R>, dim3(static_cast<unsigned>(ctas)), dim3(W == 1 ? echo::kSelRows * 32 : W * 32), 0,
+  const uint32_t ctas = W == 1 ? (P.n + echo::kSelRows - 1) / echo::kSelRows : P.n;
+  cudaError_t e = launch_pdl(echo::block_select_kernel<W, R>, dim3(ctas), dim3(W == 1 ? echo::kSelRows * 32 : W * 32), 0,
                              stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block selection launch");
 }
@@ -654,16 +661,17 @@ static int go_select(const echo::SelectParams &P, cudaStream_t stream) {
 int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   echo::SelectParams P{};
   P.scores = a->scores, P.ctx_len = a->ctx_len;
-  P.n = static_cast<int64_t>(a->B) * a->n_q * a->n_kv_heads;
+  P.n = static_cast<uint32_t>(a->B) * a->n_q * a->n_kv_heads;   // (below 2^31)
   P.n_q = a->n_q, P.bs = a->block_tokens, P.k = a->k, P.first = a->first, P.last = a->last;
   P.tab = {a->table, a->table_heads, a->max_blocks, a->n_kv_heads};
   P.sel = a->sel, P.sel_rows = a->sel_rows, P.len_out = a->len_out, P.status = a->dev_status;
+  P.vec = a->max_blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a->scores) % 16 == 0 && reinterpret_cast<uintptr_t>(a->table) % 16 == 0;
   // the keys of a row in the registers of as few warps as hold them
   // (few rows: 8 warps each, which have less to go through one after another)
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
   if (a->max_blocks <= 256) return go_select<1, 8>(P, stream);
-  if (a->max_blocks <= 1024) return P.n <= 4 * sms ? go_select<8, 4>(P, stream) : go_select<4, 8>(P, stream);
+  if (a->max_blocks <= 1024) return P.n <= 4u * sms ? go_select<8, 4>(P, stream) : go_select<4, 8>(P, stream);
   if (a->max_blocks <= 4096) return go_select<8, 16>(P, stream);
   return go_select<32, 32>(P, stream);
 }
