@@ -19,9 +19,10 @@
 //     as they are: a warp has the 16 summaries (8 KB) in registers after one round of loads, with
 //     no shared memory.  The 8 columns are the heads of one query token, or of several where a
 //     group has fewer, so the maximum over a group stays within a quad.
-//   Selection: a warp per (query, KV head) up to 1024 blocks, up to 32 warps beyond, with the keys in
-//     registers.  The k-th best is found from counts over the range of the scores (block_pick.cuh), then
-//     one ordered pass writes those above it and the first of its equals.
+//   Selection: one to 32 warps per (query, KV head), a thread with 4 to 32 blocks that follow one another,
+//     their scores in registers.  The k-th best is found from counts over the range of the scores
+//     (block_pick.cuh), then a sum over the threads gives each the place of what it writes: those above,
+//     and the first of its equals.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -471,8 +472,7 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   pick_clear(S);
   const int32_t *ids = P.tab.table ? P.tab.table + (static_cast<int64_t>(b) * P.tab.heads + (P.tab.heads > 1 ? h : 0)) * P.tab.max_blocks : nullptr;
   {
-    // (all loads before the first use: one by one where the branches below want them they take 78 us for
-    // 8000 rows of 1024 blocks)
+    // (all loads before the first use, not one by one where the branches below want them)
     int32_t id[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) score[r] = 0.f, id[r] = 0;
@@ -666,13 +666,20 @@ int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   P.tab = {a->table, a->table_heads, a->max_blocks, a->n_kv_heads};
   P.sel = a->sel, P.sel_rows = a->sel_rows, P.len_out = a->len_out, P.status = a->dev_status;
   P.vec = a->max_blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a->scores) % 16 == 0 && reinterpret_cast<uintptr_t>(a->table) % 16 == 0;
-  // the keys of a row in the registers of as few warps as hold them
-  // (few rows: 8 warps each, which have less to go through one after another)
+  // the keys of a row in the registers of the threads that hold them: 8 or 16 each where rows fill the SMs
+  // (8000 rows of 512 blocks: one warp 14.3 us, two 16.8, four 22.2), fewer each where they do not and a
+  // thread's own keys are what a row waits for (256 rows of 4096: 16 warps 6.4 us, 8 warps 9.2).  Both of
+  // 1024 blocks: 256 rows 4.4 and 4.3 us, 32 rows 3.5 and 3.8, 4000 rows 20.8 and 15.5
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
+  const bool few = P.n <= 4u * sms;
   if (a->max_blocks <= 256) return go_select<1, 8>(P, stream);
-  if (a->max_blocks <= 1024) return P.n <= 4u * sms ? go_select<8, 4>(P, stream) : go_select<4, 8>(P, stream);
-  if (a->max_blocks <= 4096) return go_select<8, 16>(P, stream);
+  if (a->max_blocks <= 512) return few ? go_select<4, 4>(P, stream) : go_select<1, 16>(P, stream);
+  if (a->max_blocks <= 1024) return few ? go_select<8, 4>(P, stream) : go_select<4, 8>(P, stream);
+  if (a->max_blocks <= 2048) return go_select<8, 8>(P, stream);
+  if (a->max_blocks <= 4096) return few ? go_select<16, 8>(P, stream) : go_select<8, 16>(P, stream);
+  if (a->max_blocks <= 8192) return go_select<32, 8>(P, stream);
+  if (a->max_blocks <= 16384) return go_select<32, 16>(P, stream);
   return go_select<32, 32>(P, stream);
 }
 

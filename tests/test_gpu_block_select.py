@@ -236,6 +236,17 @@ def test_select_sizes(B, n_q, Hkv, n, k):
     check_select(x, [max(n_q, n * 32 - 40 * b) for b in range(B)], 32, k, 1, 1)
 
 
+@pytest.mark.parametrize("rows", [2, 800])
+@pytest.mark.parametrize("n", [256, 509, 512, 1022, 1500, 2048, 3001, 4096, 6000, 8192, 12345, 16384, 30000])
+def test_select_every_width(rows, n):
+    """All numbers of warps and of blocks per thread, rows that start on 16-byte boundaries and not."""
+    g = np.random.default_rng(rows + n)
+    x = g.standard_normal((1, rows, 1, n)).astype(np.float32)
+    x[0, 0, 0, 5::7] = np.inf
+    x[0, 1, 0] = np.round(x[0, 1, 0] * 2) / 2
+    check_select(x[:, :min(rows, max(2, 1300000 // n))], [n * 16 - 3], 16, 37, 1, 2)
+
+
 def test_select_length_above_the_table():
     x = np.arange(8, dtype=np.float32).reshape(1, 1, 1, 8)
     sel, ln, st = (torch.zeros(1, 1, 1, 2, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda"), status())
