@@ -638,8 +638,8 @@ int echo_block_attention(const echo_block_attention_args *args, void *stream);
  * echo_block_summary: the smallest and the largest entry of the keys of a cache row, per dim,
  * over the tokens that its request holds.  Request b went from old_len[b] to new_len[b] tokens
  * (either way); the blocks that lost or gained a token and still have one are summed up anew,
- * the others' summaries stay.  A block in the tables of several requests has to be as full in
- * each that changed.
+ * the others' summaries stay (old_len[b] = 0 for a request whose tokens moved: all its blocks).
+ * A block in the tables of several requests has to be as full in each that changed.
  *   rows     [n_rows][R] cache rows of `format`, 16-byte aligned
  *   old_len  [B] int32 device, optional (NULL: 0, all blocks);  new_len [B] int32 device
  *   summary  [n_rows][2][head_dim] bf16 device, 16-byte aligned: minima, then maxima (a NaN
@@ -767,7 +767,9 @@ int echo_block_weights(const echo_block_weights_args *args, void *stream);
  * its own: the tokens of the first `sinks` slots and of the last `recent` positions stay, then
  * the heaviest by acc (a NaN is the lightest), ties to the lower slot.  Tokens that stay keep
  * their slots below `keep`; those at or above it move, in order, into the slots that fell free.
- * Attention without a window does not mind the order of a cache.
+ * Attention without a window does not mind the order of a cache.  A request that is cut has its
+ * blocks to itself: one that another request's table or another of its own entries names would be
+ * written for both.  Summaries of its blocks have to be made anew (old_len 0).
  *   rows     [n_rows][R] cache rows of `format`, 16-byte aligned: keys and values move as they are
  *   len      [B] int32 device: tokens held (clamped as above);  len_out [B] int32 device, another
  *            address: min(len, keep).  echo_block_tables from len to len_out then returns the
@@ -835,8 +837,9 @@ int echo_block_evict(const echo_block_evict_args *args, void *stream);
  * tensor cores' operand type), the own tokens' as in echo_block_attention.
  * Limits: those of echo_block_attention, n_groups in [1, 65536], n_rows at most 2^30, n_groups *
  * n_kv_heads * max_prefix_blocks below 2^31, (B * n_q * n_heads / n_kv_heads / 256 + n_groups) *
- * n_kv_heads * (max_prefix_blocks * block_tokens / 128 + 1) below 2^31 - 1024.  Launches 2 kernels, with own tokens 3 or 4; the first call that takes
- * some form of them sets it up, outside capture, as with echo_block_attention.
+ * n_kv_heads * (max_prefix_blocks * block_tokens / 128 + 1) below 2^31 - 1024.  Launches 2 kernels,
+ * with own tokens 3 or 4; the first call that takes some form of them sets it up, outside
+ * capture, as with echo_block_attention.
  */
 typedef struct echo_prefix_attention_args {
     const uint16_t *q;
