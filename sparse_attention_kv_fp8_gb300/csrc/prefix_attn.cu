@@ -61,7 +61,7 @@ struct PrefixParams {
   const float *own_o, *own_lse;       // [B n_q n_heads][D], or NULL
   uint16_t *out;
   float *lse;
-  int32_t grid;
+  int32_t grid, room;                 // CTAs; whether some are left to the own tokens
   int32_t *status;
 };
 
@@ -107,6 +107,11 @@ __device__ __forceinline__ int px_scan(int mine, int &total) {
 // begin and end inside a tile.  A CTA that changes tiles takes as long as kPxChange chunks more, so
 // whole pieces are taken where they are no longer than a share by more.
 constexpr int kPxChange = 5;
+// Where the own tokens have work for many SMs, shares of up to kPxRoom chunks leave them half: they wait for
+// those of a short prefix less than the SMs would wait for them (64 requests of 64 heads, a prefix of
+// 2048 and own tokens of up to 100 / 1000: 31.3 / 53.5 -> 26.4 / 44.6 us, of 4096 and 1000 56.5 -> 50.2;
+// shares of 8: 16 requests, 2048 and 100 19 -> 24 us).
+constexpr int kPxRoom = 6;
 constexpr int kPxFewGroups = 8;       // (more groups: their tiles are not tried)
 
 struct PxPlan {
@@ -116,6 +121,10 @@ struct PxPlan {
 __device__ __forceinline__ PxPlan px_plan(const PrefixParams &P, int total) {  // (by a whole warp)
   PxPlan x{0, 0, total};
   x.per = static_cast<int>((static_cast<uint32_t>(total) + P.grid - 1) / static_cast<uint32_t>(P.grid));
+  if (P.room) {  // (half of the SMs, as far as that makes no share longer than kPxRoom)
+    const uint32_t half = (static_cast<uint32_t>(total) + P.grid / 2) / (static_cast<uint32_t>(P.grid) / 2 + 1);
+    x.per = max(x.per, static_cast<int>(min(half, static_cast<uint32_t>(kPxRoom))));
+  }
   if (total == 0 || P.n_groups > kPxFewGroups) return x;
   const int lane = threadIdx.x & 31, len = x.per + lane;
   int64_t pieces = 0;
@@ -1155,6 +1164,7 @@ int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t st
   P.rest_o = reinterpret_cast<float *>(ws + s.rest_o), P.rest_ml = reinterpret_cast<float2 *>(ws + s.rest_ml);
   P.out = a->out, P.lse = a->lse, P.status = a->dev_status;
   P.grid = std::min(sms, echo::kPxMaxGrid);
+  P.room = a->table && static_cast<int64_t>(a->B) * a->n_kv_heads * 4 >= sms;
   if (a->table) P.own_o = reinterpret_cast<float *>(ws + s.own_o), P.own_lse = reinterpret_cast<float *>(ws + s.own_lse);
 
   int r;
