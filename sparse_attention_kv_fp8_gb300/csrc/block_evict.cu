@@ -314,7 +314,6 @@ struct EvictParams {
   int32_t *pos_out;
   int32_t *moves;                     // [B * n_kv]
   int2 *list;                         // [B * n_kv][keep] (from, to)
-  int32_t staged;                     // keys of a context fit in shared memory
   int32_t move_here;                  // moves made by the CTA that lists them
   int32_t move_ctas;
   int32_t *status;
@@ -404,7 +403,8 @@ __device__ __forceinline__ void move_tokens(const EvictParams &P, int b, int h, 
   }
 }
 
-template <int FMT, int D, int T>
+// STAGED: the keys of a context in shared memory; otherwise they are made again from what they come of
+template <int FMT, int D, int T, bool STAGED>
 __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
   constexpr int W = T / 32;
   extern __shared__ uint32_t ev_keys[];
@@ -483,13 +483,16 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
       const int i = i0 + r * T;
       if (i >= n) break;
       const uint32_t key = make_key(i, x[r], i < known ? y[r] : nxt - n + i);
-      if (P.staged) ev_keys[i] = key;
+      if constexpr (STAGED) ev_keys[i] = key;
       if (key == kMustKey) ++n_must;
       else if (key > zero) lo = min(lo, key), hi = max(hi, key);
     }
   }
   pick_stats(S, n_must, lo, hi);
-  auto key_at = [&](int i) -> uint32_t { return P.staged ? ev_keys[i] : key_of(i); };
+  auto key_at = [&](int i) -> uint32_t {
+    if constexpr (STAGED) return ev_keys[i];
+    else return key_of(i);
+  };
 
   // ----- the key above which all stay, and how many of its equals (n > keep: some go) -----
   uint32_t thr = kMustKey - 1, need = 0;
@@ -647,19 +650,20 @@ static int go_evict(echo::EvictParams P, cudaStream_t stream) {
   static std::atomic<bool> attr[kMaxDevices];
   const int64_t pairs = static_cast<int64_t>(P.B) * P.n_kv;
   const int64_t most = static_cast<int64_t>(P.max_blocks) * P.bsub * echo::kSubTokens;
-  P.staged = most <= echo::kEvStaged;
-  const int smem = P.staged ? static_cast<int>(most) * 4 : 0;
-  // (threads by the slots a pair may have: 512 CTAs' worth of either is on the device at once)
-  const bool wide = most > 8192;
+  const bool staged = most <= echo::kEvStaged;
+  const int smem = staged ? static_cast<int>(most) * 4 : 0;
   if (smem > 32768)   // (beside 9 KB of its own)
-    if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D, 1024>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
+    if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D, 1024, true>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
   int sms = 0;
   if (int rr = evict_sms(&sms)) return rr;
   const int64_t moves = std::max<int64_t>(0, std::min<int64_t>(P.keep, most - P.keep));
   P.move_here = moves <= 256;
   P.move_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((moves + 63) / 64, 8ll * sms / pairs)));
-  cudaError_t e = wide ? launch_pdl(echo::block_evict_kernel<FMT, D, 1024>, dim3(static_cast<unsigned>(pairs)), dim3(1024), smem, stream, P)
-                       : launch_pdl(echo::block_evict_kernel<FMT, D, 512>, dim3(static_cast<unsigned>(pairs)), dim3(512), smem, stream, P);
+  // threads by the slots a pair may have
+  const dim3 grid(static_cast<unsigned>(pairs));
+  cudaError_t e = most <= 8192 ? launch_pdl(echo::block_evict_kernel<FMT, D, 512, true>, grid, dim3(512), smem, stream, P)
+                : staged       ? launch_pdl(echo::block_evict_kernel<FMT, D, 1024, true>, grid, dim3(1024), smem, stream, P)
+                               : launch_pdl(echo::block_evict_kernel<FMT, D, 1024, false>, grid, dim3(1024), smem, stream, P);
   if (e == cudaSuccess && !P.move_here)
     e = launch_pdl(echo::block_move_kernel<FMT, D>, dim3(static_cast<unsigned>(pairs * P.move_ctas)), dim3(echo::kMvWarps * 32), 0, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block eviction launch");
