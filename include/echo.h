@@ -774,10 +774,10 @@ int echo_block_weights(const echo_block_weights_args *args, void *stream);
  *   len      [B] int32 device: tokens held (clamped as above);  len_out [B] int32 device, another
  *            address: min(len, keep).  echo_block_tables from len to len_out then returns the
  *            blocks that are no longer needed (before any of them is appended to)
- *   acc, acc_out [B][n_kv_heads][max_blocks * block_tokens] fp32 device: weights by slot before and
- *            after; entries past len_out are left as they were.  acc_out may be acc
+ *   acc, acc_out [B][n_kv_heads][max_blocks * block_tokens] fp32 device, 16-byte aligned: weights by
+ *            slot before and after; entries past len_out are left as they were.  acc_out may be acc
  *   pos, pos_out optional, together with pos_len and next_pos, needed for recent > 0; laid out as
- *            acc, int32: the position of each slot's token.  pos is read below pos_len[b]; the
+ *            acc, int32, 16-byte aligned: the position of each slot's token.  pos is read below pos_len[b]; the
  *            slots from there up to len[b] hold the newest tokens, the last of them at position
  *            next_pos[b] - 1.  pos_out may be pos
  * With acc_out and pos_out apart from acc and pos a call that is repeated on the same inputs gives

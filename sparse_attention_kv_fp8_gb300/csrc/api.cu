@@ -640,6 +640,8 @@ int echo_block_evict(const echo_block_evict_args *a, void *stream) {
           "len_out must not be one of the inputs");
   REQUIRE(aligned(a->rows, 16), "rows must be 16-byte aligned");
   REQUIRE(aligned(a->workspace, 256), "workspace must be 256-byte aligned");
+  REQUIRE(aligned(a->acc, 16) && aligned(a->acc_out, 16) && aligned(a->pos, 16) && aligned(a->pos_out, 16),
+          "acc, acc_out, pos and pos_out must be 16-byte aligned");
   REQUIRE(a->workspace_bytes >= block_evict_workspace_bytes(a->B, a->n_kv_heads, a->keep),
           "workspace smaller than echo_block_evict_workspace_bytes()");
   return launch_block_evict(a, static_cast<cudaStream_t>(stream));

@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(kWtWarps * 32, 4) block_weights_kernel(const W
 constexpr uint32_t kMustKey = 0xffffffffu;  // of a token that stays in any case
 constexpr int kEvBins = 2048;          // parts of the weights' range
 constexpr int kEvAhead = 8;           // slots a thread has under way
+constexpr int kEvVecs = 4;            // 16-byte pieces of weights, and of positions, a thread has under way
 constexpr int kEvStaged = 32768;      // tokens whose keys a CTA keeps in shared memory
 
 struct EvictParams {
@@ -405,11 +406,11 @@ __device__ __forceinline__ void move_tokens(const EvictParams &P, int b, int h, 
 
 // STAGED: the keys of a context in shared memory; otherwise they are made again from what they come of
 template <int FMT, int D, int T, bool STAGED>
-__global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
+__global__ void __launch_bounds__(T, 1024 / T) block_evict_kernel(const EvictParams P) {
   constexpr int W = T / 32;
-  extern __shared__ uint32_t ev_keys[];
+  extern __shared__ __align__(16) uint32_t ev_keys[];
   __shared__ PickSpace<W, kEvBins> S;
-  __shared__ uint32_t wcnt[2][W];
+  __shared__ uint32_t wcnt[3][W];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / P.n_kv, h = blockIdx.x - b * P.n_kv;
   pdl_launch_dependents();
@@ -468,24 +469,29 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
   pick_clear(S);
   const uint32_t zero = score_key(0.f);
   uint32_t lo = kMustKey, hi = 0, n_must = 0;   // (of the weights above zero)
-  for (int i0 = tid; i0 < n; i0 += kEvAhead * T) {
-    float x[kEvAhead];
-    int y[kEvAhead];
+  for (int i0 = 4 * tid; i0 < n; i0 += kEvVecs * 4 * T) {
+    uint4 x[kEvVecs], y[kEvVecs];   // (four slots each, which the table has in any case; all under way at once)
 #pragma unroll
-    for (int r = 0; r < kEvAhead; ++r) {
-      const int i = min(i0 + r * T, n - 1);
-      y[r] = 0;
-      asm volatile("ld.global.f32 %0, [%1];" : "=f"(x[r]) : "l"(acc + i));   // (all under way at once)
-      if (pos) asm volatile("ld.global.s32 %0, [%1];" : "=r"(y[r]) : "l"(pos + i));
+    for (int r = 0; r < kEvVecs; ++r) {
+      const int i = i0 + r * 4 * T;
+      x[r] = y[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < n) x[r] = load16_here(acc + i);
+      if (i < known) y[r] = load16_here(pos + i);
     }
 #pragma unroll
-    for (int r = 0; r < kEvAhead; ++r) {
-      const int i = i0 + r * T;
+    for (int r = 0; r < kEvVecs; ++r) {
+      const int i = i0 + r * 4 * T;
       if (i >= n) break;
-      const uint32_t key = make_key(i, x[r], i < known ? y[r] : nxt - n + i);
-      if constexpr (STAGED) ev_keys[i] = key;
-      if (key == kMustKey) ++n_must;
-      else if (key > zero) lo = min(lo, key), hi = max(hi, key);
+      const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w}, at[4] = {y[r].x, y[r].y, y[r].z, y[r].w};
+      uint32_t key[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        key[k] = make_key(i + k, __uint_as_float(w[k]), i + k < known ? static_cast<int>(at[k]) : nxt - n + i + k);
+        if (i + k >= n) continue;
+        if (key[k] == kMustKey) ++n_must;
+        else if (key[k] > zero) lo = min(lo, key[k]), hi = max(hi, key[k]);
+      }
+      if constexpr (STAGED) *reinterpret_cast<uint4 *>(ev_keys + i) = make_uint4(key[0], key[1], key[2], key[3]);
     }
   }
   pick_stats(S, n_must, lo, hi);
@@ -524,9 +530,7 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
     }
     if (lane == 31) wcnt[which][warp] = upto;
     __syncthreads();
-    uint32_t before = upto - mine;
-    for (int w = 0; w < warp; ++w) before += wcnt[which][w];
-    return before;
+    return upto - mine + __reduce_add_sync(~0u, lane < warp ? wcnt[which][lane % W] : 0u);
   };
   uint32_t eq0 = 0;
   if (!all_equal) {
@@ -534,42 +538,46 @@ __global__ void __launch_bounds__(T) block_evict_kernel(const EvictParams P) {
     for (int i = i0; i < i1; ++i) eq += key_at(i) == thr;
     eq0 = scan(eq, 0);
   }
-  // f(i, whether it stays) for each slot of the run
-  auto walk = [&](int from, int to, auto &&f) {
-    for (int i = from; i < to; ++i) {
-      const uint32_t key = key_at(i);
-      f(i, key > thr || (key == thr && (all_equal || eq0 < need)));
-      eq0 += key == thr;
-    }
+  // whether slot i's token is one of those that stay; called for the slots of the run one after another
+  auto stays = [&](int i) {
+    const uint32_t key = key_at(i);
+    const bool equal = key == thr, yes = key > thr || (equal && (all_equal || eq0 < need));
+    eq0 += equal;
+    return yes;
   };
-  // (as bits, 64 slots of a run at a time: all of it where keys are in shared memory)
-  uint32_t holes = 0, movers = 0;
+  // (as bits, the first 64 slots of a run: all of it where keys are in shared memory)
+  uint32_t holes = 0, movers = 0, marks[2];
   const uint32_t eq_first = eq0;
-  uint64_t marks = 0;       // of the first 64 slots: a hole, or a mover
-  walk(i0, i1, [&](int i, bool stays) {
-    const bool mark = stays == (i >= P.keep);
-    if (mark && i - i0 < 64) marks |= 1ull << (i - i0);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int from = i0 + 32 * half, to = min(from + 32, i1);
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int i = from; i < to; ++i) m |= stays(i) == (i >= P.keep) ? 1u << (i - from) : 0u;
+    const uint32_t below = P.keep >= from + 32 ? ~0u : P.keep > from ? (1u << (P.keep - from)) - 1 : 0u;
+    holes += __popc(m & below), movers += __popc(m & ~below);
+    marks[half] = m;
+  }
+  for (int i = i0 + 64; i < i1; ++i) {
+    const bool mark = stays(i) == (i >= P.keep);
     holes += mark && i < P.keep, movers += mark && i >= P.keep;
-  });
-  uint32_t hole_at = scan(holes, 1);
-  __syncthreads();
-  uint32_t mover_at = scan(movers, 0);
+  }
+  uint32_t hole_at = scan(holes, 1), mover_at = scan(movers, 2);
   int2 *list = P.list + static_cast<int64_t>(blockIdx.x) * P.keep;
   auto note = [&](int i) {
     if (i < P.keep) list[hole_at++].y = i;
     else list[mover_at++].x = i;
   };
-  for (; marks; marks &= marks - 1) note(i0 + __ffsll(marks) - 1);
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+    for (uint32_t m = marks[half]; m; m &= m - 1) note(i0 + 32 * half + __ffs(m) - 1);
   if (i1 - i0 > 64) {       // (longer runs: looked at once more)
     eq0 = eq_first;
-    walk(i0, i1, [&](int i, bool stays) {
-      if (i - i0 >= 64 && stays == (i >= P.keep)) note(i);
-    });
+    for (int i = i0; i < i1; ++i)
+      if (stays(i) == (i >= P.keep) && i - i0 >= 64) note(i);
   }
   __syncthreads();
-  uint32_t count = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) count += wcnt[0][w];
+  const uint32_t count = __reduce_add_sync(~0u, lane < W ? wcnt[2][lane % W] : 0u);
   if (tid == 0) P.moves[blockIdx.x] = count;
 
   // ----- weights and positions: those that keep their slot, then those that move -----

@@ -225,6 +225,13 @@ def test_evict_at_the_edges_of_shared_memory(slots):
     run_evict(BF16, 64, 64, 1, [slots], 300, sinks=4, recent=100, seed=9, twice=False)
 
 
+def test_evict_runs_of_more_slots_than_marks():
+    """More than 64 slots a thread."""
+    run_evict(FP4, 64, 64, 1, [70000, 66001], 800, sinks=4, recent=64, new=100, seed=13, twice=False)
+    acc = np.full((1, 1, 67008), 0.5, np.float32)
+    run_evict(FP4, 64, 64, 1, [67000], 66000, acc=acc, seed=14, twice=False)
+
+
 def test_evict_more_recent_positions_than_room():
     """Positions that repeat (a caller's mistake): more tokens are recent than may stay; the first slots do."""
     g = np.random.default_rng(8)

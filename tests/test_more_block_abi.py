@@ -110,6 +110,7 @@ CASES = [
     ("echo_block_evict", dict(pos=None, pos_out=None, pos_len=None, next_pos=None), b"recent needs pos"),
     ("echo_block_evict", dict(len_out=64), b"len_out"), ("echo_block_evict", dict(len_out=160), b"len_out"),
     ("echo_block_evict", dict(acc=None), b"NULL"), ("echo_block_evict", dict(workspace=None), b"NULL"),
+    *[("echo_block_evict", {f: 72}, b"16-byte") for f in ("acc", "acc_out", "pos", "pos_out")],
     ("echo_block_evict", dict(workspace=128), b"256-byte"), ("echo_block_evict", dict(workspace_bytes=100), b"smaller"),
     ("echo_block_evict", dict(B=1 << 23), b"2^26"),
     ("echo_prefix_attention", dict(n_groups=0), b"n_groups"), ("echo_prefix_attention", dict(n_groups=65537), b"n_groups"),
