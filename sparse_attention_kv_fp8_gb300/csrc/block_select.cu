@@ -11,18 +11,26 @@
 // reads 4 D bytes for a block whose keys take 2 D bytes a token.
 //
 // sm_103a design.
-//   Summary: a CTA of 128 threads per (block, KV head), 16-byte loads of its keys, packed
-//     minima and maxima, joined over the lanes and then the warps.  The blocks that changed
-//     are one line over the requests, found by every CTA from the lengths.
+//   Summary: a warp per (block, KV head), or a CTA where blocks are large: 16-byte loads of its keys, eight
+//     a lane under way, packed minima and maxima, joined over the lanes.  The blocks that changed are one
+//     line over the requests, found by every CTA from the lengths.  8 prompts of 16384 tokens (8 KV heads of
+//     128 dims, bf16, blocks of 64): 39 us, 4.8 TB/s; one more token for 64 requests: 5.6 us, three chained
+//     loads (length, id, keys) and a launch.
 //   Scores: 16 blocks x 8 columns with mma.m16n8k16.  The order of a contraction's dims is free,
 //     so a lane reads 16 contiguous bytes of "its" two blocks per 8 dims of a quarter and feeds them
 //     as they are: a warp has the 16 summaries (8 KB) in registers after one round of loads, with
 //     no shared memory.  The 8 columns are the heads of one query token, or of several where a
 //     group has fewer, so the maximum over a group stays within a quad.
+//     16 requests of up to 131072 tokens, blocks of 64, 64 heads on 8 of 128 dims: 19.5 us, 0.81 of the copy
+//     rate.  Many query tokens (512 of them against 1024 blocks: 97 us, 177 TFLOP/s) are bound by
+//     instructions, 235 for 16 products of 8 columns; the tensor cores' own operands in shared memory would
+//     serve them better.
 //   Selection: one to 32 warps per (query, KV head), a thread with 4 to 32 blocks that follow one another,
 //     their scores in registers.  The k-th best is found from counts over the range of the scores
 //     (block_pick.cuh), then a sum over the threads gives each the place of what it writes: those above,
 //     and the first of its equals.
+//     8000 rows of 1024 blocks: 29 us, bound by instructions (the pipe of comparisons 62% busy); 256 rows of
+//     2048: 6 us, of which a launch and the chain of loads, counts and barriers are nearly all.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -92,17 +100,17 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
-template <int FMT, int D>
+// TEAM threads take a block: a warp, or the CTA
+template <int FMT, int D, int TEAM>
 __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const SummaryParams P) {
   constexpr bool kFp4 = FMT == ECHO_BLOCK_FP4;
   constexpr int kWords = kFp4 ? 16 : 4;               // pairs of dims that a thread holds
   constexpr int kLanes = D / (2 * kWords);            // threads of a token
-  constexpr int kTeam = kFp4 ? 32 : kSumThreads;      // threads of a block: a warp has 64 4-bit keys in flight
-  constexpr int kTeams = kSumThreads / kTeam;
-  constexpr int kTokens = kTeam / kLanes;             // tokens a round
+  constexpr int kTeams = kSumThreads / TEAM;
+  constexpr int kTokens = TEAM / kLanes;              // tokens a round
   constexpr int kRounds = 8;                          // rounds of loads in flight
   extern __shared__ int32_t sum_cu[];                 // [B + 1] exclusive sums of the redone blocks
-  __shared__ uint32_t part[kFp4 ? 1 : 4][2][D / 2];
+  __shared__ uint32_t part[TEAM == 32 ? 1 : 4][2][D / 2];
   __shared__ int32_t wsum[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
   __syncthreads();
   const int64_t units = static_cast<int64_t>(sum_cu[P.B]) * P.tab.n_kv;
 
-  const int t0 = tid % kTeam / kLanes, c = tid % kLanes;
+  const int t0 = tid % TEAM / kLanes, c = tid % kLanes;
   // where a (block, KV head) lies and how many tokens it has; row -1: past the end, or not there
   int64_t row = -1, next_row = -1;
   int n = 0, next_n = 0;
@@ -152,16 +160,16 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
     next_row = P.tab.row(b, h, e);
     next_n = min(P.bs, held_len(P.new_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, nullptr, false) - e * P.bs);
   };
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kTeams + tid / kTeam, stride = static_cast<int64_t>(gridDim.x) * kTeams;
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kTeams + tid / TEAM, stride = static_cast<int64_t>(gridDim.x) * kTeams;
   look_up(u0);
   for (int64_t u = u0; u < units; u += stride) {
     row = next_row, n = next_n;
     if (row < 0 || row >= P.n_rows) {  // (the same for the whole team)
-      if (row >= 0 && tid % kTeam == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
+      if (row >= 0 && tid % TEAM == 0) set_status(P.status, ECHO_DEV_BAD_INDEX);
       look_up(u + stride);
       continue;
     }
-    // (rounds past the last token read it again: a minimum does not mind)
+    // (lanes past the last token read it again: a minimum does not mind)
     const uint8_t *src = P.rows + row * P.row_bytes;
     uint32_t lo[kWords], hi[kWords];
 #pragma unroll
@@ -172,8 +180,8 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
         const int tk = min(t + r * kTokens + t0, n - 1);
+        if (t + r * kTokens >= n) break;
         if constexpr (kFp4) {
-          if (t + r * kTokens >= n) break;
           const uint8_t *sub = src + (tk / kSubTokens) * Fp4Sub<D>::kBytes;
           x[r] = load16_here(sub + (tk % kSubTokens) * (D / 2) + c * 16);
           sc[r] = load2_here(sub + Fp4Sub<D>::kKeyScales + (tk % kSubTokens) * (D / 16) + c * 2);
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
       if (t == 0) look_up(u + stride);  // (while the loads are under way)
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
-        if (kFp4 && t + r * kTokens >= n) break;
+        if (t + r * kTokens >= n) break;
         const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
         if constexpr (kFp4) {
           const uint32_t s2 = e4m3x2_to_half2(sc[r]);
@@ -206,11 +214,11 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
         }
       }
     }
-    if constexpr (kFp4) {
+    if constexpr (TEAM == 32) {
       // Joined over the lanes of the same dims, each of which hands half of its words over and keeps the
-      // other: minima, and maxima as minima of what is less, first (28 shuffles a lane, not 96).  What is
-      // left are D / 32 words from word `at` on: one store.
-      constexpr int kLeft = 32 / kTokens;
+      // other: minima, and maxima as minima of what is less, first (4 bits: 28 shuffles a lane, not 96).
+      // What is left are D / 32 words from word `at` on: one store.
+      constexpr int kLeft = 2 * kWords / kTokens;
       const uint32_t flip = lane & 16 ? 0x80008000u : 0u;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -229,10 +237,12 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
       }
       uint32_t v[kLeft];
 #pragma unroll
-      for (int i = 0; i < kLeft; ++i) {  // (6 significant bits: exact in bf16, a power of two less too)
-        const uint32_t y = lo[i] ^ flip;
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-        v[i] = pack2<false>(f.x * P.k_scale, f.y * P.k_scale);
+      for (int i = 0; i < kLeft; ++i) {  // (4 bits: 6 significant ones, exact in bf16, a power of two less too)
+        v[i] = lo[i] ^ flip;
+        if constexpr (kFp4) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+          v[i] = pack2<false>(f.x * P.k_scale, f.y * P.k_scale);
+        }
       }
       uint32_t *dst = P.summary + row * D + (lane & 16 ? D / 2 : 0) + at;
       if constexpr (kLeft == 4) *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -583,18 +593,19 @@ static int sm_count(int *sms) {
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block selection device");
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int TEAM>
 static int go_summary(const echo::SummaryParams &P, cudaStream_t stream) {
   static std::atomic<bool> attr[kMaxDevices];
   const int smem = (P.B + 1) * 4;
   if (smem > 40960)
-    if (int rr = smem_limit_once(attr, echo::block_summary_kernel<FMT, D>, (16384 + 1) * 4, "block summary smem attribute")) return rr;
+    if (int rr = smem_limit_once(attr, echo::block_summary_kernel<FMT, D, TEAM>, (16384 + 1) * 4, "block summary smem attribute")) return rr;
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
   const int64_t most = static_cast<int64_t>(P.B) * P.tab.max_blocks * P.tab.n_kv;
-  const int64_t ctas = FMT == ECHO_BLOCK_FP4 ? (most + 3) / 4 : most;   // (4 bits: a warp per block)
+  constexpr int kTeams = echo::kSumThreads / TEAM;
+  const int64_t ctas = (most + kTeams - 1) / kTeams;
   const int64_t grid = std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 16);
-  cudaError_t e = launch_pdl(echo::block_summary_kernel<FMT, D>, dim3(static_cast<unsigned>(grid)), dim3(echo::kSumThreads), smem, stream, P);
+  cudaError_t e = launch_pdl(echo::block_summary_kernel<FMT, D, TEAM>, dim3(static_cast<unsigned>(grid)), dim3(echo::kSumThreads), smem, stream, P);
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block summary launch");
 }
 
@@ -608,9 +619,16 @@ int launch_block_summary(const echo_block_summary_args *a, cudaStream_t stream) 
   P.summary = reinterpret_cast<uint32_t *>(a->summary);
   P.k_scale = std::ldexp(1.f, -a->k_shift);
   P.status = a->dev_status;
+  // A warp a block: no barriers, and no threads without a token (8 prompts of 16384 tokens, 8 KV heads of
+  // 128 dims, bf16, blocks of 16 / 32 / 64: 86 / 52 / 41 us by CTAs, 42 / 40 / 40 by warps; in 4 bits
+  // blocks of 64 took 45, take 26).  Larger blocks of bf16 by CTAs: a warp has 16 keys under way at once,
+  // and a step that changes one block of each request would wait for all of it.
   if (a->format == ECHO_BLOCK_FP4)
-    return a->head_dim == 128 ? go_summary<ECHO_BLOCK_FP4, 128>(P, stream) : go_summary<ECHO_BLOCK_FP4, 64>(P, stream);
-  return a->head_dim == 128 ? go_summary<ECHO_BLOCK_BF16, 128>(P, stream) : go_summary<ECHO_BLOCK_BF16, 64>(P, stream);
+    return a->head_dim == 128 ? go_summary<ECHO_BLOCK_FP4, 128, 32>(P, stream) : go_summary<ECHO_BLOCK_FP4, 64, 32>(P, stream);
+  if (a->block_tokens * a->head_dim <= 64 * 128)
+    return a->head_dim == 128 ? go_summary<ECHO_BLOCK_BF16, 128, 32>(P, stream) : go_summary<ECHO_BLOCK_BF16, 64, 32>(P, stream);
+  return a->head_dim == 128 ? go_summary<ECHO_BLOCK_BF16, 128, echo::kSumThreads>(P, stream)
+                            : go_summary<ECHO_BLOCK_BF16, 64, echo::kSumThreads>(P, stream);
 }
 
 int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
