@@ -81,6 +81,13 @@ def test_summary_nan_keys_and_bad_ids():
     assert (got[7, 0] == c.k[7].min(0)).all() and (got[7, 1] == c.k[7].max(0)).all()
 
 
+@pytest.mark.parametrize("fmt", [BF16, FP4])
+@pytest.mark.parametrize("D,bs", [(128, 128), (64, 256), (128, 208)])
+def test_summary_of_large_blocks(fmt, D, bs):
+    check_summary(fmt, D, bs, 2, [0, 1, bs - 1, bs, bs + 1, 3 * bs + 5, 7], None, seed=7)
+    check_summary(fmt, D, bs, 2, [5, bs, bs + 60, 2 * bs, 2 * bs, 0], [4, bs - 1, bs, 2 * bs, bs + 1, 9], gaps=0.2, seed=8)
+
+
 # ---------------------------------------------------------------------------
 # scores
 # ---------------------------------------------------------------------------
