@@ -675,7 +675,8 @@ int echo_block_summary(const echo_block_summary_args *args, void *stream);
  *   ctx_len  [B] int32 device
  *   scores   [B][n_q][n_kv_heads][max_blocks] fp32 device
  * Limits: max_blocks * block_tokens below 2^31 - 1024, B * n_kv_heads * (max_blocks / 64 + 1)
- * and B * n_q * n_heads below 2^31.  Launches 1 kernel.
+ * and B * n_q * n_heads below 2^31, n_q times the heads of a group (in whole eights) below 2^30.
+ * Launches 1 kernel.
  */
 typedef struct echo_block_scores_args {
     const uint16_t *q;

@@ -563,6 +563,9 @@ int echo_block_scores(const echo_block_scores_args *a, void *stream) {
   TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
   REQUIRE(static_cast<long long>(a->B) * a->n_kv_heads <= ((1ll << 31) - 1) / (a->max_blocks / 64 + 1),
           "B * n_kv_heads * (max_blocks / 64 + 1) must be below 2^31");
+  // (a group's columns are padded to whole eights and counted in 31 bits)
+  REQUIRE(static_cast<long long>(a->n_q) * ((a->n_heads / a->n_kv_heads + 7) / 8 * 8) < (1ll << 30),
+          "n_q * n_heads / n_kv_heads, whole eights of heads, must be below 2^30");
   REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
   REQUIRE(std::isfinite(a->scale), "scale must be finite");
   if (a->B == 0) return ECHO_OK;

@@ -95,6 +95,7 @@ CASES = [
     ("echo_block_scores", dict(head_dim=32), b"head_dim"), ("echo_block_scores", dict(summary=None), b"NULL"),
     ("echo_block_scores", dict(scores=None), b"NULL"), ("echo_block_scores", dict(n_rows=0), b"n_rows"),
     ("echo_block_scores", dict(B=65536, max_blocks=1 << 20, block_tokens=16, n_heads=8), b"2^31"),
+    ("echo_block_scores", dict(B=1, n_q=65536, n_heads=16384, n_kv_heads=1, table_heads=1), b"2^30"),
     ("echo_block_select", dict(k=0), b"k must"), ("echo_block_select", dict(first=-1), b"first"), ("echo_block_select", dict(last=4), b"first"),
     ("echo_block_select", dict(max_blocks=32769), b"32768"), ("echo_block_select", dict(table=None), b"sel_rows"),
     ("echo_block_select", dict(scores=None), b"NULL"), ("echo_block_select", dict(sel=None), b"NULL"),
