@@ -93,6 +93,15 @@ __device__ __forceinline__ PxGroup px_group(const PrefixParams &P, int g, bool r
 // (below 2^31 over all groups: the host checks the sizes)
 __device__ __forceinline__ int px_units(const PrefixParams &P, const PxGroup &x) { return P.n_kv * x.tiles * x.chunks; }
 
+// Group g (the same for the whole warp): from the lane that has it, `mine`, where there is one a lane.
+__device__ __forceinline__ PxGroup px_group_of(const PrefixParams &P, const PxGroup &mine, int g) {
+  if (P.n_groups > 32) return px_group(P, g, false);
+  PxGroup x;
+  x.b0 = __shfl_sync(~0u, mine.b0, g), x.rows = __shfl_sync(~0u, mine.rows, g), x.len = __shfl_sync(~0u, mine.len, g);
+  x.tiles = __shfl_sync(~0u, mine.tiles, g), x.chunks = __shfl_sync(~0u, mine.chunks, g);
+  return x;
+}
+
 // exclusive sum over the lanes of a warp, and the total
 __device__ __forceinline__ int px_scan(int mine, int &total) {
   int upto = mine;
@@ -122,7 +131,7 @@ struct PxPlan {
   int whole, per, total;
 };
 
-__device__ __forceinline__ PxPlan px_plan(const PrefixParams &P, int total) {  // (by a whole warp)
+__device__ __forceinline__ PxPlan px_plan(const PrefixParams &P, const PxGroup &mine, int total) {  // (by a whole warp)
   PxPlan x{0, 0, total};
   x.per = static_cast<int>((static_cast<uint32_t>(total) + P.grid - 1) / static_cast<uint32_t>(P.grid));
   if (P.room) {  // (half of the SMs, as far as that makes no share longer than kPxRoom)
@@ -133,7 +142,7 @@ __device__ __forceinline__ PxPlan px_plan(const PrefixParams &P, int total) {  /
   const int lane = threadIdx.x & 31, len = x.per + lane;
   int64_t pieces = 0;
   for (int g = 0; g < P.n_groups; ++g) {
-    const PxGroup y = px_group(P, g, false);
+    const PxGroup y = px_group_of(P, mine, g);
     pieces += static_cast<int64_t>(P.n_kv) * y.tiles * ((static_cast<uint32_t>(y.chunks) + len - 1) / static_cast<uint32_t>(len));
   }
   const uint32_t fits = __ballot_sync(~0u, lane <= kPxChange && pieces <= P.grid);
@@ -160,13 +169,14 @@ struct PxLine {
     const int lane = threadIdx.x & 31;
     const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
     int mine = 0, total;
-    for (int i = g0; i < g1; ++i) mine += px_units(P, px_group(P, i, report));
+    PxGroup last{};
+    for (int i = g0; i < g1; ++i) last = px_group(P, i, report), mine += px_units(P, last);
     const int before = px_scan(mine, total);
-    const PxPlan plan = px_plan(P, total);
+    const PxPlan plan = px_plan(P, last, total);
     if (plan.whole) {
       int at = blockIdx.x;
       for (g = 0; g < P.n_groups; ++g) {
-        x = px_group(P, g, false);
+        x = px_group_of(P, last, g);
         int len;
         const int pieces = px_pieces(plan, x, len), all = P.n_kv * x.tiles * pieces;
         if (at >= all) {
@@ -199,7 +209,7 @@ struct PxLine {
     const int src = __ffs(__ballot_sync(~0u, own)) - 1;
     g = __shfl_sync(~0u, at, src);
     off = __shfl_sync(~0u, off, src);
-    x = px_group(P, g, false);
+    x = px_group_of(P, last, g);
     const uint32_t tile = static_cast<uint32_t>(off) / static_cast<uint32_t>(x.chunks);
     c = off - tile * x.chunks;
     h = tile / static_cast<uint32_t>(x.tiles), t = tile - h * x.tiles;
@@ -902,8 +912,50 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
   const int64_t all = static_cast<int64_t>(P.B) * P.n_q * P.n_heads;
   const int64_t at_row = static_cast<int64_t>(blockIdx.x) * (kPxMergeWarps / RW) + warp / RW, row = at_row < all ? at_row : all - 1;
   pdl_launch_dependents();
+  // (Where the row's tile lies is found before the wait: it comes of the call's inputs alone, and the
+  // prefix's kernel, which lets this one and the own tokens' start, has waited for whatever wrote them.)
+  const uint32_t bj = static_cast<uint32_t>(row) / static_cast<uint32_t>(P.n_heads), head = static_cast<uint32_t>(row) - bj * P.n_heads;
+  const int b = bj / static_cast<uint32_t>(P.n_q), j = bj - b * P.n_q, h = head / static_cast<uint32_t>(P.group);
+
+  // where the row's tile lies on the line
+  const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
+  int mine = 0, u = 0, total, at = -1, r = 0;
+  PxGroup last{};
+  for (int g = g0; g < g1; ++g) {
+    const PxGroup x = last = px_group(P, g, false);
+    const int in = (b - x.b0) * P.n_q * P.group;   // (rows of a request outside the group are not below x.rows)
+    if (at < 0 && x.chunks > 0 && b >= x.b0 && in < x.rows) at = g, u = mine, r = in + j * P.group + head - h * P.group;
+    mine += px_units(P, x);
+  }
+  u += px_scan(mine, total);
+  const PxPlan plan = px_plan(P, last, total);
+  const uint32_t who = __ballot_sync(~0u, at >= 0);
+  int first = 0, pieces = 0, step = 1;   // the tile's first CTA, how many pieces it has, their CTAs' distance
+  if (who) {
+    const int src = __ffs(who) - 1;
+    at = __shfl_sync(~0u, at, src);
+    u = __shfl_sync(~0u, u, src);
+    r = __shfl_sync(~0u, r, src);
+    const PxGroup x = px_group_of(P, last, at);
+    const int tile = r / kPxRows;
+    if (plan.whole) {
+      int len;
+      for (int g = 0; g < at; ++g) {
+        const PxGroup y = px_group_of(P, last, g);
+        first += P.n_kv * y.tiles * px_pieces(plan, y, len);
+      }
+      pieces = px_pieces(plan, x, len);
+      first += h * pieces * x.tiles + tile;
+      step = x.tiles;
+    } else {
+      u += (h * x.tiles + tile) * x.chunks;
+      first = u / plan.per;
+      pieces = (u + x.chunks - 1) / plan.per - first + 1;
+    }
+    r %= kPxRows;
+  }
+
   pdl_wait();
-  // what every row may need is under way while its tile is looked for
   auto load = [&](const float *o, float (&x)[kPer]) {
     if constexpr (kPer == 4) {
       const float4 y = *reinterpret_cast<const float4 *>(o);
@@ -927,46 +979,6 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
     own_lse = P.own_lse[row];
     load(P.own_o + row * D + lane * kPer, own_x);
   }
-  const uint32_t bj = static_cast<uint32_t>(row) / static_cast<uint32_t>(P.n_heads), head = static_cast<uint32_t>(row) - bj * P.n_heads;
-  const int b = bj / static_cast<uint32_t>(P.n_q), j = bj - b * P.n_q, h = head / static_cast<uint32_t>(P.group);
-
-  // where the row's tile lies on the line
-  const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
-  int mine = 0, u = 0, total, at = -1, r = 0;
-  for (int g = g0; g < g1; ++g) {
-    const PxGroup x = px_group(P, g, false);
-    const int in = (b - x.b0) * P.n_q * P.group;   // (rows of a request outside the group are not below x.rows)
-    if (at < 0 && x.chunks > 0 && b >= x.b0 && in < x.rows) at = g, u = mine, r = in + j * P.group + head - h * P.group;
-    mine += px_units(P, x);
-  }
-  u += px_scan(mine, total);
-  const PxPlan plan = px_plan(P, total);
-  const uint32_t who = __ballot_sync(~0u, at >= 0);
-  int first = 0, pieces = 0, step = 1;   // the tile's first CTA, how many pieces it has, their CTAs' distance
-  if (who) {
-    const int src = __ffs(who) - 1;
-    at = __shfl_sync(~0u, at, src);
-    u = __shfl_sync(~0u, u, src);
-    r = __shfl_sync(~0u, r, src);
-    const PxGroup x = px_group(P, at, false);
-    const int tile = r / kPxRows;
-    if (plan.whole) {
-      int len;
-      for (int g = 0; g < at; ++g) {
-        const PxGroup y = px_group(P, g, false);
-        first += P.n_kv * y.tiles * px_pieces(plan, y, len);
-      }
-      pieces = px_pieces(plan, x, len);
-      first += h * pieces * x.tiles + tile;
-      step = x.tiles;
-    } else {
-      u += (h * x.tiles + tile) * x.chunks;
-      first = u / plan.per;
-      pieces = (u + x.chunks - 1) / plan.per - first + 1;
-    }
-    r %= kPxRows;
-  }
-
   float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
