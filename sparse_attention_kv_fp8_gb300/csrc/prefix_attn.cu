@@ -956,39 +956,27 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
   }
 
   pdl_wait();
-  auto load = [&](const float *o, float (&x)[kPer]) {
+  auto load = [&](const float *o, float (&x)[kPer]) {   // (under way from here on)
     if constexpr (kPer == 4) {
-      const float4 y = *reinterpret_cast<const float4 *>(o);
-      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+      const uint4 y = load16_here(o);
+      x[0] = __uint_as_float(y.x), x[1] = __uint_as_float(y.y), x[2] = __uint_as_float(y.z), x[3] = __uint_as_float(y.w);
     } else {
-      const float2 y = *reinterpret_cast<const float2 *>(o);
-      x[0] = y.x, x[1] = y.y;
+      const uint2 y = load8_here(o);
+      x[0] = __uint_as_float(y.x), x[1] = __uint_as_float(y.y);
     }
   };
-  float own_x[kPer], first_x[kPer], own_lse = -INFINITY;
+  float own_x[kPer], own_lse = -INFINITY;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) own_x[k] = 0.f;
-  float2 first_ml = make_float2(-INFINITY, 0.f);
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) first_x[k] = 0.f;
-  if (mine_of == 0) {
-    first_ml = P.first_ml[row];
-    load(P.first_o + row * D + lane * kPer, first_x);
-  }
   if (mine_of == 0 && P.own_o) {
-    own_lse = P.own_lse[row];
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(own_lse) : "l"(P.own_lse + row));
     load(P.own_o + row * D + lane * kPer, own_x);
   }
   float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  if (pieces > 0 && first_ml.x != -INFINITY) {
-    top = first_ml.x, sum = first_ml.y;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = first_x[k];
-  }
   constexpr int kAhead = RW > 1 ? 6 : 4;
-  for (int p0 = 1 + mine_of; p0 < pieces; p0 += kAhead * RW) {   // pieces p0, p0 + RW, ...
+  for (int p0 = mine_of; p0 < pieces; p0 += kAhead * RW) {   // pieces p0, p0 + RW, ...
     float2 ml[kAhead];
     float x[kAhead][kPer];
 #pragma unroll
@@ -997,10 +985,11 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 #pragma unroll
       for (int k = 0; k < kPer; ++k) x[p][k] = 0.f;
       const int i = p0 + p * RW;
-      if (i < pieces) {
-        const int64_t from = static_cast<int64_t>(first + i * step) * kPxRows + r;
-        ml[p] = P.rest_ml[from];
-        load(P.rest_o + from * D + lane * kPer, x[p]);
+      if (i < pieces) {   // (the first in a row per query row, the others in their CTAs' slots)
+        const int64_t from = i ? static_cast<int64_t>(first + i * step) * kPxRows + r : row;
+        const uint2 y = load8_here((i ? P.rest_ml : P.first_ml) + from);
+        ml[p] = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
+        load((i ? P.rest_o : P.first_o) + from * D + lane * kPer, x[p]);
       }
     }
     float up = top;
