@@ -27,10 +27,10 @@
 //     fp32: pieces that begin with a tile in a row per query row, the others in a slot per CTA.
 //     The merge kernel takes them in order, so results do not depend on timing.
 //   64 requests of 64 heads (8 KV heads of 128 dims), a prefix of 32768: bf16 64 us, 1050 TFLOP/s (256
-//     requests: 217 us, 1260), 4 bits 74 us.  The tensor cores are busy half of the time and the exponentials'
+//     requests: 216 us, 1270), 4 bits 72 us.  The tensor cores are busy half of the time and the exponentials'
 //     pipe a quarter: a warpgroup's chunk is a chain (scores, maximum, weights, hand-over) that two sub-tiles
 //     cover only in part; more would need registers for a third.  A prefix of 131072 for 8 requests:
-//     91 us, 0.89 of the copy rate.  Short ones (1000 tokens: 12.5 us) are two kernels' chains of latencies.
+//     89 us, 0.92 of the copy rate.  Short ones (1000 tokens: 10.5 us) are two kernels' chains of latencies.
 #include <algorithm>
 #include <cmath>
 
@@ -122,7 +122,8 @@ __device__ __forceinline__ int px_scan(int mine, int &total) {
 constexpr int kPxChange = 5;
 // Where the own tokens have work for many SMs, shares of up to kPxRoom chunks leave them half: they wait for
 // those of a short prefix less than the SMs would wait for them (64 requests of 64 heads, a prefix of
-// 2048 and own tokens of up to 100 / 1000: 31.3 / 53.5 -> 26.4 / 44.6 us, of 4096 and 1000 56.5 -> 50.2;
+// 2048 and own tokens of up to 100 / 1000: 31.3 / 53.5 -> 26.4 / 44.6 us, of 4096 and 1000 56.5 -> 50.2,
+// before the merge took less;
 // shares of 8: 16 requests, 2048 and 100 19 -> 24 us).
 constexpr int kPxRoom = 6;
 constexpr int kPxFewGroups = 8;       // (more groups: their tiles are not tried)
