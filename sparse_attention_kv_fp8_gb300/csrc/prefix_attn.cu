@@ -1186,8 +1186,8 @@ int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t st
     o.k_shift = a->k_shift, o.v_shift = a->v_shift;
     if (int rr = launch_block_attention_f32(&o, reinterpret_cast<float *>(ws + s.own_o), stream)) return rr;
   }
-  // four warps a row where there are few (1024 rows of 19 pieces: 42.6 -> 39.1 us in all), one where
-  // there are many, which all look up where they are (4096 rows of 9 pieces: 65 us, with four 72.7)
+  // four warps a row where there are few rows (1024 of a prefix of 2048: 13.5 us in all, with one 15.2), one
+  // where four would make several waves of CTAs (4096 of a prefix of 32768: 63.7 us, with four 70.3)
   e = a->head_dim == 128 ? (rows <= 2048 ? go_merge<128, 4>(P, rows, stream) : go_merge<128, 1>(P, rows, stream))
                          : (rows <= 2048 ? go_merge<64, 4>(P, rows, stream) : go_merge<64, 1>(P, rows, stream));
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "prefix attention merge launch");
