@@ -21,8 +21,8 @@
 //     as they are: a warp has the 16 summaries (8 KB) in registers after one round of loads, with
 //     no shared memory.  The 8 columns are the heads of one query token, or of several where a
 //     group has fewer, so the maximum over a group stays within a quad.
-//     16 requests of up to 131072 tokens, blocks of 64, 64 heads on 8 of 128 dims: 19.5 us, 0.81 of the copy
-//     rate.  Many query tokens (512 of them against 1024 blocks: 97 us, 177 TFLOP/s) are bound by
+//     64 requests of up to 131072 tokens, blocks of 64, 64 heads on 8 of 128 dims: 70 us, 0.89 of the copy
+//     rate; 16 of them 22 us (0.72: start and end), 17 where L2 still has the summaries.  Many query tokens (512 of them against 1024 blocks: 97 us, 177 TFLOP/s) are bound by
 //     instructions, 235 for 16 products of 8 columns; the tensor cores' own operands in shared memory would
 //     serve them better.
 //   Selection: one to 32 warps per (query, KV head), a thread with 4 to 32 blocks that follow one another,
@@ -647,10 +647,11 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   P.scores = a->scores, P.status = a->dev_status;
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
-  // a tile per warp, or more where that still leaves every SM several CTAs
+  // a tile per warp, or more where that still leaves every SM the 4 CTAs that it holds at once (16 requests of
+  // 131072 tokens, 8 KV heads, from L2: 17 us; with 3 or 12 CTAs an SM 21 and 19)
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads, per_cta = echo::kScoreWarps * 16;
   const int64_t ctas = (a->max_blocks + per_cta - 1) / per_cta;
-  P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas * pairs / (12 * sms))));
+  P.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas * pairs / (4 * sms))));
   P.ctas = static_cast<int>((ctas + P.tiles - 1) / P.tiles);
   // columns (a prompt's query tokens) over several CTAs where blocks and heads give the SMs too few; a
   // token whose heads do not fit one chunk stays with one thread, which joins them
