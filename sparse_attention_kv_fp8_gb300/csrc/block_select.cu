@@ -541,7 +541,10 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
     auto bin = [&](float s) { return static_cast<int>(min(__float2uint_rz(fmaf(s, step, from)), kSelBins - 1u)); };
     uint32_t key;
     pick_kth(S, want, each, [](float s) { return s == s; }, bin, [](float s) { return score_key(s); }, key, need);
-    thr = key_score(key);
+    // The search by halving may end at a key that no score has, with none of its equals needed.  All but one of
+    // them are floats between two scores; 0x7fffffff, between the keys of zero and of the largest number below
+    // it, would be -0.0, which equals zero: the key of that number parts them as well.
+    thr = key_score(key - (key == 0x7fffffffu));
   }
 
   // ----- the blocks in order -----
