@@ -44,6 +44,7 @@ constexpr int kPxMaxGrid = 160;
 constexpr float kPxLazy = 8.f;        // log2 of how far a score may exceed its row's maximum
 constexpr float kPxLift = 7.f;        // fp16 weights are kept 2^7 up (their subnormals begin 2^-21 below the maximum)
 constexpr float kPxNone = -3.4028234664e38f;
+constexpr float kPxMinScale = 1e-37f; // of a row's scores: not zero, a masked score's infinity stays what it is
 
 struct PrefixParams {
   const uint16_t *q;
@@ -497,7 +498,9 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
       const bool rows = active && w4 * 32 < L.sub_rows(s);  // of this warp
       if (lane == 0) ctl->line[warp] = L;
       __syncwarp();
-      const float c = P.scale_log2 * (F16 && active ? qscale[s * 128 + w4 * 32 + lane] : 1.f);
+      // (a row of zeros has the least scale; times a small softmax scale it would be zero, and a masked score's
+      // infinity times that NaN: the host's bound on scale_log2 holds for the product)
+      const float c = F16 && active ? fmaxf(P.scale_log2 * qscale[s * 128 + w4 * 32 + lane], kPxMinScale) : P.scale_log2;
       float m = kPxNone, l = 0.f;
       for (int i = 0; active && i < n; ++i) {
         if (!px_wait(&ctl->s_full[s], ph_s, abort, P.status)) {
@@ -1163,7 +1166,7 @@ int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t st
   P.len = a->prefix_len, P.start = a->group_start, P.n_groups = a->n_groups;
   P.B = a->B, P.n_q = a->n_q, P.n_heads = a->n_heads, P.n_kv = a->n_kv_heads, P.group = a->n_heads / a->n_kv_heads;
   // (not zero: it has to leave a masked score's infinity what it is)
-  P.scale_log2 = std::max(std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift), 1e-37f);
+  P.scale_log2 = std::max(std::ldexp(std::fabs(a->scale) * 1.4426950408889634f, -a->k_shift), echo::kPxMinScale);
   P.v_scale = std::ldexp(1.f, -a->v_shift);
   P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
   P.first_o = reinterpret_cast<float *>(ws), P.first_ml = reinterpret_cast<float2 *>(ws + s.first_ml);
