@@ -833,9 +833,9 @@ int echo_block_evict(const echo_block_evict_args *args, void *stream);
  *            sets ECHO_DEV_BAD_INDEX, and the outputs of the requests around it are unspecified
  *   workspace device, 256-byte aligned, echo_prefix_attention_workspace_bytes() bytes; one workspace
  *            serves calls that run one after another
- * Prefix tokens past its length may hold any bytes.  Scores, the softmax and all sums are fp32; the
- * prefix's softmax weights enter its value product in 16 bits (bf16, with ECHO_BLOCK_FP4 fp16; the
- * tensor cores' operand type), the own tokens' as in echo_block_attention.
+ * Prefix tokens past its length may hold any bytes.  Scores, the softmax and all sums are fp32;
+ * softmax weights enter the value product as in echo_block_attention, the prefix's and the own
+ * tokens' (two bf16 terms; one fp16 term with ECHO_BLOCK_FP4).
  * Limits: those of echo_block_attention, n_groups in [1, 65536], n_rows at most 2^30, n_groups *
  * n_kv_heads * max_prefix_blocks below 2^31, (B * n_q * n_heads / n_kv_heads / 256 + n_groups) *
  * n_kv_heads * (max_prefix_blocks * block_tokens / 128 + 1) below 2^31 - 1024.  Launches 2 kernels,

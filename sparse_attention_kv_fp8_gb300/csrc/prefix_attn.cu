@@ -13,13 +13,13 @@
 //   A CTA holds the queries of a tile of up to 256 rows (two sub-tiles of 128) in shared memory
 //     and walks over chunks of 128 prefix tokens:  S = Q K^T (tcgen05.mma, M = 128 rows, N = 128
 //     tokens) into tensor memory, softmax by a warpgroup per sub-tile (a thread per row), P back
-//     into the tensor memory that S took (16 bit, half its columns), O += P V with P as the
-//     tensor-memory operand and V read along the tokens.  While one sub-tile's warpgroup is at
+//     into the tensor memory that S took (two bf16 terms of 64 columns each, or one in fp16), O += P V
+//     with P as the tensor-memory operand and V read along the tokens, once for each term.  While one sub-tile's warpgroup is at
 //     its softmax, the tensor cores work for the other; one thread issues all products, which
 //     run in the order of their issue, so S may overwrite the P that the product before it read.
 //   Blocks come by TMA, a box per run of tokens inside a block, into a ring of key and value
 //     tiles in the 128-byte swizzle.  4-bit rows come as they are (one bulk copy per sub-block of
-//     16 tokens) and eight warps convert them, exactly, to fp16 tiles.
+//     16 tokens) and four warps, two sub-blocks each, convert them, exactly, to fp16 tiles.
 //   Lazy maximum as in the decode kernel: O is rescaled (in tensor memory) only when a score
 //     exceeds its row's maximum by 2^8.
 //   All chunks of all (group, KV head, row tile) form one line, cut into equal pieces by the
@@ -535,9 +535,11 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
               for (int x = 0; x < 4; ++x) tops[x] = px_max3(tops[x], v[b][k + 2 * x], v[b][k + 2 * x + 1]);
           const float2 c2 = make_float2(c, c);
           float2 sums[2];
-          uint32_t p[16];
-          // weights of 32 tokens.  (One 16-bit term: 2^-9 (2^-12 in 4 bits) of a weight at most, of random
-          // sign; a second term would cost half as many products again)
+          uint32_t p[16], rest[F16 ? 1 : 16];
+          // Weights of 32 tokens.  In bf16 two terms, the second the bf16 of what the first leaves out, as in the
+          // decode kernel (one term: 2^-8 of a weight at most; the outputs' distance to 64 bits is then 2.1e-3
+          // where all of two terms' 1.65e-3 is their own rounding to bf16; half as many products less, 64 us for
+          // 83).  With 4-bit rows one fp16 term, as there: 2^-11 (two: 102 us for 72).
           auto weights = [&](int b) {
             const float2 m2 = make_float2(-m, -m);
 #pragma unroll
@@ -546,7 +548,16 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
               const float2 e = make_float2(ex2(y.x), ex2(y.y));
               sums[k & 1] = __fadd2_rn(sums[k & 1], e);
               p[k] = pack2<F16>(e.x, e.y);
+              if constexpr (!F16) {
+                const float2 left = __ffma2_rn(make_float2(__uint_as_float(p[k] << 16), __uint_as_float(p[k] & 0xffff0000u)),
+                                               make_float2(-1.f, -1.f), e);
+                rest[k] = pack2<F16>(left.x, left.y);
+              }
             }
+          };
+          auto put = [&](int b) {
+            px_st16(s_at + b * 16, p);
+            if constexpr (!F16) px_st16(s_at + 64 + b * 16, rest);
           };
           // The first weights are worked out with the maximum as it was, beside the search for the new
           // one, which seldom is far above it; if it is (and with a piece's first chunk) again.
@@ -584,17 +595,17 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
             sums[0] = sums[1] = make_float2(0.f, 0.f);
             weights(0);
           }
-          px_st16(s_at, p);
+          put(0);
           weights(1);
-          px_st16(s_at + 16, p);
+          put(1);
           px_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->p_full[s][0]);
           weights(2);
-          px_st16(s_at + 32, p);
+          put(2);
           weights(3);
-          px_st16(s_at + 48, p);
+          put(3);
           l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
           px_wait_st();
         } else if (lane == 0) {
@@ -761,12 +772,15 @@ __global__ void __launch_bounds__(PxCfg<FMT, D>::kThreads, 1)
         mma_commit(&ctl->s_full[s]);
         mbar_arrive(&ctl->s_full[s]);
       };
-      auto values = [&](int s, int tile, int half, bool more) {  // O of sub-tile s, half the tokens
+      auto values = [&](int s, int tile, int half, bool more) {  // O of sub-tile s, half the tokens, the terms of P
         tc_fence_after();
         const PxDesc b(px_mn_desc(ring + (tile % C::kSlots) * C::kTile, C::kBlock));
 #pragma unroll
         for (int kk = 0; kk < kPxChunk / 32; ++kk)
-          px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + half * 32 + kk * 8, b, (half * 64 + kk * 16) * 128 >> 4, kIdescO, more || kk > 0);
+#pragma unroll
+          for (int term = 0; term < (F16 ? 1 : 2); ++term)
+            px_mma_ts(tmem + 256 + s * D, tmem + s * 128 + term * 64 + half * 32 + kk * 8, b, (half * 64 + kk * 16) * 128 >> 4, kIdescO,
+                      more || kk > 0 || term > 0);
       };
       auto release = [&](int tile) { mma_commit(&ctl->kv_empty[tile % C::kSlots]); };
       for (bool more = true; more && ok; more = ok && L.next(P)) {
