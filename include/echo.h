@@ -703,6 +703,8 @@ int echo_block_scores(const echo_block_scores_args *args, void *stream);
  *   table    optional;  sel_rows [B][n_q][n_kv_heads][k] int32 device, optional (with a table):
  *            the blocks' rows, -1 beside -1
  *   len_out  [B][n_q] int32 device, optional: len (at least 0)
+ *   n_rows   rows of the cache that the table speaks of, 0 where the caller does not say: then only an
+ *            entry that no cache has (a row of 2^31 - 1 or above) is outside
  * echo_block_attention reads them with the queries folded into the requests: B * n_q requests of
  * one query token, table = sel_rows, sel, table_heads = n_kv_heads, max_blocks = k, ctx_len =
  * len_out.  With n_q == 1, sel is a selection for echo_prefetch_recall over a pool of block rows.
@@ -720,6 +722,7 @@ typedef struct echo_block_select_args {
     int32_t *sel_rows;
     int32_t *len_out;
     int32_t *dev_status;
+    int32_t n_rows;
 } echo_block_select_args;
 
 int echo_block_select(const echo_block_select_args *args, void *stream);
@@ -1027,7 +1030,7 @@ const char *echo_last_error_string(void);
    echo_stage.flags; 1.5: echo_pool_validate, echo_pool_validate_host; 1.6: block rows,
    echo_block_tables, echo_qk_norm_rope, echo_block_attention; 1.7: k_shift, v_shift;
    1.8: echo_block_summary, echo_block_scores, echo_block_select, echo_block_weights,
-   echo_block_evict, echo_prefix_attention). */
+   echo_block_evict, echo_prefix_attention; 1.9: n_rows of echo_block_select_args). */
 int32_t echo_version(void);
 
 /* Storage law of the metadata arrays of one pool (section 5.1): 4*n_h + 13*n_g. */

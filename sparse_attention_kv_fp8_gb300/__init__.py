@@ -127,7 +127,7 @@ class c_block_select_args(ctypes.Structure):
     _fields_ = [("scores", _P), ("ctx_len", _P), ("B", _I32), ("n_q", _I32), ("n_kv_heads", _I32),
                 ("block_tokens", _I32), ("k", _I32), ("first", _I32), ("last", _I32), ("table", _P),
                 ("table_heads", _I32), ("max_blocks", _I32), ("sel", _P), ("sel_rows", _P), ("len_out", _P),
-                ("dev_status", _P)]
+                ("dev_status", _P), ("n_rows", _I32)]
 
 
 class c_block_weights_args(ctypes.Structure):
@@ -746,10 +746,10 @@ def echo_block_scores(args: c_block_scores_args, stream=None):
 
 
 def make_block_select_args(scores, ctx_len, sel, block_tokens: int = 64, first: int = 0, last: int = 0, table=None,
-                           sel_rows=None, len_out=None, dev_status=None) -> c_block_select_args:
+                           sel_rows=None, len_out=None, dev_status=None, n_rows: int = 0) -> c_block_select_args:
     """Arguments of echo_block_select (see include/echo.h).  scores [B][n_q][n_kv_heads][max_blocks]
     fp32; ctx_len [B], sel and sel_rows [B][n_q][n_kv_heads][k], len_out [B][n_q] int32; table as
-    above or None."""
+    above or None; n_rows the cache's rows (0: not given), outside which no block is chosen."""
     B, n_q, Hk, n = (int(x) for x in scores.shape)
     a = c_block_select_args()
     a.scores, a.ctx_len = _typed(scores, "scores", _F32, (B, n_q, Hk, n)), _typed(ctx_len, "ctx_len", _INT, (B,))
@@ -763,7 +763,7 @@ def make_block_select_args(scores, ctx_len, sel, block_tokens: int = 64, first: 
     a.k, a.first, a.last = int(sel.shape[3]), int(first), int(last)
     a.sel_rows = _typed(sel_rows, "sel_rows", _INT, tuple(sel.shape))
     a.len_out = _typed(len_out, "len_out", _INT, (B, n_q))
-    a.dev_status = _typed(dev_status, "dev_status", _INT)
+    a.dev_status, a.n_rows = _typed(dev_status, "dev_status", _INT), int(n_rows)
     a._keep = (scores, ctx_len, sel, table, sel_rows, len_out, dev_status)
     return a
 

@@ -176,7 +176,7 @@ int echo_selftest_wait_timeout(int32_t which, int32_t *dev_status, void *stream)
   return launch_wait_probe(which, dev_status, static_cast<cudaStream_t>(stream));
 }
 
-int32_t echo_version(void) { return (1 << 16) | 8; }
+int32_t echo_version(void) { return (1 << 16) | 9; }
 
 int64_t echo_metadata_bytes(int64_t n_h, int64_t n_g) {
   return static_cast<int64_t>(sizeof(int32_t)) * n_h +
@@ -580,6 +580,7 @@ int echo_block_select(const echo_block_select_args *a, void *stream) {
   REQUIRE(a->B >= 0 && a->n_q >= 1 && a->n_q <= 65536, "bad sizes (B %d, n_q %d)", a->B, a->n_q);
   TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
   REQUIRE(a->max_blocks <= 32768, "max_blocks must be at most 32768 (got %d)", a->max_blocks);
+  REQUIRE(a->n_rows >= 0, "n_rows must be >= 0 (got %d)", a->n_rows);
   REQUIRE(a->k >= 1 && a->k <= (1 << 20), "k must be in [1, 2^20] (got %d)", a->k);
   REQUIRE(a->first >= 0 && a->last >= 0 && static_cast<long long>(a->first) + a->last <= a->k,
           "first and last must not be negative, their sum at most k (got %d, %d, k %d)", a->first, a->last, a->k);

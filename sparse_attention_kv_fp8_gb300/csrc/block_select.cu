@@ -450,6 +450,8 @@ struct SelectParams {
   uint32_t n;         // rows: (query, KV head)
   int32_t n_q, bs, k, first, last;
   BlockTable tab;     // (table: optional)
+  int32_t ids, more;  // block ids below `ids` have a row for each KV head, id `ids` for heads below `more` (a
+                      // table of each head's rows: 0)
   int32_t *sel, *sel_rows, *len_out;
   int32_t vec;        // rows of `scores` and of the table lie on 16-byte boundaries
   int32_t *status;
@@ -480,6 +482,7 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   float score[R], lo = INFINITY, hi = -INFINITY;  // (range of the finite ones)
   uint32_t must = 0, n_ok = 0, n_must;
   pick_clear(S);
+  const int32_t ids_end = P.tab.table ? P.ids + (h < P.more) : 1;   // of this head's entries
   const int32_t *ids = P.tab.table ? P.tab.table + (static_cast<int64_t>(b) * P.tab.heads + (P.tab.heads > 1 ? h : 0)) * P.tab.max_blocks : nullptr;
   {
     // (all loads before the first use, not one by one where the branches below want them)
@@ -507,9 +510,12 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
       }
     }
     const uint32_t plain = max(nb - P.first - P.last, 0);   // blocks that are neither of the first nor of the last
+    int32_t top = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool there = i0 + r < nb && id[r] >= 0, by_score = static_cast<uint32_t>(i0 + r - P.first) < plain;
+      const bool there = i0 + r < nb && static_cast<uint32_t>(id[r]) < static_cast<uint32_t>(ids_end);
+      const bool by_score = static_cast<uint32_t>(i0 + r - P.first) < plain;
+      if (i0 + r < nb) top = max(top, id[r]);
       float s = score[r] == score[r] ? score[r] : -INFINITY;
       must |= there && !by_score ? 1u << r : 0u;
       s = there && by_score ? s : NAN;
@@ -517,6 +523,7 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
       if (fabsf(s) < INFINITY) lo = fminf(lo, s), hi = fmaxf(hi, s);
       score[r] = s;
     }
+    if (ids && top >= ids_end) set_status(P.status, ECHO_DEV_BAD_INDEX);
   }
   static_assert(R <= 32, "a bit of `must` each");
   {  // (counts of 32768 at most: both in one word)
@@ -686,6 +693,8 @@ int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   P.n = static_cast<uint32_t>(a->B) * a->n_q * a->n_kv_heads;   // (below 2^31)
   P.n_q = a->n_q, P.bs = a->block_tokens, P.k = a->k, P.first = a->first, P.last = a->last;
   P.tab = {a->table, a->table_heads, a->max_blocks, a->n_kv_heads};
+  const int32_t rows = a->n_rows > 0 ? a->n_rows : 0x7fffffff, heads = a->table_heads > 1 ? 1 : a->n_kv_heads;
+  P.ids = rows / heads, P.more = rows % heads;
   P.sel = a->sel, P.sel_rows = a->sel_rows, P.len_out = a->len_out, P.status = a->dev_status;
   P.vec = a->max_blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a->scores) % 16 == 0 && reinterpret_cast<uintptr_t>(a->table) % 16 == 0;
   // the keys of a row in the registers of the threads that hold them: 8 or 16 each where rows fill the SMs
