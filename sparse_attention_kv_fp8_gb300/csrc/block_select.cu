@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(const
   pdl_wait();
   const int len = held_len(P.ctx_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, P.status,
                            part == 0 && h == 0 && c_from == 0 && threadIdx.x == 0);
-  const int blocks = (len + P.bs - 1) / P.bs, c_end = min(c_from + P.span, P.cols);
+  // (a block may have any number of tokens: the sum passes 31 bits)
+  const int blocks = (static_cast<uint32_t>(len) + P.bs - 1) / static_cast<uint32_t>(P.bs), c_end = min(c_from + P.span, P.cols);
   const int first = part * (kScoreWarps * 16) * P.tiles;
   if (first >= blocks) return;
 
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
   const int b = static_cast<uint32_t>(bj) / static_cast<uint32_t>(P.n_q), j = bj - b * P.n_q;
   const float *src = P.scores + static_cast<int64_t>(row) * P.tab.max_blocks;
   const int ctx = held_len(P.ctx_len[b], static_cast<int64_t>(P.tab.max_blocks) * P.bs, P.status, j == 0 && h == 0 && tid == 0);
-  const int len = max(ctx - (P.n_q - 1 - j), 0), nb = static_cast<uint32_t>(len + P.bs - 1) / static_cast<uint32_t>(P.bs);
+  const int len = max(ctx - (P.n_q - 1 - j), 0), nb = (static_cast<uint32_t>(len) + P.bs - 1) / static_cast<uint32_t>(P.bs);
   if (P.len_out && h == 0 && tid == 0) P.len_out[bj] = len;
 
   // Scores of blocks i0 and up; NaN: not to be chosen by its score (a block that is not there or not held,
