@@ -82,7 +82,8 @@ __device__ __forceinline__ int2 redone(const SummaryParams &P, int b, bool repor
   const int n = held_len(P.new_len[b], most, P.status, report);
   const int o = P.old_len ? held_len(P.old_len[b], most, P.status, report) : 0;
   if (n == o) return make_int2(0, 0);
-  return make_int2(min(o, n) / P.bs, (n + P.bs - 1) / P.bs);
+  // (the sum passes 31 bits for the longest contexts in blocks of more than 1024 tokens)
+  return make_int2(min(o, n) / P.bs, (static_cast<uint32_t>(n) + P.bs - 1) / static_cast<uint32_t>(P.bs));
 }
 
 template <int FMT>

@@ -1,9 +1,10 @@
-"""Blocks of more tokens than half of the 31 bits that count them: echo_block_scores and
-echo_block_select take any number."""
+"""Contexts of nearly 2^31 tokens, and blocks of any number of them: block counts that the 31 bits of a
+length do not hold on the way (echo_block_scores, echo_block_select, echo_block_summary)."""
 import numpy as np
 import pytest
 import torch
 
+import more_ref as mr
 import sparse_attention_kv_fp8_gb300 as echo
 from helpers import dev
 
@@ -32,3 +33,23 @@ def test_one_block_holds_the_context(bs, n):
     sel, ln = torch.full((1, 1, 1, 3), -7, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
     echo.echo_block_select(echo.make_block_select_args(scores, ctx, sel, block_tokens=bs, table=table, len_out=ln, dev_status=st))
     assert sel.flatten().tolist() == (list(range(want)) + [-1] * 3)[:3] and int(ln) == n and int(st) == 0
+
+
+@pytest.mark.parametrize("bs,blocks", [(1792, 1198372), (1296, 1657008), (512, (1 << 22) - 2)])
+def test_summaries_of_the_longest_contexts(bs, blocks):
+    """2^31 - 1024 tokens or a little less, of which three blocks are held, beside a short context."""
+    g = np.random.default_rng(0)
+    c = mr.Cache(echo.BLOCK_FP4, bs, 64, 1, 5, g)
+    table = np.full((2, blocks), -1, np.int32)
+    table[0, [0, blocks // 2, blocks - 1]] = [1, 3, 0]
+    table[1, 0] = 4
+    n = [blocks * bs - 7, 30]
+    out, st = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.spoil(0, range(bs - 7, bs))
+    c.spoil(4, range(30, bs))
+    echo.echo_block_summary(echo.make_block_summary_args(c.dev(), dev(table), dev(np.array(n, np.int32)), 1, out, fmt=echo.BLOCK_FP4,
+                                                         block_tokens=bs, dev_status=st))
+    want = np.zeros((5, 2, 64))
+    for r, m in ((1, bs), (3, bs), (0, bs - 7), (4, 30)):
+        want[r, 0], want[r, 1] = c.k[r, :m].min(0), c.k[r, :m].max(0)
+    assert (out.double().cpu().numpy() == want).all() and int(st) == 0
