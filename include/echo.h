@@ -789,8 +789,8 @@ int echo_block_weights(const echo_block_weights_args *args, void *stream);
  * not moved, with ECHO_DEV_BAD_INDEX.
  *   workspace  device, 256-byte aligned, echo_block_evict_workspace_bytes() bytes; one workspace
  *            serves calls that run one after another
- * Limits: keep >= 1, 0 <= sinks, recent, sinks + recent <= keep, max_blocks * block_tokens below
- * 2^31 - 1024, B * n_kv_heads below 2^26.  Launches 1 kernel, or 2 where more than 256 tokens of
+ * Limits: keep >= 1, 0 <= sinks, recent, sinks + recent <= keep, max_blocks * block_tokens at most
+ * 2^31 - 2^16, B * n_kv_heads below 2^26.  Launches 1 kernel, or 2 where more than 256 tokens of
  * a request and KV head may move.
  */
 typedef struct echo_block_evict_args {

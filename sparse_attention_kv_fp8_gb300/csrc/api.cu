@@ -633,6 +633,9 @@ int echo_block_evict(const echo_block_evict_args *a, void *stream) {
   TRY(check_evict_sizes(a->B, a->n_kv_heads, a->keep));
   TRY(check_block_rows(a->format, a->block_tokens, a->head_dim));
   TRY(check_block_table(a->table_heads, a->n_kv_heads, a->max_blocks, a->block_tokens));
+  // (a step over the slots, up to 16384 of them at once, stays within 31 bits)
+  REQUIRE(static_cast<long long>(a->max_blocks) * a->block_tokens <= (1ll << 31) - (1 << 16),
+          "max_blocks * block_tokens must be at most 2^31 - 2^16");
   REQUIRE(a->n_rows >= 1, "n_rows must be >= 1");
   REQUIRE(a->sinks >= 0 && a->recent >= 0 && static_cast<long long>(a->sinks) + a->recent <= a->keep,
           "sinks and recent must not be negative, their sum at most keep (got %d, %d, keep %d)", a->sinks, a->recent, a->keep);
