@@ -833,7 +833,8 @@ int echo_block_evict(const echo_block_evict_args *args, void *stream);
  *   prefix_len    [n_groups] int32 device, any length (0: none; it may end inside a block); above
  *            max_prefix_blocks * block_tokens it is clamped with ECHO_DEV_BAD_INDEX
  *   group_start   [n_groups + 1] int32 device, ascending, from 0 to B at most; a value that is not
- *            sets ECHO_DEV_BAD_INDEX, and the outputs of the requests around it are unspecified
+ *            sets ECHO_DEV_BAD_INDEX, and the outputs of the requests around it (where groups then
+ *            overlap, of all) are unspecified
  *   workspace device, 256-byte aligned, echo_prefix_attention_workspace_bytes() bytes; one workspace
  *            serves calls that run one after another
  * Prefix tokens past its length may hold any bytes.  Scores, the softmax and all sums are fp32;

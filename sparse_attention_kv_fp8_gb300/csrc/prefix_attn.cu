@@ -91,8 +91,12 @@ __device__ __forceinline__ PxGroup px_group(const PrefixParams &P, int g, bool r
   x.chunks = (x.len + kPxChunk - 1) / kPxChunk;
   return x;
 }
-// (below 2^31 over all groups: the host checks the sizes)
+// (below 2^31 - 1024 over groups that do not overlap: the host checks the sizes)
 __device__ __forceinline__ int px_units(const PrefixParams &P, const PxGroup &x) { return P.n_kv * x.tiles * x.chunks; }
+// Group starts that are not ascending make groups overlap, and their line may be longer: sums stop at kPxMost,
+// and a line of that length is taken for an empty one.
+constexpr uint32_t kPxMost = 0x7fffffffu;
+__device__ __forceinline__ uint32_t px_add(uint32_t a, uint32_t b) { return min(a + b, kPxMost); }
 
 // Group g (the same for the whole warp): from the lane that has it, `mine`, where there is one a lane.
 __device__ __forceinline__ PxGroup px_group_of(const PrefixParams &P, const PxGroup &mine, int g) {
@@ -103,16 +107,17 @@ __device__ __forceinline__ PxGroup px_group_of(const PrefixParams &P, const PxGr
   return x;
 }
 
-// exclusive sum over the lanes of a warp, and the total
-__device__ __forceinline__ int px_scan(int mine, int &total) {
-  int upto = mine;
+// exclusive sum over the lanes of a warp, and the total (0 instead of kPxMost)
+__device__ __forceinline__ int px_scan(uint32_t mine, int &total) {
+  uint32_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(~0u, upto, d);
-    if ((threadIdx.x & 31) >= d) upto += y;
+    const uint32_t y = __shfl_up_sync(~0u, upto, d);
+    if ((threadIdx.x & 31) >= d) upto = px_add(upto, y);
   }
-  total = __shfl_sync(~0u, upto, 31);
-  return upto - mine;
+  const uint32_t all = __shfl_sync(~0u, upto, 31);
+  total = all == kPxMost ? 0 : static_cast<int>(all);
+  return static_cast<int>(upto - mine);
 }
 
 // How the tiles are cut.  Whole: every tile of group g into ceil(chunks / whole) equal pieces, one
@@ -170,10 +175,11 @@ struct PxLine {
   __device__ __forceinline__ bool begin(const PrefixParams &P, bool report) {
     const int lane = threadIdx.x & 31;
     const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
-    int mine = 0, total;
+    uint32_t sum = 0;
+    int total;
     PxGroup last{};
-    for (int i = g0; i < g1; ++i) last = px_group(P, i, report), mine += px_units(P, last);
-    const int before = px_scan(mine, total);
+    for (int i = g0; i < g1; ++i) last = px_group(P, i, report), sum = px_add(sum, px_units(P, last));
+    const int before = px_scan(sum, total), mine = sum;
     const PxPlan plan = px_plan(P, last, total);
     if (plan.whole) {
       int at = blockIdx.x;
@@ -937,17 +943,18 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
 
   // where the row's tile lies on the line
   const int run = (P.n_groups + 31) / 32, g0 = min(lane * run, P.n_groups), g1 = min(g0 + run, P.n_groups);
-  int mine = 0, u = 0, total, at = -1, r = 0;
+  uint32_t mine = 0;
+  int u = 0, total, at = -1, r = 0;
   PxGroup last{};
   for (int g = g0; g < g1; ++g) {
     const PxGroup x = last = px_group(P, g, false);
     const int in = (b - x.b0) * P.n_q * P.group;   // (rows of a request outside the group are not below x.rows)
     if (at < 0 && x.chunks > 0 && b >= x.b0 && in < x.rows) at = g, u = mine, r = in + j * P.group + head - h * P.group;
-    mine += px_units(P, x);
+    mine = px_add(mine, px_units(P, x));
   }
   u += px_scan(mine, total);
   const PxPlan plan = px_plan(P, last, total);
-  const uint32_t who = __ballot_sync(~0u, at >= 0);
+  const uint32_t who = __ballot_sync(~0u, at >= 0 && total > 0);
   int first = 0, pieces = 0, step = 1;   // the tile's first CTA, how many pieces it has, their CTAs' distance
   if (who) {
     const int src = __ffs(who) - 1;
