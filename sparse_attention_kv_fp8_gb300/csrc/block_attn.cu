@@ -288,8 +288,11 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) block_attn_kernel(const Bloc
   float2 *fin = reinterpret_cast<float2 *>(ba_smem + C::kOffFin);     // [kRows]
   const int heads = P.n_kv * P.mgroups;
   pdl_launch_dependents();  // (what follows waits for this grid's end all the same)
+  // (Beside: the call's inputs are read without a wait of this grid's own.  The kernel before let this one start
+  // after its own wait, so whatever wrote them had ended before; that this grid sees it rests on that order and
+  // goes beyond what the documents promise, which is sight after a wait only.)
   if (!P.beside) pdl_wait();
-  else __threadfence();     // (the kernel before began after its own wait: what came before that is there)
+  else __threadfence();
 
   // ===== this CTA's range of the line: chunks 0 .. n_chunks from its first =====
   LinePos cur;

@@ -20,8 +20,8 @@
 //     place); keys go from memory to registers with nothing in between, two sub-blocks of 16
 //     tokens a warp at a time (4 bits: one, and the codes of four under way), the exponentials of a
 //     column summed over the quad; a lane adds what its token had, read a round ahead.  16 requests of up to
-//     32768 tokens, 64 heads on 8 of 128 dims: bf16 130 us (0.96 of the copy rate), 4 bits 74 us
-//     (0.51: conversions and products; what a token had, read where it was added, cost another 50).
+//     32768 tokens, 64 heads on 8 of 128 dims: bf16 130 us (0.96 of the copy rate; 138 to 146 on new inputs
+//     every call), 4 bits 74 us (0.51: conversions and products; what a token had, read where it was added, cost another 50).
 //   Eviction: a CTA per (b, h) finds the weight of the last token that stays from counts over the
 //     range of the weights (block_pick.cuh), and lists holes and movers in order; the
 //     moves follow in the same CTA when they are few, else in a second kernel over the whole GPU.

@@ -101,7 +101,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 namespace echo_host {
 
 // Launch that may be made ready while the kernel before it on the stream still runs (programmatic
-// stream serialization): for kernels that call pdl_wait() before they touch any memory.
+// stream serialization): for kernels that call pdl_wait() before they touch any memory (prefix attention's
+// own tokens and merge read the call's inputs before: they say why).
 // Their loads are plain ones: the non-coherent path (__ldg) is for data that nothing writes while
 // the kernel is there, and the kernel before it, still running then, may write any input.
 template <typename... Params, typename... Args>

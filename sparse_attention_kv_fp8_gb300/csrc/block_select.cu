@@ -14,7 +14,7 @@
 //   Summary: a warp per (block, KV head), or a CTA where blocks are large: 16-byte loads of its keys, eight
 //     a lane under way, packed minima and maxima, joined over the lanes.  The blocks that changed are one
 //     line over the requests, found by every CTA from the lengths.  8 prompts of 16384 tokens (8 KV heads of
-//     128 dims, bf16, blocks of 64): 38 us, 4.8 TB/s; one more token for 64 requests: 5.4 us, three chained
+//     128 dims, bf16, blocks of 64): 39-40 us, 4.6-4.75 TB/s; one more token for 64 requests: 5.4 us, three chained
 //     loads (length, id, keys) and a launch.
 //   Scores: 16 blocks x 8 columns with mma.m16n8k16.  The order of a contraction's dims is free,
 //     so a lane reads 16 contiguous bytes of "its" two blocks per 8 dims of a quarter and feeds them
@@ -22,15 +22,15 @@
 //     no shared memory.  The 8 columns are the heads of one query token, or of several where a
 //     group has fewer, so the maximum over a group stays within a quad.
 //     64 requests of up to 131072 tokens, blocks of 64, 64 heads on 8 of 128 dims: 70 us, 0.89 of the copy
-//     rate; 16 of them 22 us (0.72: start and end), 17 where L2 still has the summaries.  Many query tokens (512 of them against 1024 blocks: 97 us, 177 TFLOP/s) are bound by
+//     rate; 16 of them 22-23 us (0.70: start and end), 17 where L2 still has the summaries.  Many query tokens (512 of them against 1024 blocks: 97 us, 177 TFLOP/s) are bound by
 //     instructions, 235 for 16 products of 8 columns; the tensor cores' own operands in shared memory would
 //     serve them better.
 //   Selection: one to 32 warps per (query, KV head), a thread with 4 to 32 blocks that follow one another,
 //     their scores in registers.  The k-th best is found from counts over the range of the scores
 //     (block_pick.cuh), then a sum over the threads gives each the place of what it writes: those above,
 //     and the first of its equals.
-//     8000 rows of 1024 blocks: 29 us, bound by instructions (the pipe of comparisons 62% busy); 256 rows of
-//     2048: 6 us, of which a launch and the chain of loads, counts and barriers are nearly all.
+//     8000 rows of 1024 blocks: 30 us, bound by instructions (the pipe of comparisons 63% busy); 256 rows of
+//     2048: 6.5 us, of which a launch and the chain of loads, counts and barriers are nearly all.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -700,9 +700,9 @@ int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   P.sel = a->sel, P.sel_rows = a->sel_rows, P.len_out = a->len_out, P.status = a->dev_status;
   P.vec = a->max_blocks % 4 == 0 && reinterpret_cast<uintptr_t>(a->scores) % 16 == 0 && reinterpret_cast<uintptr_t>(a->table) % 16 == 0;
   // the keys of a row in the registers of the threads that hold them: 8 or 16 each where rows fill the SMs
-  // (8000 rows of 512 blocks: one warp 14.3 us, two 16.8, four 22.2), fewer each where they do not and a
-  // thread's own keys are what a row waits for (256 rows of 4096: 16 warps 6.4 us, 8 warps 9.2).  Both of
-  // 1024 blocks: 256 rows 4.4 and 4.3 us, 32 rows 3.5 and 3.8, 4000 rows 20.8 and 15.5
+  // (8000 rows of 512 blocks: one warp 15.2 us, two 17.6, four 23.3), fewer each where they do not and a
+  // thread's own keys are what a row waits for (256 rows of 4096: 16 warps 6.6 us, 8 warps 8.5).  Both of
+  // 1024 blocks: 256 rows 4.6 and 4.4 us, 32 rows 3.6 and 3.9, 4000 rows 22.1 and 16.4
   int sms = 0;
   if (int rr = sm_count(&sms)) return rr;
   const bool few = P.n <= 4u * sms;

@@ -26,11 +26,12 @@
 //     lengths on the device, one per CTA.  Each (tile, piece) leaves its maxima, sums and O in
 //     fp32: pieces that begin with a tile in a row per query row, the others in a slot per CTA.
 //     The merge kernel takes them in order, so results do not depend on timing.
-//   64 requests of 64 heads (8 KV heads of 128 dims), a prefix of 32768: bf16 64 us, 1050 TFLOP/s (256
-//     requests: 216 us, 1270), 4 bits 72 us.  The tensor cores are busy half of the time and the exponentials'
-//     pipe a quarter: a warpgroup's chunk is a chain (scores, maximum, weights, hand-over) that two sub-tiles
-//     cover only in part; more would need registers for a third.  A prefix of 131072 for 8 requests:
-//     89 us, 0.92 of the copy rate.  Short ones (1000 tokens: 10.5 us) are two kernels' chains of latencies.
+//   64 requests of 64 heads (8 KV heads of 128 dims), a prefix of 32768: bf16 84 us, 810 TFLOP/s of 4 D a row
+//     and token (256 requests: 287 us, 955), 4 bits 72 us.  The tensor cores are busy half of the time (half as
+//     many products again in bf16, for the weights' second term) and the exponentials' pipe a fifth: a
+//     warpgroup's chunk is a chain (scores, maximum, weights, hand-over) that two sub-tiles cover only in part;
+//     more would need registers for a third.  A prefix of 131072 for 8 requests, one sub-tile: 107 us, 0.76 of
+//     the copy rate, the chain.  Short ones (1000 tokens: 11 us) are two kernels' chains of latencies.
 #include <algorithm>
 #include <cmath>
 
@@ -128,9 +129,8 @@ __device__ __forceinline__ int px_scan(uint32_t mine, int &total) {
 constexpr int kPxChange = 5;
 // Where the own tokens have work for many SMs, shares of up to kPxRoom chunks leave them half: they wait for
 // those of a short prefix less than the SMs would wait for them (64 requests of 64 heads, a prefix of
-// 2048 and own tokens of up to 100 / 1000: 31.3 / 53.5 -> 26.4 / 44.6 us, of 4096 and 1000 56.5 -> 50.2,
-// before the merge took less;
-// shares of 8: 16 requests, 2048 and 100 19 -> 24 us).
+// 2048 and own tokens of up to 100 / 1000: 31.0 / 52.3 -> 25.7 / 43.2 us, of 4096 and 1000 56.7 -> 49.7; 16
+// requests, 2048 and 100 21.9 -> 18.7).
 constexpr int kPxRoom = 6;
 constexpr int kPxFewGroups = 8;       // (more groups: their tiles are not tried)
 
@@ -365,8 +365,8 @@ struct PxCfg {
   // Warpgroups: two of softmax, one of the producer and the issuer (and two idle warps), one that
   // converts.  A launch gives every thread the same registers (168 of 384 threads, 128 of 512); they
   // are handed over to the softmax, whose threads keep a row of 128 scores.  (Two threads a row, 64
-  // scores each, meet for the maximum in every chunk: 70 us where one takes 65, with half the row
-  // each still 0.75 us a chunk.)
+  // scores each, meet for the maximum in every chunk: 70 us where one took 65, both with one term a
+  // weight.)
   static constexpr int kLoadWarp = 8, kConvWarp = 12;
   static constexpr int kThreads = 32 * (kConvWarp + kConvWarps);
   static constexpr int kRegs = kFp4 ? 128 : 168, kRegsSoft = kFp4 ? 176 : 208, kRegsLoad = kFp4 ? 80 : 88, kRegsConv = kFp4 ? 80 : 0;
@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(kPxMergeWarps * 32) prefix_merge_kernel(const 
   const int64_t at_row = static_cast<int64_t>(blockIdx.x) * (kPxMergeWarps / RW) + warp / RW, row = at_row < all ? at_row : all - 1;
   pdl_launch_dependents();
   // (Where the row's tile lies is found before the wait: it comes of the call's inputs alone, and the
-  // prefix's kernel, which lets this one and the own tokens' start, has waited for whatever wrote them.)
+  // prefix's kernel, which lets this one and the own tokens' start, has waited for whatever wrote them.
+  // That it is seen here without a wait goes, as in the own tokens' kernel, beyond what the documents promise.)
   const uint32_t bj = static_cast<uint32_t>(row) / static_cast<uint32_t>(P.n_heads), head = static_cast<uint32_t>(row) - bj * P.n_heads;
   const int b = bj / static_cast<uint32_t>(P.n_q), j = bj - b * P.n_q, h = head / static_cast<uint32_t>(P.group);
 
@@ -1210,8 +1211,8 @@ int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t st
     o.k_shift = a->k_shift, o.v_shift = a->v_shift;
     if (int rr = launch_block_attention_f32(&o, reinterpret_cast<float *>(ws + s.own_o), stream)) return rr;
   }
-  // four warps a row where there are few rows (1024 of a prefix of 2048: 13.5 us in all, with one 15.2), one
-  // where four would make several waves of CTAs (4096 of a prefix of 32768: 63.7 us, with four 70.3)
+  // four warps a row where there are few rows (1024 of a prefix of 2048: 14.8 us in all, with one 16.4), one
+  // where four would make several waves of CTAs (4096 of a prefix of 32768: 83.4 us, with four 90.2)
   e = a->head_dim == 128 ? (rows <= 2048 ? go_merge<128, 4>(P, rows, stream) : go_merge<128, 1>(P, rows, stream))
                          : (rows <= 2048 ? go_merge<64, 4>(P, rows, stream) : go_merge<64, 1>(P, rows, stream));
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "prefix attention merge launch");
