@@ -633,7 +633,8 @@ int echo_block_attention(const echo_block_attention_args *args, void *stream);
  * [B][max_blocks] block ids shared by the KV heads (table_heads == 1) or
  * [B][n_kv_heads][max_blocks] rows (table_heads == n_kv_heads); a negative entry is a block
  * that is not held, one outside the rows counts as such and sets ECHO_DEV_BAD_INDEX, as does a
- * length above max_blocks * block_tokens, which is clamped.
+ * length above max_blocks * block_tokens, which is clamped.  These calls and the next two take up to
+ * 65536 query tokens, heads and KV heads each.
  *
  * echo_block_summary: the smallest and the largest entry of the keys of a cache row, per dim,
  * over the tokens that its request holds.  Request b went from old_len[b] to new_len[b] tokens
@@ -708,8 +709,8 @@ int echo_block_scores(const echo_block_scores_args *args, void *stream);
  * echo_block_attention reads them with the queries folded into the requests: B * n_q requests of
  * one query token, table = sel_rows, sel, table_heads = n_kv_heads, max_blocks = k, ctx_len =
  * len_out.  With n_q == 1, sel is a selection for echo_prefetch_recall over a pool of block rows.
- * Limits: k >= 1, 0 <= first, last, first + last <= k, max_blocks <= 32768, B * n_q * n_kv_heads
- * below 2^31.  Launches 1 kernel.
+ * Limits: k in [1, 2^20], 0 <= first, last, first + last <= k, max_blocks <= 32768, B * n_q *
+ * n_kv_heads below 2^31.  Launches 1 kernel.
  */
 typedef struct echo_block_select_args {
     const float *scores;

@@ -617,13 +617,6 @@ __global__ void __launch_bounds__(kMvWarps * 32) block_move_kernel(const EvictPa
 
 namespace echo_host {
 
-static int evict_sms(int *sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block eviction device");
-}
-
 int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream) {
   echo::WeightParams P{};
   P.q = a->q, P.rows = reinterpret_cast<const uint8_t *>(a->rows);
@@ -637,7 +630,7 @@ int launch_block_weights(const echo_block_weights_args *a, cudaStream_t stream) 
   P.lse = a->lse, P.acc = a->acc, P.acc_out = a->acc_out, P.decay = a->decay;
   P.status = a->dev_status;
   int sms = 0;
-  if (int rr = evict_sms(&sms)) return rr;
+  if (int rr = sm_count(&sms, "block eviction device")) return rr;
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads;
   const int64_t nsub = static_cast<int64_t>(a->max_blocks) * P.bsub;
   // two sub-blocks a warp, or more where every SM still has several CTAs (a CTA's first loads and queries
@@ -670,7 +663,7 @@ static int go_evict(echo::EvictParams P, cudaStream_t stream) {
   if (smem > 32768)   // (beside 9 KB of its own)
     if (int rr = smem_limit_once(attr, echo::block_evict_kernel<FMT, D, 1024, true>, echo::kEvStaged * 4, "block eviction smem attribute")) return rr;
   int sms = 0;
-  if (int rr = evict_sms(&sms)) return rr;
+  if (int rr = sm_count(&sms, "block eviction device")) return rr;
   const int64_t moves = std::max<int64_t>(0, std::min<int64_t>(P.keep, most - P.keep));
   P.move_here = moves <= 256;
   P.move_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((moves + 63) / 64, 8ll * sms / pairs)));

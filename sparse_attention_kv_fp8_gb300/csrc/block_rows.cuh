@@ -100,6 +100,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 
 namespace echo_host {
 
+// SMs of the current device; `what` names the call in the error
+inline int sm_count(int *sms, const char *what) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, what);
+}
+
 // Launch that may be made ready while the kernel before it on the stream still runs (programmatic
 // stream serialization): for kernels that call pdl_wait() before they touch any memory (prefix attention's
 // own tokens and merge read the call's inputs before: they say why).

@@ -598,13 +598,6 @@ __global__ void __launch_bounds__(W == 1 ? kSelRows * 32 : W * 32) block_select_
 
 namespace echo_host {
 
-static int sm_count(int *sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "block selection device");
-}
-
 template <int FMT, int D, int TEAM>
 static int go_summary(const echo::SummaryParams &P, cudaStream_t stream) {
   static std::atomic<bool> attr[kMaxDevices];
@@ -612,7 +605,7 @@ static int go_summary(const echo::SummaryParams &P, cudaStream_t stream) {
   if (smem > 40960)
     if (int rr = smem_limit_once(attr, echo::block_summary_kernel<FMT, D, TEAM>, (16384 + 1) * 4, "block summary smem attribute")) return rr;
   int sms = 0;
-  if (int rr = sm_count(&sms)) return rr;
+  if (int rr = sm_count(&sms, "block selection device")) return rr;
   const int64_t most = static_cast<int64_t>(P.B) * P.tab.max_blocks * P.tab.n_kv;
   constexpr int kTeams = echo::kSumThreads / TEAM;
   const int64_t ctas = (most + kTeams - 1) / kTeams;
@@ -658,7 +651,7 @@ int launch_block_scores(const echo_block_scores_args *a, cudaStream_t stream) {
   P.scale = std::fabs(a->scale), P.q_sign = a->scale < 0.f ? 0x80008000u : 0u;
   P.scores = a->scores, P.status = a->dev_status;
   int sms = 0;
-  if (int rr = sm_count(&sms)) return rr;
+  if (int rr = sm_count(&sms, "block selection device")) return rr;
   // a tile per warp, or more where that still leaves every SM the 4 CTAs that it holds at once (16 requests of
   // 131072 tokens, 8 KV heads, from L2: 17 us; with 3 or 12 CTAs an SM 21 and 19)
   const int64_t pairs = static_cast<int64_t>(a->B) * a->n_kv_heads, per_cta = echo::kScoreWarps * 16;
@@ -704,7 +697,7 @@ int launch_block_select(const echo_block_select_args *a, cudaStream_t stream) {
   // thread's own keys are what a row waits for (256 rows of 4096: 16 warps 6.6 us, 8 warps 8.5).  Both of
   // 1024 blocks: 256 rows 4.6 and 4.4 us, 32 rows 3.6 and 3.9, 4000 rows 22.1 and 16.4
   int sms = 0;
-  if (int rr = sm_count(&sms)) return rr;
+  if (int rr = sm_count(&sms, "block selection device")) return rr;
   const bool few = P.n <= 4u * sms;
   if (a->max_blocks <= 256) return go_select<1, 8>(P, stream);
   if (a->max_blocks <= 512) return few ? go_select<4, 4>(P, stream) : go_select<1, 16>(P, stream);

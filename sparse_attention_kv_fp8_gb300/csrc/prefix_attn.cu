@@ -1171,10 +1171,8 @@ static cudaError_t go_merge(const echo::PrefixParams &P, int64_t rows, cudaStrea
 }
 
 int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "prefix attention device");
+  int sms = 0;
+  if (int rr = sm_count(&sms, "prefix attention device")) return rr;
   const int64_t rows = static_cast<int64_t>(a->B) * a->n_q * a->n_heads;
   const PxSpace s = px_space(rows, a->n_q * (a->n_heads / a->n_kv_heads), a->head_dim);
   uint8_t *ws = static_cast<uint8_t *>(a->workspace);
@@ -1213,7 +1211,7 @@ int launch_prefix_attention(const echo_prefix_attention_args *a, cudaStream_t st
   }
   // four warps a row where there are few rows (1024 of a prefix of 2048: 14.8 us in all, with one 16.4), one
   // where four would make several waves of CTAs (4096 of a prefix of 32768: 83.4 us, with four 90.2)
-  e = a->head_dim == 128 ? (rows <= 2048 ? go_merge<128, 4>(P, rows, stream) : go_merge<128, 1>(P, rows, stream))
+  const cudaError_t e = a->head_dim == 128 ? (rows <= 2048 ? go_merge<128, 4>(P, rows, stream) : go_merge<128, 1>(P, rows, stream))
                          : (rows <= 2048 ? go_merge<64, 4>(P, rows, stream) : go_merge<64, 1>(P, rows, stream));
   return e == cudaSuccess ? ECHO_OK : cuda_fail(e, "prefix attention merge launch");
 }
