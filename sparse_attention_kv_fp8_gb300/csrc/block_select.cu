@@ -14,7 +14,7 @@
 //   Summary: a warp per (block, KV head), or a CTA where blocks are large: 16-byte loads of its keys, eight
 //     a lane under way, packed minima and maxima, joined over the lanes.  The blocks that changed are one
 //     line over the requests, found by every CTA from the lengths.  8 prompts of 16384 tokens (8 KV heads of
-//     128 dims, bf16, blocks of 64): 39-40 us, 4.6-4.75 TB/s; one more token for 64 requests: 5.4 us, three chained
+//     128 dims, bf16, blocks of 64): 39-41 us, 4.5-4.75 TB/s; one more token for 64 requests: 5.4 us, three chained
 //     loads (length, id, keys) and a launch.
 //   Scores: 16 blocks x 8 columns with mma.m16n8k16.  The order of a contraction's dims is free,
 //     so a lane reads 16 contiguous bytes of "its" two blocks per 8 dims of a quarter and feeds them
